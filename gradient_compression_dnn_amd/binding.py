@@ -24,6 +24,11 @@ GC_MAX_BIN_LEN = 4096
 GC_MAX_MESSAGES = 64
 GC_MAX_SEGMENT_LEN = 0xFFFC0000
 GC_MAX_REPLICAS = 16
+GC_F32, GC_BF16, GC_F16 = 0, 1, 2
+GC_TOKENS_I32, GC_TOKENS_I64 = 0, 1
+GC_MUON_SCALE_NONE, GC_MUON_SCALE_SHAPE, GC_MUON_SCALE_RMS = 0, 1, 2
+GC_MAX_MATRIX_DIM = 1 << 20
+GC_MAX_ORTH_STEPS = 16
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgradcomp.so")
 
@@ -57,6 +62,17 @@ class gc_dgc_options(ctypes.Structure):
 class gc_adacomp_options(ctypes.Structure):
     _fields_ = [("scale_factor", ctypes.c_float), ("rule", ctypes.c_int),
                 ("reserved", ctypes.c_uint32 * 2)]
+
+
+class gc_orth_options(ctypes.Structure):
+    _fields_ = [("steps", ctypes.c_int), ("eps", ctypes.c_float),
+                ("coef", (ctypes.c_float * 3) * GC_MAX_ORTH_STEPS), ("reserved", ctypes.c_uint32 * 2)]
+
+
+class gc_muon_options(ctypes.Structure):
+    _fields_ = [("orth", gc_orth_options), ("momentum", ctypes.c_float), ("lr", ctypes.c_float),
+                ("weight_decay", ctypes.c_float), ("momentum_kind", ctypes.c_int), ("scale", ctypes.c_int),
+                ("reserved", ctypes.c_uint32)]
 
 
 _lib = None
@@ -108,6 +124,21 @@ _SIGS = {
     "gc_slimdp_explore": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_uint64, ctypes.c_uint64, _P, _P,
                                          ctypes.c_size_t, _P]),
     "gc_slimdp_core_values": (ctypes.c_int, [_P, _P, _P, _P, _P]),
+    "gc_embed_lookup": (ctypes.c_int, [_P, ctypes.c_int, ctypes.c_uint32, _P, _P, ctypes.c_int, ctypes.c_uint64,
+                                       ctypes.c_float, _P, ctypes.c_int, ctypes.c_uint64, _P]),
+    "gc_embed_workspace_bytes": (ctypes.c_size_t, [_P, ctypes.c_int, ctypes.c_uint32, ctypes.c_uint64]),
+    "gc_embed_grad": (ctypes.c_int, [_P, ctypes.c_int, ctypes.c_uint32, _P, ctypes.c_int, ctypes.c_uint64, _P,
+                                     ctypes.c_int, ctypes.c_uint64, ctypes.c_float, _P, ctypes.c_int, _P,
+                                     ctypes.c_size_t, _P]),
+    "gc_embed_message_cap": (ctypes.c_uint64, [_P, ctypes.c_int, ctypes.c_uint32, ctypes.c_uint64]),
+    "gc_embed_message": (ctypes.c_int, [_P, ctypes.c_int, ctypes.c_uint32, _P, ctypes.c_int, ctypes.c_uint64, _P,
+                                        ctypes.c_int, ctypes.c_uint64, ctypes.c_float, _P, _P, ctypes.c_size_t, _P]),
+    "gc_matrix_plan_create": (ctypes.c_int, [_P, _P, _P]),
+    "gc_matrix_plan_destroy": (None, [_P]),
+    "gc_matrix_plan_upload": (ctypes.c_int, [_P]),
+    "gc_matrix_plan_workspace_bytes": (ctypes.c_size_t, [_P]),
+    "gc_orthogonalize": (ctypes.c_int, [_P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "gc_muon_step": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "gc_timing_enable": (ctypes.c_int, [ctypes.c_char_p]),
     "gc_timing_take": (ctypes.c_int, [ctypes.c_char_p, _P, _P]),
     "gc_stream_probe": (ctypes.c_int, [_P, _P, _P, _P, _P, ctypes.c_uint64, _P]),
@@ -118,7 +149,9 @@ KERNELS = ("dgc_norm", "dgc_prep", "dgc_prepare", "dgc_sample", "dgc_bound", "dg
            "ada_fold", "ada_emit", "ada_residual",
            "pack_plan", "pack_write", "pack_relayout", "pack_rewrite", "pack_main", "pack_fix", "unpack_layout",
            "unpack_write", "decode_index", "decode", "dcd",
-           "dcd_decode", "dcd_mix", "ecd_compress", "ecd_update", "slimdp_values", "stream_probe")
+           "dcd_decode", "dcd_mix", "ecd_compress", "ecd_update", "slimdp_values", "stream_probe",
+           "embed_lookup", "embed_rank", "embed_merge", "embed_heads", "embed_rows", "embed_sum", "embed_join",
+           "embed_empty", "orth_norm", "orth_scale", "orth_split", "orth_gram", "orth_poly", "orth_apply")
 
 
 def gc_timing_enable(kernels) -> None:
@@ -509,3 +542,166 @@ def gc_slimdp_core_values(core_plan: Plan, core: Sparse, delta, values):
     msg = core.checked(core_plan, "core")
     _check(load().gc_slimdp_core_values(core_plan.handle, ctypes.byref(msg), _f32(delta, core_plan.n_total, "delta"),
                                         _f32(values, core_plan.total_k, "values"), _stream(values)))
+
+
+# ------------------------------------------------------------- embedding
+_FLOAT_TYPES = {torch.float32: GC_F32, torch.bfloat16: GC_BF16, torch.float16: GC_F16}
+_TOKEN_TYPES = {torch.int32: GC_TOKENS_I32, torch.int64: GC_TOKENS_I64}
+
+
+def _tokens(tokens):
+    """(pointer, GC_TOKENS_*, count) of a contiguous CUDA int32 or int64 tensor of any shape."""
+    if not torch.is_tensor(tokens) or tokens.dtype not in _TOKEN_TYPES or not tokens.is_cuda or not tokens.is_contiguous():
+        raise ValueError("tokens: need a contiguous CUDA int32 or int64 tensor")
+    return _ptr(tokens), _TOKEN_TYPES[tokens.dtype], tokens.numel()
+
+
+def _batch_rows(t, tokens, cols: int, name: str):
+    """(pointer, GC_* type, row stride) of a batch: the tokens' shape with
+    cols appended, one stride between its rows, unit stride inside them."""
+    ok = torch.is_tensor(t) and t.dtype in _FLOAT_TYPES and t.is_cuda and t.dim() >= 1
+    if not ok or tuple(t.shape) != (*tokens.shape, cols) or t.device != tokens.device:
+        raise ValueError(f"{name}: need a CUDA fp32, bf16 or fp16 tensor of shape {(*tokens.shape, cols)} "
+                         "on the tokens' device")
+    if t.numel() == 0:
+        return _ptr(t), _FLOAT_TYPES[t.dtype], cols
+    if cols > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    # dimensions of more than one row, from the last: each must continue the one behind it
+    stride, step = None, None
+    for size, st in list(zip(t.shape[:-1], t.stride()[:-1]))[::-1]:
+        if size == 1:
+            continue
+        if stride is None:
+            stride = st
+        elif st != step:
+            raise ValueError(f"{name}: rows must be one stride apart")
+        step = st * size
+    stride = cols if stride is None else stride
+    if stride < cols:
+        raise ValueError(f"{name}: rows must not overlap")
+    return _ptr(t), _FLOAT_TYPES[t.dtype], stride
+
+
+def _one_device(*tensors):
+    """The tensors' common device, made the current one for a call (the
+    library enqueues on the current device)."""
+    if not all(torch.is_tensor(t) and t.is_cuda and t.device == tensors[0].device for t in tensors):
+        raise ValueError("need CUDA tensors on one device")
+    return torch.cuda.device(tensors[0].device)
+
+
+def _embed_cols(plan: Plan, seg: int, rows: int) -> int:
+    """Columns of segment seg read as rows x cols."""
+    if not 0 <= seg < plan.nseg or rows < 1 or int(plan.table[seg, 1]) % rows:
+        raise ValueError("seg must be a segment of the plan and rows divide its length")
+    return int(plan.table[seg, 1]) // rows
+
+
+def gc_embed_lookup(plan: Plan, seg: int, rows: int, w, tokens: torch.Tensor, scale: float, y: torch.Tensor):
+    """y[...] = scale * w's row tokens[...]; y has the tokens' shape with the
+    columns appended, in fp32, bf16 or fp16, its rows one stride apart."""
+    cols = _embed_cols(plan, seg, rows)
+    tp, tt, n = _tokens(tokens)
+    yp, yt, ys = _batch_rows(y, tokens, cols, "y")
+    with _one_device(w, tokens, y):
+        _check(load().gc_embed_lookup(plan.handle, int(seg), int(rows), _f32(w, plan.n_total, "w"), tp, tt, n,
+                                      float(scale), yp, yt, ys, _stream(y)))
+
+
+def gc_embed_workspace_bytes(plan: Plan, seg: int, rows: int, n_tokens: int) -> int:
+    return int(load().gc_embed_workspace_bytes(plan.handle, int(seg), int(rows), int(n_tokens)))
+
+
+def gc_embed_grad(plan: Plan, seg: int, rows: int, dy: torch.Tensor, tokens: torch.Tensor, scale: float, g,
+                  accumulate: bool, ws: torch.Tensor):
+    """The lookup's gradient, written over (accumulate False) or added to
+    segment seg of g; dy as gc_embed_lookup's y."""
+    cols = _embed_cols(plan, seg, rows)
+    tp, tt, n = _tokens(tokens)
+    dp, dt, ds = _batch_rows(dy, tokens, cols, "dy")
+    with _one_device(dy, tokens, g, ws):
+        _check(load().gc_embed_grad(plan.handle, int(seg), int(rows), dp, dt, ds, tp, tt, n, float(scale),
+                                    _f32(g, plan.n_total, "g"), int(bool(accumulate)), *_ws(ws), _stream(g)))
+
+
+def gc_embed_message_cap(plan: Plan, seg: int, rows: int, n_tokens: int) -> int:
+    return int(load().gc_embed_message_cap(plan.handle, int(seg), int(rows), int(n_tokens)))
+
+
+def gc_embed_message(plan: Plan, seg: int, rows: int, dy: torch.Tensor, tokens: torch.Tensor, scale: float,
+                     out: Sparse, ws: torch.Tensor):
+    """The lookup's gradient as a message of the rows that have tokens."""
+    cols = _embed_cols(plan, seg, rows)
+    tp, tt, n = _tokens(tokens)
+    dp, dt, ds = _batch_rows(dy, tokens, cols, "dy")
+    msg = out.checked(plan, "out")
+    with _one_device(dy, tokens, out.idx, out.val, out.seg_off, ws):
+        _check(load().gc_embed_message(plan.handle, int(seg), int(rows), dp, dt, ds, tp, tt, n, float(scale),
+                                       ctypes.byref(msg), *_ws(ws), _stream(out.val)))
+
+
+# -------------------------------------------------------- matrix updates
+class MatrixPlan:
+    """The weight matrices among a plan's segments (gc_matrix_plan): rows[s]
+    is segment s's row count, 0 for a segment that is no matrix."""
+
+    def __init__(self, plan: Plan, rows):
+        r = np.asarray(rows, dtype=np.int64).reshape(-1)
+        if len(r) != plan.nseg or (r < 0).any() or (r > 0xFFFFFFFF).any():
+            raise ValueError("rows: need one count >= 0 per segment of the plan")
+        self.n_total = plan.n_total
+        arr = (ctypes.c_uint32 * len(r))(*[int(v) for v in r])
+        h = ctypes.c_void_p()
+        _check(load().gc_matrix_plan_create(plan.handle, arr, ctypes.byref(h)))
+        self.handle = h
+
+    def __del__(self):
+        h = getattr(self, "handle", None)
+        if h is not None and h.value and _lib is not None:
+            _lib.gc_matrix_plan_destroy(h)
+            self.handle = None
+
+    def upload(self) -> None:
+        """Put the tables on the current device (gc_matrix_plan_upload)."""
+        _check(load().gc_matrix_plan_upload(self.handle))
+
+    def workspace_bytes(self) -> int:
+        return int(load().gc_matrix_plan_workspace_bytes(self.handle))
+
+    def workspace(self, device="cuda") -> torch.Tensor:
+        return torch.empty(self.workspace_bytes(), dtype=torch.uint8, device=device)
+
+
+def orth_options(steps: int = 5, coef=(3.4445, -4.7750, 2.0315), eps: float = 1e-7) -> gc_orth_options:
+    """coef: (a, b, c) for every step, or one such triple per step."""
+    each = [tuple(coef)] * steps if np.ndim(coef) == 1 else [tuple(c) for c in coef]
+    if len(each) != steps or any(len(c) != 3 for c in each):
+        raise ValueError("coef: need (a, b, c), or one triple per step")
+    o = gc_orth_options(int(steps), float(eps))
+    for k, c in enumerate(each[:GC_MAX_ORTH_STEPS]):
+        o.coef[k][:] = [float(v) for v in c]
+    return o
+
+
+def muon_options(momentum: float, lr: float, weight_decay: float = 0.0, nesterov: bool = True,
+                 scale: int = GC_MUON_SCALE_SHAPE, steps: int = 5, coef=(3.4445, -4.7750, 2.0315),
+                 eps: float = 1e-7) -> gc_muon_options:
+    return gc_muon_options(orth_options(steps, coef, eps), float(momentum), float(lr), float(weight_decay),
+                           GC_MOMENTUM_NESTEROV if nesterov else GC_MOMENTUM_VANILLA, int(scale), 0)
+
+
+def gc_orthogonalize(mplan: MatrixPlan, D, O, opt: gc_orth_options, ws: torch.Tensor):
+    """Every matrix of D orthogonalised into O (which may be D)."""
+    n = mplan.n_total
+    with _one_device(D, O, ws):
+        _check(load().gc_orthogonalize(mplan.handle, _f32(D, n, "D"), _f32(O, n, "O"), ctypes.byref(opt), *_ws(ws),
+                                       _stream(O)))
+
+
+def gc_muon_step(mplan: MatrixPlan, G, U, W, opt: gc_muon_options, ws: torch.Tensor):
+    """U <- m U + G, W <- (1 - lr wd) W - lr s orthogonalised(D) on every matrix."""
+    n = mplan.n_total
+    with _one_device(G, U, W, ws):
+        _check(load().gc_muon_step(mplan.handle, _f32(G, n, "G"), _f32(U, n, "U"), _f32(W, n, "W"), ctypes.byref(opt),
+                                   *_ws(ws), _stream(W)))

@@ -17,6 +17,9 @@
  *             §3 (core and explorer selection, significance, key caching)
  *             and the experimental setup (Quant-DP baseline: random
  *             quantization with buckets of 512).
+ *   The embedding's lookup and gradient and the orthogonalised matrix update
+ *   (Newton-Schulz products, as the Muon optimiser applies them) come from no
+ *   page: they are given by their formulas at each call.
  *
  * Conventions shared by every call
  * --------------------------------
@@ -581,6 +584,167 @@ gc_status gc_slimdp_explore(const gc_plan *plan, const gc_plan *core_plan, const
 gc_status gc_slimdp_core_values(const gc_plan *core_plan, const gc_sparse *core,
                                 const float *delta, float *values, hipStream_t stream);
 
+/* ------------------------------------------------------------- embedding */
+/*
+ * The embedding of a flat model buffer: segment `seg` of the plan read as
+ * `rows` x cols, row-major, cols = length / rows (rows must divide the
+ * length).  A batch is n_tokens token ids (int32 or int64) and one dense row
+ * per token, y or dy: cols elements of fp32, bf16 or fp16, `stride` elements
+ * from one row to the next (stride >= cols; the elements between are neither
+ * read nor written).  An id outside [0, rows) is padding: its row of y is
+ * +0, and its row of dy is not read and counts for nothing.
+ */
+#define GC_F32   0
+#define GC_BF16  1
+#define GC_F16   2
+#define GC_TOKENS_I32  0
+#define GC_TOKENS_I64  1
+
+/*
+ * y_i = fl32(scale * w[t_i]), rounded to nearest (ties to even) once more
+ * for bf16 and fp16.
+ *   w [n_total] in, tokens [n_tokens] in, y out.  scale finite.
+ * n_tokens == 0 enqueues nothing.  Needs neither workspace nor the plan's
+ * tables on the device.
+ * Errors: GC_EINVAL (null, seg or rows that do not fit the plan, unknown
+ *         types, stride < cols, misaligned buffers, scale not finite),
+ *         GC_ERANGE (n_tokens >= 2^31, n_tokens * stride > 2^48, or
+ *         n_tokens * cols past 2^42).
+ */
+gc_status gc_embed_lookup(const gc_plan *plan, int seg, uint32_t rows, const float *w,
+                          const void *tokens, int token_type, uint64_t n_tokens, float scale,
+                          void *y, int y_type, uint64_t y_stride, hipStream_t stream);
+
+/*
+ * The gradient of the lookup.  For every row r with at least one token,
+ *   S_r = sum in fp32 of dy_i over the positions i with t_i = r;
+ *   accumulate == 0: g[r] = fl32(scale * S_r), every other row +0;
+ *   accumulate != 0: g[r] = fl32(g[r] + fl32(scale * S_r)), no other row is
+ *                    touched.
+ * The order of a sum is fixed by the tokens alone: positions are ordered by
+ * (row, position) and cut into blocks of 32; a row's positions of one block
+ * are added in order from +0.  A row that lies in more than one block has
+ * block sums s_0, s_1, ...; the sums Z_w of s_w, s_{w+16}, s_{w+32}, ...
+ * (each in order from +0) are formed and added in the order Z_0, Z_1, ...,
+ * Z_15.
+ *   g  [n_total] out (in/out if accumulate); only the segment is touched.
+ *   ws : gc_embed_workspace_bytes(plan, seg, rows, n_tokens) bytes (0 on an
+ *        argument error).  n_tokens == 0 needs none (ws may be NULL).
+ * Errors: as gc_embed_lookup; GC_ECAPACITY (ws too small).
+ */
+size_t    gc_embed_workspace_bytes(const gc_plan *plan, int seg, uint32_t rows, uint64_t n_tokens);
+gc_status gc_embed_grad(const gc_plan *plan, int seg, uint32_t rows, const void *dy, int dy_type,
+                        uint64_t dy_stride, const void *tokens, int token_type, uint64_t n_tokens,
+                        float scale, float *g, int accumulate, void *ws, size_t ws_bytes,
+                        hipStream_t stream);
+
+/*
+ * The same gradient as a message for gc_pack or gc_decompress_accumulate:
+ * the rows that have tokens, ascending, all their columns, idx the flat
+ * indices and val = fl32(scale * S_r).  seg_off is 0 up to seg and the entry
+ * count behind it (the plan's other segments are empty); seg_scale is not
+ * written.  Entries past the count are left as they were.
+ *   out->cap >= gc_embed_message_cap(...) = min(n_tokens, rows) * cols.
+ * A DGC stream of such a message needs up to gc_dgc_pack_bound with a density
+ * of 1/1.
+ * Errors: as gc_embed_grad; GC_ECAPACITY also for out->cap.
+ */
+uint64_t  gc_embed_message_cap(const gc_plan *plan, int seg, uint32_t rows, uint64_t n_tokens);
+gc_status gc_embed_message(const gc_plan *plan, int seg, uint32_t rows, const void *dy, int dy_type,
+                           uint64_t dy_stride, const void *tokens, int token_type,
+                           uint64_t n_tokens, float scale, gc_sparse *out, void *ws,
+                           size_t ws_bytes, hipStream_t stream);
+
+/* ----------------------------------------------------- matrix updates */
+/*
+ * Segments of a plan that are weight matrices, for updates that treat a
+ * matrix as a whole (Muon).  Opaque and immutable; it keeps nothing of the
+ * gc_plan.
+ *   rows[nseg] (host): the rows R of segment s, row-major, with C = length /
+ *   R columns; 0 for a segment that is no matrix, which the calls below
+ *   neither read nor write.
+ * Host only: touches no device.  The tables go to a device as a gc_plan's do
+ * (first use, or gc_matrix_plan_upload: one hipMalloc and one synchronous
+ * copy per device).
+ * Errors: GC_EINVAL (null, rows that do not divide a length, no matrix),
+ *         GC_ENOTSUP (more than GC_MAX_MATRIX_DIM rows or columns).
+ */
+#define GC_MAX_MATRIX_DIM  (1u << 20)
+typedef struct gc_matrix_plan gc_matrix_plan;
+gc_status gc_matrix_plan_create(const gc_plan *plan, const uint32_t *rows, gc_matrix_plan **out);
+void      gc_matrix_plan_destroy(gc_matrix_plan *mplan);
+gc_status gc_matrix_plan_upload(const gc_matrix_plan *mplan);
+/* Device workspace bytes of gc_orthogonalize and gc_muon_step (0 for NULL). */
+size_t    gc_matrix_plan_workspace_bytes(const gc_matrix_plan *mplan);
+
+/*
+ * Every matrix D (R x C) of the plan, orthogonalised by Newton-Schulz
+ * products:
+ *   X_0 = D / (||D||_F + eps)   (the norm in double; X = D^T where R > C)
+ *   X_{k+1} = a_k X_k + (b_k A + c_k A^2) X_k,  A = X_k X_k^T,
+ *   k = 0 .. steps - 1, (a_k, b_k, c_k) = coef[k];   O = X_steps (transposed
+ *   back).
+ * Each step maps every singular value s of X to a s + b s^3 + c s^5 and
+ * keeps the singular vectors.  With (3.4445, -4.7750, 2.0315) five steps
+ * bring all but the smallest to between about 0.7 and 1.2.
+ * Products are formed from operands of 22 bits with fp32 sums; the result is
+ * as near to the exact one as fp32 products are.  Unlike the other calls'
+ * results it is no fixed sequence of IEEE operations, but the same call on
+ * the same device gives the same bits.
+ * D = 0 gives O = +-0.  A matrix with a NaN or Inf becomes NaN altogether and
+ * leaves the others alone.
+ *   D [n_total] in, O [n_total] out; O may be D, or must not overlap it.
+ *   ws : gc_matrix_plan_workspace_bytes bytes.
+ * Errors: GC_EINVAL (null, steps, eps negative or not finite, reserved not 0,
+ *         coefficients that are not finite, or with which singular values
+ *         of at most 1 at the start may pass 8 before the last step (1e12
+ *         after it), those of b A + c A^2 2^14, or all fall below 1e-12;
+ *         overlapping buffers), GC_ECAPACITY (ws).
+ */
+#define GC_MAX_ORTH_STEPS  16
+typedef struct gc_orth_options {
+    int      steps;                        /* 1 .. GC_MAX_ORTH_STEPS */
+    float    eps;                          /* >= 0                   */
+    float    coef[GC_MAX_ORTH_STEPS][3];   /* a, b, c of each step   */
+    uint32_t reserved[2];                  /* must be 0              */
+} gc_orth_options;
+gc_status gc_orthogonalize(const gc_matrix_plan *mplan, const float *D, float *O,
+                           const gc_orth_options *opt, void *ws, size_t ws_bytes,
+                           hipStream_t stream);
+
+/*
+ * One Muon step on every matrix of the plan, from the gradient that
+ * gc_decompress_accumulate (or the learner itself) left in G:
+ *   U <- fl32(fl32(m*U) + G)
+ *   D  = U (GC_MOMENTUM_VANILLA) or fl32(fl32(m*U) + G), U the new one
+ *        (GC_MOMENTUM_NESTEROV)
+ *   O  = D orthogonalised as above
+ *   W <- fl32(fl32(d*W) - fl32(l*O)),  d = fl32(1 - lr * weight_decay),
+ *        l = fl32(lr * s)  (formed in double)
+ *   s = 1 (GC_MUON_SCALE_NONE), sqrt(max(1, R / C)) (GC_MUON_SCALE_SHAPE) or
+ *       0.2 sqrt(max(R, C)) (GC_MUON_SCALE_RMS).
+ * Where momentum correction already ran in DGC's V, m = 0 leaves it at that
+ * (U then holds G).
+ *   G [n_total] in, U, W [n_total] in/out; none overlaps another.
+ * Errors: as gc_orthogonalize; GC_EINVAL also for momentum outside [0, 1), lr
+ *         or weight_decay not finite, weight_decay < 0, an unknown
+ *         momentum_kind or scale.
+ */
+#define GC_MUON_SCALE_NONE   0
+#define GC_MUON_SCALE_SHAPE  1
+#define GC_MUON_SCALE_RMS    2
+typedef struct gc_muon_options {
+    gc_orth_options orth;
+    float    momentum;       /* 0 <= m < 1        */
+    float    lr;
+    float    weight_decay;   /* >= 0              */
+    int      momentum_kind;  /* GC_MOMENTUM_*     */
+    int      scale;          /* GC_MUON_SCALE_*   */
+    uint32_t reserved;       /* must be 0         */
+} gc_muon_options;
+gc_status gc_muon_step(const gc_matrix_plan *mplan, const float *G, float *U, float *W,
+                       const gc_muon_options *opt, void *ws, size_t ws_bytes, hipStream_t stream);
+
 /* ----------------------------------------------------------- measurement */
 /*
  * Kernel timing for measurement tools (off by default).  While enabled, each
@@ -596,7 +760,10 @@ gc_status gc_slimdp_core_values(const gc_plan *core_plan, const gc_sparse *core,
  *             unpack_count, unpack_scan, unpack_write, decode_index,
  *             decode, dcd, dcd_decode, dcd_mix, ecd_compress, ecd_update,
  *             slimdp_values, stream_probe (Slim-DP selection reuses the
- *             dgc_* names).
+ *             dgc_* names), embed_lookup, embed_rank, embed_merge,
+ *             embed_heads, embed_rows, embed_sum, embed_join, embed_empty,
+ *             orth_norm, orth_scale, orth_split, orth_gram, orth_poly,
+ *             orth_apply.
  * gc_timing_take waits for the recorded events of one kernel and returns the
  * summed duration in milliseconds and the number of launches, then forgets
  * them.  Host-thread safe; not for use while a stream is being captured.
