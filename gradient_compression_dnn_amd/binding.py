@@ -151,7 +151,7 @@ KERNELS = ("dgc_norm", "dgc_prep", "dgc_prepare", "dgc_sample", "dgc_bound", "dg
            "unpack_write", "decode_index", "decode", "dcd",
            "dcd_decode", "dcd_mix", "ecd_compress", "ecd_update", "slimdp_values", "stream_probe",
            "embed_lookup", "embed_rank", "embed_merge", "embed_heads", "embed_rows", "embed_sum", "embed_join",
-           "embed_empty", "orth_norm", "orth_scale", "orth_split", "orth_gram", "orth_poly", "orth_apply")
+           "embed_small", "embed_empty", "orth_norm", "orth_scale", "orth_split", "orth_gram", "orth_poly", "orth_apply")
 
 
 def gc_timing_enable(kernels) -> None:
@@ -256,6 +256,7 @@ class Plan:
     def __init__(self, table, n_total: int | None = None):
         t = np.asarray(table, dtype=np.int64).reshape(-1, 4)
         self.table = t
+        self.lengths = t[:, 1].tolist()
         self.n_total = int(n_total if n_total is not None else (t[-1, 0] + t[-1, 1] if len(t) else 0))
         arr = (gc_segment * max(len(t), 1))()
         for i, (o, n, lt, k) in enumerate(t):
@@ -549,27 +550,13 @@ _FLOAT_TYPES = {torch.float32: GC_F32, torch.bfloat16: GC_BF16, torch.float16: G
 _TOKEN_TYPES = {torch.int32: GC_TOKENS_I32, torch.int64: GC_TOKENS_I64}
 
 
-def _tokens(tokens):
-    """(pointer, GC_TOKENS_*, count) of a contiguous CUDA int32 or int64 tensor of any shape."""
-    if not torch.is_tensor(tokens) or tokens.dtype not in _TOKEN_TYPES or not tokens.is_cuda or not tokens.is_contiguous():
-        raise ValueError("tokens: need a contiguous CUDA int32 or int64 tensor")
-    return _ptr(tokens), _TOKEN_TYPES[tokens.dtype], tokens.numel()
-
-
-def _batch_rows(t, tokens, cols: int, name: str):
-    """(pointer, GC_* type, row stride) of a batch: the tokens' shape with
-    cols appended, one stride between its rows, unit stride inside them."""
-    ok = torch.is_tensor(t) and t.dtype in _FLOAT_TYPES and t.is_cuda and t.dim() >= 1
-    if not ok or tuple(t.shape) != (*tokens.shape, cols) or t.device != tokens.device:
-        raise ValueError(f"{name}: need a CUDA fp32, bf16 or fp16 tensor of shape {(*tokens.shape, cols)} "
-                         "on the tokens' device")
-    if t.numel() == 0:
-        return _ptr(t), _FLOAT_TYPES[t.dtype], cols
+def _row_stride(t, name: str) -> int:
+    """The one stride between a batch's rows, which are contiguous in themselves."""
+    cols = t.shape[-1]
     if cols > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    # dimensions of more than one row, from the last: each must continue the one behind it
     stride, step = None, None
-    for size, st in list(zip(t.shape[:-1], t.stride()[:-1]))[::-1]:
+    for size, st in list(zip(t.shape[:-1], t.stride()[:-1]))[::-1]:  # each must continue the one behind it
         if size == 1:
             continue
         if stride is None:
@@ -580,33 +567,59 @@ def _batch_rows(t, tokens, cols: int, name: str):
     stride = cols if stride is None else stride
     if stride < cols:
         raise ValueError(f"{name}: rows must not overlap")
-    return _ptr(t), _FLOAT_TYPES[t.dtype], stride
+    return stride
 
 
-def _one_device(*tensors):
-    """The tensors' common device, made the current one for a call (the
-    library enqueues on the current device)."""
-    if not all(torch.is_tensor(t) and t.is_cuda and t.device == tensors[0].device for t in tensors):
-        raise ValueError("need CUDA tensors on one device")
-    return torch.cuda.device(tensors[0].device)
-
-
-def _embed_cols(plan: Plan, seg: int, rows: int) -> int:
-    """Columns of segment seg read as rows x cols."""
-    if not 0 <= seg < plan.nseg or rows < 1 or int(plan.table[seg, 1]) % rows:
+def _batch(plan: Plan, seg: int, rows: int, tokens, t, name: str):
+    """((t pointer, GC_* type, row stride), (tokens pointer, GC_TOKENS_*, count))
+    of a batch: tokens contiguous, of any shape; t their shape with the
+    columns of segment seg, read as rows x columns, appended."""
+    if not 0 <= seg < plan.nseg or rows < 1 or plan.lengths[seg] % rows:
         raise ValueError("seg must be a segment of the plan and rows divide its length")
-    return int(plan.table[seg, 1]) // rows
+    cols = plan.lengths[seg] // rows
+    if not torch.is_tensor(tokens) or not tokens.is_cuda or not tokens.is_contiguous() or tokens.dtype not in _TOKEN_TYPES:
+        raise ValueError("tokens: need a contiguous CUDA int32 or int64 tensor")
+    if not torch.is_tensor(t) or t.dtype not in _FLOAT_TYPES or t.shape[:-1] != tokens.shape or t.shape[-1:] != (cols,):
+        raise ValueError(f"{name}: need an fp32, bf16 or fp16 tensor of shape {(*tokens.shape, cols)}")
+    stride = cols if t.is_contiguous() else _row_stride(t, name)
+    return ((t.data_ptr(), _FLOAT_TYPES[t.dtype], stride),
+            (tokens.data_ptr(), _TOKEN_TYPES[tokens.dtype], tokens.numel()))
+
+
+# the raw handle without a Stream object around it (about 1 us less per call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+class _Device:
+    """The tensors' device, made the current one for a call (the library
+    enqueues on the current device), and its current stream."""
+
+    def __init__(self, *tensors):
+        dev = tensors[0].device
+        for t in tensors:
+            if not t.is_cuda or t.device != dev:
+                raise ValueError("need CUDA tensors on one device")
+        self.index = dev.index
+
+    def __enter__(self):
+        self.before = torch.cuda.current_device()
+        if self.before != self.index:
+            torch.cuda.set_device(self.index)
+        return _raw_stream(self.index)
+
+    def __exit__(self, *exc):
+        if self.before != self.index:
+            torch.cuda.set_device(self.before)
 
 
 def gc_embed_lookup(plan: Plan, seg: int, rows: int, w, tokens: torch.Tensor, scale: float, y: torch.Tensor):
     """y[...] = scale * w's row tokens[...]; y has the tokens' shape with the
     columns appended, in fp32, bf16 or fp16, its rows one stride apart."""
-    cols = _embed_cols(plan, seg, rows)
-    tp, tt, n = _tokens(tokens)
-    yp, yt, ys = _batch_rows(y, tokens, cols, "y")
-    with _one_device(w, tokens, y):
-        _check(load().gc_embed_lookup(plan.handle, int(seg), int(rows), _f32(w, plan.n_total, "w"), tp, tt, n,
-                                      float(scale), yp, yt, ys, _stream(y)))
+    batch, toks = _batch(plan, seg, rows, tokens, y, "y")
+    wp = _f32(w, plan.n_total, "w")
+    with _Device(y, tokens, w) as stream:
+        _check(load().gc_embed_lookup(plan.handle, seg, rows, wp, *toks, scale, *batch, stream))
 
 
 def gc_embed_workspace_bytes(plan: Plan, seg: int, rows: int, n_tokens: int) -> int:
@@ -617,12 +630,11 @@ def gc_embed_grad(plan: Plan, seg: int, rows: int, dy: torch.Tensor, tokens: tor
                   accumulate: bool, ws: torch.Tensor):
     """The lookup's gradient, written over (accumulate False) or added to
     segment seg of g; dy as gc_embed_lookup's y."""
-    cols = _embed_cols(plan, seg, rows)
-    tp, tt, n = _tokens(tokens)
-    dp, dt, ds = _batch_rows(dy, tokens, cols, "dy")
-    with _one_device(dy, tokens, g, ws):
-        _check(load().gc_embed_grad(plan.handle, int(seg), int(rows), dp, dt, ds, tp, tt, n, float(scale),
-                                    _f32(g, plan.n_total, "g"), int(bool(accumulate)), *_ws(ws), _stream(g)))
+    batch, toks = _batch(plan, seg, rows, tokens, dy, "dy")
+    gp, space = _f32(g, plan.n_total, "g"), _ws(ws)
+    with _Device(g, dy, tokens, ws) as stream:
+        _check(load().gc_embed_grad(plan.handle, seg, rows, *batch, *toks, scale, gp, int(bool(accumulate)), *space,
+                                    stream))
 
 
 def gc_embed_message_cap(plan: Plan, seg: int, rows: int, n_tokens: int) -> int:
@@ -632,13 +644,10 @@ def gc_embed_message_cap(plan: Plan, seg: int, rows: int, n_tokens: int) -> int:
 def gc_embed_message(plan: Plan, seg: int, rows: int, dy: torch.Tensor, tokens: torch.Tensor, scale: float,
                      out: Sparse, ws: torch.Tensor):
     """The lookup's gradient as a message of the rows that have tokens."""
-    cols = _embed_cols(plan, seg, rows)
-    tp, tt, n = _tokens(tokens)
-    dp, dt, ds = _batch_rows(dy, tokens, cols, "dy")
-    msg = out.checked(plan, "out")
-    with _one_device(dy, tokens, out.idx, out.val, out.seg_off, ws):
-        _check(load().gc_embed_message(plan.handle, int(seg), int(rows), dp, dt, ds, tp, tt, n, float(scale),
-                                       ctypes.byref(msg), *_ws(ws), _stream(out.val)))
+    batch, toks = _batch(plan, seg, rows, tokens, dy, "dy")
+    msg, space = out.checked(plan, "out"), _ws(ws)
+    with _Device(out.val, out.idx, out.seg_off, dy, tokens, ws) as stream:
+        _check(load().gc_embed_message(plan.handle, seg, rows, *batch, *toks, scale, ctypes.byref(msg), *space, stream))
 
 
 # -------------------------------------------------------- matrix updates
@@ -694,14 +703,14 @@ def muon_options(momentum: float, lr: float, weight_decay: float = 0.0, nesterov
 def gc_orthogonalize(mplan: MatrixPlan, D, O, opt: gc_orth_options, ws: torch.Tensor):
     """Every matrix of D orthogonalised into O (which may be D)."""
     n = mplan.n_total
-    with _one_device(D, O, ws):
-        _check(load().gc_orthogonalize(mplan.handle, _f32(D, n, "D"), _f32(O, n, "O"), ctypes.byref(opt), *_ws(ws),
-                                       _stream(O)))
+    args = _f32(D, n, "D"), _f32(O, n, "O"), ctypes.byref(opt), *_ws(ws)
+    with _Device(O, D, ws) as stream:
+        _check(load().gc_orthogonalize(mplan.handle, *args, stream))
 
 
 def gc_muon_step(mplan: MatrixPlan, G, U, W, opt: gc_muon_options, ws: torch.Tensor):
     """U <- m U + G, W <- (1 - lr wd) W - lr s orthogonalised(D) on every matrix."""
     n = mplan.n_total
-    with _one_device(G, U, W, ws):
-        _check(load().gc_muon_step(mplan.handle, _f32(G, n, "G"), _f32(U, n, "U"), _f32(W, n, "W"), ctypes.byref(opt),
-                                   *_ws(ws), _stream(W)))
+    args = _f32(G, n, "G"), _f32(U, n, "U"), _f32(W, n, "W"), ctypes.byref(opt), *_ws(ws)
+    with _Device(W, G, U, ws) as stream:
+        _check(load().gc_muon_step(mplan.handle, *args, stream))

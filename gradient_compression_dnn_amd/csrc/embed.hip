@@ -6,16 +6,17 @@
 //   g[r] = fl32(scale * sum of dy_i over the positions i with t_i = r)
 //
 // The sum of a row takes its positions in ascending order, so positions are
-// sorted by (row, position) first.  The sort is stable and makes no use of
-// atomics, hence every sum has one order and the result one bit pattern:
-//   rank   each tile of 4096 tokens is ranked by counting: the rank of i is
-//          the number of keys below key_i, or equal and before i.  16.8 M
-//          comparisons a tile, no pass over the tile has to wait for another.
-//   merge  8 sorted runs at a time: an element's rank in the merged run is
-//          its own plus, for each other run, a binary search.
-//   sum    32 sorted positions by 256 columns per wave.  A row whose run lies
-//          inside the block is finished there; a run that crosses blocks
-//          leaves one partial sum per block.
+// sorted by (row, position) first.  The sort is stable and its result does not
+// hang on the order of any atomics, hence every sum has one order and the
+// result one bit pattern:
+//   rank   each tile of 2048 tokens is ranked by counting: the rank of i is
+//          the number of keys below key_i, or equal and before i.  4.2 M
+//          comparisons a tile, and nothing waits for another pass.
+//   merge  16 sorted runs at a time: an element's rank in the merged run is
+//          its own plus its place in each other run.
+//   sum    16 sorted positions by 256 (fp32) or 512 columns per wave.  A row
+//          whose run lies inside the block is finished there; a run that
+//          crosses blocks leaves one partial sum per block.
 //   join   the partial sums of each crossing run.
 #include <algorithm>
 #include <string>
@@ -34,19 +35,22 @@ struct __attribute__((packed, aligned(4))) F32x4 {
 struct __attribute__((packed, aligned(4))) U32x4 {
     uint32_t v[4];
 };
-struct __attribute__((packed, aligned(2))) U16x4 {
-    uint16_t v[4];
+struct __attribute__((packed, aligned(2))) U16x8 {
+    uint16_t v[8];
 };
 
+// Storage types: a lane moves kCols columns, 16 bytes, at a time.
 struct F32 {
     using Store = float;
     using Vec = F32x4;
+    static constexpr int kCols = 4;
     static __device__ __forceinline__ float to_f32(float x) { return x; }
     static __device__ __forceinline__ float from_f32(float x) { return x; }
 };
 struct BF16 {
     using Store = uint16_t;
-    using Vec = U16x4;
+    using Vec = U16x8;
+    static constexpr int kCols = 8;
     static __device__ __forceinline__ float to_f32(uint16_t x) { return dev_u2f(uint32_t(x) << 16); }
     static __device__ __forceinline__ uint16_t from_f32(float x) {
         return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x));
@@ -54,7 +58,8 @@ struct BF16 {
 };
 struct F16 {
     using Store = uint16_t;
-    using Vec = U16x4;
+    using Vec = U16x8;
+    static constexpr int kCols = 8;
     static __device__ __forceinline__ float to_f32(uint16_t x) {
         return static_cast<float>(__builtin_bit_cast(_Float16, x));
     }
@@ -63,28 +68,35 @@ struct F16 {
     }
 };
 
-// 4 columns of a row from column c on; those at or past cols are 0 / dropped.
-template <class T>
-__device__ __forceinline__ void load_cols(const typename T::Store *row, uint32_t c, uint32_t cols, float (&v)[4]) {
-    if (c + 4 <= cols) {
-        const auto t = *reinterpret_cast<const typename T::Vec *>(row + c);
+// N columns of a row from column c on; those at or past cols are 0 / dropped.
+// A vector access needs all of them, so a row's last lane goes by elements.
+template <class T, int N = T::kCols>
+__device__ __forceinline__ void load_cols(const typename T::Store *row, uint32_t c, uint32_t cols, float (&v)[N]) {
+    if (c + N <= cols) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) v[u] = T::to_f32(t.v[u]);
+        for (int k = 0; k < N; k += T::kCols) {
+            const auto t = *reinterpret_cast<const typename T::Vec *>(row + c + k);
+#pragma unroll
+            for (int u = 0; u < T::kCols; ++u) v[k + u] = T::to_f32(t.v[u]);
+        }
     } else {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) v[u] = c + u < cols ? T::to_f32(row[c + u]) : 0.0f;
+        for (int u = 0; u < N; ++u) v[u] = c + u < cols ? T::to_f32(row[c + u]) : 0.0f;
     }
 }
-template <class T>
-__device__ __forceinline__ void store_cols(typename T::Store *row, uint32_t c, uint32_t cols, const float (&v)[4]) {
-    if (c + 4 <= cols) {
-        typename T::Vec t;
+template <class T, int N = T::kCols>
+__device__ __forceinline__ void store_cols(typename T::Store *row, uint32_t c, uint32_t cols, const float (&v)[N]) {
+    if (c + N <= cols) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) t.v[u] = T::from_f32(v[u]);
-        *reinterpret_cast<typename T::Vec *>(row + c) = t;
+        for (int k = 0; k < N; k += T::kCols) {
+            typename T::Vec t;
+#pragma unroll
+            for (int u = 0; u < T::kCols; ++u) t.v[u] = T::from_f32(v[k + u]);
+            *reinterpret_cast<typename T::Vec *>(row + c + k) = t;
+        }
     } else {
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < N; ++u)
             if (c + u < cols) row[c + u] = T::from_f32(v[u]);
     }
 }
@@ -97,7 +109,7 @@ __device__ __forceinline__ uint32_t token_key(const Tok *tokens, uint64_t i, uin
 }
 
 // ------------------------------------------------------------------ lookup
-// A flat grid over the groups of 4 columns of all tokens: kLookupVecs per
+// A flat grid over the groups of kCols columns of all tokens: kLookupVecs per
 // thread, a workgroup's stride apart, all loads issued before the first
 // store.
 constexpr int kLookupVecs = 4;
@@ -107,10 +119,11 @@ __global__ __launch_bounds__(kBlock) void embed_lookup_kernel(const float *__res
                                                               uint64_t ntok, uint32_t rows, uint32_t cols,
                                                               uint32_t vecs, float scale,
                                                               typename T::Store *__restrict__ y, uint64_t ystride) {
+    constexpr int N = T::kCols;
     const uint64_t first = static_cast<uint64_t>(blockIdx.x) * (kBlock * kLookupVecs);
     const uint64_t tok0 = first / vecs;
     const uint32_t rem0 = static_cast<uint32_t>(first - tok0 * vecs);
-    float v[kLookupVecs][4];
+    float v[kLookupVecs][N];
     uint64_t at[kLookupVecs];
     uint32_t col[kLookupVecs];
 #pragma unroll
@@ -118,49 +131,56 @@ __global__ __launch_bounds__(kBlock) void embed_lookup_kernel(const float *__res
         const uint32_t r = rem0 + threadIdx.x + j * kBlock;  // vecs < 2^30: no wrap
         const uint32_t dt = r / vecs;
         at[j] = tok0 + dt;
-        col[j] = (r - dt * vecs) * 4;
+        col[j] = (r - dt * vecs) * N;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) v[j][u] = 0.0f;
+        for (int u = 0; u < N; ++u) v[j][u] = 0.0f;
         if (at[j] < ntok) {
             const uint32_t key = token_key(tokens, at[j], rows);
-            if (key < rows) load_cols<F32>(w + static_cast<uint64_t>(key) * cols, col[j], cols, v[j]);
+            if (key < rows) load_cols<F32, N>(w + static_cast<uint64_t>(key) * cols, col[j], cols, v[j]);
         }
     }
 #pragma unroll
     for (int j = 0; j < kLookupVecs; ++j) {
         if (at[j] < ntok) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) v[j][u] = scale * v[j][u];
+            for (int u = 0; u < N; ++u) v[j][u] = scale * v[j][u];
             store_cols<T>(y + at[j] * ystride, col[j], cols, v[j]);
         }
     }
 }
 
 // -------------------------------------------------------------------- sort
-constexpr uint32_t kTile = 4096;   // tokens ranked together
+constexpr uint32_t kTile = 2048;   // tokens ranked together
 constexpr int kRankThreads = 1024; // 16 waves: 64 tokens, each wave a 16th of the tile's keys
 constexpr uint32_t kRankWaves = kRankThreads / kWave;
-constexpr uint32_t kWays = 8;      // runs merged at a time
+constexpr uint32_t kWays = 16;     // runs merged at a time
+
+// Crossing runs, listed by the sum for the join: blocks whose last run goes
+// on, those of more than kJoinWaves partial sums apart.
+struct Lists {
+    uint32_t *count;  // [2]: short, long
+    uint32_t *few, *many;
+};
 
 // Workgroup x ranks tokens [64 x, 64 x + 64) inside their tile; workgroups
-// from `nrank` on clear the dense gradient meanwhile (nfill > 0), 4 x 1024
-// threads' stores each.  A row that has tokens is written again by the sum,
-// one launch later.
+// from `nrank` on clear the dense gradient meanwhile (nfill > 0), 16 x 1024
+// elements each.  A row that has tokens is written again by the sum, one
+// launch later.
 template <class Tok>
 __global__ __launch_bounds__(kRankThreads) void embed_rank_kernel(const Tok *__restrict__ tokens, uint32_t n,
                                                                   uint32_t rows, uint32_t *__restrict__ key_out,
-                                                                  uint32_t *__restrict__ pos_out, uint32_t nrank,
-                                                                  float *__restrict__ fill, uint64_t nfill) {
+                                                                  uint32_t *__restrict__ pos_out, uint32_t *list_count,
+                                                                  uint32_t nrank, float *__restrict__ fill,
+                                                                  uint64_t nfill) {
     if (blockIdx.x >= nrank) {
         const uint64_t base = static_cast<uint64_t>(blockIdx.x - nrank) * (kRankThreads * 16);
+        const BufRsrc r = chunk_buf(fill + base, static_cast<uint32_t>(umin64(nfill - base, kRankThreads * 16)));
         const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint64_t e = base + (static_cast<uint64_t>(j) * kRankThreads + threadIdx.x) * 4;
-            if (e < nfill) store_cols<F32>(fill + e, 0, static_cast<uint32_t>(umin64(nfill - e, 4)), zero);
-        }
+        for (int j = 0; j < 4; ++j) store4(r, (j * kRankThreads + threadIdx.x) * 4, zero);
         return;
     }
+    if (blockIdx.x == 0 && threadIdx.x < 2) list_count[threadIdx.x] = 0;
     __shared__ uint32_t keys[kTile];
     __shared__ uint32_t part[kRankWaves][kWave];
     const uint32_t i0 = blockIdx.x * kWave;
@@ -170,22 +190,36 @@ __global__ __launch_bounds__(kRankThreads) void embed_rank_kernel(const Tok *__r
     for (uint32_t j = threadIdx.x; j < cnt4; j += kRankThreads)
         keys[j] = j < cnt ? token_key(tokens, t0 + j, rows) : 0xFFFFFFFFu;  // above every key
     __syncthreads();
-    const uint32_t li = i0 - t0 + lane_id();  // this lane's token inside the tile
+    const uint32_t l0 = i0 - t0, li = l0 + lane_id();  // this lane's token inside the tile
     const bool have = li < cnt;
     const uint32_t key = have ? keys[li] : 0u;
     const uint32_t w = wave_id();
-    // wave w counts over its 16th of the tile's keys, in groups of 4
+    // wave w counts over its 16th of the tile's keys, in groups of 4: <= key
+    // in front of the 64 tokens, < key behind them, by position among them
     const uint32_t groups = cnt4 / 4, per = (groups + kRankWaves - 1) / kRankWaves;
     const uint32_t g0 = min(w * per, groups), g1 = min(g0 + per, groups);
+    const uint32_t a = min(max(l0 / 4, g0), g1), b = min(max(l0 / 4 + kWave / 4, g0), g1);
     uint32_t below = 0;
-    for (uint32_t g = g0; g < g1; ++g) {
+    auto count = [&](uint32_t from, uint32_t to, uint32_t limit) {
+#pragma unroll 4
+        for (uint32_t g = from; g < to; ++g) {
+            const uint4 k = *reinterpret_cast<const uint4 *>(&keys[4 * g]);
+            below += k.x < limit;
+            below += k.y < limit;
+            below += k.z < limit;
+            below += k.w < limit;
+        }
+    };
+    count(g0, a, key + 1);
+    for (uint32_t g = a; g < b; ++g) {
         const uint4 k = *reinterpret_cast<const uint4 *>(&keys[4 * g]);
         const uint32_t j = 4 * g;
-        below += k.x < key || (k.x == key && j < li);
-        below += k.y < key || (k.y == key && j + 1 < li);
-        below += k.z < key || (k.z == key && j + 2 < li);
-        below += k.w < key || (k.w == key && j + 3 < li);
+        below += k.x < key + (j < li);
+        below += k.y < key + (j + 1 < li);
+        below += k.z < key + (j + 2 < li);
+        below += k.w < key + (j + 3 < li);
     }
+    count(b, g1, key);
     part[w][lane_id()] = below;
     __syncthreads();
     if (w == 0 && have) {
@@ -197,49 +231,107 @@ __global__ __launch_bounds__(kRankThreads) void embed_rank_kernel(const Tok *__r
     }
 }
 
-// One element per thread of sorted runs of `run` elements: its rank in the
-// run merged from kWays of them.  Runs before its own count keys <= key,
-// runs after it keys < key; the kWays searches advance together.
-__global__ __launch_bounds__(kBlock) void embed_merge_kernel(const uint32_t *__restrict__ key_in,
-                                                             const uint32_t *__restrict__ pos_in, uint32_t n,
-                                                             uint64_t run, int steps, uint32_t *__restrict__ key_out,
-                                                             uint32_t *__restrict__ pos_out) {
-    const uint64_t i = static_cast<uint64_t>(blockIdx.x) * kBlock + threadIdx.x;
-    if (i >= n) return;
-    const uint64_t mine = i / run, g0 = mine / kWays * kWays;
-    const uint32_t key = key_in[i];
-    // search b: the count of run g0 + b's elements that come before this one
-    uint64_t lo[kWays], hi[kWays];
+// Workgroup x: 256 consecutive elements of one run, which are sorted, with
+// first key kmin and last kmax.  In each of the other runs of its group, four
+// bounds (keys below kmin, up to kmin, below kmax, up to kmax) place the
+// elements equal to either, however many there are; the others are placed
+// between the two inner bounds, whose keys fit LDS unless a run is much denser
+// there.  What bounds this is latency: wave b takes run b, 64 probes cut its
+// range to a 64th, and each element's 16 searches are spread over 4 threads.
+// (The code is kept short for the same reason: with the 16 runs unrolled it
+// took 20 to 24 us at 16,000 to 32,000 tokens, most of them instruction
+// fetches.)
+constexpr int kMergeThreads = 1024;
+constexpr uint32_t kMergeElems = 256;
+constexpr uint32_t kMergeKeys = 512;  // keys of one other run held in LDS
+constexpr uint32_t kMergeParts = kMergeThreads / kMergeElems;
+static_assert(kTile % kMergeElems == 0, "a workgroup's elements lie in one run");
+static_assert(kMergeThreads / kWave == int(kWays), "one wave per run");
+
+__global__ __launch_bounds__(kMergeThreads) void embed_merge_kernel(const uint32_t *__restrict__ key_in,
+                                                                    const uint32_t *__restrict__ pos_in, uint32_t n,
+                                                                    uint32_t run, uint32_t *__restrict__ key_out,
+                                                                    uint32_t *__restrict__ pos_out) {
+    __shared__ uint32_t bound[kWays][4];
+    __shared__ uint32_t between[kWays][kMergeKeys];
+    __shared__ uint32_t places[kMergeParts][kMergeElems];
+    const uint32_t e0 = blockIdx.x * kMergeElems;
+    const uint32_t mine = e0 / run, g0 = mine / kWays * kWays;
+    const uint32_t cnt = min(n - e0, kMergeElems);
+    const uint32_t e = threadIdx.x % kMergeElems, q = threadIdx.x / kMergeElems;
+    const uint32_t i = e0 + min(e, cnt - 1);
+    const uint32_t key = key_in[i], pos = pos_in[i];
+    const uint32_t kmin = key_in[e0], kmax = key_in[e0 + cnt - 1];
+    auto run_start = [&](uint32_t b) { return static_cast<uint32_t>(umin64(static_cast<uint64_t>(g0 + b) * run, n)); };
+    {
+        const uint32_t b = __builtin_amdgcn_readfirstlane(wave_id());
+        const uint32_t start = run_start(b), size = g0 + b == mine ? 0 : run_start(b + 1) - start;
+        uint32_t lo[4], len[4];
 #pragma unroll
-    for (uint32_t b = 0; b < kWays; ++b) {
-        lo[b] = umin64((g0 + b) * run, n);
-        hi[b] = umin64((g0 + b + 1) * run, n);
-        if (g0 + b == mine) lo[b] = hi[b] = i;
-    }
-    for (int s = 0; s < steps; ++s) {
+        for (int t = 0; t < 4; ++t) {
+            lo[t] = start;
+            len[t] = size;
+        }
+        for (uint32_t longest = size; longest;) {
+            uint32_t k[4];
+            // probe l: the last key of the l-th 64th, of the range's last piece past its end
 #pragma unroll
-        for (uint32_t b = 0; b < kWays; ++b) {
-            const uint64_t mid = (lo[b] + hi[b]) / 2;
-            const uint32_t k = key_in[umin64(mid, n - 1)];
-            const bool before = k < key || (k == key && g0 + b < mine);
-            if (lo[b] < hi[b]) {
-                if (before) lo[b] = mid + 1;
-                else hi[b] = mid;
+            for (int t = 0; t < 4; ++t)
+                k[t] = len[t] ? key_in[lo[t] + min((lane_id() + 1) * ((len[t] + kWave - 1) / kWave), len[t]) - 1] : 0u;
+            longest = 0;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const uint32_t limit = (t < 2 ? kmin : kmax) + (t & 1);
+                const uint32_t step = (len[t] + kWave - 1) / kWave, hi = lo[t] + len[t];
+                const uint32_t pieces = static_cast<uint32_t>(__popcll(__ballot(k[t] < limit)));
+                if (len[t]) {
+                    lo[t] = static_cast<uint32_t>(umin64(lo[t] + static_cast<uint64_t>(pieces) * step, hi));
+                    len[t] = step == 1 ? 0 : min(step, hi - lo[t]);
+                }
+                longest = max(longest, len[t]);
             }
         }
+        const uint32_t inner = kmin < kmax ? lo[2] - lo[1] : 0;
+        for (uint32_t j = lane_id(); j < min(inner, kMergeKeys); j += kWave) between[b][j] = key_in[lo[1] + j];
+        const uint32_t l = lane_id();
+        if (l < 4) bound[b][l] = (l == 0 ? lo[0] : l == 1 ? lo[1] : l == 2 ? lo[2] : lo[3]) - start;
     }
-    uint64_t rank = 0;
+    __syncthreads();
+    uint32_t rank = 0;
+    for (uint32_t b = q * (kWays / kMergeParts); b < (q + 1) * (kWays / kMergeParts); ++b) {
+        if (g0 + b == mine) continue;
+        const uint32_t before = g0 + b < mine ? 1 : 0;  // equal keys of earlier runs come first
+        const uint32_t first = bound[b][1], inner = kmin < kmax ? bound[b][2] - first : 0;
+        uint32_t lo = 0;
+        if (inner <= kMergeKeys) {
+            for (uint32_t half = kMergeKeys; half; half >>= 1)
+                if (lo + half <= inner && between[b][lo + half - 1] < key + before) lo += half;
+        } else {
+            uint32_t hi = inner;
+            while (lo < hi) {
+                const uint32_t mid = (lo + hi) / 2;
+                if (key_in[run_start(b) + first + mid] < key + before) lo = mid + 1;
+                else hi = mid;
+            }
+        }
+        rank += key == kmin ? bound[b][before] : key == kmax ? bound[b][2 + before] : first + lo;
+    }
+    places[q][e] = rank;
+    __syncthreads();
+    if (threadIdx.x >= cnt) return;
+    rank = i - mine * run;
 #pragma unroll
-    for (uint32_t b = 0; b < kWays; ++b) rank += lo[b] - umin64((g0 + b) * run, n);
-    key_out[g0 * run + rank] = key;
-    pos_out[g0 * run + rank] = pos_in[i];
+    for (uint32_t p = 0; p < kMergeParts; ++p) rank += places[p][e];
+    const uint64_t to = static_cast<uint64_t>(g0) * run + rank;
+    key_out[to] = key;
+    pos_out[to] = pos;
 }
 
 // ------------------------------------------------------- distinct rows
 // A head is a sorted position whose row differs from the one before it.
 // heads_before[b] is the number of heads in front of block b of kSpan sorted
 // positions, which places the block's rows in a message.
-constexpr uint32_t kSpan = 32;
+constexpr uint32_t kSpan = 16;
 constexpr uint32_t kHeadTile = 4096;
 constexpr int kHeadThreads = 1024;
 
@@ -247,6 +339,9 @@ __device__ __forceinline__ bool is_head(const uint32_t *key, uint32_t q, uint32_
     const uint32_t k = key[q];
     return k < rows && (q == 0 || key[q - 1] != k);
 }
+
+// Long batches only: the heads of each tile.
+constexpr uint32_t kCountTiles = 16;  // up to this many tiles every workgroup counts those before it itself
 
 __global__ __launch_bounds__(kHeadThreads) void embed_heads_kernel(const uint32_t *__restrict__ key, uint32_t n,
                                                                    uint32_t rows, uint32_t *__restrict__ tile_heads) {
@@ -261,17 +356,28 @@ __global__ __launch_bounds__(kHeadThreads) void embed_heads_kernel(const uint32_
     if (threadIdx.x == 0) tile_heads[blockIdx.x] = total;
 }
 
-// Workgroup x places tile x; the last one writes the message's offsets.
+// Workgroup x places tile x (tile_heads null: it counts the heads in front
+// of its tile first); the last one writes the message's offsets.
 __global__ __launch_bounds__(kHeadThreads) void embed_rows_kernel(const uint32_t *__restrict__ key, uint32_t n,
                                                                   uint32_t rows, uint32_t cols,
                                                                   const uint32_t *__restrict__ tile_heads,
                                                                   uint32_t *__restrict__ heads_before,
                                                                   uint32_t *__restrict__ seg_off, int nseg, int seg) {
     uint32_t before = 0, total;
-    for (uint32_t t = threadIdx.x; t < blockIdx.x; t += kHeadThreads) before += tile_heads[t];
+    if (tile_heads) {
+        for (uint32_t t = threadIdx.x; t < blockIdx.x; t += kHeadThreads) before += tile_heads[t];
+    } else {
+#pragma unroll 4
+        for (uint32_t q = 4 * threadIdx.x; q < blockIdx.x * kHeadTile; q += 4 * kHeadThreads) {
+            const uint4 k = *reinterpret_cast<const uint4 *>(key + q);  // workspace arrays are 256-byte aligned
+            const uint32_t p = q ? key[q - 1] : ~k.x;
+            before += (k.x < rows && k.x != p) + (k.y < rows && k.y != k.x) + (k.z < rows && k.z != k.y) +
+                      (k.w < rows && k.w != k.z);
+        }
+    }
     (void)block_exclusive_scan<uint32_t, kHeadThreads>(before, &total);
     before = total;
-    // thread t owns 4 consecutive positions of the tile; 8 threads a block
+    // thread t owns 4 consecutive positions of the tile; 4 threads a block
     const uint64_t q0 = static_cast<uint64_t>(blockIdx.x) * kHeadTile + 4u * threadIdx.x;
     uint32_t c = 0;
 #pragma unroll
@@ -294,159 +400,314 @@ struct SumOut {
     int add;
 };
 
+template <int N>
 __device__ __forceinline__ void put_row(const SumOut &o, uint32_t row, uint32_t rank, uint32_t c, uint32_t cols,
-                                        float scale, const float (&acc)[4]) {
+                                        float scale, const float (&acc)[N]) {
     if (c >= cols) return;
-    float v[4];
+    float v[N];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) v[u] = scale * acc[u];
+    for (int u = 0; u < N; ++u) v[u] = scale * acc[u];
     if (o.g) {
         float *p = o.g + static_cast<uint64_t>(row) * cols;
         if (o.add) {
-            float old[4];
-            load_cols<F32>(p, c, cols, old);
+            float old[N];
+            load_cols<F32, N>(p, c, cols, old);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) v[u] = old[u] + v[u];
+            for (int u = 0; u < N; ++u) v[u] = old[u] + v[u];
         }
-        store_cols<F32>(p, c, cols, v);
+        store_cols<F32, N>(p, c, cols, v);
     } else {
         const uint64_t at = static_cast<uint64_t>(rank) * cols;
-        store_cols<F32>(o.val + at, c, cols, v);
+        store_cols<F32, N>(o.val + at, c, cols, v);
         const uint32_t i0 = o.idx0 + row * cols + c;
-        if (c + 4 <= cols) {
-            *reinterpret_cast<U32x4 *>(o.idx + at + c) = U32x4{{i0, i0 + 1, i0 + 2, i0 + 3}};
+        if (c + N <= cols) {
+#pragma unroll
+            for (uint32_t k = 0; k < N; k += 4)
+                *reinterpret_cast<U32x4 *>(o.idx + at + c + k) = U32x4{{i0 + k, i0 + k + 1, i0 + k + 2, i0 + k + 3}};
         } else {
 #pragma unroll
-            for (uint32_t u = 0; u < 4; ++u)
+            for (uint32_t u = 0; u < N; ++u)
                 if (c + u < cols) o.idx[at + c + u] = i0 + u;
         }
     }
 }
 
-// Wave (block b of kSpan sorted positions, slab of 256 columns).  The
-// block's keys and positions are held one per lane; the rows are loaded 8 at
-// a time and added in order.  part[2 b] holds the sum of a run that comes
-// from the block before, part[2 b + 1] of one that begins here and goes on.
-constexpr uint32_t kSlab = 256;
-constexpr uint32_t kAhead = 8;
+// Workgroup (block b of kSpan sorted positions, slab of 64 kCols columns).  A
+// piece is a run's part of the block: wave w takes the block's pieces w,
+// w + waves, ... and adds each one's rows in order.  part[2 b] holds the sum of
+// a run that comes from the block before, part[2 b + 1] of one that begins
+// here and goes on; the latter is listed for the join.
+// The body is one short loop: unrolled over the 16 positions it ran 3 times
+// longer at 20 tokens and 4 times at 32,000, for its instruction fetches.
+constexpr uint32_t kJoinWaves = 16;
+
+// acc += rows dy[pos[l]] for lanes l in [from, to) of the wave's lpos.
+template <class T>
+__device__ __forceinline__ void add_rows(const typename T::Store *__restrict__ dy, uint64_t stride, uint32_t lpos,
+                                         uint32_t from, uint32_t to, uint32_t c, uint32_t cols,
+                                         float (&acc)[T::kCols]) {
+    constexpr int N = T::kCols, kAhead = 4;
+    for (uint32_t j = from; j < to; j += kAhead) {
+        float v[kAhead][N];
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+            const uint32_t p = __builtin_amdgcn_readlane(lpos, min(j + a, to - 1));
+            if (c < cols) load_cols<T>(dy + p * stride, c, cols, v[a]);
+        }
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a)
+            if (j + a < to)
+#pragma unroll
+                for (int u = 0; u < N; ++u) acc[u] = acc[u] + v[a][u];
+    }
+}
 
 template <class T>
-__global__ __launch_bounds__(kBlock) void embed_sum_kernel(const typename T::Store *__restrict__ dy, uint64_t stride,
-                                                           const uint32_t *__restrict__ key,
-                                                           const uint32_t *__restrict__ pos, uint32_t n, uint32_t rows,
-                                                           uint32_t cols, uint32_t slabs, uint64_t nwaves, float scale,
-                                                           SumOut out, float *__restrict__ part, uint32_t ldpart) {
-    const uint64_t wv = static_cast<uint64_t>(blockIdx.x) * kWaves + __builtin_amdgcn_readfirstlane(wave_id());
-    if (wv >= nwaves) return;
-    const uint32_t b = static_cast<uint32_t>(wv / slabs);
-    const uint32_t c = static_cast<uint32_t>(wv - static_cast<uint64_t>(b) * slabs) * kSlab + 4u * lane_id();
-    const uint32_t q0 = b * kSpan;
-    const uint32_t cnt = min(n - q0, kSpan);
+__global__ __launch_bounds__(1024) void embed_sum_kernel(const typename T::Store *__restrict__ dy, uint64_t stride,
+                                                         const uint32_t *__restrict__ key,
+                                                         const uint32_t *__restrict__ pos, uint32_t n, uint32_t rows,
+                                                         uint32_t cols, uint32_t slabs, float scale, SumOut out,
+                                                         float *__restrict__ part, uint32_t ldpart, Lists lists) {
+    constexpr int N = T::kCols;
+    const uint32_t waves = blockDim.x / kWave, w = __builtin_amdgcn_readfirstlane(wave_id());
+    const uint32_t b = blockIdx.x / slabs, slab = blockIdx.x - b * slabs;
+    const uint32_t c = (slab * kWave + lane_id()) * N;
+    const uint32_t q0 = b * kSpan, cnt = min(n - q0, kSpan);
     const uint32_t l = min(static_cast<uint32_t>(lane_id()), cnt - 1);
     const uint32_t lkey = key[q0 + l], lpos = pos[q0 + l];
     const uint32_t prev = q0 > 0 ? key[q0 - 1] : 0xFFFFFFFFu;
     const uint32_t next = q0 + cnt < n ? key[q0 + cnt] : 0xFFFFFFFFu;
-    uint32_t rank = out.g ? 0u : out.heads_before[b];  // rank of the next head
-    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    bool from_before = prev == static_cast<uint32_t>(__builtin_amdgcn_readlane(lkey, 0));
-    for (uint32_t j0 = 0; j0 < cnt; j0 += kAhead) {
-        float v[kAhead][4];
+    const uint32_t rank0 = out.g ? 0u : out.heads_before[b];
+    // lanes at which a piece begins; padding is none
+    const uint32_t lbefore = __shfl_up(lkey, 1, kWave);
+    uint32_t starts = static_cast<uint32_t>(__ballot(lane_id() < int(cnt) && lkey < rows && (lane_id() == 0 || lbefore != lkey)));
+    const bool from_before = prev == static_cast<uint32_t>(__builtin_amdgcn_readlane(lkey, 0));
+    const uint32_t live = static_cast<uint32_t>(__popcll(__ballot(lane_id() < int(cnt) && lkey < rows)));  // padding sorts last
+    for (uint32_t p = 0; starts; ++p) {
+        const uint32_t from = static_cast<uint32_t>(__builtin_ctz(starts));
+        starts &= starts - 1;
+        if (p % waves != w) continue;
+        const uint32_t to = starts ? static_cast<uint32_t>(__builtin_ctz(starts)) : live;
+        const uint32_t k = __builtin_amdgcn_readlane(lkey, from);
+        float acc[N];
 #pragma unroll
-        for (uint32_t j = 0; j < kAhead; ++j) {
-            const uint32_t jj = min(j0 + j, cnt - 1);
-            const uint32_t k = __builtin_amdgcn_readlane(lkey, jj), p = __builtin_amdgcn_readlane(lpos, jj);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) v[j][u] = 0.0f;
-            if (k < rows && c < cols) load_cols<T>(dy + p * stride, c, cols, v[j]);
-        }
-#pragma unroll
-        for (uint32_t j = 0; j < kAhead; ++j) {
-            if (j0 + j < cnt) {
-                const uint32_t jj = j0 + j;
-                const uint32_t k = __builtin_amdgcn_readlane(lkey, jj);
-                const bool last = jj + 1 == cnt;
-                const uint32_t after = last ? next : static_cast<uint32_t>(__builtin_amdgcn_readlane(lkey, min(jj + 1, cnt - 1)));
-#pragma unroll
-                for (int u = 0; u < 4; ++u) acc[u] = acc[u] + v[j][u];
-                if (k < rows && (last || after != k)) {
-                    const bool goes_on = last && after == k;
-                    if (from_before || goes_on) {
-                        float *p = part + (2ull * b + (from_before ? 0 : 1)) * ldpart;
-                        if (c < cols) store_cols<F32>(p, c, cols, acc);
-                    } else {
-                        put_row(out, k, rank, c, cols, scale, acc);
-                    }
-                    if (!from_before) ++rank;
-                }
-                if (after != k) {
-                    from_before = false;
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) acc[u] = 0.0f;
-                }
+        for (int u = 0; u < N; ++u) acc[u] = 0.0f;
+        add_rows<T>(dy, stride, lpos, from, to, c, cols, acc);
+        const bool goes_on = to == cnt && next == k, comes = from_before && p == 0;
+        if (comes || goes_on) {
+            if (c < cols) store_cols<F32, N>(part + (2ull * b + (comes ? 0 : 1)) * ldpart, c, cols, acc);
+            if (!comes && slab == 0 && lane_id() == 0) {
+                // more than kJoinWaves partials: the run still holds position kJoinWaves blocks on
+                const uint64_t far = q0 + static_cast<uint64_t>(kJoinWaves) * kSpan;
+                const bool many = far < n && key[far] == k;
+                (many ? lists.many : lists.few)[atomicAdd(&lists.count[many ? 1 : 0], 1u)] = b;
             }
+        } else {
+            put_row(out, k, rank0 + p - (from_before ? 1 : 0), c, cols, scale, acc);
         }
     }
 }
 
-// Workgroup (block b, slab): if a run begins in block b and crosses into the
-// next, adds its partial sums: wave w takes partials w, w + 16, ... in order,
-// then the 16 sums are added in wave order.
-constexpr int kJoinThreads = 1024;
-constexpr uint32_t kJoinWaves = kJoinThreads / kWave;
+// A batch of at most kSmall tokens in one launch.  Every workgroup of 16
+// waves ranks the batch for itself in LDS; workgroup (group g of 16 runs, slab)
+// sums a run per wave, block by block of 16 sorted positions as the other
+// path's partial sums (at most 16 blocks, so they are added in order); the
+// workgroups behind them clear the rows that have no token (dense).
+constexpr uint32_t kSmall = 256;
+constexpr int kSmallThreads = 1024;
+constexpr uint32_t kSmallWaves = kSmallThreads / kWave;
+static_assert(kSmall <= kSpan * kJoinWaves, "a run of a small batch has at most kJoinWaves partial sums");
 
-__global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(const uint32_t *__restrict__ key, uint32_t n,
-                                                                  uint32_t rows, uint32_t cols, uint32_t slabs,
-                                                                  float scale, SumOut out,
-                                                                  const float *__restrict__ part, uint32_t ldpart) {
-    const uint32_t b = blockIdx.x / slabs;
-    const uint32_t c = (blockIdx.x - b * slabs) * kSlab + 4u * lane_id();
-    const uint32_t q0 = b * kSpan;  // the grid covers blocks that have a next one
-    const uint32_t k = key[q0 + kSpan - 1];
-    if (k >= rows || key[q0 + kSpan] != k || (q0 > 0 && key[q0 - 1] == k)) return;
-    // blocks whose first position still holds this row
+template <class T, class Tok>
+__global__ __launch_bounds__(kSmallThreads) void embed_small_kernel(const typename T::Store *__restrict__ dy,
+                                                                    uint64_t stride, const Tok *__restrict__ tokens,
+                                                                    uint32_t n, uint32_t rows, uint32_t cols,
+                                                                    uint32_t slabs, uint32_t nsum, float scale,
+                                                                    SumOut out, uint64_t fill,
+                                                                    uint32_t *__restrict__ seg_off, int nseg, int seg) {
+    constexpr int N = T::kCols;
+    constexpr uint32_t kParts = kSmallThreads / kSmall;
+    __shared__ uint32_t raw[kSmall], key[kSmall + 1], pos[kSmall], part[kParts][kSmall], run_at[kSmall + 1], nruns, live;
+    const uint32_t t = threadIdx.x, e = t % kSmall, q = t / kSmall;
+    if (t < kSmall) raw[t] = t < n ? token_key(tokens, t, rows) : 0xFFFFFFFFu;
+    if (t == 0) key[n] = 0xFFFFFFFFu;
+    __syncthreads();
+    {
+        // rank of token e: thread q of its 4 compares it with a quarter of the batch
+        const uint32_t mine = raw[e], n4 = (n + 3) / 4, per = (n4 + kParts - 1) / kParts;
+        uint32_t below = 0;
+        for (uint32_t g = q * per; g < min((q + 1) * per, n4); ++g) {
+            const uint4 k = *reinterpret_cast<const uint4 *>(&raw[4 * g]);
+            const uint32_t j = 4 * g;
+            below += k.x < mine + (j < e);
+            below += k.y < mine + (j + 1 < e);
+            below += k.z < mine + (j + 2 < e);
+            below += k.w < mine + (j + 3 < e);
+        }
+        part[q][e] = below;
+    }
+    __syncthreads();
+    if (t < n) {
+        uint32_t rank = 0;
+#pragma unroll
+        for (uint32_t p = 0; p < kParts; ++p) rank += part[p][t];
+        key[rank] = raw[t];
+        pos[rank] = t;
+    }
+    __syncthreads();
+    // the runs' first positions, and the end of the last
+    {
+        const bool in = t < n && key[t] < rows, head = in && (t == 0 || key[t - 1] != key[t]);
+        uint32_t total;
+        const uint32_t at = block_exclusive_scan<uint32_t, kSmallThreads>(head ? 1u : 0u, &total);
+        if (head) run_at[at] = t;
+        if (t < n && (in && (t + 1 == n || key[t + 1] >= rows))) live = t + 1;
+        if (t == 0) {
+            nruns = total;
+            if (total == 0) live = 0;
+        }
+    }
+    __syncthreads();
+    const uint32_t runs = nruns;
+    if (blockIdx.x >= nsum) {
+        // 16 elements per thread of rows without a token
+        const uint64_t base = static_cast<uint64_t>(blockIdx.x - nsum) * (kSmallThreads * 16);
+        const uint32_t cnt = static_cast<uint32_t>(umin64(fill - base, kSmallThreads * 16));
+        const BufRsrc r = chunk_buf(out.g + base, cnt);
+        const uint32_t r0 = static_cast<uint32_t>(base / cols);
+        auto held = [&](uint32_t row) {  // whether a row has a token
+            uint32_t lo = 0, hi = runs;
+            while (lo < hi) {
+                const uint32_t mid = (lo + hi) / 2;
+                if (key[run_at[mid]] < row) lo = mid + 1;
+                else hi = mid;
+            }
+            return lo < runs && key[run_at[lo]] == row;
+        };
+        const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const uint32_t rem = static_cast<uint32_t>(base - static_cast<uint64_t>(r0) * cols);
+        for (uint32_t j = 0; j < 4; ++j) {
+            const uint32_t x = (j * kSmallThreads + t) * 4;
+            if (x >= cnt) break;
+            const uint32_t first = r0 + (rem + x) / cols, last = r0 + (rem + x + 3) / cols;
+            if (first == last && !held(first)) {
+                store4(r, x, zero);
+            } else if (first != last) {
+                for (uint32_t u = 0; u < 4 && x + u < cnt; ++u)
+                    if (!held(r0 + (rem + x + u) / cols)) out.g[base + x + u] = 0.0f;
+            }
+        }
+        return;
+    }
+    if (seg_off && blockIdx.x == 0)
+        for (int s = t; s <= nseg; s += kSmallThreads) seg_off[s] = s <= seg ? 0u : runs * cols;
+    const uint32_t g = blockIdx.x / slabs, slab = blockIdx.x - g * slabs;
+    const uint32_t c = (slab * kWave + lane_id()) * N;
+    const uint32_t r = g * kSmallWaves + __builtin_amdgcn_readfirstlane(wave_id());
+    if (r >= runs) return;
+    const uint32_t from = run_at[r], to = r + 1 < runs ? run_at[r + 1] : live;
+    float sum[N];
+    for (uint32_t b = from / kSpan; b * kSpan < to; ++b) {
+        const uint32_t q0 = b * kSpan, lo = max(from, q0) - q0, hi = min(to, q0 + kSpan) - q0;
+        const uint32_t lpos = pos[min(q0 + (lane_id() & (kSpan - 1)), n - 1)];
+        float acc[N];
+#pragma unroll
+        for (int u = 0; u < N; ++u) acc[u] = 0.0f;
+        add_rows<T>(dy, stride, lpos, __builtin_amdgcn_readfirstlane(lo), __builtin_amdgcn_readfirstlane(hi), c, cols, acc);
+#pragma unroll
+        for (int u = 0; u < N; ++u) sum[u] = b == from / kSpan ? acc[u] : sum[u] + acc[u];
+    }
+    put_row(out, key[from], r, c, cols, scale, sum);
+}
+
+// The partial sums of the listed runs: part[2 b + 1], then part[2 (b + i)].
+// Runs of at most kJoinWaves partials take a wave each and are added in
+// order; for longer ones wave w of a workgroup adds partials w, w + 16, ...,
+// and then the 16 sums are added in wave order.
+constexpr int kJoinThreads = kJoinWaves * kWave;
+constexpr uint32_t kJoinSlab = kWave * 4;
+
+__device__ __forceinline__ uint32_t run_blocks(const uint32_t *__restrict__ key, uint32_t n, uint32_t b, uint32_t k) {
     const uint32_t nblocks = (n + kSpan - 1) / kSpan;
     uint32_t end = b + 1;
     for (;;) {
         const uint32_t bl = end + lane_id();
         const uint64_t m = __ballot(bl < nblocks && key[min(bl, nblocks - 1) * kSpan] == k);
-        if (m == ~0ull) {
-            end += kWave;
-        } else {
-            end += __builtin_ctzll(~m);
-            break;
-        }
+        if (m != ~0ull) return end + static_cast<uint32_t>(__builtin_ctzll(~m)) - b;
+        end += kWave;
     }
-    const uint32_t count = end - b;  // partials: part[2 b + 1], then part[2 (b + i)]
-    const uint32_t w = wave_id();
-    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (c < cols) {
-        for (uint32_t i = w; i < count; i += kJoinWaves) {
-            float v[4];
-            load_cols<F32>(part + (2ull * (b + i) + (i == 0 ? 1 : 0)) * ldpart, c, cols, v);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) acc[u] = acc[u] + v[u];
-        }
-    }
+}
+
+// The rank among the distinct rows of block b's last run, which begins there.
+__device__ __forceinline__ uint32_t last_rank(const SumOut &out, const uint32_t *__restrict__ key, uint32_t rows,
+                                              uint32_t b) {
+    if (out.g) return 0;
+    const uint32_t q = b * kSpan + min(static_cast<uint32_t>(lane_id()), kSpan - 1);
+    const uint64_t heads = __ballot(lane_id() < int(kSpan) && is_head(key, q, rows));
+    return out.heads_before[b] + static_cast<uint32_t>(__popcll(heads)) - 1;
+}
+
+__global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(const uint32_t *__restrict__ key, uint32_t n,
+                                                                  uint32_t rows, uint32_t cols, uint32_t slabs,
+                                                                  float scale, SumOut out,
+                                                                  const float *__restrict__ part, uint32_t ldpart,
+                                                                  Lists lists) {
     __shared__ float4 sums[kJoinWaves][kWave];
-    sums[w][lane_id()] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    __syncthreads();
-    if (w != 0) return;
-    uint32_t rank = 0;
-    if (!out.g) {
-        // heads of block b in front of the crossing run (its last head)
-        const uint32_t q = q0 + min(static_cast<uint32_t>(lane_id()), kSpan - 1);
-        const uint64_t heads = __ballot(lane_id() < int(kSpan) && is_head(key, q, rows));
-        rank = out.heads_before[b] + static_cast<uint32_t>(__popcll(heads)) - 1;
+    const uint32_t w = __builtin_amdgcn_readfirstlane(wave_id());
+    const uint64_t nfew = static_cast<uint64_t>(lists.count[0]) * slabs, nmany = static_cast<uint64_t>(lists.count[1]) * slabs;
+    for (uint64_t it = blockIdx.x; it < nmany; it += gridDim.x) {
+        const uint32_t at = static_cast<uint32_t>(it / slabs);
+        const uint32_t b = lists.many[at];
+        const uint32_t c = static_cast<uint32_t>(it - static_cast<uint64_t>(at) * slabs) * kJoinSlab + 4u * lane_id();
+        const uint32_t k = key[b * kSpan + kSpan - 1];
+        const uint32_t count = run_blocks(key, n, b, k);
+        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (c < cols) {
+#pragma unroll 4
+            for (uint32_t i = w; i < count; i += kJoinWaves) {
+                float v[4];
+                load_cols<F32>(part + (2ull * (b + i) + (i == 0 ? 1 : 0)) * ldpart, c, cols, v);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) acc[u] = acc[u] + v[u];
+            }
+        }
+        __syncthreads();  // the sums of the item before have been read
+        sums[w][lane_id()] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        __syncthreads();
+        if (w == 0) {
+#pragma unroll
+            for (uint32_t i = 1; i < kJoinWaves; ++i) {
+                const float4 s = sums[i][lane_id()];
+                acc[0] = acc[0] + s.x;
+                acc[1] = acc[1] + s.y;
+                acc[2] = acc[2] + s.z;
+                acc[3] = acc[3] + s.w;
+            }
+            put_row(out, k, last_rank(out, key, rows, b), c, cols, scale, acc);
+        }
     }
-    const uint32_t used = min(count, kJoinWaves);
-    for (uint32_t i = 1; i < used; ++i) {
-        const float4 s = sums[i][lane_id()];
-        acc[0] = acc[0] + s.x;
-        acc[1] = acc[1] + s.y;
-        acc[2] = acc[2] + s.z;
-        acc[3] = acc[3] + s.w;
+    // workgroup by workgroup, so that few items use many compute units
+    for (uint64_t it = static_cast<uint64_t>(w) * gridDim.x + blockIdx.x; it < nfew; it += static_cast<uint64_t>(gridDim.x) * kJoinWaves) {
+        const uint32_t at = static_cast<uint32_t>(it / slabs);
+        const uint32_t b = lists.few[at];
+        const uint32_t c = static_cast<uint32_t>(it - static_cast<uint64_t>(at) * slabs) * kJoinSlab + 4u * lane_id();
+        const uint32_t k = key[b * kSpan + kSpan - 1];
+        const uint32_t count = run_blocks(key, n, b, k);
+        float v[kJoinWaves][4];
+#pragma unroll
+        for (uint32_t i = 0; i < kJoinWaves; ++i) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) v[i][u] = 0.0f;
+            if (i < count && c < cols) load_cols<F32>(part + (2ull * (b + i) + (i == 0 ? 1 : 0)) * ldpart, c, cols, v[i]);
+        }
+        float acc[4] = {v[0][0], v[0][1], v[0][2], v[0][3]};
+#pragma unroll
+        for (uint32_t i = 1; i < kJoinWaves; ++i)
+            if (i < count)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) acc[u] = acc[u] + v[i][u];
+        put_row(out, k, last_rank(out, key, rows, b), c, cols, scale, acc);
     }
-    put_row(out, k, rank, c, cols, scale, acc);
 }
 
 // --------------------------------------------------------------- host side
@@ -455,6 +716,7 @@ constexpr uint64_t kMaxGrid = 0x7FFFFFFF;
 
 struct EmbedWs {
     uint32_t *key[2], *pos[2], *heads_before, *tile_heads;
+    Lists lists;
     float *part;
     uint32_t ldpart;
     size_t bytes;
@@ -470,6 +732,9 @@ EmbedWs embed_ws(void *ws, uint64_t n, uint32_t cols) {
     const uint64_t blocks = ceil_div(n, kSpan);
     w.heads_before = c.take<uint32_t>(blocks);
     w.tile_heads = c.take<uint32_t>(ceil_div(n, kHeadTile));
+    w.lists.count = c.take<uint32_t>(2);
+    w.lists.few = c.take<uint32_t>(blocks);
+    w.lists.many = c.take<uint32_t>(blocks / kJoinWaves + 1);
     w.ldpart = (cols + 3u) & ~3u;
     w.part = c.take<float>(2 * blocks * w.ldpart);
     w.bytes = c.used + 256;  // room to round the base up to 256 bytes
@@ -533,46 +798,68 @@ gc_status embed_backward(const char *fn, const gc_plan *plan, int seg, uint32_t 
     const uint32_t n = static_cast<uint32_t>(n64);
     EmbedWs w = embed_ws(align256(ws), n64, cols);
     const uint64_t nfill = ceil_div(fill, kRankThreads * 16), nrank = ceil_div(n, kWave);
-    const uint32_t slabs = (cols + kSlab - 1) / kSlab, blocks = static_cast<uint32_t>(ceil_div(n, kSpan));
-    const uint64_t waves = static_cast<uint64_t>(blocks) * slabs;
-    if (nrank + nfill > kMaxGrid || waves > kMaxGrid)
+    const uint32_t blocks = static_cast<uint32_t>(ceil_div(n, kSpan));
+    const uint32_t per = kWave * (type == GC_F32 ? F32::kCols : BF16::kCols);
+    const uint32_t slabs = static_cast<uint32_t>(ceil_div(cols, per));
+    const uint64_t sums = static_cast<uint64_t>(blocks) * slabs;
+    if (nrank + nfill > kMaxGrid || sums > kMaxGrid)
         return set_error(GC_ERANGE, std::string(fn) + ": n_tokens * cols is above the supported range");
+    if (n <= kSmall) {
+        const uint32_t nsum = static_cast<uint32_t>(ceil_div(n, kSmallWaves)) * slabs;
+        with_type(type, [&](auto t) {
+            with_tokens(token_type, [&](auto tok) {
+                using T = decltype(t);
+                using Tok = decltype(tok);
+                GC_LAUNCH("embed_small", stream,
+                          embed_small_kernel<T, Tok><<<static_cast<unsigned>(nsum + nfill), kSmallThreads, 0, stream>>>(
+                              static_cast<const typename T::Store *>(dy), stride, static_cast<const Tok *>(tokens), n,
+                              rows, cols, slabs, nsum, scale, out, fill, seg_off, plan->nseg, seg));
+            });
+        });
+        hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return hip_error(e, fn);
+        return GC_OK;
+    }
     with_tokens(token_type, [&](auto tok) {
         GC_LAUNCH("embed_rank", stream,
                   embed_rank_kernel<<<static_cast<unsigned>(nrank + nfill), kRankThreads, 0, stream>>>(
-                      static_cast<const decltype(tok) *>(tokens), n, rows, w.key[0], w.pos[0],
+                      static_cast<const decltype(tok) *>(tokens), n, rows, w.key[0], w.pos[0], w.lists.count,
                       static_cast<uint32_t>(nrank), out.g, fill));
     });
     int cur = 0;
     for (uint64_t run = kTile; run < n; run *= kWays) {
-        int steps = 1;  // a search over `run` elements ends after floor(log2 run) + 1 halvings
-        while ((run >> steps) != 0) ++steps;
         GC_LAUNCH("embed_merge", stream,
-                  embed_merge_kernel<<<grid_1d(n, kBlock), kBlock, 0, stream>>>(w.key[cur], w.pos[cur], n, run, steps,
-                                                                              w.key[cur ^ 1], w.pos[cur ^ 1]));
+                  embed_merge_kernel<<<grid_1d(n, kMergeElems), kMergeThreads, 0, stream>>>(
+                      w.key[cur], w.pos[cur], n, static_cast<uint32_t>(run), w.key[cur ^ 1], w.pos[cur ^ 1]));
         cur ^= 1;
     }
     if (!out.g) {
         const unsigned tiles = grid_1d(n, kHeadTile);
-        if (tiles > 1)
+        uint32_t *tile_heads = tiles > kCountTiles ? w.tile_heads : nullptr;
+        if (tile_heads)
             GC_LAUNCH("embed_heads", stream,
-                      embed_heads_kernel<<<tiles, kHeadThreads, 0, stream>>>(w.key[cur], n, rows, w.tile_heads));
+                      embed_heads_kernel<<<tiles, kHeadThreads, 0, stream>>>(w.key[cur], n, rows, tile_heads));
         GC_LAUNCH("embed_rows", stream,
-                  embed_rows_kernel<<<tiles, kHeadThreads, 0, stream>>>(w.key[cur], n, rows, cols, w.tile_heads,
+                  embed_rows_kernel<<<tiles, kHeadThreads, 0, stream>>>(w.key[cur], n, rows, cols, tile_heads,
                                                                       w.heads_before, seg_off, plan->nseg, seg));
         out.heads_before = w.heads_before;
     }
+    // one piece per wave while the chip holds them all at once, else 4 waves a block
+    const int threads = sums <= 512 ? 1024 : 256;
     with_type(type, [&](auto t) {
         using T = decltype(t);
         GC_LAUNCH("embed_sum", stream,
-                  embed_sum_kernel<T><<<grid_1d(waves, kWaves), kBlock, 0, stream>>>(
+                  embed_sum_kernel<T><<<static_cast<unsigned>(sums), threads, 0, stream>>>(
                       static_cast<const typename T::Store *>(dy), stride, w.key[cur], w.pos[cur], n, rows, cols, slabs,
-                      waves, scale, out, w.part, w.ldpart));
+                      scale, out, w.part, w.ldpart, w.lists));
     });
-    if (blocks > 1)
+    {
+        const uint32_t jslabs = static_cast<uint32_t>(ceil_div(cols, kJoinSlab));
+        const unsigned grid = static_cast<unsigned>(umin64(ceil_div(static_cast<uint64_t>(blocks - 1) * jslabs, 2), 512));
         GC_LAUNCH("embed_join", stream,
-                  embed_join_kernel<<<(blocks - 1) * slabs, kJoinThreads, 0, stream>>>(
-                      w.key[cur], n, rows, cols, slabs, scale, out, w.part, w.ldpart));
+                  embed_join_kernel<<<grid, kJoinThreads, 0, stream>>>(w.key[cur], n, rows, cols, jslabs, scale, out,
+                                                                     w.part, w.ldpart, w.lists));
+    }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return hip_error(e, fn);
     return GC_OK;
@@ -602,7 +889,7 @@ extern "C" gc_status gc_embed_lookup(const gc_plan *plan, int seg, uint32_t rows
     if (st != GC_OK) return st;
     if (n_tokens == 0) return GC_OK;
     if (!w) return set_error(GC_EINVAL, "gc_embed_lookup: buffers must be non-null");
-    const uint32_t vecs = static_cast<uint32_t>(ceil_div(cols, 4));
+    const uint32_t vecs = static_cast<uint32_t>(ceil_div(cols, y_type == GC_F32 ? F32::kCols : BF16::kCols));
     const uint64_t grid = ceil_div(n_tokens * vecs, kBlock * kLookupVecs);
     if (grid > kMaxGrid) return set_error(GC_ERANGE, "gc_embed_lookup: n_tokens * cols is above the supported range");
     with_type(y_type, [&](auto t) {

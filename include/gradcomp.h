@@ -622,7 +622,7 @@ gc_status gc_embed_lookup(const gc_plan *plan, int seg, uint32_t rows, const flo
  *   accumulate != 0: g[r] = fl32(g[r] + fl32(scale * S_r)), no other row is
  *                    touched.
  * The order of a sum is fixed by the tokens alone: positions are ordered by
- * (row, position) and cut into blocks of 32; a row's positions of one block
+ * (row, position) and cut into blocks of 16; a row's positions of one block
  * are added in order from +0.  A row that lies in more than one block has
  * block sums s_0, s_1, ...; the sums Z_w of s_w, s_{w+16}, s_{w+32}, ...
  * (each in order from +0) are formed and added in the order Z_0, Z_1, ...,
@@ -761,7 +761,8 @@ gc_status gc_muon_step(const gc_matrix_plan *mplan, const float *G, float *U, fl
  *             decode, dcd, dcd_decode, dcd_mix, ecd_compress, ecd_update,
  *             slimdp_values, stream_probe (Slim-DP selection reuses the
  *             dgc_* names), embed_lookup, embed_rank, embed_merge,
- *             embed_heads, embed_rows, embed_sum, embed_join, embed_empty,
+ *             embed_heads, embed_rows, embed_sum, embed_join, embed_small,
+ *             embed_empty,
  *             orth_norm, orth_scale, orth_split, orth_gram, orth_poly,
  *             orth_apply.
  * gc_timing_take waits for the recorded events of one kernel and returns the
