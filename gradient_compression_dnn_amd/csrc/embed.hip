@@ -27,30 +27,21 @@ namespace gc {
 
 namespace {
 
-// Accesses of 4 elements with the alignment of one: the hardware's unaligned
-// mode takes them as one access, so odd offsets and strides need no variant.
-struct __attribute__((packed, aligned(4))) F32x4 {
-    float v[4];
-};
-struct __attribute__((packed, aligned(4))) U32x4 {
-    uint32_t v[4];
-};
-struct __attribute__((packed, aligned(2))) U16x8 {
-    uint16_t v[8];
+// N elements with the alignment of one: the hardware's unaligned mode takes
+// 8 or 16 bytes as one access, so odd offsets and strides need no variant.
+template <class S, int N>
+struct __attribute__((packed, aligned(sizeof(S)))) Pack {
+    S v[N];
 };
 
-// Storage types: a lane moves kCols columns, 16 bytes, at a time.
+// Storage types.
 struct F32 {
     using Store = float;
-    using Vec = F32x4;
-    static constexpr int kCols = 4;
     static __device__ __forceinline__ float to_f32(float x) { return x; }
     static __device__ __forceinline__ float from_f32(float x) { return x; }
 };
 struct BF16 {
     using Store = uint16_t;
-    using Vec = U16x8;
-    static constexpr int kCols = 8;
     static __device__ __forceinline__ float to_f32(uint16_t x) { return dev_u2f(uint32_t(x) << 16); }
     static __device__ __forceinline__ uint16_t from_f32(float x) {
         return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x));
@@ -58,8 +49,6 @@ struct BF16 {
 };
 struct F16 {
     using Store = uint16_t;
-    using Vec = U16x8;
-    static constexpr int kCols = 8;
     static __device__ __forceinline__ float to_f32(uint16_t x) {
         return static_cast<float>(__builtin_bit_cast(_Float16, x));
     }
@@ -70,29 +59,31 @@ struct F16 {
 
 // N columns of a row from column c on; those at or past cols are 0 / dropped.
 // A vector access needs all of them, so a row's last lane goes by elements.
-template <class T, int N = T::kCols>
+template <class T, int N>
 __device__ __forceinline__ void load_cols(const typename T::Store *row, uint32_t c, uint32_t cols, float (&v)[N]) {
+    constexpr int kVec = N * int(sizeof(typename T::Store)) <= 16 ? N : 16 / int(sizeof(typename T::Store));
     if (c + N <= cols) {
 #pragma unroll
-        for (int k = 0; k < N; k += T::kCols) {
-            const auto t = *reinterpret_cast<const typename T::Vec *>(row + c + k);
+        for (int k = 0; k < N; k += kVec) {
+            const auto t = *reinterpret_cast<const Pack<typename T::Store, kVec> *>(row + c + k);
 #pragma unroll
-            for (int u = 0; u < T::kCols; ++u) v[k + u] = T::to_f32(t.v[u]);
+            for (int u = 0; u < kVec; ++u) v[k + u] = T::to_f32(t.v[u]);
         }
     } else {
 #pragma unroll
         for (int u = 0; u < N; ++u) v[u] = c + u < cols ? T::to_f32(row[c + u]) : 0.0f;
     }
 }
-template <class T, int N = T::kCols>
+template <class T, int N>
 __device__ __forceinline__ void store_cols(typename T::Store *row, uint32_t c, uint32_t cols, const float (&v)[N]) {
+    constexpr int kVec = N * int(sizeof(typename T::Store)) <= 16 ? N : 16 / int(sizeof(typename T::Store));
     if (c + N <= cols) {
 #pragma unroll
-        for (int k = 0; k < N; k += T::kCols) {
-            typename T::Vec t;
+        for (int k = 0; k < N; k += kVec) {
+            Pack<typename T::Store, kVec> t;
 #pragma unroll
-            for (int u = 0; u < T::kCols; ++u) t.v[u] = T::from_f32(v[k + u]);
-            *reinterpret_cast<typename T::Vec *>(row + c + k) = t;
+            for (int u = 0; u < kVec; ++u) t.v[u] = T::from_f32(v[k + u]);
+            *reinterpret_cast<Pack<typename T::Store, kVec> *>(row + c + k) = t;
         }
     } else {
 #pragma unroll
@@ -109,17 +100,19 @@ __device__ __forceinline__ uint32_t token_key(const Tok *tokens, uint64_t i, uin
 }
 
 // ------------------------------------------------------------------ lookup
-// A flat grid over the groups of kCols columns of all tokens: kLookupVecs per
+// A flat grid over the groups of kLookupCols columns of all tokens: kLookupVecs per
 // thread, a workgroup's stride apart, all loads issued before the first
 // store.
 constexpr int kLookupVecs = 4;
+template <class T>
+constexpr int kLookupCols = 16 / int(sizeof(typename T::Store));  // 16 bytes of y
 
 template <class T, class Tok>
 __global__ __launch_bounds__(kBlock) void embed_lookup_kernel(const float *__restrict__ w, const Tok *__restrict__ tokens,
                                                               uint64_t ntok, uint32_t rows, uint32_t cols,
                                                               uint32_t vecs, float scale,
                                                               typename T::Store *__restrict__ y, uint64_t ystride) {
-    constexpr int N = T::kCols;
+    constexpr int N = kLookupCols<T>;
     const uint64_t first = static_cast<uint64_t>(blockIdx.x) * (kBlock * kLookupVecs);
     const uint64_t tok0 = first / vecs;
     const uint32_t rem0 = static_cast<uint32_t>(first - tok0 * vecs);
@@ -144,7 +137,7 @@ __global__ __launch_bounds__(kBlock) void embed_lookup_kernel(const float *__res
         if (at[j] < ntok) {
 #pragma unroll
             for (int u = 0; u < N; ++u) v[j][u] = scale * v[j][u];
-            store_cols<T>(y + at[j] * ystride, col[j], cols, v[j]);
+            store_cols<T, N>(y + at[j] * ystride, col[j], cols, v[j]);
         }
     }
 }
@@ -159,7 +152,7 @@ constexpr uint32_t kWays = 16;     // runs merged at a time
 // on, those of more than kJoinWaves partial sums apart.
 struct Lists {
     uint32_t *count;  // [2]: short, long
-    uint32_t *few, *many;
+    uint2 *few, *many;  // block, row
 };
 
 // Workgroup x ranks tokens [64 x, 64 x + 64) inside their tile; workgroups
@@ -400,9 +393,16 @@ struct SumOut {
     int add;
 };
 
+// What a row's sum is added to, loaded before the row's own loads are waited
+// for (added gradients only).
+template <int N>
+__device__ __forceinline__ void old_row(const SumOut &o, uint32_t row, uint32_t c, uint32_t cols, float (&old)[N]) {
+    if (o.g && o.add && c < cols) load_cols<F32, N>(o.g + static_cast<uint64_t>(row) * cols, c, cols, old);
+}
+
 template <int N>
 __device__ __forceinline__ void put_row(const SumOut &o, uint32_t row, uint32_t rank, uint32_t c, uint32_t cols,
-                                        float scale, const float (&acc)[N]) {
+                                        float scale, const float (&acc)[N], const float (&old)[N]) {
     if (c >= cols) return;
     float v[N];
 #pragma unroll
@@ -410,8 +410,6 @@ __device__ __forceinline__ void put_row(const SumOut &o, uint32_t row, uint32_t 
     if (o.g) {
         float *p = o.g + static_cast<uint64_t>(row) * cols;
         if (o.add) {
-            float old[N];
-            load_cols<F32, N>(p, c, cols, old);
 #pragma unroll
             for (int u = 0; u < N; ++u) v[u] = old[u] + v[u];
         }
@@ -423,7 +421,7 @@ __device__ __forceinline__ void put_row(const SumOut &o, uint32_t row, uint32_t 
         if (c + N <= cols) {
 #pragma unroll
             for (uint32_t k = 0; k < N; k += 4)
-                *reinterpret_cast<U32x4 *>(o.idx + at + c + k) = U32x4{{i0 + k, i0 + k + 1, i0 + k + 2, i0 + k + 3}};
+                *reinterpret_cast<Pack<uint32_t, 4> *>(o.idx + at + c + k) = Pack<uint32_t, 4>{{i0 + k, i0 + k + 1, i0 + k + 2, i0 + k + 3}};
         } else {
 #pragma unroll
             for (uint32_t u = 0; u < N; ++u)
@@ -432,27 +430,34 @@ __device__ __forceinline__ void put_row(const SumOut &o, uint32_t row, uint32_t 
     }
 }
 
-// Workgroup (block b of kSpan sorted positions, slab of 64 kCols columns).  A
+// Workgroup (block b of kSpan sorted positions, slab of 256 columns).  A
 // piece is a run's part of the block: wave w takes the block's pieces w,
 // w + waves, ... and adds each one's rows in order.  part[2 b] holds the sum of
 // a run that comes from the block before, part[2 b + 1] of one that begins
 // here and goes on; the latter is listed for the join.
 // The body is one short loop: unrolled over the 16 positions it ran 3 times
 // longer at 20 tokens and 4 times at 32,000, for its instruction fetches.
+// Each lane has 4 columns in every type: the sums leave in fp32, 16 bytes a
+// lane next to each other; with 8 columns of a 16-bit dy the two stores of a
+// lane took 27 us where fp32's took 22, on twice the bytes read.
 constexpr uint32_t kJoinWaves = 16;
+constexpr int kLaneCols = 4;
+constexpr uint32_t kSlab = kWave * kLaneCols;
 
+// Two rows ahead: one took 43 us at 32,000 tokens by 1,500 fp16 columns where
+// two take 37, eight 40 (most pieces are a row or two).
 // acc += rows dy[pos[l]] for lanes l in [from, to) of the wave's lpos.
 template <class T>
 __device__ __forceinline__ void add_rows(const typename T::Store *__restrict__ dy, uint64_t stride, uint32_t lpos,
                                          uint32_t from, uint32_t to, uint32_t c, uint32_t cols,
-                                         float (&acc)[T::kCols]) {
-    constexpr int N = T::kCols, kAhead = 4;
+                                         float (&acc)[kLaneCols]) {
+    constexpr int N = kLaneCols, kAhead = 2;
     for (uint32_t j = from; j < to; j += kAhead) {
         float v[kAhead][N];
 #pragma unroll
         for (int a = 0; a < kAhead; ++a) {
             const uint32_t p = __builtin_amdgcn_readlane(lpos, min(j + a, to - 1));
-            if (c < cols) load_cols<T>(dy + p * stride, c, cols, v[a]);
+            if (c < cols && j + a < to) load_cols<T, N>(dy + p * stride, c, cols, v[a]);
         }
 #pragma unroll
         for (int a = 0; a < kAhead; ++a)
@@ -468,7 +473,7 @@ __global__ __launch_bounds__(1024) void embed_sum_kernel(const typename T::Store
                                                          const uint32_t *__restrict__ pos, uint32_t n, uint32_t rows,
                                                          uint32_t cols, uint32_t slabs, float scale, SumOut out,
                                                          float *__restrict__ part, uint32_t ldpart, Lists lists) {
-    constexpr int N = T::kCols;
+    constexpr int N = kLaneCols;
     const uint32_t waves = blockDim.x / kWave, w = __builtin_amdgcn_readfirstlane(wave_id());
     const uint32_t b = blockIdx.x / slabs, slab = blockIdx.x - b * slabs;
     const uint32_t c = (slab * kWave + lane_id()) * N;
@@ -489,7 +494,8 @@ __global__ __launch_bounds__(1024) void embed_sum_kernel(const typename T::Store
         if (p % waves != w) continue;
         const uint32_t to = starts ? static_cast<uint32_t>(__builtin_ctz(starts)) : live;
         const uint32_t k = __builtin_amdgcn_readlane(lkey, from);
-        float acc[N];
+        float acc[N], old[N];
+        old_row(out, k, c, cols, old);
 #pragma unroll
         for (int u = 0; u < N; ++u) acc[u] = 0.0f;
         add_rows<T>(dy, stride, lpos, from, to, c, cols, acc);
@@ -500,10 +506,10 @@ __global__ __launch_bounds__(1024) void embed_sum_kernel(const typename T::Store
                 // more than kJoinWaves partials: the run still holds position kJoinWaves blocks on
                 const uint64_t far = q0 + static_cast<uint64_t>(kJoinWaves) * kSpan;
                 const bool many = far < n && key[far] == k;
-                (many ? lists.many : lists.few)[atomicAdd(&lists.count[many ? 1 : 0], 1u)] = b;
+                (many ? lists.many : lists.few)[atomicAdd(&lists.count[many ? 1 : 0], 1u)] = make_uint2(b, k);
             }
         } else {
-            put_row(out, k, rank0 + p - (from_before ? 1 : 0), c, cols, scale, acc);
+            put_row(out, k, rank0 + p - (from_before ? 1 : 0), c, cols, scale, acc, old);
         }
     }
 }
@@ -525,7 +531,7 @@ __global__ __launch_bounds__(kSmallThreads) void embed_small_kernel(const typena
                                                                     uint32_t slabs, uint32_t nsum, float scale,
                                                                     SumOut out, uint64_t fill,
                                                                     uint32_t *__restrict__ seg_off, int nseg, int seg) {
-    constexpr int N = T::kCols;
+    constexpr int N = kLaneCols;
     constexpr uint32_t kParts = kSmallThreads / kSmall;
     __shared__ uint32_t raw[kSmall], key[kSmall + 1], pos[kSmall], part[kParts][kSmall], run_at[kSmall + 1], nruns, live;
     const uint32_t t = threadIdx.x, e = t % kSmall, q = t / kSmall;
@@ -606,7 +612,8 @@ __global__ __launch_bounds__(kSmallThreads) void embed_small_kernel(const typena
     const uint32_t r = g * kSmallWaves + __builtin_amdgcn_readfirstlane(wave_id());
     if (r >= runs) return;
     const uint32_t from = run_at[r], to = r + 1 < runs ? run_at[r + 1] : live;
-    float sum[N];
+    float sum[N], old[N];
+    old_row(out, key[from], c, cols, old);
     for (uint32_t b = from / kSpan; b * kSpan < to; ++b) {
         const uint32_t q0 = b * kSpan, lo = max(from, q0) - q0, hi = min(to, q0 + kSpan) - q0;
         const uint32_t lpos = pos[min(q0 + (lane_id() & (kSpan - 1)), n - 1)];
@@ -617,7 +624,7 @@ __global__ __launch_bounds__(kSmallThreads) void embed_small_kernel(const typena
 #pragma unroll
         for (int u = 0; u < N; ++u) sum[u] = b == from / kSpan ? acc[u] : sum[u] + acc[u];
     }
-    put_row(out, key[from], r, c, cols, scale, sum);
+    put_row(out, key[from], r, c, cols, scale, sum, old);
 }
 
 // The partial sums of the listed runs: part[2 b + 1], then part[2 (b + i)].
@@ -625,7 +632,6 @@ __global__ __launch_bounds__(kSmallThreads) void embed_small_kernel(const typena
 // order; for longer ones wave w of a workgroup adds partials w, w + 16, ...,
 // and then the 16 sums are added in wave order.
 constexpr int kJoinThreads = kJoinWaves * kWave;
-constexpr uint32_t kJoinSlab = kWave * 4;
 
 __device__ __forceinline__ uint32_t run_blocks(const uint32_t *__restrict__ key, uint32_t n, uint32_t b, uint32_t k) {
     const uint32_t nblocks = (n + kSpan - 1) / kSpan;
@@ -647,6 +653,21 @@ __device__ __forceinline__ uint32_t last_rank(const SumOut &out, const uint32_t 
     return out.heads_before[b] + static_cast<uint32_t>(__popcll(heads)) - 1;
 }
 
+// acc += partials first, first + step, ... of the run that begins in block b.
+__device__ __forceinline__ void add_partials(const float *__restrict__ part, uint32_t ldpart, uint32_t b, uint32_t first,
+                                             uint32_t step, uint32_t count, uint32_t c, uint32_t cols, float (&acc)[4]) {
+    if (c >= cols) return;
+#pragma unroll 4
+    for (uint32_t i = first; i < count; i += step) {
+        // the rows of part are padded to 4 columns, so their last lane reads whole vectors too
+        const float4 v = *reinterpret_cast<const float4 *>(part + (2ull * (b + i) + (i == 0 ? 1 : 0)) * ldpart + c);
+        acc[0] = acc[0] + v.x;
+        acc[1] = acc[1] + v.y;
+        acc[2] = acc[2] + v.z;
+        acc[3] = acc[3] + v.w;
+    }
+}
+
 __global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(const uint32_t *__restrict__ key, uint32_t n,
                                                                   uint32_t rows, uint32_t cols, uint32_t slabs,
                                                                   float scale, SumOut out,
@@ -657,25 +678,17 @@ __global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(const uint32_t
     const uint64_t nfew = static_cast<uint64_t>(lists.count[0]) * slabs, nmany = static_cast<uint64_t>(lists.count[1]) * slabs;
     for (uint64_t it = blockIdx.x; it < nmany; it += gridDim.x) {
         const uint32_t at = static_cast<uint32_t>(it / slabs);
-        const uint32_t b = lists.many[at];
-        const uint32_t c = static_cast<uint32_t>(it - static_cast<uint64_t>(at) * slabs) * kJoinSlab + 4u * lane_id();
-        const uint32_t k = key[b * kSpan + kSpan - 1];
+        const uint32_t b = lists.many[at].x, k = lists.many[at].y;
+        const uint32_t c = static_cast<uint32_t>(it - static_cast<uint64_t>(at) * slabs) * kSlab + 4u * lane_id();
         const uint32_t count = run_blocks(key, n, b, k);
-        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (c < cols) {
-#pragma unroll 4
-            for (uint32_t i = w; i < count; i += kJoinWaves) {
-                float v[4];
-                load_cols<F32>(part + (2ull * (b + i) + (i == 0 ? 1 : 0)) * ldpart, c, cols, v);
-#pragma unroll
-                for (int u = 0; u < 4; ++u) acc[u] = acc[u] + v[u];
-            }
-        }
+        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f}, old[4];
+        old_row(out, k, c, cols, old);
+        add_partials(part, ldpart, b, w, kJoinWaves, count, c, cols, acc);
         __syncthreads();  // the sums of the item before have been read
         sums[w][lane_id()] = make_float4(acc[0], acc[1], acc[2], acc[3]);
         __syncthreads();
         if (w == 0) {
-#pragma unroll
+#pragma unroll 5
             for (uint32_t i = 1; i < kJoinWaves; ++i) {
                 const float4 s = sums[i][lane_id()];
                 acc[0] = acc[0] + s.x;
@@ -683,30 +696,19 @@ __global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(const uint32_t
                 acc[2] = acc[2] + s.z;
                 acc[3] = acc[3] + s.w;
             }
-            put_row(out, k, last_rank(out, key, rows, b), c, cols, scale, acc);
+            put_row(out, k, last_rank(out, key, rows, b), c, cols, scale, acc, old);
         }
     }
-    // workgroup by workgroup, so that few items use many compute units
-    for (uint64_t it = static_cast<uint64_t>(w) * gridDim.x + blockIdx.x; it < nfew; it += static_cast<uint64_t>(gridDim.x) * kJoinWaves) {
+    // spread over the workgroups, from the last: the first ones had the long runs
+    for (uint64_t it = static_cast<uint64_t>(w) * gridDim.x + (gridDim.x - 1 - blockIdx.x); it < nfew; it += static_cast<uint64_t>(gridDim.x) * kJoinWaves) {
         const uint32_t at = static_cast<uint32_t>(it / slabs);
-        const uint32_t b = lists.few[at];
-        const uint32_t c = static_cast<uint32_t>(it - static_cast<uint64_t>(at) * slabs) * kJoinSlab + 4u * lane_id();
-        const uint32_t k = key[b * kSpan + kSpan - 1];
+        const uint32_t b = lists.few[at].x, k = lists.few[at].y;
+        const uint32_t c = static_cast<uint32_t>(it - static_cast<uint64_t>(at) * slabs) * kSlab + 4u * lane_id();
         const uint32_t count = run_blocks(key, n, b, k);
-        float v[kJoinWaves][4];
-#pragma unroll
-        for (uint32_t i = 0; i < kJoinWaves; ++i) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) v[i][u] = 0.0f;
-            if (i < count && c < cols) load_cols<F32>(part + (2ull * (b + i) + (i == 0 ? 1 : 0)) * ldpart, c, cols, v[i]);
-        }
-        float acc[4] = {v[0][0], v[0][1], v[0][2], v[0][3]};
-#pragma unroll
-        for (uint32_t i = 1; i < kJoinWaves; ++i)
-            if (i < count)
-#pragma unroll
-                for (int u = 0; u < 4; ++u) acc[u] = acc[u] + v[i][u];
-        put_row(out, k, last_rank(out, key, rows, b), c, cols, scale, acc);
+        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f}, old[4];
+        old_row(out, k, c, cols, old);
+        add_partials(part, ldpart, b, 0, 1, count, c, cols, acc);
+        put_row(out, k, last_rank(out, key, rows, b), c, cols, scale, acc, old);
     }
 }
 
@@ -733,8 +735,8 @@ EmbedWs embed_ws(void *ws, uint64_t n, uint32_t cols) {
     w.heads_before = c.take<uint32_t>(blocks);
     w.tile_heads = c.take<uint32_t>(ceil_div(n, kHeadTile));
     w.lists.count = c.take<uint32_t>(2);
-    w.lists.few = c.take<uint32_t>(blocks);
-    w.lists.many = c.take<uint32_t>(blocks / kJoinWaves + 1);
+    w.lists.few = c.take<uint2>(blocks);
+    w.lists.many = c.take<uint2>(blocks / kJoinWaves + 1);
     w.ldpart = (cols + 3u) & ~3u;
     w.part = c.take<float>(2 * blocks * w.ldpart);
     w.bytes = c.used + 256;  // room to round the base up to 256 bytes
@@ -799,8 +801,7 @@ gc_status embed_backward(const char *fn, const gc_plan *plan, int seg, uint32_t 
     EmbedWs w = embed_ws(align256(ws), n64, cols);
     const uint64_t nfill = ceil_div(fill, kRankThreads * 16), nrank = ceil_div(n, kWave);
     const uint32_t blocks = static_cast<uint32_t>(ceil_div(n, kSpan));
-    const uint32_t per = kWave * (type == GC_F32 ? F32::kCols : BF16::kCols);
-    const uint32_t slabs = static_cast<uint32_t>(ceil_div(cols, per));
+    const uint32_t slabs = static_cast<uint32_t>(ceil_div(cols, kSlab));
     const uint64_t sums = static_cast<uint64_t>(blocks) * slabs;
     if (nrank + nfill > kMaxGrid || sums > kMaxGrid)
         return set_error(GC_ERANGE, std::string(fn) + ": n_tokens * cols is above the supported range");
@@ -854,10 +855,9 @@ gc_status embed_backward(const char *fn, const gc_plan *plan, int seg, uint32_t 
                       scale, out, w.part, w.ldpart, w.lists));
     });
     {
-        const uint32_t jslabs = static_cast<uint32_t>(ceil_div(cols, kJoinSlab));
-        const unsigned grid = static_cast<unsigned>(umin64(ceil_div(static_cast<uint64_t>(blocks - 1) * jslabs, 2), 512));
+        const unsigned grid = static_cast<unsigned>(umin64(ceil_div(static_cast<uint64_t>(blocks - 1) * slabs, 2), 512));
         GC_LAUNCH("embed_join", stream,
-                  embed_join_kernel<<<grid, kJoinThreads, 0, stream>>>(w.key[cur], n, rows, cols, jslabs, scale, out,
+                  embed_join_kernel<<<grid, kJoinThreads, 0, stream>>>(w.key[cur], n, rows, cols, slabs, scale, out,
                                                                      w.part, w.ldpart, w.lists));
     }
     hipError_t e = hipGetLastError();
@@ -889,7 +889,7 @@ extern "C" gc_status gc_embed_lookup(const gc_plan *plan, int seg, uint32_t rows
     if (st != GC_OK) return st;
     if (n_tokens == 0) return GC_OK;
     if (!w) return set_error(GC_EINVAL, "gc_embed_lookup: buffers must be non-null");
-    const uint32_t vecs = static_cast<uint32_t>(ceil_div(cols, y_type == GC_F32 ? F32::kCols : BF16::kCols));
+    const uint32_t vecs = static_cast<uint32_t>(ceil_div(cols, y_type == GC_F32 ? kLookupCols<F32> : kLookupCols<BF16>));
     const uint64_t grid = ceil_div(n_tokens * vecs, kBlock * kLookupVecs);
     if (grid > kMaxGrid) return set_error(GC_ERANGE, "gc_embed_lookup: n_tokens * cols is above the supported range");
     with_type(y_type, [&](auto t) {
