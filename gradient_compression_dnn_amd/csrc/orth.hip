@@ -17,9 +17,12 @@
 // rows of both: X X^T and A A^T (A is symmetric) as they stand, B X = B T^T
 // with T = X^T, which is kept beside X.  A and B are symmetric: only tiles on
 // and below the diagonal are computed, the others are their mirror images.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <functional>
 #include <new>
+#include <queue>
 #include <string>
 #include <vector>
 
@@ -67,19 +70,23 @@ struct MatDev {
     uint32_t reserved;
 };
 
-// A workgroup's work: a matrix and a tile (norm: a chunk).
+// A workgroup's work: a matrix and a tile (norm: a chunk); products: its
+// stages [k0, k1) of 32 columns of the common index, and where a part of a
+// split tile goes; joins: k1 parts from `slot` on.
 struct Item {
-    uint32_t mat, i, j, reserved;
+    uint32_t mat, i, j, k0, k1, slot;
 };
+constexpr uint32_t kNoSlot = 0xFFFFFFFFu;
 
-constexpr int kTM = 128, kTN = 128;  // output tile of a product
-constexpr int kTK = 32;              // columns of the common index per stage
-constexpr int kSplitTile = 64;       // orth_split's tile
+constexpr int kSplitTile = 64;  // orth_split's tile
+
+// The work lists: D's chunks and tiles, and per kind of product its items and
+// the joins of its split tiles.
+enum List { kChunks, kTiles, kGram, kGramJoin, kSquare, kSquareJoin, kApply, kApplyJoin, kLists };
 
 struct OrthDev {
     const MatDev *mat;
-    const Item *chunks, *tri, *rect, *tiles;
-    uint32_t nmat, nchunks, ntri, nrect, ntiles;
+    const Item *list[kLists];
 };
 
 }  // namespace
@@ -88,8 +95,10 @@ struct OrthDev {
 struct gc_matrix_plan {
     uint64_t n_total = 0;
     uint64_t xhalves = 0, ahalves = 0;  // halves of one X (or T) array and of one A (or B) array
+    uint32_t slots = 0;                 // parts of split tiles held at once
+    bool large = false;                 // tiles of 256 x 256
     std::vector<gc::MatDev> mat;
-    std::vector<gc::Item> chunks, tri, rect, tiles;
+    std::vector<gc::Item> list[gc::kLists];
     std::mutex mu;
     std::vector<std::pair<int, void *>> dev_blob;
 };
@@ -100,7 +109,7 @@ namespace {
 
 // ----------------------------------------------------------- tables, scales
 struct Blob {
-    size_t mat, chunks, tri, rect, tiles, total;
+    size_t mat, list[kLists], total;
 };
 
 Blob blob_layout(const gc_matrix_plan *p) {
@@ -113,10 +122,7 @@ Blob blob_layout(const gc_matrix_plan *p) {
         return at;
     };
     L.mat = take(sizeof(MatDev) * p->mat.size());
-    L.chunks = take(sizeof(Item) * p->chunks.size());
-    L.tri = take(sizeof(Item) * p->tri.size());
-    L.rect = take(sizeof(Item) * p->rect.size());
-    L.tiles = take(sizeof(Item) * p->tiles.size());
+    for (int l = 0; l < kLists; ++l) L.list[l] = take(sizeof(Item) * p->list[l].size());
     L.total = o < 256 ? 256 : o;
     return L;
 }
@@ -144,10 +150,8 @@ gc_status orth_device(const gc_matrix_plan *cplan, OrthDev *out) {
             e = hipMalloc(&blob, L.total);
             if (e != hipSuccess) return hip_error(e, "hipMalloc(matrix plan tables)");
             std::memcpy(host.data() + L.mat, p->mat.data(), sizeof(MatDev) * p->mat.size());
-            std::memcpy(host.data() + L.chunks, p->chunks.data(), sizeof(Item) * p->chunks.size());
-            std::memcpy(host.data() + L.tri, p->tri.data(), sizeof(Item) * p->tri.size());
-            std::memcpy(host.data() + L.rect, p->rect.data(), sizeof(Item) * p->rect.size());
-            std::memcpy(host.data() + L.tiles, p->tiles.data(), sizeof(Item) * p->tiles.size());
+            for (int l = 0; l < kLists; ++l)
+                if (!p->list[l].empty()) std::memcpy(host.data() + L.list[l], p->list[l].data(), sizeof(Item) * p->list[l].size());
             e = hipMemcpy(blob, host.data(), L.total, hipMemcpyHostToDevice);
             if (e != hipSuccess) {
                 (void)hipFree(blob);
@@ -158,19 +162,12 @@ gc_status orth_device(const gc_matrix_plan *cplan, OrthDev *out) {
     }
     auto *b = static_cast<uint8_t *>(blob);
     out->mat = reinterpret_cast<const MatDev *>(b + L.mat);
-    out->chunks = reinterpret_cast<const Item *>(b + L.chunks);
-    out->tri = reinterpret_cast<const Item *>(b + L.tri);
-    out->rect = reinterpret_cast<const Item *>(b + L.rect);
-    out->tiles = reinterpret_cast<const Item *>(b + L.tiles);
-    out->nmat = static_cast<uint32_t>(p->mat.size());
-    out->nchunks = static_cast<uint32_t>(p->chunks.size());
-    out->ntri = static_cast<uint32_t>(p->tri.size());
-    out->nrect = static_cast<uint32_t>(p->rect.size());
-    out->ntiles = static_cast<uint32_t>(p->tiles.size());
+    for (int l = 0; l < kLists; ++l) out->list[l] = reinterpret_cast<const Item *>(b + L.list[l]);
     return GC_OK;
 }
 
-// Exponents of one step's split arrays: X 2^ex, A 2^ea, B 2^eb.
+// Exponents of one step's split arrays: X 2^ex, A 2^ea, B 2^eb, where B now is
+// a I + b A + c A^2.
 struct Scales {
     int ex, ea, eb;
 };
@@ -197,7 +194,7 @@ bool orth_scales(const gc_orth_options &o, Scales *s) {
         double px = 0.0, pb = 0.0;
         for (int i = 0; i <= kPoints; ++i) {
             const double x = top * i / kPoints, q = (b + c * x * x) * x * x;
-            pb = std::max(pb, std::fabs(q));
+            pb = std::max(pb, std::fabs(a + q));
             px = std::max(px, std::fabs((a + q) * x));
         }
         const double t2 = top * top, half = 0.5 * top / kPoints;
@@ -211,10 +208,21 @@ bool orth_scales(const gc_orth_options &o, Scales *s) {
     return true;
 }
 
+// --------------------------------------------------------------- tile shapes
+// kTile x kTile per workgroup by kWR x kWC waves, kStages stages of 32 columns
+// of both planes in LDS.
+struct Large {
+    static constexpr int kTile = 256, kWR = 2, kWC = 4, kStages = 2;
+};
+struct Small {
+    static constexpr int kTile = 128, kWR = 2, kWC = 2, kStages = 4;
+};
+
 // --------------------------------------------------------------- workspace
 struct OrthWs {
     _Float16 *X[2], *T[2], *A, *B;
-    double *partial, *inv;
+    double *sums, *inv;
+    float *partial;
     size_t bytes;
 };
 
@@ -227,8 +235,10 @@ OrthWs orth_ws(void *ws, const gc_matrix_plan *p) {
     }
     w.A = c.take<_Float16>(p->ahalves);
     w.B = c.take<_Float16>(p->ahalves);
-    w.partial = c.take<double>(p->chunks.size());
+    w.sums = c.take<double>(p->list[kChunks].size());
     w.inv = c.take<double>(p->mat.size());
+    const uint64_t tile = p->large ? Large::kTile : Small::kTile;
+    w.partial = c.take<float>(p->slots * tile * tile);
     w.bytes = c.used + 256;  // room to round the base up to 256 bytes
     return w;
 }
@@ -250,7 +260,7 @@ __device__ __forceinline__ float direction(const Source &s, float u, float g) {
 // One chunk of kChunk elements of a matrix: the momentum update and the
 // chunk's sum of D^2 in double.
 __global__ __launch_bounds__(kBlock) void orth_norm_kernel(const Item *__restrict__ items, const MatDev *__restrict__ mats,
-                                                           Source s, double *__restrict__ partial) {
+                                                           Source s, double *__restrict__ sums) {
     const Item it = items[blockIdx.x];
     const MatDev M = mats[it.mat];
     const uint64_t first = static_cast<uint64_t>(it.i) * kChunk;
@@ -282,16 +292,16 @@ __global__ __launch_bounds__(kBlock) void orth_norm_kernel(const Item *__restric
             sum += d * d;
         }
     sum = block_tree_sum(sum);
-    if (threadIdx.x == 0) partial[M.chunk0 + it.i] = sum;
+    if (threadIdx.x == 0) sums[M.chunk0 + it.i] = sum;
 }
 
 // Per matrix: 1 / (||D|| + eps); 0 for D = 0, NaN where D is not finite.
 __global__ __launch_bounds__(kBlock) void orth_scale_kernel(const MatDev *__restrict__ mats,
-                                                            const double *__restrict__ partial, float eps,
+                                                            const double *__restrict__ sums, float eps,
                                                             double *__restrict__ inv) {
     const MatDev M = mats[blockIdx.x];
     double sum = 0.0;
-    for (uint32_t c = threadIdx.x; c < M.nchunk; c += kBlock) sum += partial[M.chunk0 + c];
+    for (uint32_t c = threadIdx.x; c < M.nchunk; c += kBlock) sum += sums[M.chunk0 + c];
     sum = block_tree_sum(sum);
     if (threadIdx.x == 0)
         inv[blockIdx.x] = sum == 0.0 ? 0.0 : sum - sum == 0.0 ? 1.0 / (sqrt(sum) + static_cast<double>(eps)) : __builtin_nan("");
@@ -347,19 +357,26 @@ __global__ __launch_bounds__(kBlock) void orth_split_kernel(const Item *__restri
 }
 
 // ---------------------------------------------------------------- products
-enum Phase { kGram, kPoly, kApply, kLast };
+// One product of the chain: P Q^T for every tile of an item list.
+//   kSym    P, Q symmetric or equal: the result is symmetric, tiles on and
+//           below the diagonal are computed and mirrored
+//   kNext   the next X and T = X^T
+//   kOut    the result itself, in fp32, or applied to the weights
+enum Kind { kSym, kNext, kOut };
 
 struct GemmArgs {
     const Item *items;
     const MatDev *mats;
-    const _Float16 *X, *T;  // this step's
-    _Float16 *A, *B;
-    _Float16 *Xn, *Tn;      // the next step's
-    float acc, add;         // result = acc * (P Q^T) + add * (the addend as stored)
-    // kLast: the result, or the weights it is applied to
-    float *O, *W;
+    const _Float16 *P, *Q;  // operands; P null: of X's shape, else m x m
+    uint32_t px, qx;        // whether an operand is an X (or T) array
+    const _Float16 *D;      // kSym: symmetric addend, or null
+    float acc, add, diag;   // result = acc * (P Q^T) + add * D + diag * I
+    _Float16 *S;            // kSym: result
+    _Float16 *Xn, *Tn;      // kNext: results
+    float *O, *W;           // kOut: the result, or the weights it is applied to
     float decay, lr;        // W <- decay W - lr s O
     int shape;              // GC_MUON_SCALE_*
+    float *partial;         // tiles of split items, fp32
 };
 
 // s of a matrix for GC_MUON_SCALE_*.
@@ -369,152 +386,287 @@ __device__ __forceinline__ double shape_scale(int shape, uint32_t R, uint32_t C)
     return 1.0;
 }
 
-// One 128 x 128 tile of P Q^T by 4 waves of 64 x 64 (4 x 4 matrix-core tiles
-// of 16 x 16).  A stage holds 32 columns of both planes of 128 rows of P and
-// Q, 32 KB; two stages alternate, the next one's global loads are in flight
-// while this one is multiplied.  Inside a 128-byte row the 16-byte parts are
-// permuted by (row >> 1) & 7, so that the 16 rows a matrix-core operand
-// reads at once lie in different banks.
-template <Phase kPhase>
-__global__ __launch_bounds__(kBlock) void orth_gemm_kernel(GemmArgs g) {
+template <class T>
+struct Shape : T {
+    static constexpr int kWaves = T::kWR * T::kWC, kThreads = kWaves * int(kWave);
+    static constexpr int kWaveRows = T::kTile / T::kWR, kWaveCols = T::kTile / T::kWC;
+    static constexpr int kRA = kWaveRows / 16, kRB = kWaveCols / 16;  // matrix-core tiles of a wave
+    static constexpr int kStageBytes = 2 * T::kTile * 128;            // rows of P, then of Q
+    static constexpr int kLoads = kStageBytes / kThreads / 16;        // 1 KB loads per wave and stage
+    // epilogue: 64 columns of 64 rows of a wave, fp32, columns padded
+    static constexpr int kOutLd = 68;
+    static constexpr int kOutBytes = kWaves * 64 * kOutLd * 4;
+    static constexpr int kLds = kStageBytes * T::kStages > kOutBytes ? kStageBytes * T::kStages : kOutBytes;
+    static_assert(kWaveCols == 64 && kWaveRows % 64 == 0, "the epilogue's blocks");
+};
+
+typedef __attribute__((address_space(1))) const char GlobalChar;
+typedef __attribute__((address_space(3))) char LdsChar;
+
+// The kLoads loads of a stage: rows [8 q, 8 q + 8) of P and Q straight into
+// LDS.  Lane l fills 16 bytes of row l / 8; inside a row part c stands at
+// c ^ ((row >> 1) & 7), so that the 16 rows a matrix-core operand reads at once
+// lie in different banks (counted: no conflicts).
+template <class C>
+__device__ __forceinline__ void load_stage(const char *from, uint64_t row8, int32_t odd, char *__restrict__ to) {
+#pragma unroll
+    for (int q = 0; q < C::kLoads; ++q)
+        __builtin_amdgcn_global_load_lds((GlobalChar *)(from + q * row8 + (q & 1 ? odd : 0)), (LdsChar *)(to + q * 1024), 16, 0, 0);
+}
+
+template <class C>
+__device__ __forceinline__ void multiply_stage(const char *__restrict__ lds, uint32_t pr, uint32_t qr,
+                                               f32x4 (&acc)[C::kRA][C::kRB]) {
+    // rows 16 a + (lane & 15): a row's parts are permuted alike in every group of 16
+    const uint32_t row = lane_id() & 15, part = lane_id() >> 4;
+    const uint32_t hi = row * 128 + ((part ^ ((row >> 1) & 7)) << 4), lo = hi ^ 64;
+    const char *p = lds + pr * 128, *q = lds + (C::kTile + qr) * 128;
+    auto at = [](const char *x) { return *reinterpret_cast<const h8 *>(x); };
+    h8 qh[C::kRB], ql[C::kRB];
+#pragma unroll
+    for (int b = 0; b < C::kRB; ++b) {
+        ql[b] = at(q + b * 2048 + lo);
+        qh[b] = at(q + b * 2048 + hi);
+    }
+    // one row of tiles ahead, and no further: hoisted, the loads do not fit the registers
+    h8 ph = at(p + hi), pl = at(p + lo);
+#pragma unroll
+    for (int a = 0; a < C::kRA; ++a) {
+        h8 nh = ph, nl = pl;
+        if (a + 1 < C::kRA) {
+            nh = at(p + (a + 1) * 2048 + hi);
+            nl = at(p + (a + 1) * 2048 + lo);
+        }
+#pragma unroll
+        for (int b = 0; b < C::kRB; ++b) acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ph, ql[b], acc[a][b], 0, 0, 0);
+#pragma unroll
+        for (int b = 0; b < C::kRB; ++b) acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(pl, qh[b], acc[a][b], 0, 0, 0);
+#pragma unroll
+        for (int b = 0; b < C::kRB; ++b) acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ph, qh[b], acc[a][b], 0, 0, 0);
+        ph = nh;
+        pl = nl;
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+// One stage: the loads of a later one go out, then this one is multiplied.
+// The two are different stages of LDS, which the restrict parameters tell the
+// compiler: without them it waits for the loads before it reads.
+template <class C, bool kActive>
+__device__ __forceinline__ void do_stage(const char *__restrict__ cur, char *__restrict__ next, const char *from,
+                                         uint64_t row8, int32_t odd, bool load, uint32_t pr, uint32_t qr,
+                                         f32x4 (&acc)[C::kRA][C::kRB]) {
+    if (load) load_stage<C>(from, row8, odd, next);
+    if (kActive) multiply_stage<C>(cur, pr, qr, acc);
+}
+
+// nk stages.  A wave whose rows or columns lie outside the matrix loads its
+// share and multiplies nothing (a loop of its own: with the branch inside, the
+// sums were copied at every stage).
+template <class C, bool kActive>
+__device__ __forceinline__ void all_stages(char *lds, char *to, const char *from, uint64_t row8, int32_t odd, bool load,
+                                           uint32_t nk, uint32_t pr, uint32_t qr, f32x4 (&acc)[C::kRA][C::kRB]) {
+#pragma unroll
+    for (int s = 0; s < C::kStages - 1; ++s)
+        if (load && uint32_t(s) < nk) load_stage<C>(from + s * 128, row8, odd, to + s * C::kStageBytes);
+    uint32_t cur = 0, next = C::kStages - 1;
+    for (uint32_t k = 0; k < nk; ++k) {
+        // stage k has landed (the later ones may be under way), and every
+        // wave is done with the stage that is loaded next
+        if (C::kStages > 2 && k + 3 <= nk) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(2 * C::kLoads) : "memory");
+        else if (C::kStages > 2 && k + 2 <= nk) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(C::kLoads) : "memory");
+        else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        do_stage<C, kActive>(lds + cur * C::kStageBytes, to + next * C::kStageBytes,
+                             from + static_cast<uint64_t>(k + C::kStages - 1) * 128, row8, odd,
+                             load && k + C::kStages - 1 < nk, pr, qr, acc);
+        cur = cur + 1 == C::kStages ? 0 : cur + 1;
+        next = next + 1 == C::kStages ? 0 : next + 1;
+    }
+}
+
+// x[0..n) to O, or applied to W, at flat element `at`.
+__device__ __forceinline__ void put_out(const GemmArgs &g, uint64_t at, uint32_t n, float step, const float (&x)[4]) {
+    if (n == 4) {
+        F32x4 v;
+        if (g.W) v = *reinterpret_cast<const F32x4 *>(g.W + at);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) v.v[u] = g.W ? g.decay * v.v[u] - step * x[u] : x[u];
+        *reinterpret_cast<F32x4 *>((g.W ? g.W : g.O) + at) = v;
+        return;
+    }
+#pragma unroll
+    for (uint32_t u = 0; u < 4; ++u)
+        if (u < n) {
+            if (g.W) g.W[at + u] = g.decay * g.W[at + u] - step * x[u];
+            else g.O[at + u] = x[u];
+        }
+}
+
+// The wave's rows [64 h, 64 h + 64) of its tile, which `out` holds as
+// [column][row]: scaled, addend and diagonal added, and written out.
+template <Kind kKind, class C>
+__device__ void write_block(const GemmArgs &g, const MatDev &M, float *out, uint32_t i0, uint32_t j0, bool mirror) {
+    const uint32_t hi4 = (lane_id() & 15) * 4, lo = lane_id() >> 4;
+    // along i: row j of T, or of the symmetric result
+    const double sc = kKind == kOut && g.W ? shape_scale(g.shape, M.R, M.C) : 1.0;
+    const float step = static_cast<float>(static_cast<double>(g.lr) * sc);
+#pragma unroll 2
+    for (uint32_t t = 0; t < 16; ++t) {
+        const uint32_t jj = t * 4 + lo, i = i0 + hi4, j = j0 + jj;
+        float4 v = *reinterpret_cast<const float4 *>(out + jj * C::kOutLd + hi4);
+        float x[4] = {v.x * g.acc, v.y * g.acc, v.z * g.acc, v.w * g.acc};
+        if (kKind == kSym && g.D) {
+            const _Float16 *p = g.D + M.a + static_cast<uint64_t>(j) * M.mp * 2 + split_at(i);
+            const h4 dh = *reinterpret_cast<const h4 *>(p), dl = *reinterpret_cast<const h4 *>(p + 32);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) x[u] = x[u] + g.add * (static_cast<float>(dh[u]) + static_cast<float>(dl[u]));
+        }
+        if (kKind == kSym)
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (i + u == j && i + u < M.m) x[u] = x[u] + g.diag;
+        if (kKind == kOut) {
+            if (M.flip) {
+                put_out(g, M.off + static_cast<uint64_t>(j) * M.C + i, j < M.n && i < M.m ? min(M.m - i, 4u) : 0, step, x);
+            } else {
+                *reinterpret_cast<float4 *>(out + jj * C::kOutLd + hi4) = make_float4(x[0], x[1], x[2], x[3]);
+            }
+            continue;
+        }
+        h4 h, l;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            _Float16 a, b;
+            split(x[u], a, b);
+            h[u] = a;
+            l[u] = b;
+        }
+        _Float16 *p = (kKind == kSym ? g.S + M.a : g.Tn + M.x) + static_cast<uint64_t>(j) * M.mp * 2 + split_at(i);
+        *reinterpret_cast<h4 *>(p) = h;
+        *reinterpret_cast<h4 *>(p + 32) = l;
+        if (kKind == kNext || mirror) *reinterpret_cast<float4 *>(out + jj * C::kOutLd + hi4) = make_float4(x[0], x[1], x[2], x[3]);
+    }
+    // along j: row i of X, or of the mirror image
+    if (kKind == kSym && !mirror) return;
+    if (kKind == kOut && M.flip) return;
+#pragma unroll 2
+    for (uint32_t t = 0; t < 16; ++t) {
+        const uint32_t ii = t * 4 + lo, i = i0 + ii, j = j0 + hi4;
+        float x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] = out[(hi4 + u) * C::kOutLd + ii];
+        if (kKind == kOut) {
+            put_out(g, M.off + static_cast<uint64_t>(i) * M.C + j, i < M.m && j < M.n ? min(M.n - j, 4u) : 0, step, x);
+            continue;
+        }
+        h4 h, l;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            _Float16 a, b;
+            split(x[u], a, b);
+            h[u] = a;
+            l[u] = b;
+        }
+        _Float16 *p = kKind == kSym ? g.S + M.a + static_cast<uint64_t>(i) * M.mp * 2 + split_at(j)
+                                    : g.Xn + M.x + static_cast<uint64_t>(i) * M.np * 2 + split_at(j);
+        *reinterpret_cast<h4 *>(p) = h;
+        *reinterpret_cast<h4 *>(p + 32) = l;
+    }
+}
+
+// One item: stages [it.k0, it.k1) of tile (it.i, it.j).  A whole tile is
+// written out; a part of a split one leaves its sums in it.slot, in register
+// order, and orth_join_kernel adds the parts.
+template <Kind kKind, class C>
+__global__ __launch_bounds__(C::kThreads) void orth_gemm_kernel(GemmArgs g) {
+    __shared__ __attribute__((aligned(128))) char lds[C::kLds];
     const Item it = g.items[blockIdx.x];
     const MatDev M = g.mats[it.mat];
-    const _Float16 *P, *Q;
-    uint32_t ld;  // padded length of the common index
-    if (kPhase == kGram) {
-        P = g.X + M.x;
-        Q = P;
-        ld = M.np;
-    } else if (kPhase == kPoly) {
-        P = g.A + M.a;
-        Q = P;
-        ld = M.mp;
-    } else {
-        P = g.B + M.a;
-        Q = g.T + M.x;
-        ld = M.mp;
+    const uint32_t w = __builtin_amdgcn_readfirstlane(wave_id()), lane = lane_id();
+    const uint32_t i0 = it.i * C::kTile, j0 = it.j * C::kTile;
+    // rows of this tile that exist (multiples of 128)
+    const uint32_t rows_p = min(uint32_t(C::kTile), M.mp - i0), rows_q = min(uint32_t(C::kTile), (kKind == kSym ? M.mp : M.np) - j0);
+    // the waves of a SIMD differ in row half and column half, so that a tile
+    // with half its rows or columns costs half
+    const uint32_t wr = w / C::kWC, wc = (w + wr * (C::kWC / 2)) % C::kWC;
+    const uint32_t pr = wr * C::kWaveRows, qr = wc * C::kWaveCols;
+    const bool active = pr < rows_p && qr < rows_q;
+    f32x4 acc[C::kRA][C::kRB];
+#pragma unroll
+    for (int a = 0; a < C::kRA; ++a)
+#pragma unroll
+        for (int b = 0; b < C::kRB; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    {
+        // this wave's loads: kLoads groups of 8 rows, all of P or all of Q
+        const uint32_t row = w * C::kLoads * 8;  // of the stage
+        const bool of_p = row < uint32_t(C::kTile);
+        const uint32_t r = of_p ? row : row - C::kTile;
+        const uint32_t ld = (of_p ? g.px : g.qx) ? (kKind == kSym ? M.np : M.mp) : M.mp;
+        const char *base = reinterpret_cast<const char *>(
+            (of_p ? g.P + (g.px ? M.x : M.a) : g.Q + (g.qx ? M.x : M.a)) + static_cast<uint64_t>((of_p ? i0 : j0) + r) * ld * 2);
+        const bool load = r < (of_p ? rows_p : rows_q);
+        // part of this lane's LDS place in its row, for even groups; odd ones differ by the bit of 4 parts
+        const uint32_t part = (lane & 7) ^ (lane >> 4);
+        const char *from = base + static_cast<uint64_t>(lane >> 3) * ld * 4 + part * 16 + static_cast<uint64_t>(it.k0) * 128;
+        const int32_t odd = part & 4 ? -64 : 64;
+        const uint64_t row8 = static_cast<uint64_t>(ld) * 32;
+        char *to = lds + row * 128;
+        const uint32_t nk = it.k1 - it.k0;
+        if (active) all_stages<C, true>(lds, to, from, row8, odd, load, nk, pr, qr, acc);
+        else all_stages<C, false>(lds, to, from, row8, odd, load, nk, pr, qr, acc);
     }
-    const uint32_t i0 = it.i * kTM, j0 = it.j * kTN;
-    const uint32_t kreal = kPhase == kGram ? M.n : M.m;
-    const uint32_t nk = (kreal + kTK - 1) / kTK;
-    __shared__ _Float16 lp[2][kTM * 64], lq[2][kTN * 64];
-    const uint32_t t = threadIdx.x, lane = lane_id(), w = wave_id();
-    // staging: 8 parts of 16 bytes a row, thread t takes part t & 7 of rows t / 8 + 32 s
-    const uint32_t part = t & 7, row = t >> 3;
-    const _Float16 *ps = P + static_cast<uint64_t>(i0 + row) * ld * 2 + part * 8;
-    const _Float16 *qs = Q + static_cast<uint64_t>(j0 + row) * ld * 2 + part * 8;
-    const uint64_t rstep = static_cast<uint64_t>(32) * ld * 2;
-    h8 rp[4], rq[4];
-    auto fetch = [&](uint32_t k) {
+    if (it.slot != kNoSlot) {
+        if (!active) return;
+        f32x4 *p = reinterpret_cast<f32x4 *>(g.partial + static_cast<uint64_t>(it.slot) * C::kTile * C::kTile) + w * (C::kRA * C::kRB * kWave) + lane;
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            rp[s] = *reinterpret_cast<const h8 *>(ps + s * rstep + k * 64);
-            rq[s] = *reinterpret_cast<const h8 *>(qs + s * rstep + k * 64);
-        }
-    };
-    auto stash = [&](int buf) {
+        for (int a = 0; a < C::kRA; ++a)
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const uint32_t r = row + 32 * s, at = r * 64 + (part ^ ((r >> 1) & 7)) * 8;
-            *reinterpret_cast<h8 *>(&lp[buf][at]) = rp[s];
-            *reinterpret_cast<h8 *>(&lq[buf][at]) = rq[s];
-        }
-    };
-    const uint32_t wi = (w >> 1) * 64, wj = (w & 1) * 64;  // the wave's corner in the tile
-    const uint32_t fr = lane & 15, fc = lane >> 4;         // operand row and 16-byte part
-    f32x4 acc[4][4];
+            for (int b = 0; b < C::kRB; ++b) p[(a * C::kRB + b) * kWave] = acc[a][b];
+        return;
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (!active) return;
+    float *out = reinterpret_cast<float *>(lds) + w * (64 * C::kOutLd);
+    const uint32_t col = lane & 15, four = (lane >> 4) * 4;
 #pragma unroll
-    for (int a = 0; a < 4; ++a)
-#pragma unroll
-        for (int b = 0; b < 4; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    fetch(0);
-    stash(0);
-    __syncthreads();
-    for (uint32_t k = 0; k < nk; ++k) {
-        const int buf = k & 1;
-        if (k + 1 < nk) fetch(k + 1);
-        h8 ph[4], pl[4], qh[4], ql[4];
-#pragma unroll
-        for (int a = 0; a < 4; ++a) {
-            const uint32_t ri = wi + 16 * a + fr, rj = wj + 16 * a + fr;
-            const uint32_t si = (ri >> 1) & 7, sj = (rj >> 1) & 7;
-            ph[a] = *reinterpret_cast<const h8 *>(&lp[buf][ri * 64 + (fc ^ si) * 8]);
-            pl[a] = *reinterpret_cast<const h8 *>(&lp[buf][ri * 64 + ((fc + 4) ^ si) * 8]);
-            qh[a] = *reinterpret_cast<const h8 *>(&lq[buf][rj * 64 + (fc ^ sj) * 8]);
-            ql[a] = *reinterpret_cast<const h8 *>(&lq[buf][rj * 64 + ((fc + 4) ^ sj) * 8]);
-        }
+    for (int h = 0; h < C::kRA / 4; ++h) {
 #pragma unroll
         for (int a = 0; a < 4; ++a)
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ph[a], ql[b], acc[a][b], 0, 0, 0);
-                acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(pl[a], qh[b], acc[a][b], 0, 0, 0);
-                acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ph[a], qh[b], acc[a][b], 0, 0, 0);
-            }
-        if (k + 1 < nk) stash(buf ^ 1);
-        __syncthreads();
+            for (int b = 0; b < C::kRB; ++b)
+                *reinterpret_cast<f32x4 *>(out + (16 * b + col) * C::kOutLd + 16 * a + four) = acc[4 * h + a][b];
+        write_block<kKind, C>(g, M, out, i0 + pr + 64 * h, j0 + qr, it.i != it.j);
     }
-    // lane: column j = fr, rows 4 fc .. 4 fc + 3 of each 16 x 16 tile
-    const bool mirror = (kPhase == kGram || kPhase == kPoly) && it.i != it.j;
-    const double sc = kPhase == kLast && g.W ? shape_scale(g.shape, M.R, M.C) : 1.0;
-    const float step = static_cast<float>(static_cast<double>(g.lr) * sc);
-#pragma unroll
-    for (int a = 0; a < 4; ++a)
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const uint32_t i = i0 + wi + 16 * a + 4 * fc, j = j0 + wj + 16 * b + fr;
-            float v[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) v[u] = acc[a][b][u] * g.acc;
-            if (kPhase != kGram) {
-                // the addend, read along the other index: A is symmetric, T = X^T
-                const _Float16 *p = kPhase == kPoly ? g.A + M.a + static_cast<uint64_t>(j) * M.mp * 2
-                                                    : g.T + M.x + static_cast<uint64_t>(j) * M.mp * 2;
-                const h4 hi = *reinterpret_cast<const h4 *>(p + split_at(i));
-                const h4 lo = *reinterpret_cast<const h4 *>(p + split_at(i) + 32);
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    v[u] = v[u] + g.add * (static_cast<float>(hi[u]) + static_cast<float>(lo[u]));
-            }
-            if (kPhase == kLast) {
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    if (i + u < M.m && j < M.n) {
-                        const uint64_t at = M.off + (M.flip ? static_cast<uint64_t>(j) * M.C + i + u
-                                                            : static_cast<uint64_t>(i + u) * M.C + j);
-                        if (g.W) g.W[at] = g.decay * g.W[at] - step * v[u];
-                        else g.O[at] = v[u];
-                    }
-                }
-                continue;
-            }
-            h4 hi, lo;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                _Float16 x, y;
-                split(v[u], x, y);
-                hi[u] = x;
-                lo[u] = y;
-            }
-            // [j][i .. i + 3], and [i + u][j] where that is another place
-            _Float16 *pt = kPhase == kGram   ? g.A + M.a + static_cast<uint64_t>(j) * M.mp * 2
-                           : kPhase == kPoly ? g.B + M.a + static_cast<uint64_t>(j) * M.mp * 2
-                                             : g.Tn + M.x + static_cast<uint64_t>(j) * M.mp * 2;
-            *reinterpret_cast<h4 *>(pt + split_at(i)) = hi;
-            *reinterpret_cast<h4 *>(pt + split_at(i) + 32) = lo;
-            if (kPhase == kApply || mirror) {
-                _Float16 *px = kPhase == kGram   ? g.A + M.a
-                               : kPhase == kPoly ? g.B + M.a
-                                                 : g.Xn + M.x;
-                const uint32_t ldx = kPhase == kApply ? M.np : M.mp;
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    _Float16 *q = px + static_cast<uint64_t>(i + u) * ldx * 2 + split_at(j);
-                    q[0] = hi[u];
-                    q[32] = lo[u];
-                }
-            }
-        }
+}
+
+// The parts of a split tile, added in order: one 64 x 64 block per wave, a
+// workgroup of one wave each.
+template <Kind kKind, class C>
+__global__ __launch_bounds__(kWave) void orth_join_kernel(GemmArgs g) {
+    __shared__ float out[64 * C::kOutLd];
+    constexpr uint32_t kBlocks = C::kWaves * (C::kRA / 4);
+    const Item it = g.items[blockIdx.x / kBlocks];
+    const MatDev M = g.mats[it.mat];
+    const uint32_t part = blockIdx.x % kBlocks, w = part / (C::kRA / 4), h = part % (C::kRA / 4), lane = threadIdx.x;
+    const uint32_t wr = w / C::kWC, wc = (w + wr * (C::kWC / 2)) % C::kWC;
+    const uint32_t i0 = it.i * C::kTile + wr * C::kWaveRows + 64 * h, j0 = it.j * C::kTile + wc * C::kWaveCols;
+    if (i0 >= M.mp || j0 >= (kKind == kSym ? M.mp : M.np)) return;
+    const uint32_t col = lane & 15, four = (lane >> 4) * 4;
+    const f32x4 *p = reinterpret_cast<const f32x4 *>(g.partial + static_cast<uint64_t>(it.slot) * C::kTile * C::kTile) +
+                     w * (C::kRA * C::kRB * kWave) + 4 * h * C::kRB * kWave + lane;
+    constexpr uint64_t kStep = static_cast<uint64_t>(C::kTile) * C::kTile / 4;
+#pragma unroll 4
+    for (uint32_t t = 0; t < 16; ++t) {  // tile 4 a + b of the block
+        f32x4 v = p[t * kWave];
+#pragma unroll 4
+        for (uint32_t s = 1; s < it.k1; ++s) v = v + p[s * kStep + t * kWave];
+        *reinterpret_cast<f32x4 *>(out + (16 * (t & 3) + col) * C::kOutLd + 16 * (t >> 2) + four) = v;
+    }
+    write_block<kKind, C>(g, M, out, i0, j0, it.i != it.j);
 }
 
 // --------------------------------------------------------------- host side
@@ -538,55 +690,181 @@ gc_status check_orth(const char *fn, const gc_matrix_plan *p, const gc_orth_opti
     return GC_OK;
 }
 
+template <Kind kKind, class C>
+void product_of(const char *name, const gc_matrix_plan *p, const OrthDev &d, List l, GemmArgs g, hipStream_t stream) {
+    g.items = d.list[l];
+    GC_LAUNCH(name, stream,
+              orth_gemm_kernel<kKind, C><<<static_cast<unsigned>(p->list[l].size()), C::kThreads, 0, stream>>>(g));
+    const List joins = static_cast<List>(l + 1);
+    if (p->list[joins].empty()) return;
+    g.items = d.list[joins];
+    const unsigned blocks = static_cast<unsigned>(p->list[joins].size()) * C::kWaves * (C::kRA / 4);
+    GC_LAUNCH("orth_join", stream, orth_join_kernel<kKind, C><<<blocks, kWave, 0, stream>>>(g));
+}
+
+template <Kind kKind>
+void product(const char *name, const gc_matrix_plan *p, const OrthDev &d, List l, const GemmArgs &g, hipStream_t stream) {
+    if (p->large) product_of<kKind, Shape<Large>>(name, p, d, l, g, stream);
+    else product_of<kKind, Shape<Small>>(name, p, d, l, g, stream);
+}
+
 gc_status orthogonalize(const char *fn, const gc_matrix_plan *p, const gc_orth_options &o, const Scales *sc, Source src,
                         float *O, float *W, float decay, float lr, int shape, void *ws, hipStream_t stream) {
     OrthDev d;
     gc_status st = orth_device(p, &d);
     if (st != GC_OK) return st;
     const OrthWs w = orth_ws(align256(ws), p);
-    GC_LAUNCH("orth_norm", stream, orth_norm_kernel<<<d.nchunks, kBlock, 0, stream>>>(d.chunks, d.mat, src, w.partial));
-    GC_LAUNCH("orth_scale", stream, orth_scale_kernel<<<d.nmat, kBlock, 0, stream>>>(d.mat, w.partial, o.eps, w.inv));
+    auto size = [&](List l) { return static_cast<unsigned>(p->list[l].size()); };
+    auto pow2 = [](double c, int e) { return static_cast<float>(std::ldexp(c, e)); };
+    GC_LAUNCH("orth_norm", stream,
+              orth_norm_kernel<<<size(kChunks), kBlock, 0, stream>>>(d.list[kChunks], d.mat, src, w.sums));
+    GC_LAUNCH("orth_scale", stream,
+              orth_scale_kernel<<<static_cast<unsigned>(p->mat.size()), kBlock, 0, stream>>>(d.mat, w.sums, o.eps, w.inv));
     GC_LAUNCH("orth_split", stream,
-              orth_split_kernel<<<d.ntiles, kBlock, 0, stream>>>(d.tiles, d.mat, src, w.inv,
-                                                               static_cast<float>(std::ldexp(1.0, sc[0].ex)), w.X[0], w.T[0]));
-    auto pow2 = [](int e) { return static_cast<float>(std::ldexp(1.0, e)); };
+              orth_split_kernel<<<size(kTiles), kBlock, 0, stream>>>(d.list[kTiles], d.mat, src, w.inv, pow2(1.0, sc[0].ex),
+                                                                   w.X[0], w.T[0]));
     int cur = 0;
     for (int k = 0; k < o.steps; ++k) {
         const Scales &s = sc[k];
+        const double a = o.coef[k][0], b = o.coef[k][1], c = o.coef[k][2];
         GemmArgs g{};
         g.mats = d.mat;
-        g.X = w.X[cur];
-        g.T = w.T[cur];
-        g.A = w.A;
-        g.B = w.B;
-        g.Xn = w.X[cur ^ 1];
-        g.Tn = w.T[cur ^ 1];
-        g.items = d.tri;
-        g.acc = pow2(s.ea - 2 * s.ex);
-        GC_LAUNCH("orth_gram", stream, orth_gemm_kernel<kGram><<<d.ntri, kBlock, 0, stream>>>(g));
-        g.acc = static_cast<float>(std::ldexp(static_cast<double>(o.coef[k][2]), s.eb - 2 * s.ea));
-        g.add = static_cast<float>(std::ldexp(static_cast<double>(o.coef[k][1]), s.eb - s.ea));
-        GC_LAUNCH("orth_poly", stream, orth_gemm_kernel<kPoly><<<d.ntri, kBlock, 0, stream>>>(g));
-        g.items = d.rect;
+        g.partial = w.partial;
+        g.P = g.Q = w.X[cur];
+        g.px = g.qx = 1;
+        g.acc = pow2(1.0, s.ea - 2 * s.ex);
+        g.S = w.A;
+        product<kSym>("orth_gram", p, d, kGram, g, stream);
+        g.P = g.Q = g.D = w.A;
+        g.px = g.qx = 0;
+        g.acc = pow2(c, s.eb - 2 * s.ea);
+        g.add = pow2(b, s.eb - s.ea);
+        g.diag = pow2(a, s.eb);
+        g.S = w.B;
+        product<kSym>("orth_poly", p, d, kSquare, g, stream);
         const bool last = k + 1 == o.steps;
-        const int en = last ? 0 : sc[k + 1].ex;
-        g.acc = pow2(en - s.eb - s.ex);
-        g.add = static_cast<float>(std::ldexp(static_cast<double>(o.coef[k][0]), en - s.ex));
+        g.P = w.B;
+        g.Q = w.T[cur];
+        g.qx = 1;
+        g.acc = pow2(1.0, (last ? 0 : sc[k + 1].ex) - s.eb - s.ex);
+        cur ^= 1;
         if (last) {
             g.O = O;
             g.W = W;
             g.decay = decay;
             g.lr = lr;
             g.shape = shape;
-            GC_LAUNCH("orth_apply", stream, orth_gemm_kernel<kLast><<<d.nrect, kBlock, 0, stream>>>(g));
+            product<kOut>("orth_apply", p, d, kApply, g, stream);
         } else {
-            GC_LAUNCH("orth_apply", stream, orth_gemm_kernel<kApply><<<d.nrect, kBlock, 0, stream>>>(g));
+            g.Xn = w.X[cur];
+            g.Tn = w.T[cur];
+            product<kNext>("orth_apply", p, d, kApply, g, stream);
         }
-        cur ^= 1;
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return hip_error(e, fn);
     return GC_OK;
+}
+
+// ------------------------------------------------------------- work lists
+// A tile of a product before it is planned.
+struct Tile {
+    uint32_t mat, i, j, stages;
+    float weight;  // share of a whole tile's rows and columns that exists
+};
+
+// How long a list takes on 256 compute units, one item on each at a time, in
+// stages of a whole tile: items by falling length to the unit that is free
+// first.  kItemCost: an item's first loads and its writing out; kPartCost: a
+// part's sums written and read again, on the memory's account.
+constexpr uint32_t kUnits = 256;
+
+struct Costs {
+    double stage, item, part, join;
+};
+
+double makespan(const std::vector<Tile> &tiles, uint32_t cap, const Costs &c) {
+    std::vector<double> lengths;
+    double parts = 0.0, joins = 0.0;
+    for (const Tile &t : tiles) {
+        const uint32_t n = static_cast<uint32_t>(ceil_div(t.stages, cap));
+        for (uint32_t q = 0; q < n; ++q)
+            lengths.push_back(c.item + c.stage * std::max(0.4f, t.weight) * static_cast<double>(t.stages) / n);
+        if (n > 1) {
+            parts += n;
+            joins = c.join;
+        }
+    }
+    std::sort(lengths.begin(), lengths.end(), std::greater<double>());
+    std::priority_queue<double, std::vector<double>, std::greater<double>> free_at;
+    for (uint32_t u = 0; u < kUnits; ++u) free_at.push(0.0);
+    double end = 0.0;
+    for (double l : lengths) {
+        const double t = free_at.top() + l;
+        free_at.pop();
+        free_at.push(t);
+        end = std::max(end, t);
+    }
+    return end + parts * c.part + joins;
+}
+
+// The cap on a tile's stages (longer ones are split evenly) that the model
+// finds fastest, and its time.
+std::pair<uint32_t, double> best_cap(const std::vector<Tile> &tiles, const Costs &c) {
+    uint32_t longest = 1;
+    for (const Tile &t : tiles) longest = std::max(longest, t.stages);
+    std::pair<uint32_t, double> best{longest, makespan(tiles, longest, c)};
+    for (uint32_t n = 2; n <= 32 && longest / n >= 4; ++n) {
+        const uint32_t cap = static_cast<uint32_t>(ceil_div(longest, n));
+        const double t = makespan(tiles, cap, c);
+        if (t < best.second) best = {cap, t};
+    }
+    return best;
+}
+
+// The items of a list, longest first.  Workgroup b runs on XCD b % 8: in each
+// round of 256 items an XCD takes 32 that are next to each other, so that its
+// L2 holds the rows they share.
+void plan_list(const std::vector<Tile> &tiles, uint32_t cap, std::vector<Item> *items, std::vector<Item> *joins,
+               uint32_t *slots) {
+    std::vector<Item> all;
+    uint32_t slot = 0;
+    for (const Tile &t : tiles) {
+        const uint32_t n = static_cast<uint32_t>(ceil_div(t.stages, cap));
+        if (n > 1) joins->push_back({t.mat, t.i, t.j, 0, n, slot});
+        for (uint32_t q = 0; q < n; ++q) {
+            const uint32_t k0 = static_cast<uint32_t>(static_cast<uint64_t>(t.stages) * q / n);
+            const uint32_t k1 = static_cast<uint32_t>(static_cast<uint64_t>(t.stages) * (q + 1) / n);
+            all.push_back({t.mat, t.i, t.j, k0, k1, n > 1 ? slot++ : kNoSlot});
+        }
+    }
+    std::stable_sort(all.begin(), all.end(), [](const Item &a, const Item &b) { return a.k1 - a.k0 > b.k1 - b.k0; });
+    items->resize(all.size());
+    constexpr size_t kXcds = 8;
+    for (size_t base = 0; base < all.size(); base += kUnits) {
+        const size_t n = std::min<size_t>(kUnits, all.size() - base);
+        size_t from = base;
+        for (size_t x = 0; x < kXcds; ++x)
+            for (size_t t = x; t < n; t += kXcds) (*items)[base + t] = all[from++];
+    }
+    *slots = std::max(*slots, slot);
+}
+
+// The tiles of a product, neighbours in a block of 4 rows next to each other.
+std::vector<Tile> tiles_of(const std::vector<MatDev> &mats, uint32_t tile, List l) {
+    std::vector<Tile> out;
+    for (uint32_t id = 0; id < mats.size(); ++id) {
+        const MatDev &M = mats[id];
+        const uint32_t rows = M.mp, cols = l == kApply ? M.np : M.mp;
+        const uint32_t nr = (rows + tile - 1) / tile, nc = (cols + tile - 1) / tile;
+        const uint32_t stages = static_cast<uint32_t>(ceil_div(l == kGram ? M.n : M.m, 32));
+        auto share = [&](uint32_t all, uint32_t at) { return static_cast<float>(std::min(tile, all - at * tile)) / tile; };
+        for (uint32_t ib = 0; ib < nr; ib += 4)
+            for (uint32_t j = 0; j < nc; ++j)
+                for (uint32_t i = ib; i < std::min(ib + 4, nr); ++i)
+                    if (l == kApply || j <= i) out.push_back({id, i, j, stages, share(rows, i) * share(cols, j)});
+    }
+    return out;
 }
 
 // The tables of every matrix.
@@ -613,15 +891,33 @@ void fill_plan(gc_matrix_plan *p, const gc_plan *plan, const uint32_t *rows) {
         a += 2 * static_cast<uint64_t>(M.mp) * M.mp;
         chunk0 += M.nchunk;
         const uint32_t id = static_cast<uint32_t>(p->mat.size());
-        for (uint32_t c = 0; c < M.nchunk; ++c) p->chunks.push_back({id, c, 0, 0});
-        for (uint32_t i = 0; i < M.mp / kTM; ++i)
-            for (uint32_t j = 0; j <= i; ++j) p->tri.push_back({id, i, j, 0});
-        for (uint32_t j = 0; j < M.np / kTN; ++j)
-            for (uint32_t i = 0; i < M.mp / kTM; ++i) p->rect.push_back({id, i, j, 0});
+        for (uint32_t c = 0; c < M.nchunk; ++c) p->list[kChunks].push_back({id, c, 0, 0, 0, 0});
         for (uint32_t i = 0; i < M.mp / kSplitTile; ++i)
-            for (uint32_t j = 0; j < M.np / kSplitTile; ++j) p->tiles.push_back({id, i, j, 0});
+            for (uint32_t j = 0; j < M.np / kSplitTile; ++j) p->list[kTiles].push_back({id, i, j, 0, 0, 0});
         p->mat.push_back(M);
     }
+    // the tile shape and splits that the model finds fastest for one step
+    const Costs costs[2] = {{0.55, 5.0, 0.025, 6.0}, {1.85, 12.0, 0.1, 6.0}};  // us: Small, Large
+    double best = 0.0;
+    uint32_t caps[3] = {};
+    constexpr List kProducts[3] = {kGram, kSquare, kApply};
+    for (int large = 0; large < 2; ++large) {
+        double time = 0.0;
+        uint32_t cap[3];
+        for (int q = 0; q < 3; ++q) {
+            const auto b = best_cap(tiles_of(p->mat, large ? Large::kTile : Small::kTile, kProducts[q]), costs[large]);
+            cap[q] = b.first;
+            time += b.second;
+        }
+        if (large == 0 || time < best) {
+            best = time;
+            p->large = large;
+            std::copy(cap, cap + 3, caps);
+        }
+    }
+    for (int q = 0; q < 3; ++q)
+        plan_list(tiles_of(p->mat, p->large ? Large::kTile : Small::kTile, kProducts[q]), caps[q], &p->list[kProducts[q]],
+                  &p->list[kProducts[q] + 1], &p->slots);
     p->xhalves = x;
     p->ahalves = a;
 }

@@ -698,7 +698,7 @@ size_t    gc_matrix_plan_workspace_bytes(const gc_matrix_plan *mplan);
  * Errors: GC_EINVAL (null, steps, eps negative or not finite, reserved not 0,
  *         coefficients that are not finite, or with which singular values
  *         of at most 1 at the start may pass 8 before the last step (1e12
- *         after it), those of b A + c A^2 2^14, or all fall below 1e-12;
+ *         after it), those of a I + b A + c A^2 2^14, or all fall below 1e-12;
  *         overlapping buffers), GC_ECAPACITY (ws).
  */
 #define GC_MAX_ORTH_STEPS  16
@@ -764,7 +764,7 @@ gc_status gc_muon_step(const gc_matrix_plan *mplan, const float *G, float *U, fl
  *             embed_heads, embed_rows, embed_sum, embed_join, embed_small,
  *             embed_empty,
  *             orth_norm, orth_scale, orth_split, orth_gram, orth_poly,
- *             orth_apply.
+ *             orth_apply, orth_join.
  * gc_timing_take waits for the recorded events of one kernel and returns the
  * summed duration in milliseconds and the number of launches, then forgets
  * them.  Host-thread safe; not for use while a stream is being captured.
