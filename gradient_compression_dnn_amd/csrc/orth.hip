@@ -84,9 +84,14 @@ constexpr int kSplitTile = 64;  // orth_split's tile
 // the joins of its split tiles.
 enum List { kChunks, kTiles, kGram, kGramJoin, kSquare, kSquareJoin, kApply, kApplyJoin, kLists };
 
+// Products are planned for a workgroup on each of 256 compute units; unit u
+// has items [first[u], first[u + 1]) of its list.
+constexpr uint32_t kUnits = 256;
+
 struct OrthDev {
     const MatDev *mat;
     const Item *list[kLists];
+    const uint32_t *first[kLists];
 };
 
 }  // namespace
@@ -99,6 +104,7 @@ struct gc_matrix_plan {
     bool large = false;                 // tiles of 256 x 256
     std::vector<gc::MatDev> mat;
     std::vector<gc::Item> list[gc::kLists];
+    std::vector<uint32_t> first[gc::kLists];  // products only
     std::mutex mu;
     std::vector<std::pair<int, void *>> dev_blob;
 };
@@ -109,7 +115,7 @@ namespace {
 
 // ----------------------------------------------------------- tables, scales
 struct Blob {
-    size_t mat, list[kLists], total;
+    size_t mat, list[kLists], first[kLists], total;
 };
 
 Blob blob_layout(const gc_matrix_plan *p) {
@@ -122,7 +128,10 @@ Blob blob_layout(const gc_matrix_plan *p) {
         return at;
     };
     L.mat = take(sizeof(MatDev) * p->mat.size());
-    for (int l = 0; l < kLists; ++l) L.list[l] = take(sizeof(Item) * p->list[l].size());
+    for (int l = 0; l < kLists; ++l) {
+        L.list[l] = take(sizeof(Item) * p->list[l].size());
+        L.first[l] = take(sizeof(uint32_t) * p->first[l].size());
+    }
     L.total = o < 256 ? 256 : o;
     return L;
 }
@@ -150,8 +159,11 @@ gc_status orth_device(const gc_matrix_plan *cplan, OrthDev *out) {
             e = hipMalloc(&blob, L.total);
             if (e != hipSuccess) return hip_error(e, "hipMalloc(matrix plan tables)");
             std::memcpy(host.data() + L.mat, p->mat.data(), sizeof(MatDev) * p->mat.size());
-            for (int l = 0; l < kLists; ++l)
+            for (int l = 0; l < kLists; ++l) {
                 if (!p->list[l].empty()) std::memcpy(host.data() + L.list[l], p->list[l].data(), sizeof(Item) * p->list[l].size());
+                if (!p->first[l].empty())
+                    std::memcpy(host.data() + L.first[l], p->first[l].data(), sizeof(uint32_t) * p->first[l].size());
+            }
             e = hipMemcpy(blob, host.data(), L.total, hipMemcpyHostToDevice);
             if (e != hipSuccess) {
                 (void)hipFree(blob);
@@ -162,7 +174,10 @@ gc_status orth_device(const gc_matrix_plan *cplan, OrthDev *out) {
     }
     auto *b = static_cast<uint8_t *>(blob);
     out->mat = reinterpret_cast<const MatDev *>(b + L.mat);
-    for (int l = 0; l < kLists; ++l) out->list[l] = reinterpret_cast<const Item *>(b + L.list[l]);
+    for (int l = 0; l < kLists; ++l) {
+        out->list[l] = reinterpret_cast<const Item *>(b + L.list[l]);
+        out->first[l] = reinterpret_cast<const uint32_t *>(b + L.first[l]);
+    }
     return GC_OK;
 }
 
@@ -366,6 +381,7 @@ enum Kind { kSym, kNext, kOut };
 
 struct GemmArgs {
     const Item *items;
+    const uint32_t *first;
     const MatDev *mats;
     const _Float16 *P, *Q;  // operands; P null: of X's shape, else m x m
     uint32_t px, qx;        // whether an operand is an X (or T) array
@@ -504,16 +520,17 @@ __device__ __forceinline__ void put_out(const GemmArgs &g, uint64_t at, uint32_t
         }
 }
 
-// The wave's rows [64 h, 64 h + 64) of its tile, which `out` holds as
-// [column][row]: scaled, addend and diagonal added, and written out.
-template <Kind kKind, class C>
-__device__ void write_block(const GemmArgs &g, const MatDev &M, float *out, uint32_t i0, uint32_t j0, bool mirror) {
+// A block of 64 x 64 results, which `out` holds as [column][row]: scaled,
+// addend and diagonal added, and written out, by one wave or a team of kTeam.
+template <Kind kKind, class C, int kTeam>
+__device__ __forceinline__ void write_block(const GemmArgs &g, const MatDev &M, float *out, uint32_t i0, uint32_t j0, bool mirror) {
+    const uint32_t w = kTeam > 1 ? wave_id() : 0;
     const uint32_t hi4 = (lane_id() & 15) * 4, lo = lane_id() >> 4;
     // along i: row j of T, or of the symmetric result
     const double sc = kKind == kOut && g.W ? shape_scale(g.shape, M.R, M.C) : 1.0;
     const float step = static_cast<float>(static_cast<double>(g.lr) * sc);
 #pragma unroll 2
-    for (uint32_t t = 0; t < 16; ++t) {
+    for (uint32_t t = w; t < 16; t += kTeam) {
         const uint32_t jj = t * 4 + lo, i = i0 + hi4, j = j0 + jj;
         float4 v = *reinterpret_cast<const float4 *>(out + jj * C::kOutLd + hi4);
         float x[4] = {v.x * g.acc, v.y * g.acc, v.z * g.acc, v.w * g.acc};
@@ -551,8 +568,9 @@ __device__ void write_block(const GemmArgs &g, const MatDev &M, float *out, uint
     // along j: row i of X, or of the mirror image
     if (kKind == kSym && !mirror) return;
     if (kKind == kOut && M.flip) return;
+    if (kTeam > 1) __syncthreads();
 #pragma unroll 2
-    for (uint32_t t = 0; t < 16; ++t) {
+    for (uint32_t t = w; t < 16; t += kTeam) {
         const uint32_t ii = t * 4 + lo, i = i0 + ii, j = j0 + hi4;
         float x[4];
 #pragma unroll
@@ -576,97 +594,109 @@ __device__ void write_block(const GemmArgs &g, const MatDev &M, float *out, uint
     }
 }
 
-// One item: stages [it.k0, it.k1) of tile (it.i, it.j).  A whole tile is
-// written out; a part of a split one leaves its sums in it.slot, in register
-// order, and orth_join_kernel adds the parts.
+// A unit's items, one after the other: stages [it.k0, it.k1) of tile (it.i,
+// it.j).  A whole tile is written out; a part of a split one leaves its sums in
+// it.slot, in register order, and orth_join_kernel adds the parts.
 template <Kind kKind, class C>
 __global__ __launch_bounds__(C::kThreads) void orth_gemm_kernel(GemmArgs g) {
     __shared__ __attribute__((aligned(128))) char lds[C::kLds];
-    const Item it = g.items[blockIdx.x];
-    const MatDev M = g.mats[it.mat];
     const uint32_t w = __builtin_amdgcn_readfirstlane(wave_id()), lane = lane_id();
-    const uint32_t i0 = it.i * C::kTile, j0 = it.j * C::kTile;
-    // rows of this tile that exist (multiples of 128)
-    const uint32_t rows_p = min(uint32_t(C::kTile), M.mp - i0), rows_q = min(uint32_t(C::kTile), (kKind == kSym ? M.mp : M.np) - j0);
-    // the waves of a SIMD differ in row half and column half, so that a tile
-    // with half its rows or columns costs half
-    const uint32_t wr = w / C::kWC, wc = (w + wr * (C::kWC / 2)) % C::kWC;
-    const uint32_t pr = wr * C::kWaveRows, qr = wc * C::kWaveCols;
-    const bool active = pr < rows_p && qr < rows_q;
-    f32x4 acc[C::kRA][C::kRB];
-#pragma unroll
-    for (int a = 0; a < C::kRA; ++a)
-#pragma unroll
-        for (int b = 0; b < C::kRB; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    {
-        // this wave's loads: kLoads groups of 8 rows, all of P or all of Q
-        const uint32_t row = w * C::kLoads * 8;  // of the stage
-        const bool of_p = row < uint32_t(C::kTile);
-        const uint32_t r = of_p ? row : row - C::kTile;
-        const uint32_t ld = (of_p ? g.px : g.qx) ? (kKind == kSym ? M.np : M.mp) : M.mp;
-        const char *base = reinterpret_cast<const char *>(
-            (of_p ? g.P + (g.px ? M.x : M.a) : g.Q + (g.qx ? M.x : M.a)) + static_cast<uint64_t>((of_p ? i0 : j0) + r) * ld * 2);
-        const bool load = r < (of_p ? rows_p : rows_q);
-        // part of this lane's LDS place in its row, for even groups; odd ones differ by the bit of 4 parts
-        const uint32_t part = (lane & 7) ^ (lane >> 4);
-        const char *from = base + static_cast<uint64_t>(lane >> 3) * ld * 4 + part * 16 + static_cast<uint64_t>(it.k0) * 128;
-        const int32_t odd = part & 4 ? -64 : 64;
-        const uint64_t row8 = static_cast<uint64_t>(ld) * 32;
-        char *to = lds + row * 128;
-        const uint32_t nk = it.k1 - it.k0;
-        if (active) all_stages<C, true>(lds, to, from, row8, odd, load, nk, pr, qr, acc);
-        else all_stages<C, false>(lds, to, from, row8, odd, load, nk, pr, qr, acc);
-    }
-    if (it.slot != kNoSlot) {
-        if (!active) return;
-        f32x4 *p = reinterpret_cast<f32x4 *>(g.partial + static_cast<uint64_t>(it.slot) * C::kTile * C::kTile) + w * (C::kRA * C::kRB * kWave) + lane;
+    const uint32_t end = g.first[blockIdx.x + 1];
+    for (uint32_t at = g.first[blockIdx.x]; at < end; ++at) {
+        const Item it = g.items[at];
+        const MatDev M = g.mats[it.mat];
+        // every wave is done with the LDS of the item before
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        const uint32_t i0 = it.i * C::kTile, j0 = it.j * C::kTile;
+        // rows of this tile that exist (multiples of 128)
+        const uint32_t rows_p = min(uint32_t(C::kTile), M.mp - i0), rows_q = min(uint32_t(C::kTile), (kKind == kSym ? M.mp : M.np) - j0);
+        // the waves of a SIMD differ in row half and column half, so that a tile
+        // with half its rows or columns costs half
+        const uint32_t wr = w / C::kWC, wc = (w + wr * (C::kWC / 2)) % C::kWC;
+        const uint32_t pr = wr * C::kWaveRows, qr = wc * C::kWaveCols;
+        const bool active = pr < rows_p && qr < rows_q;
+        f32x4 acc[C::kRA][C::kRB];
 #pragma unroll
         for (int a = 0; a < C::kRA; ++a)
 #pragma unroll
-            for (int b = 0; b < C::kRB; ++b) p[(a * C::kRB + b) * kWave] = acc[a][b];
-        return;
-    }
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    if (!active) return;
-    float *out = reinterpret_cast<float *>(lds) + w * (64 * C::kOutLd);
-    const uint32_t col = lane & 15, four = (lane >> 4) * 4;
+            for (int b = 0; b < C::kRB; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        {
+            // this wave's loads: kLoads groups of 8 rows, all of P or all of Q
+            const uint32_t row = w * C::kLoads * 8;  // of the stage
+            const bool of_p = row < uint32_t(C::kTile);
+            const uint32_t r = of_p ? row : row - C::kTile;
+            const uint32_t ld = (of_p ? g.px : g.qx) ? (kKind == kSym ? M.np : M.mp) : M.mp;
+            const char *base = reinterpret_cast<const char *>(
+                (of_p ? g.P + (g.px ? M.x : M.a) : g.Q + (g.qx ? M.x : M.a)) + static_cast<uint64_t>((of_p ? i0 : j0) + r) * ld * 2);
+            const bool load = r < (of_p ? rows_p : rows_q);
+            // part of this lane's LDS place in its row, for even groups; odd ones differ by the bit of 4 parts
+            const uint32_t part = (lane & 7) ^ (lane >> 4);
+            const char *from = base + static_cast<uint64_t>(lane >> 3) * ld * 4 + part * 16 + static_cast<uint64_t>(it.k0) * 128;
+            const int32_t odd = part & 4 ? -64 : 64;
+            const uint64_t row8 = static_cast<uint64_t>(ld) * 32;
+            char *to = lds + row * 128;
+            const uint32_t nk = it.k1 - it.k0;
+            if (active) all_stages<C, true>(lds, to, from, row8, odd, load, nk, pr, qr, acc);
+            else all_stages<C, false>(lds, to, from, row8, odd, load, nk, pr, qr, acc);
+        }
+        if (it.slot != kNoSlot) {
+            if (!active) continue;
+            f32x4 *p = reinterpret_cast<f32x4 *>(g.partial + static_cast<uint64_t>(it.slot) * C::kTile * C::kTile) + w * (C::kRA * C::kRB * kWave) + lane;
 #pragma unroll
-    for (int h = 0; h < C::kRA / 4; ++h) {
+            for (int a = 0; a < C::kRA; ++a)
 #pragma unroll
-        for (int a = 0; a < 4; ++a)
+                for (int b = 0; b < C::kRB; ++b) p[(a * C::kRB + b) * kWave] = acc[a][b];
+            continue;
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if (!active) continue;
+        float *out = reinterpret_cast<float *>(lds) + w * (64 * C::kOutLd);
+        const uint32_t col = lane & 15, four = (lane >> 4) * 4;
 #pragma unroll
-            for (int b = 0; b < C::kRB; ++b)
-                *reinterpret_cast<f32x4 *>(out + (16 * b + col) * C::kOutLd + 16 * a + four) = acc[4 * h + a][b];
-        write_block<kKind, C>(g, M, out, i0 + pr + 64 * h, j0 + qr, it.i != it.j);
+        for (int h = 0; h < C::kRA / 4; ++h) {
+#pragma unroll
+            for (int a = 0; a < 4; ++a)
+#pragma unroll
+                for (int b = 0; b < C::kRB; ++b)
+                    *reinterpret_cast<f32x4 *>(out + (16 * b + col) * C::kOutLd + 16 * a + four) = acc[4 * h + a][b];
+            write_block<kKind, C, 1>(g, M, out, i0 + pr + 64 * h, j0 + qr, it.i != it.j);
+        }
     }
 }
 
-// The parts of a split tile, added in order: one 64 x 64 block per wave, a
-// workgroup of one wave each.
+// The parts of a split tile, added in order: a 64 x 64 block per workgroup of
+// 4 waves.
 template <Kind kKind, class C>
-__global__ __launch_bounds__(kWave) void orth_join_kernel(GemmArgs g) {
-    __shared__ float out[64 * C::kOutLd];
+__global__ __launch_bounds__(kBlock) void orth_join_kernel(GemmArgs g) {
+    __shared__ __attribute__((aligned(16))) float out[64 * C::kOutLd];
     constexpr uint32_t kBlocks = C::kWaves * (C::kRA / 4);
     const Item it = g.items[blockIdx.x / kBlocks];
     const MatDev M = g.mats[it.mat];
-    const uint32_t part = blockIdx.x % kBlocks, w = part / (C::kRA / 4), h = part % (C::kRA / 4), lane = threadIdx.x;
+    const uint32_t part = blockIdx.x % kBlocks, w = part / (C::kRA / 4), h = part % (C::kRA / 4), lane = lane_id();
     const uint32_t wr = w / C::kWC, wc = (w + wr * (C::kWC / 2)) % C::kWC;
     const uint32_t i0 = it.i * C::kTile + wr * C::kWaveRows + 64 * h, j0 = it.j * C::kTile + wc * C::kWaveCols;
     if (i0 >= M.mp || j0 >= (kKind == kSym ? M.mp : M.np)) return;
     const uint32_t col = lane & 15, four = (lane >> 4) * 4;
+    // tiles 4 a + b of the block: a is this wave's
+    const uint32_t a = wave_id();
     const f32x4 *p = reinterpret_cast<const f32x4 *>(g.partial + static_cast<uint64_t>(it.slot) * C::kTile * C::kTile) +
-                     w * (C::kRA * C::kRB * kWave) + 4 * h * C::kRB * kWave + lane;
+                     w * (C::kRA * C::kRB * kWave) + (4 * h + a) * C::kRB * kWave + lane;
     constexpr uint64_t kStep = static_cast<uint64_t>(C::kTile) * C::kTile / 4;
-#pragma unroll 4
-    for (uint32_t t = 0; t < 16; ++t) {  // tile 4 a + b of the block
-        f32x4 v = p[t * kWave];
-#pragma unroll 4
-        for (uint32_t s = 1; s < it.k1; ++s) v = v + p[s * kStep + t * kWave];
-        *reinterpret_cast<f32x4 *>(out + (16 * (t & 3) + col) * C::kOutLd + 16 * (t >> 2) + four) = v;
-    }
-    write_block<kKind, C>(g, M, out, i0, j0, it.i != it.j);
+    f32x4 v[C::kRB];
+#pragma unroll
+    for (int b = 0; b < C::kRB; ++b) v[b] = p[b * kWave];
+#pragma unroll 2
+    for (uint32_t s = 1; s < it.k1; ++s)
+#pragma unroll
+        for (int b = 0; b < C::kRB; ++b) v[b] = v[b] + p[s * kStep + b * kWave];
+#pragma unroll
+    for (int b = 0; b < C::kRB; ++b) *reinterpret_cast<f32x4 *>(out + (16 * b + col) * C::kOutLd + 16 * a + four) = v[b];
+    __syncthreads();
+    write_block<kKind, C, kWaves>(g, M, out, i0, j0, it.i != it.j);
 }
 
 // --------------------------------------------------------------- host side
@@ -693,13 +723,14 @@ gc_status check_orth(const char *fn, const gc_matrix_plan *p, const gc_orth_opti
 template <Kind kKind, class C>
 void product_of(const char *name, const gc_matrix_plan *p, const OrthDev &d, List l, GemmArgs g, hipStream_t stream) {
     g.items = d.list[l];
+    g.first = d.first[l];
     GC_LAUNCH(name, stream,
-              orth_gemm_kernel<kKind, C><<<static_cast<unsigned>(p->list[l].size()), C::kThreads, 0, stream>>>(g));
+              orth_gemm_kernel<kKind, C><<<static_cast<unsigned>(p->first[l].size() - 1), C::kThreads, 0, stream>>>(g));
     const List joins = static_cast<List>(l + 1);
     if (p->list[joins].empty()) return;
     g.items = d.list[joins];
     const unsigned blocks = static_cast<unsigned>(p->list[joins].size()) * C::kWaves * (C::kRA / 4);
-    GC_LAUNCH("orth_join", stream, orth_join_kernel<kKind, C><<<blocks, kWave, 0, stream>>>(g));
+    GC_LAUNCH("orth_join", stream, orth_join_kernel<kKind, C><<<blocks, kBlock, 0, stream>>>(g));
 }
 
 template <Kind kKind>
@@ -773,81 +804,84 @@ struct Tile {
     float weight;  // share of a whole tile's rows and columns that exists
 };
 
-// How long a list takes on 256 compute units, one item on each at a time, in
-// stages of a whole tile: items by falling length to the unit that is free
-// first.  kItemCost: an item's first loads and its writing out; kPartCost: a
-// part's sums written and read again, on the memory's account.
-constexpr uint32_t kUnits = 256;
-
+// us of a stage of a whole tile, of an item (first loads, writing out), of a
+// part's sums written and read again, on the memory's account, and of a join.
 struct Costs {
     double stage, item, part, join;
 };
 
-double makespan(const std::vector<Tile> &tiles, uint32_t cap, const Costs &c) {
-    std::vector<double> lengths;
-    double parts = 0.0, joins = 0.0;
+// What the units do, in XCD-major order: units 32 x .. 32 x + 31 are on XCD x.
+struct Schedule {
+    std::vector<Item> items[kUnits], joins;
+    uint32_t slots = 0;
+    double time = 0.0;
+};
+
+// Tiles by falling length to the unit with the least to do, as long as that
+// stays within `limit`; the others are cut to fill what the units have left
+// (pieces of at least 4 stages).  False if the work does not fit.
+bool fill_units(const std::vector<Tile> &tiles, const Costs &c, double limit, Schedule *s) {
+    auto stage = [&](const Tile &t) { return c.stage * std::max(0.4, static_cast<double>(t.weight)); };
+    typedef std::pair<double, uint32_t> Load;
+    std::priority_queue<Load, std::vector<Load>, std::greater<Load>> least;
+    for (uint32_t u = 0; u < kUnits; ++u) least.push({0.0, u});
+    std::vector<const Tile *> cut;
     for (const Tile &t : tiles) {
-        const uint32_t n = static_cast<uint32_t>(ceil_div(t.stages, cap));
-        for (uint32_t q = 0; q < n; ++q)
-            lengths.push_back(c.item + c.stage * std::max(0.4f, t.weight) * static_cast<double>(t.stages) / n);
-        if (n > 1) {
-            parts += n;
-            joins = c.join;
+        const Load l = least.top();
+        const double end = l.first + c.item + stage(t) * t.stages;
+        if (end > limit * (1.0 + 1e-9)) {
+            cut.push_back(&t);
+            continue;
         }
+        least.pop();
+        least.push({end, l.second});
+        s->items[l.second].push_back({t.mat, t.i, t.j, 0, t.stages, kNoSlot});
+        s->time = std::max(s->time, end);
     }
-    std::sort(lengths.begin(), lengths.end(), std::greater<double>());
-    std::priority_queue<double, std::vector<double>, std::greater<double>> free_at;
-    for (uint32_t u = 0; u < kUnits; ++u) free_at.push(0.0);
-    double end = 0.0;
-    for (double l : lengths) {
-        const double t = free_at.top() + l;
-        free_at.pop();
-        free_at.push(t);
-        end = std::max(end, t);
+    for (const Tile *t : cut) {
+        uint32_t k = 0;
+        const uint32_t slot = s->slots;
+        while (k < t->stages) {
+            const Load l = least.top();
+            const double room = limit - l.first - c.item;
+            const uint32_t left = t->stages - k;
+            uint32_t n = room <= 0.0 ? 0 : static_cast<uint32_t>(std::min<double>(left, room / stage(*t)));
+            if (n < left && left - n < 4) n = left > 4 ? left - 4 : 0;  // no short rest
+            if (n < left && n < 4) return false;
+            if (n == 0 || (k == 0 && n == left)) return false;
+            least.pop();
+            const double end = l.first + c.item + stage(*t) * n;
+            least.push({end, l.second});
+            s->time = std::max(s->time, end);
+            s->items[l.second].push_back({t->mat, t->i, t->j, k, k + n, s->slots++});
+            k += n;
+        }
+        // a cut tile does not fit the unit with the least to do, so it has parts
+        s->joins.push_back({t->mat, t->i, t->j, 0, s->slots - slot, slot});
     }
-    return end + parts * c.part + joins;
+    return true;
 }
 
-// The cap on a tile's stages (longer ones are split evenly) that the model
-// finds fastest, and its time.
-std::pair<uint32_t, double> best_cap(const std::vector<Tile> &tiles, const Costs &c) {
-    uint32_t longest = 1;
-    for (const Tile &t : tiles) longest = std::max(longest, t.stages);
-    std::pair<uint32_t, double> best{longest, makespan(tiles, longest, c)};
-    for (uint32_t n = 2; n <= 32 && longest / n >= 4; ++n) {
-        const uint32_t cap = static_cast<uint32_t>(ceil_div(longest, n));
-        const double t = makespan(tiles, cap, c);
-        if (t < best.second) best = {cap, t};
-    }
-    return best;
-}
-
-// The items of a list, longest first.  Workgroup b runs on XCD b % 8: in each
-// round of 256 items an XCD takes 32 that are next to each other, so that its
-// L2 holds the rows they share.
-void plan_list(const std::vector<Tile> &tiles, uint32_t cap, std::vector<Item> *items, std::vector<Item> *joins,
-               uint32_t *slots) {
-    std::vector<Item> all;
-    uint32_t slot = 0;
+// The fastest schedule in the model: limits from an even share of the work up.
+Schedule schedule(std::vector<Tile> tiles, const Costs &c) {
+    auto length = [&](const Tile &t) { return std::max(0.4f, t.weight) * static_cast<float>(t.stages); };
+    std::stable_sort(tiles.begin(), tiles.end(), [&](const Tile &a, const Tile &b) { return length(a) > length(b); });
+    double share = 0.0, longest = 0.0;
     for (const Tile &t : tiles) {
-        const uint32_t n = static_cast<uint32_t>(ceil_div(t.stages, cap));
-        if (n > 1) joins->push_back({t.mat, t.i, t.j, 0, n, slot});
-        for (uint32_t q = 0; q < n; ++q) {
-            const uint32_t k0 = static_cast<uint32_t>(static_cast<uint64_t>(t.stages) * q / n);
-            const uint32_t k1 = static_cast<uint32_t>(static_cast<uint64_t>(t.stages) * (q + 1) / n);
-            all.push_back({t.mat, t.i, t.j, k0, k1, n > 1 ? slot++ : kNoSlot});
+        share += (c.item + c.stage * length(t)) / kUnits;
+        longest = std::max(longest, c.item + c.stage * length(t));
+    }
+    Schedule best;
+    best.time = -1.0;
+    const double top = 2.0 * share + longest;  // no tile is cut there
+    for (double limit = share;; limit = std::min(top, limit * 1.05 + 0.5)) {
+        Schedule s;
+        if (fill_units(tiles, c, limit, &s)) {
+            s.time += s.slots * c.part + (s.joins.empty() ? 0.0 : c.join);
+            if (best.time < 0.0 || s.time < best.time) best = std::move(s);
         }
+        if (limit >= top) return best;
     }
-    std::stable_sort(all.begin(), all.end(), [](const Item &a, const Item &b) { return a.k1 - a.k0 > b.k1 - b.k0; });
-    items->resize(all.size());
-    constexpr size_t kXcds = 8;
-    for (size_t base = 0; base < all.size(); base += kUnits) {
-        const size_t n = std::min<size_t>(kUnits, all.size() - base);
-        size_t from = base;
-        for (size_t x = 0; x < kXcds; ++x)
-            for (size_t t = x; t < n; t += kXcds) (*items)[base + t] = all[from++];
-    }
-    *slots = std::max(*slots, slot);
 }
 
 // The tiles of a product, neighbours in a block of 4 rows next to each other.
@@ -896,28 +930,37 @@ void fill_plan(gc_matrix_plan *p, const gc_plan *plan, const uint32_t *rows) {
             for (uint32_t j = 0; j < M.np / kSplitTile; ++j) p->list[kTiles].push_back({id, i, j, 0, 0, 0});
         p->mat.push_back(M);
     }
-    // the tile shape and splits that the model finds fastest for one step
-    const Costs costs[2] = {{0.55, 5.0, 0.025, 6.0}, {1.85, 12.0, 0.1, 6.0}};  // us: Small, Large
-    double best = 0.0;
-    uint32_t caps[3] = {};
+    // the tile shape and the schedules that the model finds fastest for one step
+    const Costs costs[2] = {{0.85, 8.0, 0.03, 8.0}, {2.25, 16.0, 0.12, 10.0}};  // us: Small, Large
     constexpr List kProducts[3] = {kGram, kSquare, kApply};
+    Schedule best[3];
     for (int large = 0; large < 2; ++large) {
-        double time = 0.0;
-        uint32_t cap[3];
+        Schedule s[3];
+        double time = 0.0, before = 0.0;
         for (int q = 0; q < 3; ++q) {
-            const auto b = best_cap(tiles_of(p->mat, large ? Large::kTile : Small::kTile, kProducts[q]), costs[large]);
-            cap[q] = b.first;
-            time += b.second;
+            s[q] = schedule(tiles_of(p->mat, large ? Large::kTile : Small::kTile, kProducts[q]), costs[large]);
+            time += s[q].time;
+            before += best[q].time;
         }
-        if (large == 0 || time < best) {
-            best = time;
+        if (large == 0 || time < before) {
             p->large = large;
-            std::copy(cap, cap + 3, caps);
+            for (int q = 0; q < 3; ++q) best[q] = std::move(s[q]);
         }
     }
-    for (int q = 0; q < 3; ++q)
-        plan_list(tiles_of(p->mat, p->large ? Large::kTile : Small::kTile, kProducts[q]), caps[q], &p->list[kProducts[q]],
-                  &p->list[kProducts[q] + 1], &p->slots);
+    for (int q = 0; q < 3; ++q) {
+        // workgroup b runs on XCD b % 8; units next to each other, with tiles next to
+        // each other, share an XCD and its L2
+        std::vector<Item> &items = p->list[kProducts[q]];
+        std::vector<uint32_t> &first = p->first[kProducts[q]];
+        for (uint32_t b = 0; b < kUnits; ++b) {
+            const std::vector<Item> &of = best[q].items[b % 8 * (kUnits / 8) + b / 8];
+            first.push_back(static_cast<uint32_t>(items.size()));
+            items.insert(items.end(), of.begin(), of.end());
+        }
+        first.push_back(static_cast<uint32_t>(items.size()));
+        p->list[kProducts[q] + 1] = std::move(best[q].joins);
+        p->slots = std::max(p->slots, best[q].slots);
+    }
     p->xhalves = x;
     p->ahalves = a;
 }
