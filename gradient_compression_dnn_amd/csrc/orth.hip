@@ -102,6 +102,7 @@ struct gc_matrix_plan {
     uint64_t xhalves = 0, ahalves = 0;  // halves of one X (or T) array and of one A (or B) array
     uint32_t slots = 0;                 // parts of split tiles held at once
     bool large = false;                 // tiles of 256 x 256
+    bool pairs = false;                 // two steps at a time
     std::vector<gc::MatDev> mat;
     std::vector<gc::Item> list[gc::kLists];
     std::vector<uint32_t> first[gc::kLists];  // products only
@@ -185,6 +186,8 @@ gc_status orth_device(const gc_matrix_plan *cplan, OrthDev *out) {
 // a I + b A + c A^2.
 struct Scales {
     int ex, ea, eb;
+    int es, eq;  // of a pair of steps from this one on: S = B A, and Q
+    bool pair;   // whether a pair may begin here
 };
 
 // The largest exponent that keeps |v| <= bound below 60000 in fp16.
@@ -200,7 +203,7 @@ int exponent_for(double bound) { return static_cast<int>(std::floor(std::log2(60
 // 5.2e-6 where fp32 gives 2.7e-7).  So false, a refusal, if X's bound passes 8
 // before the last step, B's 2^14, the result's 1e12, or one vanishes.
 bool orth_scales(const gc_orth_options &o, Scales *s) {
-    double top = 1.0 + 1.0 / 64;
+    double top = 1.0 + 1.0 / 64, before = 0.0;
     for (int k = 0; k <= o.steps; ++k) {
         s[k].ex = exponent_for(top);
         if (k == o.steps) break;
@@ -217,6 +220,14 @@ bool orth_scales(const gc_orth_options &o, Scales *s) {
         px += half * (std::fabs(a) + 3 * std::fabs(b) * t2 + 5 * std::fabs(c) * t2 * t2);
         s[k].ea = exponent_for(t2 * (1.0 + 1.0 / 64));
         s[k].eb = exponent_for(std::max(pb, 1e-12) * (1.0 + 1.0 / 64));
+        // S = B A has values s |p(s)|, Q = B' B at most the product of the two bounds
+        s[k].es = exponent_for(top * px * (1.0 + 1.0 / 64));
+        s[k].pair = false;
+        if (k > 0) {
+            s[k - 1].eq = exponent_for(before * pb * (1.0 + 1.0 / 32));
+            s[k - 1].pair = before * pb <= 16384.0;
+        }
+        before = pb;
         top = px * (1.0 + 1.0 / 64);
         if (!(top <= (k + 1 == o.steps ? 1e12 : 8.0)) || !(pb <= 16384.0) || !(top > 1e-12)) return false;
     }
@@ -235,7 +246,7 @@ struct Small {
 
 // --------------------------------------------------------------- workspace
 struct OrthWs {
-    _Float16 *X[2], *T[2], *A, *B;
+    _Float16 *X[2], *T[2], *A, *B, *S;
     double *sums, *inv;
     float *partial;
     size_t bytes;
@@ -250,6 +261,7 @@ OrthWs orth_ws(void *ws, const gc_matrix_plan *p) {
     }
     w.A = c.take<_Float16>(p->ahalves);
     w.B = c.take<_Float16>(p->ahalves);
+    w.S = c.take<_Float16>(p->pairs ? p->ahalves : 0);
     w.sums = c.take<double>(p->list[kChunks].size());
     w.inv = c.take<double>(p->mat.size());
     const uint64_t tile = p->large ? Large::kTile : Small::kTile;
@@ -409,10 +421,8 @@ struct Shape : T {
     static constexpr int kRA = kWaveRows / 16, kRB = kWaveCols / 16;  // matrix-core tiles of a wave
     static constexpr int kStageBytes = 2 * T::kTile * 128;            // rows of P, then of Q
     static constexpr int kLoads = kStageBytes / kThreads / 16;        // 1 KB loads per wave and stage
-    // epilogue: 64 columns of 64 rows of a wave, fp32, columns padded
-    static constexpr int kOutLd = 68;
-    static constexpr int kOutBytes = kWaves * 64 * kOutLd * 4;
-    static constexpr int kLds = kStageBytes * T::kStages > kOutBytes ? kStageBytes * T::kStages : kOutBytes;
+    static constexpr int kLds = kStageBytes * T::kStages;
+    static_assert(kWaves * 64 * 64 * 4 <= kLds, "a block of results per wave");
     static_assert(kWaveCols == 64 && kWaveRows % 64 == 0, "the epilogue's blocks");
 };
 
@@ -520,77 +530,124 @@ __device__ __forceinline__ void put_out(const GemmArgs &g, uint64_t at, uint32_t
         }
 }
 
-// A block of 64 x 64 results, which `out` holds as [column][row]: scaled,
-// addend and diagonal added, and written out, by one wave or a team of kTeam.
-template <Kind kKind, class C, int kTeam>
-__device__ __forceinline__ void write_block(const GemmArgs &g, const MatDev &M, float *out, uint32_t i0, uint32_t j0, bool mirror) {
-    const uint32_t w = kTeam > 1 ? wave_id() : 0;
-    const uint32_t hi4 = (lane_id() & 15) * 4, lo = lane_id() >> 4;
-    // along i: row j of T, or of the symmetric result
-    const double sc = kKind == kOut && g.W ? shape_scale(g.shape, M.R, M.C) : 1.0;
-    const float step = static_cast<float>(static_cast<double>(g.lr) * sc);
-#pragma unroll 2
-    for (uint32_t t = w; t < 16; t += kTeam) {
-        const uint32_t jj = t * 4 + lo, i = i0 + hi4, j = j0 + jj;
-        float4 v = *reinterpret_cast<const float4 *>(out + jj * C::kOutLd + hi4);
-        float x[4] = {v.x * g.acc, v.y * g.acc, v.z * g.acc, v.w * g.acc};
-        if (kKind == kSym && g.D) {
-            const _Float16 *p = g.D + M.a + static_cast<uint64_t>(j) * M.mp * 2 + split_at(i);
-            const h4 dh = *reinterpret_cast<const h4 *>(p), dl = *reinterpret_cast<const h4 *>(p + 32);
+// A block of 64 x 64 results in LDS, [column][row], a word each: fp32 (kOut),
+// or hi and lo in its halves.  The 16 parts of 4 rows of a column are permuted
+// so that a matrix-core tile's lanes (a column's 4 rows), lanes along a column
+// and lanes along a row all meet different banks.
+constexpr uint32_t kBlockWords = 64 * 64;
+__device__ __forceinline__ uint32_t block_at(uint32_t col, uint32_t part) {
+    return col * 64 + ((part ^ (col >> 2) ^ ((col & 3) << 2)) << 2);
+}
+
+// A lane's four sums of the block's matrix-core tile (a, b): rows 16 a + 4 q,
+// q = lane / 16, of column 16 b + lane % 16.
+__device__ __forceinline__ void put_tile(uint32_t *block, uint32_t a, uint32_t b, f32x4 v) {
+    *reinterpret_cast<f32x4 *>(block + block_at(16 * b + (lane_id() & 15), 4 * a + (lane_id() >> 4))) = v;
+}
+
+// The sums of the block at (i0, j0) scaled, addend and diagonal added, and
+// split.  (A short loop over LDS: done in registers for each matrix-core tile
+// it was 12 KB of code, which small products waited for.)
+template <Kind kKind, int kTeam>
+__device__ __forceinline__ void split_block(const GemmArgs &g, const MatDev &M, uint32_t *block, uint32_t i0, uint32_t j0) {
+    const uint32_t k = lane_id() & 15, r = lane_id() >> 4, i = i0 + 4 * k;
+#pragma unroll 4
+    for (uint32_t t = kTeam > 1 ? wave_id() : 0; t < 16; t += kTeam) {
+        const uint32_t j = j0 + 4 * t + r;
+        uint32_t *at = block + block_at(4 * t + r, k);
+        const f32x4 v = *reinterpret_cast<const f32x4 *>(at);
+        float x[4] = {v[0] * g.acc, v[1] * g.acc, v[2] * g.acc, v[3] * g.acc};
+        if (kKind == kSym) {
+            if (g.D) {
+                const _Float16 *p = g.D + M.a + static_cast<uint64_t>(j) * M.mp * 2 + split_at(i);
+                const h4 dh = *reinterpret_cast<const h4 *>(p), dl = *reinterpret_cast<const h4 *>(p + 32);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) x[u] = x[u] + g.add * (static_cast<float>(dh[u]) + static_cast<float>(dl[u]));
+                for (int u = 0; u < 4; ++u) x[u] = x[u] + g.add * (static_cast<float>(dh[u]) + static_cast<float>(dl[u]));
+            }
+            const uint32_t on = j - i;  // the diagonal's place among the four, if < 4
+#pragma unroll
+            for (uint32_t u = 0; u < 4; ++u)
+                if (on == u && j < M.m) x[u] = x[u] + g.diag;
         }
-        if (kKind == kSym)
+        uint32_t y[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (i + u == j && i + u < M.m) x[u] = x[u] + g.diag;
-        if (kKind == kOut) {
+        for (int u = 0; u < 4; ++u) {
+            _Float16 h, l;
+            split(x[u], h, l);
+            y[u] = __builtin_bit_cast(uint16_t, h) | (static_cast<uint32_t>(__builtin_bit_cast(uint16_t, l)) << 16);
+        }
+        *reinterpret_cast<uint4 *>(at) = make_uint4(y[0], y[1], y[2], y[3]);
+    }
+}
+
+// Eight split values, consecutive in a split row, to p (hi) and p + 32 (lo).
+__device__ __forceinline__ void put_split(_Float16 *p, const uint32_t (&v)[8]) {
+    uint4 hi, lo;
+    hi.x = __builtin_amdgcn_perm(v[1], v[0], 0x05040100u);
+    hi.y = __builtin_amdgcn_perm(v[3], v[2], 0x05040100u);
+    hi.z = __builtin_amdgcn_perm(v[5], v[4], 0x05040100u);
+    hi.w = __builtin_amdgcn_perm(v[7], v[6], 0x05040100u);
+    lo.x = __builtin_amdgcn_perm(v[1], v[0], 0x07060302u);
+    lo.y = __builtin_amdgcn_perm(v[3], v[2], 0x07060302u);
+    lo.z = __builtin_amdgcn_perm(v[5], v[4], 0x07060302u);
+    lo.w = __builtin_amdgcn_perm(v[7], v[6], 0x07060302u);
+    *reinterpret_cast<uint4 *>(p) = hi;
+    *reinterpret_cast<uint4 *>(p + 32) = lo;
+}
+
+// Writes a block of sums out, by one wave or a team of kTeam: along its columns
+// (T, or the symmetric result) and along its rows (X, or the mirror image).
+template <Kind kKind, int kTeam>
+__device__ __forceinline__ void write_block(const GemmArgs &g, const MatDev &M, uint32_t *block, uint32_t i0, uint32_t j0,
+                                            bool mirror) {
+    const uint32_t w = kTeam > 1 ? wave_id() : 0, lane = lane_id();
+    if (kKind == kOut) {
+        const double sc = g.W ? shape_scale(g.shape, M.R, M.C) : 1.0;
+        const float step = static_cast<float>(static_cast<double>(g.lr) * sc);
+        const uint32_t k = lane & 15, r = lane >> 4;
+        // 16 lanes by 4 elements of a row of the flat buffer
+#pragma unroll 4
+        for (uint32_t t = w; t < 16; t += kTeam) {
+            float x[4];
             if (M.flip) {
+                const uint32_t jj = 4 * t + r, i = i0 + 4 * k, j = j0 + jj;
+                const uint4 v = *reinterpret_cast<const uint4 *>(block + block_at(jj, k));
+                x[0] = dev_u2f(v.x) * g.acc;
+                x[1] = dev_u2f(v.y) * g.acc;
+                x[2] = dev_u2f(v.z) * g.acc;
+                x[3] = dev_u2f(v.w) * g.acc;
                 put_out(g, M.off + static_cast<uint64_t>(j) * M.C + i, j < M.n && i < M.m ? min(M.m - i, 4u) : 0, step, x);
             } else {
-                *reinterpret_cast<float4 *>(out + jj * C::kOutLd + hi4) = make_float4(x[0], x[1], x[2], x[3]);
+                const uint32_t i = i0 + 4 * t + r, j = j0 + 4 * k;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) x[u] = dev_u2f(block[block_at(4 * k + u, t) + r]) * g.acc;
+                put_out(g, M.off + static_cast<uint64_t>(i) * M.C + j, i < M.m && j < M.n ? min(M.n - j, 4u) : 0, step, x);
             }
-            continue;
         }
-        h4 h, l;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            _Float16 a, b;
-            split(x[u], a, b);
-            h[u] = a;
-            l[u] = b;
-        }
-        _Float16 *p = (kKind == kSym ? g.S + M.a : g.Tn + M.x) + static_cast<uint64_t>(j) * M.mp * 2 + split_at(i);
-        *reinterpret_cast<h4 *>(p) = h;
-        *reinterpret_cast<h4 *>(p + 32) = l;
-        if (kKind == kNext || mirror) *reinterpret_cast<float4 *>(out + jj * C::kOutLd + hi4) = make_float4(x[0], x[1], x[2], x[3]);
+        return;
     }
-    // along j: row i of X, or of the mirror image
-    if (kKind == kSym && !mirror) return;
-    if (kKind == kOut && M.flip) return;
+    split_block<kKind, kTeam>(g, M, block, i0, j0);
     if (kTeam > 1) __syncthreads();
+    // 8 lanes by 8 values of a split row
+    const uint32_t k = lane & 7, r = lane >> 3;
+    _Float16 *to = (kKind == kSym ? g.S + M.a : g.Tn + M.x) + static_cast<uint64_t>(j0 + r) * M.mp * 2 + split_at(i0 + 8 * k);
 #pragma unroll 2
-    for (uint32_t t = w; t < 16; t += kTeam) {
-        const uint32_t ii = t * 4 + lo, i = i0 + ii, j = j0 + hi4;
-        float x[4];
+    for (uint32_t t = w; t < 8; t += kTeam) {
+        const uint32_t jj = 8 * t + r;
+        const uint4 a = *reinterpret_cast<const uint4 *>(block + block_at(jj, 2 * k));
+        const uint4 b = *reinterpret_cast<const uint4 *>(block + block_at(jj, 2 * k + 1));
+        put_split(to + static_cast<uint64_t>(8 * t) * M.mp * 2, {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w});
+    }
+    if (kKind == kSym && !mirror) return;
+    const uint32_t ld = kKind == kSym ? M.mp : M.np;
+    to = (kKind == kSym ? g.S + M.a : g.Xn + M.x) + static_cast<uint64_t>(i0 + r) * ld * 2 + split_at(j0 + 8 * k);
+#pragma unroll 2
+    for (uint32_t t = w; t < 8; t += kTeam) {
+        const uint32_t ii = 8 * t + r;
+        uint32_t v[8];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) x[u] = out[(hi4 + u) * C::kOutLd + ii];
-        if (kKind == kOut) {
-            put_out(g, M.off + static_cast<uint64_t>(i) * M.C + j, i < M.m && j < M.n ? min(M.n - j, 4u) : 0, step, x);
-            continue;
-        }
-        h4 h, l;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            _Float16 a, b;
-            split(x[u], a, b);
-            h[u] = a;
-            l[u] = b;
-        }
-        _Float16 *p = kKind == kSym ? g.S + M.a + static_cast<uint64_t>(i) * M.mp * 2 + split_at(j)
-                                    : g.Xn + M.x + static_cast<uint64_t>(i) * M.np * 2 + split_at(j);
-        *reinterpret_cast<h4 *>(p) = h;
-        *reinterpret_cast<h4 *>(p + 32) = l;
+        for (int u = 0; u < 8; ++u) v[u] = block[block_at(8 * k + u, ii >> 2) + (ii & 3)];
+        put_split(to + static_cast<uint64_t>(8 * t) * ld * 2, v);
     }
 }
 
@@ -654,16 +711,15 @@ __global__ __launch_bounds__(C::kThreads) void orth_gemm_kernel(GemmArgs g) {
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         if (!active) continue;
-        float *out = reinterpret_cast<float *>(lds) + w * (64 * C::kOutLd);
-        const uint32_t col = lane & 15, four = (lane >> 4) * 4;
+        uint32_t *block = reinterpret_cast<uint32_t *>(lds) + w * kBlockWords;
 #pragma unroll
         for (int h = 0; h < C::kRA / 4; ++h) {
 #pragma unroll
             for (int a = 0; a < 4; ++a)
 #pragma unroll
                 for (int b = 0; b < C::kRB; ++b)
-                    *reinterpret_cast<f32x4 *>(out + (16 * b + col) * C::kOutLd + 16 * a + four) = acc[4 * h + a][b];
-            write_block<kKind, C, 1>(g, M, out, i0 + pr + 64 * h, j0 + qr, it.i != it.j);
+                    put_tile(block, a, b, acc[4 * h + a][b]);
+            write_block<kKind, 1>(g, M, block, i0 + pr + 64 * h, j0 + qr, it.i != it.j);
         }
     }
 }
@@ -672,19 +728,18 @@ __global__ __launch_bounds__(C::kThreads) void orth_gemm_kernel(GemmArgs g) {
 // 4 waves.
 template <Kind kKind, class C>
 __global__ __launch_bounds__(kBlock) void orth_join_kernel(GemmArgs g) {
-    __shared__ __attribute__((aligned(16))) float out[64 * C::kOutLd];
+    __shared__ __attribute__((aligned(16))) uint32_t block[kBlockWords];
     constexpr uint32_t kBlocks = C::kWaves * (C::kRA / 4);
     const Item it = g.items[blockIdx.x / kBlocks];
     const MatDev M = g.mats[it.mat];
-    const uint32_t part = blockIdx.x % kBlocks, w = part / (C::kRA / 4), h = part % (C::kRA / 4), lane = lane_id();
+    const uint32_t part = blockIdx.x % kBlocks, w = part / (C::kRA / 4), h = part % (C::kRA / 4);
     const uint32_t wr = w / C::kWC, wc = (w + wr * (C::kWC / 2)) % C::kWC;
     const uint32_t i0 = it.i * C::kTile + wr * C::kWaveRows + 64 * h, j0 = it.j * C::kTile + wc * C::kWaveCols;
     if (i0 >= M.mp || j0 >= (kKind == kSym ? M.mp : M.np)) return;
-    const uint32_t col = lane & 15, four = (lane >> 4) * 4;
     // tiles 4 a + b of the block: a is this wave's
     const uint32_t a = wave_id();
     const f32x4 *p = reinterpret_cast<const f32x4 *>(g.partial + static_cast<uint64_t>(it.slot) * C::kTile * C::kTile) +
-                     w * (C::kRA * C::kRB * kWave) + (4 * h + a) * C::kRB * kWave + lane;
+                     w * (C::kRA * C::kRB * kWave) + (4 * h + a) * C::kRB * kWave + lane_id();
     constexpr uint64_t kStep = static_cast<uint64_t>(C::kTile) * C::kTile / 4;
     f32x4 v[C::kRB];
 #pragma unroll
@@ -694,9 +749,9 @@ __global__ __launch_bounds__(kBlock) void orth_join_kernel(GemmArgs g) {
 #pragma unroll
         for (int b = 0; b < C::kRB; ++b) v[b] = v[b] + p[s * kStep + b * kWave];
 #pragma unroll
-    for (int b = 0; b < C::kRB; ++b) *reinterpret_cast<f32x4 *>(out + (16 * b + col) * C::kOutLd + 16 * a + four) = v[b];
+    for (int b = 0; b < C::kRB; ++b) put_tile(block, a, b, v[b]);
     __syncthreads();
-    write_block<kKind, C, kWaves>(g, M, out, i0, j0, it.i != it.j);
+    write_block<kKind, kWaves>(g, M, block, i0, j0, it.i != it.j);
 }
 
 // --------------------------------------------------------------- host side
@@ -755,9 +810,31 @@ gc_status orthogonalize(const char *fn, const gc_matrix_plan *p, const gc_orth_o
               orth_split_kernel<<<size(kTiles), kBlock, 0, stream>>>(d.list[kTiles], d.mat, src, w.inv, pow2(1.0, sc[0].ex),
                                                                    w.X[0], w.T[0]));
     int cur = 0;
-    for (int k = 0; k < o.steps; ++k) {
+    // to <- acc P Q^T + add D + diag I, all m x m
+    auto square = [&](const char *name, const _Float16 *P, const _Float16 *Q, _Float16 *to, float acc, const _Float16 *D,
+                      float add, float diag) {
+        GemmArgs g{};
+        g.mats = d.mat;
+        g.partial = w.partial;
+        g.P = P;
+        g.Q = Q;
+        g.D = D;
+        g.S = to;
+        g.acc = acc;
+        g.add = add;
+        g.diag = diag;
+        product<kSym>(name, p, d, kSquare, g, stream);
+    };
+    // B = a I + b A + c A^2 of step k, into `to`
+    auto poly = [&](int k, const _Float16 *A, _Float16 *to) {
         const Scales &s = sc[k];
-        const double a = o.coef[k][0], b = o.coef[k][1], c = o.coef[k][2];
+        square("orth_poly", A, A, to, pow2(o.coef[k][2], s.eb - 2 * s.ea), A, pow2(o.coef[k][1], s.eb - s.ea),
+               pow2(o.coef[k][0], s.eb));
+    };
+    for (int k = 0; k < o.steps;) {
+        // an odd step goes first
+        const bool pair = p->pairs && (o.steps - k) % 2 == 0 && sc[k].pair;
+        const Scales &s = sc[k];
         GemmArgs g{};
         g.mats = d.mat;
         g.partial = w.partial;
@@ -766,18 +843,24 @@ gc_status orthogonalize(const char *fn, const gc_matrix_plan *p, const gc_orth_o
         g.acc = pow2(1.0, s.ea - 2 * s.ex);
         g.S = w.A;
         product<kSym>("orth_gram", p, d, kGram, g, stream);
-        g.P = g.Q = g.D = w.A;
-        g.px = g.qx = 0;
-        g.acc = pow2(c, s.eb - 2 * s.ea);
-        g.add = pow2(b, s.eb - s.ea);
-        g.diag = pow2(a, s.eb);
-        g.S = w.B;
-        product<kSym>("orth_poly", p, d, kSquare, g, stream);
-        const bool last = k + 1 == o.steps;
+        poly(k, w.A, w.B);
         g.P = w.B;
+        int ep = s.eb;
+        if (pair) {
+            // the next A is B A B, the two steps' factor Q = B' B
+            const Scales &t = sc[k + 1];
+            square("orth_pair", w.B, w.A, w.S, pow2(1.0, s.es - s.eb - s.ea), nullptr, 0.0f, 0.0f);
+            square("orth_pair", w.S, w.B, w.A, pow2(1.0, t.ea - s.es - s.eb), nullptr, 0.0f, 0.0f);
+            poly(k + 1, w.A, w.S);
+            square("orth_pair", w.S, w.B, w.A, pow2(1.0, s.eq - t.eb - s.eb), nullptr, 0.0f, 0.0f);
+            g.P = w.A;
+            ep = s.eq;
+        }
+        k += pair ? 2 : 1;
+        const bool last = k == o.steps;
+        g.px = 0;
         g.Q = w.T[cur];
-        g.qx = 1;
-        g.acc = pow2(1.0, (last ? 0 : sc[k + 1].ex) - s.eb - s.ex);
+        g.acc = pow2(1.0, (last ? 0 : sc[k].ex) - ep - s.ex);
         cur ^= 1;
         if (last) {
             g.O = O;
@@ -901,6 +984,15 @@ std::vector<Tile> tiles_of(const std::vector<MatDev> &mats, uint32_t tile, List 
     return out;
 }
 
+// Two steps at a time: with A' = B A B and Q = B' B, both m x m, the second
+// step needs no product with X of its own; 4 more products of m x m instead of
+// one X X^T and one B X, and one poly as before.  Only where every matrix has
+// kPairRows rows: below, the sums are short and the roundings of Q's entries
+// (up to a^2 = 12, which cancel in Q X) stand out against them, 1.8 times the
+// error of fp32 products at 64 x 576 and 128 x 1152, 1.0 at 300 x 2000, 0.7 and
+// 0.8 at 1500 x 6000 and 2400 x 8640 (0.8, 0.7, 0.8, 0.7 and 0.8 one at a time).
+constexpr uint32_t kPairRows = 256;
+
 // The tables of every matrix.
 void fill_plan(gc_matrix_plan *p, const gc_plan *plan, const uint32_t *rows) {
     p->n_total = plan->n_total;    uint64_t x = 0, a = 0;
@@ -933,6 +1025,8 @@ void fill_plan(gc_matrix_plan *p, const gc_plan *plan, const uint32_t *rows) {
     // the tile shape and the schedules that the model finds fastest for one step
     const Costs costs[2] = {{0.85, 8.0, 0.03, 8.0}, {2.25, 16.0, 0.12, 10.0}};  // us: Small, Large
     constexpr List kProducts[3] = {kGram, kSquare, kApply};
+    uint32_t least = 0xFFFFFFFFu;
+    for (const MatDev &M : p->mat) least = std::min(least, M.m);
     Schedule best[3];
     for (int large = 0; large < 2; ++large) {
         Schedule s[3];
@@ -944,6 +1038,7 @@ void fill_plan(gc_matrix_plan *p, const gc_plan *plan, const uint32_t *rows) {
         }
         if (large == 0 || time < before) {
             p->large = large;
+            p->pairs = least >= kPairRows && s[0].time + s[2].time > 3.0 * s[1].time;
             for (int q = 0; q < 3; ++q) best[q] = std::move(s[q]);
         }
     }
