@@ -397,6 +397,10 @@ struct GemmArgs {
     const MatDev *mats;
     const _Float16 *P, *Q;  // operands; P null: of X's shape, else m x m
     uint32_t px, qx;        // whether an operand is an X (or T) array
+    // Start behind the tile's own rows (1) or columns (2) of the common index and end with them: where P
+    // or Q has a I on its diagonal, the sums, and their roundings with them, stay small until its terms
+    // come (error at 2048 x 2048: 1.5e-6, in plain order 2.7e-6, of fp32 products 3.0e-6).
+    uint32_t turn;
     const _Float16 *D;      // kSym: symmetric addend, or null
     float acc, add, diag;   // result = acc * (P Q^T) + add * D + diag * I
     _Float16 *S;            // kSym: result
@@ -486,15 +490,26 @@ __device__ __forceinline__ void do_stage(const char *__restrict__ cur, char *__r
     if (kActive) multiply_stage<C>(cur, pr, qr, acc);
 }
 
-// nk stages.  A wave whose rows or columns lie outside the matrix loads its
+// The stages of an item: r = 0 .. n - 1 are columns 32 k on, k = first + r
+// around the common index of `all` stages.
+struct Stages {
+    uint32_t n, first, all;
+    __device__ __forceinline__ uint64_t at(uint32_t r) const {
+        const uint32_t k = first + r;
+        return static_cast<uint64_t>(k < all ? k : k - all) * 128;
+    }
+};
+
+// All stages of an item.  A wave whose rows or columns lie outside the matrix loads its
 // share and multiplies nothing (a loop of its own: with the branch inside, the
 // sums were copied at every stage).
 template <class C, bool kActive>
 __device__ __forceinline__ void all_stages(char *lds, char *to, const char *from, uint64_t row8, int32_t odd, bool load,
-                                           uint32_t nk, uint32_t pr, uint32_t qr, f32x4 (&acc)[C::kRA][C::kRB]) {
+                                           const Stages &st, uint32_t pr, uint32_t qr, f32x4 (&acc)[C::kRA][C::kRB]) {
+    const uint32_t nk = st.n;
 #pragma unroll
     for (int s = 0; s < C::kStages - 1; ++s)
-        if (load && uint32_t(s) < nk) load_stage<C>(from + s * 128, row8, odd, to + s * C::kStageBytes);
+        if (load && uint32_t(s) < nk) load_stage<C>(from + st.at(s), row8, odd, to + s * C::kStageBytes);
     uint32_t cur = 0, next = C::kStages - 1;
     for (uint32_t k = 0; k < nk; ++k) {
         // stage k has landed (the later ones may be under way), and every
@@ -505,7 +520,7 @@ __device__ __forceinline__ void all_stages(char *lds, char *to, const char *from
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         do_stage<C, kActive>(lds + cur * C::kStageBytes, to + next * C::kStageBytes,
-                             from + static_cast<uint64_t>(k + C::kStages - 1) * 128, row8, odd,
+                             from + st.at(k + C::kStages - 1), row8, odd,
                              load && k + C::kStages - 1 < nk, pr, qr, acc);
         cur = cur + 1 == C::kStages ? 0 : cur + 1;
         next = next + 1 == C::kStages ? 0 : next + 1;
@@ -690,13 +705,14 @@ __global__ __launch_bounds__(C::kThreads) void orth_gemm_kernel(GemmArgs g) {
             const bool load = r < (of_p ? rows_p : rows_q);
             // part of this lane's LDS place in its row, for even groups; odd ones differ by the bit of 4 parts
             const uint32_t part = (lane & 7) ^ (lane >> 4);
-            const char *from = base + static_cast<uint64_t>(lane >> 3) * ld * 4 + part * 16 + static_cast<uint64_t>(it.k0) * 128;
+            const char *from = base + static_cast<uint64_t>(lane >> 3) * ld * 4 + part * 16;
             const int32_t odd = part & 4 ? -64 : 64;
             const uint64_t row8 = static_cast<uint64_t>(ld) * 32;
             char *to = lds + row * 128;
-            const uint32_t nk = it.k1 - it.k0;
-            if (active) all_stages<C, true>(lds, to, from, row8, odd, load, nk, pr, qr, acc);
-            else all_stages<C, false>(lds, to, from, row8, odd, load, nk, pr, qr, acc);
+            const uint32_t all = ((g.px && kKind == kSym ? M.n : M.m) + 31) / 32;
+            const Stages st{it.k1 - it.k0, (it.k0 + (g.turn ? ((g.turn == 1 ? i0 : j0) + C::kTile) / 32 : 0)) % all, all};
+            if (active) all_stages<C, true>(lds, to, from, row8, odd, load, st, pr, qr, acc);
+            else all_stages<C, false>(lds, to, from, row8, odd, load, st, pr, qr, acc);
         }
         if (it.slot != kNoSlot) {
             if (!active) continue;
@@ -812,7 +828,7 @@ gc_status orthogonalize(const char *fn, const gc_matrix_plan *p, const gc_orth_o
     int cur = 0;
     // to <- acc P Q^T + add D + diag I, all m x m
     auto square = [&](const char *name, const _Float16 *P, const _Float16 *Q, _Float16 *to, float acc, const _Float16 *D,
-                      float add, float diag) {
+                      float add, float diag, uint32_t turn) {
         GemmArgs g{};
         g.mats = d.mat;
         g.partial = w.partial;
@@ -823,13 +839,14 @@ gc_status orthogonalize(const char *fn, const gc_matrix_plan *p, const gc_orth_o
         g.acc = acc;
         g.add = add;
         g.diag = diag;
+        g.turn = turn;
         product<kSym>(name, p, d, kSquare, g, stream);
     };
     // B = a I + b A + c A^2 of step k, into `to`
     auto poly = [&](int k, const _Float16 *A, _Float16 *to) {
         const Scales &s = sc[k];
         square("orth_poly", A, A, to, pow2(o.coef[k][2], s.eb - 2 * s.ea), A, pow2(o.coef[k][1], s.eb - s.ea),
-               pow2(o.coef[k][0], s.eb));
+               pow2(o.coef[k][0], s.eb), 0);
     };
     for (int k = 0; k < o.steps;) {
         // an odd step goes first
@@ -849,16 +866,17 @@ gc_status orthogonalize(const char *fn, const gc_matrix_plan *p, const gc_orth_o
         if (pair) {
             // the next A is B A B, the two steps' factor Q = B' B
             const Scales &t = sc[k + 1];
-            square("orth_pair", w.B, w.A, w.S, pow2(1.0, s.es - s.eb - s.ea), nullptr, 0.0f, 0.0f);
-            square("orth_pair", w.S, w.B, w.A, pow2(1.0, t.ea - s.es - s.eb), nullptr, 0.0f, 0.0f);
+            square("orth_pair", w.B, w.A, w.S, pow2(1.0, s.es - s.eb - s.ea), nullptr, 0.0f, 0.0f, 1);
+            square("orth_pair", w.S, w.B, w.A, pow2(1.0, t.ea - s.es - s.eb), nullptr, 0.0f, 0.0f, 2);
             poly(k + 1, w.A, w.S);
-            square("orth_pair", w.S, w.B, w.A, pow2(1.0, s.eq - t.eb - s.eb), nullptr, 0.0f, 0.0f);
+            square("orth_pair", w.S, w.B, w.A, pow2(1.0, s.eq - t.eb - s.eb), nullptr, 0.0f, 0.0f, 1);
             g.P = w.A;
             ep = s.eq;
         }
         k += pair ? 2 : 1;
         const bool last = k == o.steps;
         g.px = 0;
+        g.turn = 1;
         g.Q = w.T[cur];
         g.acc = pow2(1.0, (last ? 0 : sc[k].ex) - ep - s.ex);
         cur ^= 1;
@@ -988,10 +1006,11 @@ std::vector<Tile> tiles_of(const std::vector<MatDev> &mats, uint32_t tile, List 
 // step needs no product with X of its own; 4 more products of m x m instead of
 // one X X^T and one B X, and one poly as before.  Only where every matrix has
 // kPairRows rows: below, the sums are short and the roundings of Q's entries
-// (up to a^2 = 12, which cancel in Q X) stand out against them, 1.8 times the
-// error of fp32 products at 64 x 576 and 128 x 1152, 1.0 at 300 x 2000, 0.7 and
-// 0.8 at 1500 x 6000 and 2400 x 8640 (0.8, 0.7, 0.8, 0.7 and 0.8 one at a time).
-constexpr uint32_t kPairRows = 256;
+// (up to a^2 = 12, which cancel in Q X) stand out against them: at 256 x 1024
+// 1.1 times the error of fp32 products after 5 steps and 2.1 times after 3 (0.8
+// and 1.0 one at a time), at 512 x 4608 0.4 and 1.2 (0.4 and 0.8), at 1500 x 6000
+// 0.5 and 0.9 (0.4 and 0.7).
+constexpr uint32_t kPairRows = 512;
 
 // The tables of every matrix.
 void fill_plan(gc_matrix_plan *p, const gc_plan *plan, const uint32_t *rows) {
