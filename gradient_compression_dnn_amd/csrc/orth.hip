@@ -84,9 +84,8 @@ constexpr int kSplitTile = 64;  // orth_split's tile
 // the joins of its split tiles.
 enum List { kChunks, kTiles, kGram, kGramJoin, kSquare, kSquareJoin, kApply, kApplyJoin, kLists };
 
-// Products are planned for a workgroup on each of 256 compute units; unit u
+// Products are planned for the workgroups that 256 compute units hold; unit u
 // has items [first[u], first[u + 1]) of its list.
-constexpr uint32_t kUnits = 256;
 
 struct OrthDev {
     const MatDev *mat;
@@ -235,13 +234,19 @@ bool orth_scales(const gc_orth_options &o, Scales *s) {
 }
 
 // --------------------------------------------------------------- tile shapes
-// kTile x kTile per workgroup by kWR x kWC waves, kStages stages of 32 columns
-// of both planes in LDS.
+// kTile x kTile per workgroup by kWR x kWC waves, two stages of 32 columns of
+// both planes in LDS; kUnits workgroups at once on 256 compute units.  The
+// large tile reads half as much per product (the LSTM's four matrices: 2.45 ms
+// against 2.62), the small one fits small matrices and writes out while its
+// neighbour multiplies (ResNet-50's: 1.33 ms against 1.40; with four stages and
+// a unit to itself 1.43).
 struct Large {
-    static constexpr int kTile = 256, kWR = 2, kWC = 4, kStages = 2;
+    static constexpr uint32_t kUnits = 256;
+    static constexpr int kTile = 256, kWR = 2, kWC = 4;
 };
 struct Small {
-    static constexpr int kTile = 128, kWR = 2, kWC = 2, kStages = 4;
+    static constexpr uint32_t kUnits = 512;
+    static constexpr int kTile = 128, kWR = 2, kWC = 2;
 };
 
 // --------------------------------------------------------------- workspace
@@ -425,7 +430,7 @@ struct Shape : T {
     static constexpr int kRA = kWaveRows / 16, kRB = kWaveCols / 16;  // matrix-core tiles of a wave
     static constexpr int kStageBytes = 2 * T::kTile * 128;            // rows of P, then of Q
     static constexpr int kLoads = kStageBytes / kThreads / 16;        // 1 KB loads per wave and stage
-    static constexpr int kLds = kStageBytes * T::kStages;
+    static constexpr int kLds = 2 * kStageBytes;
     static_assert(kWaves * 64 * 64 * 4 <= kLds, "a block of results per wave");
     static_assert(kWaveCols == 64 && kWaveRows % 64 == 0, "the epilogue's blocks");
 };
@@ -507,23 +512,14 @@ template <class C, bool kActive>
 __device__ __forceinline__ void all_stages(char *lds, char *to, const char *from, uint64_t row8, int32_t odd, bool load,
                                            const Stages &st, uint32_t pr, uint32_t qr, f32x4 (&acc)[C::kRA][C::kRB]) {
     const uint32_t nk = st.n;
-#pragma unroll
-    for (int s = 0; s < C::kStages - 1; ++s)
-        if (load && uint32_t(s) < nk) load_stage<C>(from + st.at(s), row8, odd, to + s * C::kStageBytes);
-    uint32_t cur = 0, next = C::kStages - 1;
+    if (load) load_stage<C>(from + st.at(0), row8, odd, to);
     for (uint32_t k = 0; k < nk; ++k) {
-        // stage k has landed (the later ones may be under way), and every
-        // wave is done with the stage that is loaded next
-        if (C::kStages > 2 && k + 3 <= nk) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(2 * C::kLoads) : "memory");
-        else if (C::kStages > 2 && k + 2 <= nk) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(C::kLoads) : "memory");
-        else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        // stage k has landed, and every wave is done with the stage that is loaded next
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        do_stage<C, kActive>(lds + cur * C::kStageBytes, to + next * C::kStageBytes,
-                             from + st.at(k + C::kStages - 1), row8, odd,
-                             load && k + C::kStages - 1 < nk, pr, qr, acc);
-        cur = cur + 1 == C::kStages ? 0 : cur + 1;
-        next = next + 1 == C::kStages ? 0 : next + 1;
+        const uint32_t cur = (k & 1) * C::kStageBytes, next = C::kStageBytes - cur;
+        do_stage<C, kActive>(lds + cur, to + next, from + st.at(k + 1), row8, odd, load && k + 1 < nk, pr, qr, acc);
     }
 }
 
@@ -908,12 +904,14 @@ struct Tile {
 // us of a stage of a whole tile, of an item (first loads, writing out), of a
 // part's sums written and read again, on the memory's account, and of a join.
 struct Costs {
+    uint32_t units;
     double stage, item, part, join;
 };
 
-// What the units do, in XCD-major order: units 32 x .. 32 x + 31 are on XCD x.
+// What the units do, in XCD-major order: the first eighth is on XCD 0, ...
 struct Schedule {
-    std::vector<Item> items[kUnits], joins;
+    std::vector<std::vector<Item>> items;
+    std::vector<Item> joins;
     uint32_t slots = 0;
     double time = 0.0;
 };
@@ -925,7 +923,8 @@ bool fill_units(const std::vector<Tile> &tiles, const Costs &c, double limit, Sc
     auto stage = [&](const Tile &t) { return c.stage * std::max(0.4, static_cast<double>(t.weight)); };
     typedef std::pair<double, uint32_t> Load;
     std::priority_queue<Load, std::vector<Load>, std::greater<Load>> least;
-    for (uint32_t u = 0; u < kUnits; ++u) least.push({0.0, u});
+    s->items.resize(c.units);
+    for (uint32_t u = 0; u < c.units; ++u) least.push({0.0, u});
     std::vector<const Tile *> cut;
     for (const Tile &t : tiles) {
         const Load l = least.top();
@@ -969,7 +968,7 @@ Schedule schedule(std::vector<Tile> tiles, const Costs &c) {
     std::stable_sort(tiles.begin(), tiles.end(), [&](const Tile &a, const Tile &b) { return length(a) > length(b); });
     double share = 0.0, longest = 0.0;
     for (const Tile &t : tiles) {
-        share += (c.item + c.stage * length(t)) / kUnits;
+        share += (c.item + c.stage * length(t)) / c.units;
         longest = std::max(longest, c.item + c.stage * length(t));
     }
     Schedule best;
@@ -1042,7 +1041,7 @@ void fill_plan(gc_matrix_plan *p, const gc_plan *plan, const uint32_t *rows) {
         p->mat.push_back(M);
     }
     // the tile shape and the schedules that the model finds fastest for one step
-    const Costs costs[2] = {{0.85, 8.0, 0.03, 8.0}, {2.25, 16.0, 0.12, 10.0}};  // us: Small, Large
+    const Costs costs[2] = {{Small::kUnits, 1.3, 10.0, 0.03, 10.0}, {Large::kUnits, 2.25, 16.0, 0.12, 12.0}};  // us: Small, Large
     constexpr List kProducts[3] = {kGram, kSquare, kApply};
     uint32_t least = 0xFFFFFFFFu;
     for (const MatDev &M : p->mat) least = std::min(least, M.m);
@@ -1066,8 +1065,9 @@ void fill_plan(gc_matrix_plan *p, const gc_plan *plan, const uint32_t *rows) {
         // each other, share an XCD and its L2
         std::vector<Item> &items = p->list[kProducts[q]];
         std::vector<uint32_t> &first = p->first[kProducts[q]];
-        for (uint32_t b = 0; b < kUnits; ++b) {
-            const std::vector<Item> &of = best[q].items[b % 8 * (kUnits / 8) + b / 8];
+        const uint32_t units = static_cast<uint32_t>(best[q].items.size());
+        for (uint32_t b = 0; b < units; ++b) {
+            const std::vector<Item> &of = best[q].items[b % 8 * (units / 8) + b / 8];
             first.push_back(static_cast<uint32_t>(items.size()));
             items.insert(items.end(), of.begin(), of.end());
         }
