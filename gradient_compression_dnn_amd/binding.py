@@ -151,7 +151,8 @@ KERNELS = ("dgc_norm", "dgc_prep", "dgc_prepare", "dgc_sample", "dgc_bound", "dg
            "unpack_write", "decode_index", "decode", "dcd",
            "dcd_decode", "dcd_mix", "ecd_compress", "ecd_update", "slimdp_values", "stream_probe",
            "embed_lookup", "embed_rank", "embed_merge", "embed_heads", "embed_rows", "embed_sum", "embed_join",
-           "embed_small", "embed_empty", "orth_norm", "orth_scale", "orth_split", "orth_gram", "orth_poly", "orth_pair", "orth_apply", "orth_join")
+           "embed_small", "embed_empty", "orth_norm", "orth_scale", "orth_split", "orth_gram", "orth_poly", "orth_pair", "orth_apply", "orth_join",
+           "orth_slab", "orth_small")
 
 
 def gc_timing_enable(kernels) -> None:

@@ -81,8 +81,9 @@ constexpr uint32_t kNoSlot = 0xFFFFFFFFu;
 constexpr int kSplitTile = 64;  // orth_split's tile
 
 // The work lists: D's chunks and tiles, and per kind of product its items and
-// the joins of its split tiles.
-enum List { kChunks, kTiles, kGram, kGramJoin, kSquare, kSquareJoin, kApply, kApplyJoin, kLists };
+// the joins of its split tiles; of matrices of few rows, the slabs and the
+// matrices with their parts.
+enum List { kChunks, kTiles, kGram, kGramJoin, kSquare, kSquareJoin, kApply, kApplyJoin, kSlabs, kSmalls, kLists };
 
 // Products are planned for the workgroups that 256 compute units hold; unit u
 // has items [first[u], first[u + 1]) of its list.
@@ -102,6 +103,7 @@ struct gc_matrix_plan {
     uint32_t slots = 0;                 // parts of split tiles held at once
     bool large = false;                 // tiles of 256 x 256
     bool pairs = false;                 // two steps at a time
+    bool narrow = false;                // every matrix has at most kNarrow rows
     std::vector<gc::MatDev> mat;
     std::vector<gc::Item> list[gc::kLists];
     std::vector<uint32_t> first[gc::kLists];  // products only
@@ -261,7 +263,7 @@ OrthWs orth_ws(void *ws, const gc_matrix_plan *p) {
     WsCursor c(ws);
     OrthWs w{};
     for (int k = 0; k < 2; ++k) {
-        w.X[k] = c.take<_Float16>(p->xhalves);
+        w.X[k] = c.take<_Float16>(p->narrow ? 0 : p->xhalves);
         w.T[k] = c.take<_Float16>(p->xhalves);
     }
     w.A = c.take<_Float16>(p->ahalves);
@@ -327,7 +329,12 @@ __global__ __launch_bounds__(kBlock) void orth_norm_kernel(const Item *__restric
     if (threadIdx.x == 0) sums[M.chunk0 + it.i] = sum;
 }
 
-// Per matrix: 1 / (||D|| + eps); 0 for D = 0, NaN where D is not finite.
+// 1 / (||D|| + eps) from the sum of squares; 0 for D = 0, NaN where D is not finite.
+__device__ __forceinline__ double norm_scale(double sum, float eps) {
+    return sum == 0.0 ? 0.0 : sum - sum == 0.0 ? 1.0 / (sqrt(sum) + static_cast<double>(eps)) : __builtin_nan("");
+}
+
+// Per matrix.
 __global__ __launch_bounds__(kBlock) void orth_scale_kernel(const MatDev *__restrict__ mats,
                                                             const double *__restrict__ sums, float eps,
                                                             double *__restrict__ inv) {
@@ -335,8 +342,7 @@ __global__ __launch_bounds__(kBlock) void orth_scale_kernel(const MatDev *__rest
     double sum = 0.0;
     for (uint32_t c = threadIdx.x; c < M.nchunk; c += kBlock) sum += sums[M.chunk0 + c];
     sum = block_tree_sum(sum);
-    if (threadIdx.x == 0)
-        inv[blockIdx.x] = sum == 0.0 ? 0.0 : sum - sum == 0.0 ? 1.0 / (sqrt(sum) + static_cast<double>(eps)) : __builtin_nan("");
+    if (threadIdx.x == 0) inv[blockIdx.x] = norm_scale(sum, eps);
 }
 
 // A 64 x 64 tile of X_0, split, into X and T; the padding becomes zeros.
@@ -509,7 +515,7 @@ struct Stages {
 // share and multiplies nothing (a loop of its own: with the branch inside, the
 // sums were copied at every stage).
 template <class C, bool kActive>
-__device__ __forceinline__ void all_stages(char *lds, char *to, const char *from, uint64_t row8, int32_t odd, bool load,
+__device__ __forceinline__ void run_stages(char *lds, char *to, const char *from, uint64_t row8, int32_t odd, bool load,
                                            const Stages &st, uint32_t pr, uint32_t qr, f32x4 (&acc)[C::kRA][C::kRB]) {
     const uint32_t nk = st.n;
     if (load) load_stage<C>(from + st.at(0), row8, odd, to);
@@ -521,6 +527,27 @@ __device__ __forceinline__ void all_stages(char *lds, char *to, const char *from
         const uint32_t cur = (k & 1) * C::kStageBytes, next = C::kStageBytes - cur;
         do_stage<C, kActive>(lds + cur, to + next, from + st.at(k + 1), row8, odd, load && k + 1 < nk, pr, qr, acc);
     }
+}
+
+// acc += P Q^T over an item's stages: rows_p rows of P and rows_q of Q (multiples
+// of 64) exist, this wave has rows pr and columns qr on.
+template <class C>
+__device__ __forceinline__ void all_stages(char *lds, const _Float16 *P, uint32_t ldp, uint32_t rows_p, const _Float16 *Q,
+                                           uint32_t ldq, uint32_t rows_q, const Stages &st, bool active, uint32_t pr,
+                                           uint32_t qr, f32x4 (&acc)[C::kRA][C::kRB]) {
+    // this wave's loads: kLoads groups of 8 rows, all of P or all of Q
+    const uint32_t lane = lane_id(), row = __builtin_amdgcn_readfirstlane(wave_id()) * C::kLoads * 8;  // of the stage
+    const bool of_p = row < uint32_t(C::kTile);
+    const uint32_t r = of_p ? row : row - C::kTile, ld = of_p ? ldp : ldq;
+    const bool load = r < (of_p ? rows_p : rows_q);
+    // part of this lane's LDS place in its row, for even groups; odd ones differ by the bit of 4 parts
+    const uint32_t part = (lane & 7) ^ (lane >> 4);
+    const char *from = reinterpret_cast<const char *>((of_p ? P : Q) + static_cast<uint64_t>(r + (lane >> 3)) * ld * 2) + part * 16;
+    const int32_t odd = part & 4 ? -64 : 64;
+    const uint64_t row8 = static_cast<uint64_t>(ld) * 32;
+    char *to = lds + row * 128;
+    if (active) run_stages<C, true>(lds, to, from, row8, odd, load, st, pr, qr, acc);
+    else run_stages<C, false>(lds, to, from, row8, odd, load, st, pr, qr, acc);
 }
 
 // x[0..n) to O, or applied to W, at flat element `at`.
@@ -606,6 +633,36 @@ __device__ __forceinline__ void put_split(_Float16 *p, const uint32_t (&v)[8]) {
     *reinterpret_cast<uint4 *>(p + 32) = lo;
 }
 
+// A block of split values along its columns: row j of the split matrix at `to`
+// with columns i, from (j0, i0) on.  8 lanes by 8 values of a split row.
+template <int kTeam>
+__device__ __forceinline__ void write_columns(_Float16 *to, uint32_t ld, const uint32_t *block, uint32_t i0, uint32_t j0) {
+    const uint32_t k = lane_id() & 7, r = lane_id() >> 3;
+    to += static_cast<uint64_t>(j0 + r) * ld * 2 + split_at(i0 + 8 * k);
+#pragma unroll 2
+    for (uint32_t t = kTeam > 1 ? wave_id() : 0; t < 8; t += kTeam) {
+        const uint32_t jj = 8 * t + r;
+        const uint4 a = *reinterpret_cast<const uint4 *>(block + block_at(jj, 2 * k));
+        const uint4 b = *reinterpret_cast<const uint4 *>(block + block_at(jj, 2 * k + 1));
+        put_split(to + static_cast<uint64_t>(8 * t) * ld * 2, {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w});
+    }
+}
+
+// The same along its rows: row i, columns j.
+template <int kTeam>
+__device__ __forceinline__ void write_rows(_Float16 *to, uint32_t ld, const uint32_t *block, uint32_t i0, uint32_t j0) {
+    const uint32_t k = lane_id() & 7, r = lane_id() >> 3;
+    to += static_cast<uint64_t>(i0 + r) * ld * 2 + split_at(j0 + 8 * k);
+#pragma unroll 2
+    for (uint32_t t = kTeam > 1 ? wave_id() : 0; t < 8; t += kTeam) {
+        const uint32_t ii = 8 * t + r;
+        uint32_t v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = block[block_at(8 * k + u, ii >> 2) + (ii & 3)];
+        put_split(to + static_cast<uint64_t>(8 * t) * ld * 2, v);
+    }
+}
+
 // Writes a block of sums out, by one wave or a team of kTeam: along its columns
 // (T, or the symmetric result) and along its rows (X, or the mirror image).
 template <Kind kKind, int kTeam>
@@ -639,27 +696,15 @@ __device__ __forceinline__ void write_block(const GemmArgs &g, const MatDev &M, 
     }
     split_block<kKind, kTeam>(g, M, block, i0, j0);
     if (kTeam > 1) __syncthreads();
-    // 8 lanes by 8 values of a split row
-    const uint32_t k = lane & 7, r = lane >> 3;
-    _Float16 *to = (kKind == kSym ? g.S + M.a : g.Tn + M.x) + static_cast<uint64_t>(j0 + r) * M.mp * 2 + split_at(i0 + 8 * k);
-#pragma unroll 2
-    for (uint32_t t = w; t < 8; t += kTeam) {
-        const uint32_t jj = 8 * t + r;
-        const uint4 a = *reinterpret_cast<const uint4 *>(block + block_at(jj, 2 * k));
-        const uint4 b = *reinterpret_cast<const uint4 *>(block + block_at(jj, 2 * k + 1));
-        put_split(to + static_cast<uint64_t>(8 * t) * M.mp * 2, {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w});
-    }
+    write_columns<kTeam>(kKind == kSym ? g.S + M.a : g.Tn + M.x, M.mp, block, i0, j0);
     if (kKind == kSym && !mirror) return;
-    const uint32_t ld = kKind == kSym ? M.mp : M.np;
-    to = (kKind == kSym ? g.S + M.a : g.Xn + M.x) + static_cast<uint64_t>(i0 + r) * ld * 2 + split_at(j0 + 8 * k);
-#pragma unroll 2
-    for (uint32_t t = w; t < 8; t += kTeam) {
-        const uint32_t ii = 8 * t + r;
-        uint32_t v[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) v[u] = block[block_at(8 * k + u, ii >> 2) + (ii & 3)];
-        put_split(to + static_cast<uint64_t>(8 * t) * ld * 2, v);
-    }
+    write_rows<kTeam>(kKind == kSym ? g.S + M.a : g.Xn + M.x, kKind == kSym ? M.mp : M.np, block, i0, j0);
+}
+
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 }
 
 // A unit's items, one after the other: stages [it.k0, it.k1) of tile (it.i,
@@ -673,10 +718,7 @@ __global__ __launch_bounds__(C::kThreads) void orth_gemm_kernel(GemmArgs g) {
     for (uint32_t at = g.first[blockIdx.x]; at < end; ++at) {
         const Item it = g.items[at];
         const MatDev M = g.mats[it.mat];
-        // every wave is done with the LDS of the item before
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
+        lds_barrier();  // every wave is done with the LDS of the item before
         const uint32_t i0 = it.i * C::kTile, j0 = it.j * C::kTile;
         // rows of this tile that exist (multiples of 128)
         const uint32_t rows_p = min(uint32_t(C::kTile), M.mp - i0), rows_q = min(uint32_t(C::kTile), (kKind == kSym ? M.mp : M.np) - j0);
@@ -691,24 +733,11 @@ __global__ __launch_bounds__(C::kThreads) void orth_gemm_kernel(GemmArgs g) {
 #pragma unroll
             for (int b = 0; b < C::kRB; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         {
-            // this wave's loads: kLoads groups of 8 rows, all of P or all of Q
-            const uint32_t row = w * C::kLoads * 8;  // of the stage
-            const bool of_p = row < uint32_t(C::kTile);
-            const uint32_t r = of_p ? row : row - C::kTile;
-            const uint32_t ld = (of_p ? g.px : g.qx) ? (kKind == kSym ? M.np : M.mp) : M.mp;
-            const char *base = reinterpret_cast<const char *>(
-                (of_p ? g.P + (g.px ? M.x : M.a) : g.Q + (g.qx ? M.x : M.a)) + static_cast<uint64_t>((of_p ? i0 : j0) + r) * ld * 2);
-            const bool load = r < (of_p ? rows_p : rows_q);
-            // part of this lane's LDS place in its row, for even groups; odd ones differ by the bit of 4 parts
-            const uint32_t part = (lane & 7) ^ (lane >> 4);
-            const char *from = base + static_cast<uint64_t>(lane >> 3) * ld * 4 + part * 16;
-            const int32_t odd = part & 4 ? -64 : 64;
-            const uint64_t row8 = static_cast<uint64_t>(ld) * 32;
-            char *to = lds + row * 128;
+            const uint32_t ldp = g.px ? M.np : M.mp, ldq = g.qx && kKind == kSym ? M.np : M.mp;
             const uint32_t all = ((g.px && kKind == kSym ? M.n : M.m) + 31) / 32;
             const Stages st{it.k1 - it.k0, (it.k0 + (g.turn ? ((g.turn == 1 ? i0 : j0) + C::kTile) / 32 : 0)) % all, all};
-            if (active) all_stages<C, true>(lds, to, from, row8, odd, load, st, pr, qr, acc);
-            else all_stages<C, false>(lds, to, from, row8, odd, load, st, pr, qr, acc);
+            all_stages<C>(lds, g.P + (g.px ? M.x : M.a) + static_cast<uint64_t>(i0) * ldp * 2, ldp, rows_p,
+                          g.Q + (g.qx ? M.x : M.a) + static_cast<uint64_t>(j0) * ldq * 2, ldq, rows_q, st, active, pr, qr, acc);
         }
         if (it.slot != kNoSlot) {
             if (!active) continue;
@@ -719,9 +748,7 @@ __global__ __launch_bounds__(C::kThreads) void orth_gemm_kernel(GemmArgs g) {
                 for (int b = 0; b < C::kRB; ++b) p[(a * C::kRB + b) * kWave] = acc[a][b];
             continue;
         }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
+        lds_barrier();
         if (!active) continue;
         uint32_t *block = reinterpret_cast<uint32_t *>(lds) + w * kBlockWords;
 #pragma unroll
@@ -766,6 +793,228 @@ __global__ __launch_bounds__(kBlock) void orth_join_kernel(GemmArgs g) {
     write_block<kKind, kWaves>(g, M, block, i0, j0, it.i != it.j);
 }
 
+// ----------------------------------------------------- matrices of few rows
+// Where every matrix has at most kNarrow rows, one tile of A and B, a
+// workgroup that has X' for 128 columns has all it needs for their share of
+// the next A as well.  Two launches a step then:
+//   slab   X' = B X for its slabs of 128 columns, T' written (X itself is not
+//          needed), and the sum of X' X'^T over them, left as a part
+//   small  per matrix: the parts added in order, A, and B = a I + b A + c A^2
+// after a first slab launch that makes X_0 from D.  (29 x 1600, 5 steps: 12
+// launches instead of 23.)
+constexpr uint32_t kNarrow = 128;
+enum Slab { kFirst, kMiddle, kLast };
+
+// 128 x 128 split values as four blocks, block wave 2 (i / 64) + (j / 64 ^ i / 64).
+__device__ __forceinline__ const uint32_t *block_of(const uint32_t *words, uint32_t ib, uint32_t jb) {
+    return words + (2 * ib + (jb ^ ib)) * kBlockWords;
+}
+
+// g += Y Y^T for the wave's 64 x 64, Y's first 32 n columns in `words`.
+__device__ __forceinline__ void add_square(const uint32_t *words, uint32_t wr, uint32_t wc, uint32_t n, f32x4 (&g)[4][4]) {
+    for (uint32_t s = 0; s < n; ++s) {
+        auto operand = [&](uint32_t ib, uint32_t t, h8 &hi, h8 &lo) {  // rows 16 t + lane % 16 of row block ib
+            const uint32_t *b = block_of(words, ib, s >> 1);
+            const uint32_t r = 16 * t + (lane_id() & 15), j = 32 * (s & 1) + 8 * (lane_id() >> 4);
+            uint32_t v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] = b[block_at(j + u, r >> 2) + (r & 3)];
+            uint4 h, l;
+            h.x = __builtin_amdgcn_perm(v[1], v[0], 0x05040100u);
+            h.y = __builtin_amdgcn_perm(v[3], v[2], 0x05040100u);
+            h.z = __builtin_amdgcn_perm(v[5], v[4], 0x05040100u);
+            h.w = __builtin_amdgcn_perm(v[7], v[6], 0x05040100u);
+            l.x = __builtin_amdgcn_perm(v[1], v[0], 0x07060302u);
+            l.y = __builtin_amdgcn_perm(v[3], v[2], 0x07060302u);
+            l.z = __builtin_amdgcn_perm(v[5], v[4], 0x07060302u);
+            l.w = __builtin_amdgcn_perm(v[7], v[6], 0x07060302u);
+            hi = __builtin_bit_cast(h8, h);
+            lo = __builtin_bit_cast(h8, l);
+        };
+        h8 qh[4], ql[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) operand(wc, b, qh[b], ql[b]);
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+            h8 ph, pl;
+            operand(wr, a, ph, pl);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) g[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ph, ql[b], g[a][b], 0, 0, 0);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) g[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(pl, qh[b], g[a][b], 0, 0, 0);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) g[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ph, qh[b], g[a][b], 0, 0, 0);
+        }
+    }
+}
+
+struct FirstArgs {
+    Source s;
+    const double *sums;
+    float eps, pow2;
+};
+
+// A word of split value x.
+__device__ __forceinline__ uint32_t split_word(float x) {
+    _Float16 h, l;
+    split(x, h, l);
+    return __builtin_bit_cast(uint16_t, h) | (static_cast<uint32_t>(__builtin_bit_cast(uint16_t, l)) << 16);
+}
+
+// X_0's columns j0 .. j0 + 127 into `words`, zeros outside the matrix.
+__device__ __forceinline__ void first_slab(const MatDev &M, const FirstArgs &f, double scale, uint32_t j0, uint32_t *words) {
+    for (uint32_t e = threadIdx.x; e < kBlockWords; e += kBlock)
+        reinterpret_cast<uint4 *>(words)[e] = make_uint4(0, 0, 0, 0);
+    lds_barrier();
+    const uint32_t cols = min(M.n - j0, kNarrow);
+    auto value = [&](uint64_t at) {
+        const float g = f.s.G[at];
+        const float d = f.s.U ? direction(f.s, f.s.U[at], g) : g;
+        return split_word(static_cast<float>(static_cast<double>(d) * scale));
+    };
+    auto place = [&](uint32_t i, uint32_t j) {
+        return const_cast<uint32_t *>(block_of(words, i >> 6, j >> 6)) + block_at(j & 63, (i & 63) >> 2) + (i & 3);
+    };
+    if (M.flip) {  // D is n x m: the slab is contiguous
+        const uint64_t at = M.off + static_cast<uint64_t>(j0) * M.m;
+#pragma unroll 8
+        for (uint32_t e = threadIdx.x; e < cols * M.m; e += kBlock) *place(e % M.m, e / M.m) = value(at + e);
+    } else {
+        const uint32_t j = threadIdx.x & (kNarrow - 1);
+        if (j < cols)
+#pragma unroll 8
+            for (uint32_t i = threadIdx.x / kNarrow; i < M.m; i += kBlock / kNarrow)
+                *place(i, j) = value(M.off + static_cast<uint64_t>(i) * M.n + j0 + j);
+    }
+    lds_barrier();
+}
+
+// Slabs [it.k0, it.k1) of a matrix.
+template <Slab kSlabKind>
+__global__ __launch_bounds__(kBlock) void orth_slab_kernel(GemmArgs g, FirstArgs f) {
+    using C = Shape<Small>;
+    __shared__ __attribute__((aligned(128))) char lds[C::kLds];
+    uint32_t *words = reinterpret_cast<uint32_t *>(lds);
+    const Item it = g.items[blockIdx.x];
+    const MatDev M = g.mats[it.mat];
+    const uint32_t w = __builtin_amdgcn_readfirstlane(wave_id());
+    const uint32_t wr = w / 2, wc = (w ^ wr) & 1, pr = 64 * wr, qr = 64 * wc;
+    uint32_t *block = words + w * kBlockWords;
+    const bool active = pr < M.m, squares = active && qr < M.m;
+    double scale = 0.0;
+    if (kSlabKind == kFirst) {
+        double sum = 0.0;
+        for (uint32_t c = threadIdx.x; c < M.nchunk; c += kBlock) sum += f.sums[M.chunk0 + c];
+        scale = norm_scale(block_tree_sum(sum), f.eps) * static_cast<double>(f.pow2);
+    }
+    f32x4 sums[4][4];
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) sums[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (uint32_t s = it.k0; s < it.k1; ++s) {
+        const uint32_t j0 = s * kNarrow;
+        lds_barrier();  // the slab before is done with LDS
+        if (kSlabKind == kFirst) {
+            first_slab(M, f, scale, j0, words);
+        } else {
+            f32x4 acc[4][4];
+#pragma unroll
+            for (int a = 0; a < 4; ++a)
+#pragma unroll
+                for (int b = 0; b < 4; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            const uint32_t all = (M.m + 31) / 32;
+            all_stages<C>(lds, g.P + M.a, M.mp, kNarrow, g.Q + M.x + static_cast<uint64_t>(j0) * M.mp * 2, M.mp, kNarrow,
+                          Stages{all, 0, all}, active, pr, qr, acc);
+            lds_barrier();
+            if (active) {
+#pragma unroll
+                for (int a = 0; a < 4; ++a)
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) put_tile(block, a, b, acc[a][b]);
+                if (kSlabKind == kLast) write_block<kOut, 1>(g, M, block, pr, j0 + qr, false);
+                else split_block<kNext, 1>(g, M, block, pr, j0 + qr);
+            }
+            if (kSlabKind == kLast) continue;
+            lds_barrier();
+        }
+        if (active) write_columns<1>(g.Tn + M.x, M.mp, block, pr, j0 + qr);
+        if (squares) add_square(words, wr, wc, 4, sums);
+    }
+    if (kSlabKind == kLast || !squares) return;
+    f32x4 *p = reinterpret_cast<f32x4 *>(g.partial + static_cast<uint64_t>(it.slot) * kNarrow * kNarrow) + w * (16 * kWave) + lane_id();
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) p[(a * 4 + b) * kWave] = sums[a][b];
+}
+
+// Per matrix: A = acc * (the it.k1 parts from it.slot on, in order), and
+// B = diag I + add A + square A^2 into g.S.
+__global__ __launch_bounds__(kBlock) void orth_small_kernel(GemmArgs g, float square) {
+    __shared__ __attribute__((aligned(128))) uint32_t words[4 * kBlockWords];
+    const Item it = g.items[blockIdx.x];
+    const MatDev M = g.mats[it.mat];
+    const uint32_t w = __builtin_amdgcn_readfirstlane(wave_id());
+    const uint32_t wr = w / 2, wc = (w ^ wr) & 1;
+    const bool active = 64 * wr < M.m && 64 * wc < M.m;
+    constexpr uint32_t kStep = kNarrow * kNarrow / 4;
+    // every wave adds a quarter of each block that exists
+    for (uint32_t q = 0; q < 4; ++q) {
+        if (64 * (q / 2) >= M.m || 64 * ((q ^ (q / 2)) & 1) >= M.m) continue;
+        const f32x4 *p = reinterpret_cast<const f32x4 *>(g.partial + static_cast<uint64_t>(it.slot) * kNarrow * kNarrow) +
+                         q * (16 * kWave) + w * (4 * kWave) + lane_id();
+        f32x4 v[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) v[b] = p[b * kWave];
+#pragma unroll 4
+        for (uint32_t s = 1; s < it.k1; ++s)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) v[b] = v[b] + p[s * kStep + b * kWave];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) put_tile(words + q * kBlockWords, w, b, v[b] * g.acc);
+    }
+    lds_barrier();
+    uint32_t *block = words + w * kBlockWords;
+    auto place = [&](int a, int b) { return block + block_at(16 * b + (lane_id() & 15), 4 * a + (lane_id() >> 4)); };
+    f32x4 A[4][4];
+    if (active) {
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                uint32_t *at = place(a, b);
+                A[a][b] = *reinterpret_cast<const f32x4 *>(at);
+                *reinterpret_cast<uint4 *>(at) = make_uint4(split_word(A[a][b][0]), split_word(A[a][b][1]),
+                                                            split_word(A[a][b][2]), split_word(A[a][b][3]));
+            }
+    }
+    lds_barrier();
+    f32x4 A2[4][4];
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) A2[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (active) add_square(words, wr, wc, (M.m + 31) / 32, A2);
+    lds_barrier();  // every wave has read A
+    if (!active) return;
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const uint32_t i = 64 * wr + 16 * a + 4 * (lane_id() >> 4), j = 64 * wc + 16 * b + (lane_id() & 15);
+            uint32_t y[4];
+#pragma unroll
+            for (uint32_t u = 0; u < 4; ++u) {
+                float x = A2[a][b][u] * square + g.add * A[a][b][u];
+                if (i + u == j && j < M.m) x = x + g.diag;
+                y[u] = split_word(x);
+            }
+            *reinterpret_cast<uint4 *>(place(a, b)) = make_uint4(y[0], y[1], y[2], y[3]);
+        }
+    write_columns<1>(g.S + M.a, M.mp, block, 64 * wr, 64 * wc);
+}
+
 // --------------------------------------------------------------- host side
 void *align256(void *p) {
     return reinterpret_cast<void *>((reinterpret_cast<uintptr_t>(p) + 255) & ~uintptr_t(255));
@@ -806,6 +1055,49 @@ void product(const char *name, const gc_matrix_plan *p, const OrthDev &d, List l
     else product_of<kKind, Shape<Small>>(name, p, d, l, g, stream);
 }
 
+// The steps of a plan of matrices of few rows, behind the norm.
+gc_status narrow_steps(const char *fn, const gc_matrix_plan *p, const OrthDev &d, const OrthWs &w, const gc_orth_options &o,
+                       const Scales *sc, Source src, float *O, float *W, float decay, float lr, int shape,
+                       hipStream_t stream) {
+    auto pow2 = [](double c, int e) { return static_cast<float>(std::ldexp(c, e)); };
+    const unsigned slabs = static_cast<unsigned>(p->list[kSlabs].size()), smalls = static_cast<unsigned>(p->list[kSmalls].size());
+    GemmArgs g{};
+    g.mats = d.mat;
+    g.partial = w.partial;
+    g.P = w.B;
+    g.S = w.B;
+    g.O = O;
+    g.W = W;
+    g.decay = decay;
+    g.lr = lr;
+    g.shape = shape;
+    FirstArgs f{src, w.sums, o.eps, pow2(1.0, sc[0].ex)};
+    int cur = 0;
+    g.items = d.list[kSlabs];
+    g.Tn = w.T[0];
+    GC_LAUNCH("orth_slab", stream, orth_slab_kernel<kFirst><<<slabs, kBlock, 0, stream>>>(g, f));
+    for (int k = 0; k < o.steps; ++k) {
+        const Scales &s = sc[k];
+        g.items = d.list[kSmalls];
+        g.acc = pow2(1.0, s.ea - 2 * s.ex);
+        g.add = pow2(o.coef[k][1], s.eb - s.ea);
+        g.diag = pow2(o.coef[k][0], s.eb);
+        GC_LAUNCH("orth_small", stream,
+                  orth_small_kernel<<<smalls, kBlock, 0, stream>>>(g, pow2(o.coef[k][2], s.eb - 2 * s.ea)));
+        const bool last = k + 1 == o.steps;
+        g.items = d.list[kSlabs];
+        g.acc = pow2(1.0, (last ? 0 : sc[k + 1].ex) - s.eb - s.ex);
+        g.Q = w.T[cur];
+        g.Tn = w.T[cur ^ 1];
+        cur ^= 1;
+        if (last) GC_LAUNCH("orth_slab", stream, orth_slab_kernel<kLast><<<slabs, kBlock, 0, stream>>>(g, f));
+        else GC_LAUNCH("orth_slab", stream, orth_slab_kernel<kMiddle><<<slabs, kBlock, 0, stream>>>(g, f));
+    }
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return hip_error(e, fn);
+    return GC_OK;
+}
+
 gc_status orthogonalize(const char *fn, const gc_matrix_plan *p, const gc_orth_options &o, const Scales *sc, Source src,
                         float *O, float *W, float decay, float lr, int shape, void *ws, hipStream_t stream) {
     OrthDev d;
@@ -816,6 +1108,7 @@ gc_status orthogonalize(const char *fn, const gc_matrix_plan *p, const gc_orth_o
     auto pow2 = [](double c, int e) { return static_cast<float>(std::ldexp(c, e)); };
     GC_LAUNCH("orth_norm", stream,
               orth_norm_kernel<<<size(kChunks), kBlock, 0, stream>>>(d.list[kChunks], d.mat, src, w.sums));
+    if (p->narrow) return narrow_steps(fn, p, d, w, o, sc, src, O, W, decay, lr, shape, stream);
     GC_LAUNCH("orth_scale", stream,
               orth_scale_kernel<<<static_cast<unsigned>(p->mat.size()), kBlock, 0, stream>>>(d.mat, w.sums, o.eps, w.inv));
     GC_LAUNCH("orth_split", stream,
@@ -1011,6 +1304,24 @@ std::vector<Tile> tiles_of(const std::vector<MatDev> &mats, uint32_t tile, List 
 // 0.5 and 0.9 (0.4 and 0.7).
 constexpr uint32_t kPairRows = 512;
 
+// Matrices of few rows: slabs per workgroup so that they fill the units once
+// and no matrix has more than kMaxParts parts, which one workgroup adds.
+constexpr uint64_t kMaxParts = 16;
+
+void plan_narrow(gc_matrix_plan *p) {
+    p->narrow = true;
+    uint64_t slabs = 0;
+    for (const MatDev &M : p->mat) slabs += M.np / kNarrow;
+    for (uint32_t id = 0; id < p->mat.size(); ++id) {
+        const uint32_t n = p->mat[id].np / kNarrow;
+        const uint32_t per = static_cast<uint32_t>(std::max(ceil_div(n, kMaxParts), ceil_div(slabs, Small::kUnits)));
+        const uint32_t parts = static_cast<uint32_t>(ceil_div(n, per));
+        p->list[kSmalls].push_back({id, 0, 0, 0, parts, p->slots});
+        for (uint32_t q = 0; q < parts; ++q)
+            p->list[kSlabs].push_back({id, 0, 0, q * per, std::min((q + 1) * per, n), p->slots++});
+    }
+}
+
 // The tables of every matrix.
 void fill_plan(gc_matrix_plan *p, const gc_plan *plan, const uint32_t *rows) {
     p->n_total = plan->n_total;    uint64_t x = 0, a = 0;
@@ -1040,11 +1351,20 @@ void fill_plan(gc_matrix_plan *p, const gc_plan *plan, const uint32_t *rows) {
             for (uint32_t j = 0; j < M.np / kSplitTile; ++j) p->list[kTiles].push_back({id, i, j, 0, 0, 0});
         p->mat.push_back(M);
     }
+    p->xhalves = x;
+    p->ahalves = a;
+    uint32_t least = 0xFFFFFFFFu, most = 0;
+    for (const MatDev &M : p->mat) {
+        least = std::min(least, M.m);
+        most = std::max(most, M.m);
+    }
+    if (most <= kNarrow) {
+        plan_narrow(p);
+        return;
+    }
     // the tile shape and the schedules that the model finds fastest for one step
     const Costs costs[2] = {{Small::kUnits, 1.3, 10.0, 0.03, 10.0}, {Large::kUnits, 2.25, 16.0, 0.12, 12.0}};  // us: Small, Large
     constexpr List kProducts[3] = {kGram, kSquare, kApply};
-    uint32_t least = 0xFFFFFFFFu;
-    for (const MatDev &M : p->mat) least = std::min(least, M.m);
     Schedule best[3];
     for (int large = 0; large < 2; ++large) {
         Schedule s[3];
@@ -1075,8 +1395,6 @@ void fill_plan(gc_matrix_plan *p, const gc_plan *plan, const uint32_t *rows) {
         p->list[kProducts[q] + 1] = std::move(best[q].joins);
         p->slots = std::max(p->slots, best[q].slots);
     }
-    p->xhalves = x;
-    p->ahalves = a;
 }
 
 // Whether two buffers of n floats share an element.

@@ -764,7 +764,7 @@ gc_status gc_muon_step(const gc_matrix_plan *mplan, const float *G, float *U, fl
  *             embed_heads, embed_rows, embed_sum, embed_join, embed_small,
  *             embed_empty,
  *             orth_norm, orth_scale, orth_split, orth_gram, orth_poly,
- *             orth_pair, orth_apply, orth_join.
+ *             orth_pair, orth_apply, orth_join, orth_slab, orth_small.
  * gc_timing_take waits for the recorded events of one kernel and returns the
  * summed duration in milliseconds and the number of launches, then forgets
  * them.  Host-thread safe; not for use while a stream is being captured.
