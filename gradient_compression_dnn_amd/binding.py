@@ -578,9 +578,9 @@ def _batch(plan: Plan, seg: int, rows: int, tokens, t, name: str):
     if not 0 <= seg < plan.nseg or rows < 1 or plan.lengths[seg] % rows:
         raise ValueError("seg must be a segment of the plan and rows divide its length")
     cols = plan.lengths[seg] // rows
-    if not torch.is_tensor(tokens) or not tokens.is_cuda or not tokens.is_contiguous() or tokens.dtype not in _TOKEN_TYPES:
+    if not torch.is_tensor(tokens) or not tokens.is_cuda or tokens.dtype not in _TOKEN_TYPES or not tokens.is_contiguous():
         raise ValueError("tokens: need a contiguous CUDA int32 or int64 tensor")
-    if not torch.is_tensor(t) or t.dtype not in _FLOAT_TYPES or t.shape[:-1] != tokens.shape or t.shape[-1:] != (cols,):
+    if not torch.is_tensor(t) or t.dtype not in _FLOAT_TYPES or t.shape != (*tokens.shape, cols):
         raise ValueError(f"{name}: need an fp32, bf16 or fp16 tensor of shape {(*tokens.shape, cols)}")
     stride = cols if t.is_contiguous() else _row_stride(t, name)
     return ((t.data_ptr(), _FLOAT_TYPES[t.dtype], stride),
@@ -592,26 +592,20 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-class _Device:
-    """The tensors' device, made the current one for a call (the library
-    enqueues on the current device), and its current stream."""
-
-    def __init__(self, *tensors):
-        dev = tensors[0].device
-        for t in tensors:
-            if not t.is_cuda or t.device != dev:
-                raise ValueError("need CUDA tensors on one device")
-        self.index = dev.index
-
-    def __enter__(self):
-        self.before = torch.cuda.current_device()
-        if self.before != self.index:
-            torch.cuda.set_device(self.index)
-        return _raw_stream(self.index)
-
-    def __exit__(self, *exc):
-        if self.before != self.index:
-            torch.cuda.set_device(self.before)
+def _call(fn: str, tensors, *args):
+    """The library's call on the tensors' device, made the current one (the
+    library enqueues there), and on that device's current stream."""
+    index = tensors[0].get_device()
+    for t in tensors:
+        if index < 0 or t.get_device() != index:
+            raise ValueError("need CUDA tensors on one device")
+    if torch.cuda.current_device() == index:
+        status = getattr(load(), fn)(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = getattr(load(), fn)(*args, _raw_stream(index))
+    if status != GC_OK:
+        _check(status)
 
 
 def gc_embed_lookup(plan: Plan, seg: int, rows: int, w, tokens: torch.Tensor, scale: float, y: torch.Tensor):
@@ -619,8 +613,7 @@ def gc_embed_lookup(plan: Plan, seg: int, rows: int, w, tokens: torch.Tensor, sc
     columns appended, in fp32, bf16 or fp16, its rows one stride apart."""
     batch, toks = _batch(plan, seg, rows, tokens, y, "y")
     wp = _f32(w, plan.n_total, "w")
-    with _Device(y, tokens, w) as stream:
-        _check(load().gc_embed_lookup(plan.handle, seg, rows, wp, *toks, scale, *batch, stream))
+    _call("gc_embed_lookup", (y, tokens, w), plan.handle, seg, rows, wp, *toks, scale, *batch)
 
 
 def gc_embed_workspace_bytes(plan: Plan, seg: int, rows: int, n_tokens: int) -> int:
@@ -633,9 +626,8 @@ def gc_embed_grad(plan: Plan, seg: int, rows: int, dy: torch.Tensor, tokens: tor
     segment seg of g; dy as gc_embed_lookup's y."""
     batch, toks = _batch(plan, seg, rows, tokens, dy, "dy")
     gp, space = _f32(g, plan.n_total, "g"), _ws(ws)
-    with _Device(g, dy, tokens, ws) as stream:
-        _check(load().gc_embed_grad(plan.handle, seg, rows, *batch, *toks, scale, gp, int(bool(accumulate)), *space,
-                                    stream))
+    _call("gc_embed_grad", (g, dy, tokens, ws), plan.handle, seg, rows, *batch, *toks, scale, gp,
+          int(bool(accumulate)), *space)
 
 
 def gc_embed_message_cap(plan: Plan, seg: int, rows: int, n_tokens: int) -> int:
@@ -647,8 +639,8 @@ def gc_embed_message(plan: Plan, seg: int, rows: int, dy: torch.Tensor, tokens: 
     """The lookup's gradient as a message of the rows that have tokens."""
     batch, toks = _batch(plan, seg, rows, tokens, dy, "dy")
     msg, space = out.checked(plan, "out"), _ws(ws)
-    with _Device(out.val, out.idx, out.seg_off, dy, tokens, ws) as stream:
-        _check(load().gc_embed_message(plan.handle, seg, rows, *batch, *toks, scale, ctypes.byref(msg), *space, stream))
+    _call("gc_embed_message", (out.val, out.idx, out.seg_off, dy, tokens, ws), plan.handle, seg, rows, *batch, *toks,
+          scale, ctypes.byref(msg), *space)
 
 
 # -------------------------------------------------------- matrix updates
@@ -705,13 +697,11 @@ def gc_orthogonalize(mplan: MatrixPlan, D, O, opt: gc_orth_options, ws: torch.Te
     """Every matrix of D orthogonalised into O (which may be D)."""
     n = mplan.n_total
     args = _f32(D, n, "D"), _f32(O, n, "O"), ctypes.byref(opt), *_ws(ws)
-    with _Device(O, D, ws) as stream:
-        _check(load().gc_orthogonalize(mplan.handle, *args, stream))
+    _call("gc_orthogonalize", (O, D, ws), mplan.handle, *args)
 
 
 def gc_muon_step(mplan: MatrixPlan, G, U, W, opt: gc_muon_options, ws: torch.Tensor):
     """U <- m U + G, W <- (1 - lr wd) W - lr s orthogonalised(D) on every matrix."""
     n = mplan.n_total
     args = _f32(G, n, "G"), _f32(U, n, "U"), _f32(W, n, "W"), ctypes.byref(opt), *_ws(ws)
-    with _Device(W, G, U, ws) as stream:
-        _check(load().gc_muon_step(mplan.handle, *args, stream))
+    _call("gc_muon_step", (W, G, U, ws), mplan.handle, *args)

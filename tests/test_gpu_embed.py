@@ -96,7 +96,8 @@ class Batch:
 
 SIZES = [(1, 1, 1), (1, 1, 70), (7, 3, 1), (10, 4, 33), (50, 5, 64), (100, 255, 65), (100, 256, 31), (300, 257, 1000),
          (33, 1500, 100), (5000, 36, 4095), (5000, 31, 4096), (5000, 8, 4097), (70, 12, 9000),
-         (60, 40, 255), (3000, 7, 256), (60, 513, 256), (60, 40, 257), (4000, 3, 2049)]
+         (60, 40, 255), (3000, 7, 256), (60, 513, 256), (60, 40, 257), (4000, 3, 2049),
+         (900, 5, 6144), (900, 5, 6145)]
 
 
 @pytest.mark.parametrize("rows,cols,n", SIZES)
