@@ -722,8 +722,10 @@ __global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(const uint32_t
 }
 
 // --------------------------------------------------------------- host side
-constexpr uint64_t kMaxTokens = uint64_t(1) << 31;  // positions and blocks are u32
-constexpr uint64_t kMaxGrid = 0x7FFFFFFF;
+constexpr uint64_t kMaxTokens = uint64_t(1) << 28;
+constexpr uint64_t kMaxElems = uint64_t(1) << 35;
+// Workgroups of a launch: a grid has fewer than 2^32 threads.
+constexpr uint64_t max_grid(uint64_t threads) { return 0xFFFFFFFFull / threads; }
 
 struct EmbedWs {
     uint32_t *key[2], *pos[2], *heads_before, *tile_heads;
@@ -777,7 +779,8 @@ gc_status check_batch(const char *fn, const void *tokens, int token_type, uint64
     if (type != GC_F32 && type != GC_BF16 && type != GC_F16)
         return set_error(GC_EINVAL, at + "type must be GC_F32, GC_BF16 or GC_F16");
     if (!(scale - scale == 0.0f)) return set_error(GC_EINVAL, at + "scale must be finite");
-    if (n >= kMaxTokens) return set_error(GC_ERANGE, at + "n_tokens must be < 2^31");
+    if (n >= kMaxTokens) return set_error(GC_ERANGE, at + "n_tokens must be < 2^28");
+    if (n * cols > kMaxElems) return set_error(GC_ERANGE, at + "n_tokens * cols must be <= 2^35");
     if (n == 0) return GC_OK;
     if (!tokens || !x) return set_error(GC_EINVAL, at + "buffers must be non-null");
     if (stride < cols) return set_error(GC_EINVAL, at + "the row stride must be at least the columns");
@@ -812,8 +815,8 @@ gc_status embed_backward(const char *fn, const gc_plan *plan, int seg, uint32_t 
     const uint32_t blocks = static_cast<uint32_t>(ceil_div(n, kSpan));
     const uint32_t slabs = static_cast<uint32_t>(ceil_div(cols, kSlab));
     const uint64_t sums = static_cast<uint64_t>(blocks) * slabs;
-    if (nrank + nfill > kMaxGrid || sums > kMaxGrid)
-        return set_error(GC_ERANGE, std::string(fn) + ": n_tokens * cols is above the supported range");
+    if (nrank + nfill > max_grid(kRankThreads) || sums > max_grid(kBlock))
+        return set_error(GC_ERANGE, std::string(fn) + ": more workgroups than a launch has");
     if (n <= kSmall) {
         const uint32_t nsum = static_cast<uint32_t>(ceil_div(n, kSmallWaves)) * slabs;
         with_type(type, [&](auto t) {
@@ -902,7 +905,7 @@ extern "C" gc_status gc_embed_lookup(const gc_plan *plan, int seg, uint32_t rows
     if (!w) return set_error(GC_EINVAL, "gc_embed_lookup: buffers must be non-null");
     const uint32_t vecs = static_cast<uint32_t>(ceil_div(cols, y_type == GC_F32 ? kLookupCols<F32> : kLookupCols<BF16>));
     const uint64_t grid = ceil_div(n_tokens * vecs, kBlock * kLookupVecs);
-    if (grid > kMaxGrid) return set_error(GC_ERANGE, "gc_embed_lookup: n_tokens * cols is above the supported range");
+    if (grid > max_grid(kBlock)) return set_error(GC_ERANGE, "gc_embed_lookup: more workgroups than a launch has");
     with_type(y_type, [&](auto t) {
         with_tokens(token_type, [&](auto tok) {
             using T = decltype(t);

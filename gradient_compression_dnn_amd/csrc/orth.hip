@@ -195,7 +195,7 @@ struct Scales {
 int exponent_for(double bound) { return static_cast<int>(std::floor(std::log2(60000.0 / bound))); }
 
 // Bounds of the singular values of X, A and B at every step, from the
-// polynomial on [0, top]: sampled at 4096 points, with what it can rise
+// polynomial on [0, top]: sampled at 1024 points, with what it can rise
 // between two of them (a derivative's bound times half a spacing) and 1/64
 // for rounding.  s[k] is step k's, s[steps] the result's.
 // The bounds are worst cases; what a matrix really holds may be smaller by
@@ -209,7 +209,7 @@ bool orth_scales(const gc_orth_options &o, Scales *s) {
         s[k].ex = exponent_for(top);
         if (k == o.steps) break;
         const double a = o.coef[k][0], b = o.coef[k][1], c = o.coef[k][2];
-        constexpr int kPoints = 4096;
+        constexpr int kPoints = 1024;
         double px = 0.0, pb = 0.0;
         for (int i = 0; i <= kPoints; ++i) {
             const double x = top * i / kPoints, q = (b + c * x * x) * x * x;
@@ -1433,6 +1433,12 @@ extern "C" gc_status gc_matrix_plan_create(const gc_plan *plan, const uint32_t *
         delete p;
         return set_error(GC_EINVAL, "gc_matrix_plan_create: out of host memory");
     }
+    // grids of up to 256 threads (joins: 16 workgroups a tile) stay below 2^32
+    for (int l = 0; l < kLists; ++l)
+        if (p->list[l].size() >= (size_t(1) << 20) * (l == kGramJoin || l == kSquareJoin || l == kApplyJoin ? 1 : 16)) {
+            delete p;
+            return set_error(GC_ERANGE, "gc_matrix_plan_create: too many tiles");
+        }
     *out = p;
     return GC_OK;
 }

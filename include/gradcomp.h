@@ -608,8 +608,8 @@ gc_status gc_slimdp_core_values(const gc_plan *core_plan, const gc_sparse *core,
  * tables on the device.
  * Errors: GC_EINVAL (null, seg or rows that do not fit the plan, unknown
  *         types, stride < cols, misaligned buffers, scale not finite),
- *         GC_ERANGE (n_tokens >= 2^31, n_tokens * stride > 2^48, or
- *         n_tokens * cols past 2^42).
+ *         GC_ERANGE (n_tokens >= 2^28, n_tokens * stride > 2^48,
+ *         n_tokens * cols > 2^35, or more than a launch's 2^32 threads).
  */
 gc_status gc_embed_lookup(const gc_plan *plan, int seg, uint32_t rows, const float *w,
                           const void *tokens, int token_type, uint64_t n_tokens, float scale,
@@ -667,7 +667,8 @@ gc_status gc_embed_message(const gc_plan *plan, int seg, uint32_t rows, const vo
  * (first use, or gc_matrix_plan_upload: one hipMalloc and one synchronous
  * copy per device).
  * Errors: GC_EINVAL (null, rows that do not divide a length, no matrix),
- *         GC_ENOTSUP (more than GC_MAX_MATRIX_DIM rows or columns).
+ *         GC_ENOTSUP (more than GC_MAX_MATRIX_DIM rows or columns),
+ *         GC_ERANGE (more than 2^24 tiles of 64 x 64 or matrices).
  */
 #define GC_MAX_MATRIX_DIM  (1u << 20)
 typedef struct gc_matrix_plan gc_matrix_plan;
@@ -688,7 +689,8 @@ size_t    gc_matrix_plan_workspace_bytes(const gc_matrix_plan *mplan);
  * keeps the singular vectors.  With (3.4445, -4.7750, 2.0315) five steps
  * bring all but the smallest to between about 0.7 and 1.2.
  * Products are formed from operands of 22 bits with fp32 sums; the result is
- * as near to the exact one as fp32 products are.  Unlike the other calls'
+ * about as near to the exact one as fp32 products are.  (Entries of X_0 below
+ * 2^-18, where ||D|| is far below eps, keep an absolute 2^-40 instead.)  Unlike the other calls'
  * results it is no fixed sequence of IEEE operations, but the same call on
  * the same device gives the same bits.
  * D = 0 gives O = +-0.  A matrix with a NaN or Inf becomes NaN altogether and

@@ -296,3 +296,91 @@ def test_decoded_update_of_learners_into_weights():
     W1 = Wt.cpu().numpy()
     assert np.linalg.norm(W1[o:o + mr * mc] - want) <= tol
     assert same_bits(W1[:o], W0[:o]) and same_bits(W1[o + mr * mc:], W0[o + mr * mc:])
+
+
+@pytest.mark.parametrize("shapes", [
+    [(1100, 1500)],                      # two steps at a time, tiles cut to fill the units
+    [(2600, 600)], [(513, 2000)] * 3,    # the same, transposed and several at once
+    [(1030, 1030)], [(511, 1800)],       # one step at a time: square, and too few rows for pairs
+    [(700, 900), (30, 40), (129, 3001)],  # few rows beside many
+    [(128, 9000)], [(5, 6000), (100, 100), (1, 3)],  # few rows only: several slabs a workgroup and parts
+])
+@pytest.mark.parametrize("steps", [1, 4, 5])
+def test_every_schedule(shapes, steps):
+    rng = np.random.default_rng(25)
+    ms = Mats(shapes)
+    kinds = ["gauss", "heavy", "rank1"]
+    mats = [matrix(rng, *s, kinds[k % 3]) + matrix(rng, *s, "gauss") for k, s in enumerate(shapes)]
+    x = ms.flat(mats, rng)
+    O = torch.full((ms.n,), 5.0, device=dev())
+    say(f"schedules {shapes} steps {steps}")
+    B.gc_orthogonalize(ms.m, to_dev(x), O, B.orth_options(steps), ms.ws())
+    got = O.cpu().numpy()
+    for o, D in zip(ms.parts(got), mats):
+        check(o, D, steps)
+    assert (ms.outside(got) == 5.0).all()
+
+
+@pytest.mark.parametrize("scale", [1e-9, 1e-12])
+def test_a_norm_far_below_eps(scale):
+    """X_0's entries are near fp16's last bits then.  Every X_k is stored with
+    an absolute error of up to 2^-40 an entry or a relative one of 2^-23, and
+    the products that make the next one are off by the roundings of B's and
+    X's entries (2^-23 each), the dropped product of two low parts (2^-22 at
+    most) and the result's (2^-24): less than 2^-21 of |a X_k|, since a X is
+    nearly all of the next X while X is small.  An error grows by at most the
+    step's largest slope, 3.9 (|p'| on [0, 1.2]).  So after 5 steps
+    ||dO|| <= 3.9^5 (1 + 1/3.9 + ...) 2^-40 sqrt(m n) + 5 2^-21 ||O||,
+    the geometric sum being at most 1.35."""
+    rng = np.random.default_rng(26)
+    for shape in ((40, 130), (200, 300)):
+        D = (matrix(rng, *shape, "gauss") * np.float32(scale)).astype(np.float32)
+        ms = Mats([shape])
+        O = torch.zeros(ms.n, device=dev())
+        B.gc_orthogonalize(ms.m, to_dev(ms.flat([D], rng)), O, B.orth_options(), ms.ws())
+        want = recurrence(D, 5, COEF, 1e-7, torch.float64)
+        err = np.linalg.norm(ms.parts(O.cpu().numpy())[0] - want)
+        assert err <= 1.35 * 3.9 ** 5 * 2.0 ** -40 * (shape[0] * shape[1]) ** 0.5 + 5 * 2.0 ** -21 * np.linalg.norm(want)
+
+
+def test_padded_and_gapped_buffers_are_left_alone():
+    """Only the matrices' elements are written: a buffer whose gaps and tail
+    are NaN keeps them bit for bit, in place too."""
+    rng = np.random.default_rng(27)
+    shapes = [(64, 147), (300, 520)]
+    lens = [r * c for r, c in shapes]
+    table = W.make_table([7, lens[0], 3, lens[1]], [1] * 4, None, [2, 5, 0, 9])
+    plan = B.Plan(table, W.table_extent(table) + 13)
+    m = B.MatrixPlan(plan, [0, 64, 0, 300])
+    x = np.full(plan.n_total, np.nan, np.float32)
+    for (o, n, _, _), s in ((table[1], shapes[0]), (table[3], shapes[1])):
+        x[o:o + n] = matrix(rng, *s, "gauss").reshape(-1)
+    inside = np.zeros(plan.n_total, bool)
+    for o, n, _, _ in (table[1], table[3]):
+        inside[o:o + n] = True
+    d, ws = to_dev(x), m.workspace(dev())
+    B.gc_orthogonalize(m, d, d, B.orth_options(), ws)
+    got = d.cpu().numpy()
+    assert same_bits(got[~inside], x[~inside]) and np.isfinite(got[inside]).all()
+    U, Wt = to_dev(x * 0), to_dev(x)
+    B.gc_muon_step(m, to_dev(x), U, Wt, B.muon_options(0.9, 0.1), ws)
+    U, Wt = U.cpu().numpy(), Wt.cpu().numpy()
+    assert np.isnan(U[~inside]).all() and same_bits(Wt[~inside], x[~inside])
+    assert np.isfinite(U[inside]).all() and np.isfinite(Wt[inside]).all()
+
+
+def test_refused_calls_touch_nothing():
+    ms = Mats([(20, 30)])
+    x = torch.ones(ms.n, device=dev())
+    O = torch.full((ms.n,), 3.0, device=dev())
+    for opt in (B.orth_options(eps=-1.0), B.orth_options(1, (float("nan"), 0, 0))):
+        with pytest.raises(B.GCError):
+            B.gc_orthogonalize(ms.m, x, O, opt, ms.ws())
+    with pytest.raises(B.GCError):
+        B.gc_orthogonalize(ms.m, x, O, B.orth_options(), ms.ws()[:100])
+    with pytest.raises(ValueError):
+        B.gc_orthogonalize(ms.m, x.cpu(), O, B.orth_options(), ms.ws())
+    with pytest.raises(ValueError):
+        B.gc_orthogonalize(ms.m, x[:-1], O, B.orth_options(), ms.ws())
+    torch.cuda.synchronize()
+    assert bool((O == 3.0).all())

@@ -28,7 +28,7 @@ def _lookup(plan, seg=1, rows=10, w=FAKE, tokens=FAKE, tt=0, n=5, scale=1.0, y=F
     (dict(w=None), B.GC_EINVAL), (dict(tokens=None), B.GC_EINVAL), (dict(y=None), B.GC_EINVAL),
     (dict(tt=2), B.GC_EINVAL), (dict(tt=-1), B.GC_EINVAL), (dict(yt=3), B.GC_EINVAL), (dict(stride=11), B.GC_EINVAL),
     (dict(scale=float("nan")), B.GC_EINVAL), (dict(scale=float("inf")), B.GC_EINVAL),
-    (dict(n=1 << 31), B.GC_ERANGE), (dict(n=(1 << 31) - 1, stride=1 << 30), B.GC_ERANGE),
+    (dict(n=1 << 28), B.GC_ERANGE), (dict(n=(1 << 28) - 1, stride=1 << 30), B.GC_ERANGE),
     (dict(tokens=ctypes.c_void_p(2)), B.GC_EINVAL), (dict(tokens=ctypes.c_void_p(4), tt=1), B.GC_EINVAL),
     (dict(y=ctypes.c_void_p(2)), B.GC_EINVAL), (dict(y=ctypes.c_void_p(1), yt=1), B.GC_EINVAL),
     (dict(n=0), B.GC_OK), (dict(n=0, w=None, tokens=None, y=None), B.GC_OK),
@@ -46,7 +46,7 @@ def test_embed_null_plan_and_sizes():
     assert lib.gc_embed_workspace_bytes(None, 0, 1, 1) == 0 and lib.gc_embed_message_cap(None, 0, 1, 1) == 0
     p = _plan()
     assert B.gc_embed_workspace_bytes(p, 1, 7, 10) == 0  # 7 does not divide 120
-    assert B.gc_embed_workspace_bytes(p, 1, 10, 1 << 31) == 0
+    assert B.gc_embed_workspace_bytes(p, 1, 10, 1 << 28) == 0
     assert B.gc_embed_message_cap(p, 1, 10, 3) == 36 and B.gc_embed_message_cap(p, 1, 10, 300) == 120
     small, big = (B.gc_embed_workspace_bytes(p, 1, 10, n) for n in (1, 100_000))
     assert 0 < small < big
@@ -55,7 +55,7 @@ def test_embed_null_plan_and_sizes():
 @pytest.mark.parametrize("kw,code", [
     (dict(g=None), B.GC_EINVAL), (dict(ws=None), B.GC_EINVAL), (dict(short=1), B.GC_ECAPACITY),
     (dict(dy=None), B.GC_EINVAL), (dict(dt=7), B.GC_EINVAL), (dict(stride=3), B.GC_EINVAL),
-    (dict(scale=float("nan")), B.GC_EINVAL), (dict(n=1 << 31), B.GC_ERANGE),
+    (dict(scale=float("nan")), B.GC_EINVAL), (dict(n=1 << 28), B.GC_ERANGE),
 ])
 def test_grad_refusals(kw, code):
     p = _plan()
@@ -70,6 +70,13 @@ def test_grad_refusals(kw, code):
     msg = B.gc_sparse(FAKE.value if a["g"] else None, FAKE.value, FAKE.value, None, cap)
     assert lib.gc_embed_message(p.handle, 1, 10, a["dy"], a["dt"], a["stride"], FAKE, 0, a["n"], a["scale"],
                                 ctypes.byref(msg), a["ws"], need, None) == code
+
+
+def test_batches_of_too_many_elements():
+    # 2^20 columns: 2^15 tokens reach 2^35 elements, one more passes it
+    p = B.Plan(W.make_table([1 << 22], [1], [1]))
+    for n, code in ((1 << 15, B.GC_ECAPACITY), ((1 << 15) + 1, B.GC_ERANGE)):
+        assert B.load().gc_embed_grad(p.handle, 0, 4, FAKE, 0, 1 << 20, FAKE, 0, n, 1.0, FAKE, 0, FAKE, 0, None) == code
 
 
 def test_message_refuses_a_short_message():
