@@ -572,19 +572,20 @@ def _row_stride(t, name: str) -> int:
 
 
 def _batch(plan: Plan, seg: int, rows: int, tokens, t, name: str):
-    """((t pointer, GC_* type, row stride), (tokens pointer, GC_TOKENS_*, count))
-    of a batch: tokens contiguous, of any shape; t their shape with the
+    """(t pointer, GC_* type, row stride), (tokens pointer, GC_TOKENS_*, count)
+    of a batch (_call checks the devices): tokens contiguous, of any shape; t their shape with the
     columns of segment seg, read as rows x columns, appended."""
     if not 0 <= seg < plan.nseg or rows < 1 or plan.lengths[seg] % rows:
         raise ValueError("seg must be a segment of the plan and rows divide its length")
-    cols = plan.lengths[seg] // rows
-    if not torch.is_tensor(tokens) or not tokens.is_cuda or tokens.dtype not in _TOKEN_TYPES or not tokens.is_contiguous():
-        raise ValueError("tokens: need a contiguous CUDA int32 or int64 tensor")
-    if not torch.is_tensor(t) or t.dtype not in _FLOAT_TYPES or t.shape != (*tokens.shape, cols):
+    if not torch.is_tensor(tokens) or not torch.is_tensor(t) or not tokens.is_contiguous():
+        raise ValueError(f"tokens, {name}: need tensors, tokens contiguous")
+    cols, token_type, kind = plan.lengths[seg] // rows, _TOKEN_TYPES.get(tokens.dtype), _FLOAT_TYPES.get(t.dtype)
+    if token_type is None:
+        raise ValueError("tokens: need int32 or int64")
+    if kind is None or t.shape != (*tokens.shape, cols):
         raise ValueError(f"{name}: need an fp32, bf16 or fp16 tensor of shape {(*tokens.shape, cols)}")
     stride = cols if t.is_contiguous() else _row_stride(t, name)
-    return ((t.data_ptr(), _FLOAT_TYPES[t.dtype], stride),
-            (tokens.data_ptr(), _TOKEN_TYPES[tokens.dtype], tokens.numel()))
+    return (t.data_ptr(), kind, stride), (tokens.data_ptr(), token_type, tokens.numel())
 
 
 # the raw handle without a Stream object around it (about 1 us less per call)
@@ -595,9 +596,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 def _call(fn: str, tensors, *args):
     """The library's call on the tensors' device, made the current one (the
     library enqueues there), and on that device's current stream."""
-    index = tensors[0].get_device()
+    index = tensors[0].get_device()  # -1 for the CPU
     for t in tensors:
-        if index < 0 or t.get_device() != index:
+        if t.get_device() != index or index < 0:
             raise ValueError("need CUDA tensors on one device")
     if torch.cuda.current_device() == index:
         status = getattr(load(), fn)(*args, _raw_stream(index))

@@ -760,11 +760,11 @@ void *align256(void *p) {
 
 // The embedding's shape inside the plan: GC_OK and its columns.
 gc_status check_table(const char *fn, const gc_plan *plan, int seg, uint32_t rows, uint32_t *cols) {
-    const std::string at = std::string(fn) + ": ";
-    if (!plan) return set_error(GC_EINVAL, at + "plan is null");
-    if (seg < 0 || seg >= plan->nseg) return set_error(GC_EINVAL, at + "seg is not a segment of the plan");
+    auto fail = [&](gc_status st, const char *what) { return set_error(st, std::string(fn) + ": " + what); };
+    if (!plan) return fail(GC_EINVAL, "plan is null");
+    if (seg < 0 || seg >= plan->nseg) return fail(GC_EINVAL, "seg is not a segment of the plan");
     const uint32_t len = plan->seg[seg].len;
-    if (rows < 1 || len % rows) return set_error(GC_EINVAL, at + "rows must divide the segment's length");
+    if (rows < 1 || len % rows) return fail(GC_EINVAL, "rows must divide the segment's length");
     *cols = len / rows;
     return GC_OK;
 }
@@ -773,21 +773,21 @@ size_t type_bytes(int type) { return type == GC_F32 ? 4 : 2; }
 
 gc_status check_batch(const char *fn, const void *tokens, int token_type, uint64_t n, const void *x, int type,
                       uint64_t stride, uint32_t cols, float scale) {
-    const std::string at = std::string(fn) + ": ";
+    auto fail = [&](gc_status st, const char *what) { return set_error(st, std::string(fn) + ": " + what); };
     if (token_type != GC_TOKENS_I32 && token_type != GC_TOKENS_I64)
-        return set_error(GC_EINVAL, at + "token_type must be GC_TOKENS_I32 or GC_TOKENS_I64");
+        return fail(GC_EINVAL, "token_type must be GC_TOKENS_I32 or GC_TOKENS_I64");
     if (type != GC_F32 && type != GC_BF16 && type != GC_F16)
-        return set_error(GC_EINVAL, at + "type must be GC_F32, GC_BF16 or GC_F16");
-    if (!(scale - scale == 0.0f)) return set_error(GC_EINVAL, at + "scale must be finite");
-    if (n >= kMaxTokens) return set_error(GC_ERANGE, at + "n_tokens must be < 2^28");
-    if (n * cols > kMaxElems) return set_error(GC_ERANGE, at + "n_tokens * cols must be <= 2^35");
+        return fail(GC_EINVAL, "type must be GC_F32, GC_BF16 or GC_F16");
+    if (!(scale - scale == 0.0f)) return fail(GC_EINVAL, "scale must be finite");
+    if (n >= kMaxTokens) return fail(GC_ERANGE, "n_tokens must be < 2^28");
+    if (n * cols > kMaxElems) return fail(GC_ERANGE, "n_tokens * cols must be <= 2^35");
     if (n == 0) return GC_OK;
-    if (!tokens || !x) return set_error(GC_EINVAL, at + "buffers must be non-null");
-    if (stride < cols) return set_error(GC_EINVAL, at + "the row stride must be at least the columns");
-    if (n > 1 && stride > (uint64_t(1) << 48) / n) return set_error(GC_ERANGE, at + "n_tokens * stride must be <= 2^48");
+    if (!tokens || !x) return fail(GC_EINVAL, "buffers must be non-null");
+    if (stride < cols) return fail(GC_EINVAL, "the row stride must be at least the columns");
+    if (n > 1 && stride > (uint64_t(1) << 48) / n) return fail(GC_ERANGE, "n_tokens * stride must be <= 2^48");
     if (reinterpret_cast<uintptr_t>(tokens) % (token_type == GC_TOKENS_I32 ? 4 : 8) ||
         reinterpret_cast<uintptr_t>(x) % type_bytes(type))
-        return set_error(GC_EINVAL, at + "buffers must be aligned to their elements");
+        return fail(GC_EINVAL, "buffers must be aligned to their elements");
     return GC_OK;
 }
 

@@ -1022,17 +1022,17 @@ void *align256(void *p) {
 
 gc_status check_orth(const char *fn, const gc_matrix_plan *p, const gc_orth_options *o, const void *ws, size_t ws_bytes,
                      Scales *s) {
-    const std::string at = std::string(fn) + ": ";
-    if (!p) return set_error(GC_EINVAL, at + "matrix plan is null");
-    if (!o) return set_error(GC_EINVAL, at + "opt is null");
-    if (o->steps < 1 || o->steps > GC_MAX_ORTH_STEPS) return set_error(GC_EINVAL, at + "steps must be in [1, GC_MAX_ORTH_STEPS]");
-    if (!(o->eps >= 0.0f) || !(o->eps - o->eps == 0.0f)) return set_error(GC_EINVAL, at + "eps must be finite and >= 0");
-    if (o->reserved[0] || o->reserved[1]) return set_error(GC_EINVAL, at + "reserved fields must be 0");
+    auto fail = [&](gc_status st, const char *what) { return set_error(st, std::string(fn) + ": " + what); };
+    if (!p) return fail(GC_EINVAL, "matrix plan is null");
+    if (!o) return fail(GC_EINVAL, "opt is null");
+    if (o->steps < 1 || o->steps > GC_MAX_ORTH_STEPS) return fail(GC_EINVAL, "steps must be in [1, GC_MAX_ORTH_STEPS]");
+    if (!(o->eps >= 0.0f) || !(o->eps - o->eps == 0.0f)) return fail(GC_EINVAL, "eps must be finite and >= 0");
+    if (o->reserved[0] || o->reserved[1]) return fail(GC_EINVAL, "reserved fields must be 0");
     if (!orth_scales(*o, s))
-        return set_error(GC_EINVAL, at + "coef must be finite and keep the singular values of X at most 8");
-    if (!ws) return set_error(GC_EINVAL, at + "ws must be non-null");
+        return fail(GC_EINVAL, "coef must be finite and keep the singular values of X at most 8");
+    if (!ws) return fail(GC_EINVAL, "ws must be non-null");
     if (ws_bytes < orth_ws(nullptr, p).bytes)
-        return set_error(GC_ECAPACITY, at + "workspace smaller than gc_matrix_plan_workspace_bytes");
+        return fail(GC_ECAPACITY, "workspace smaller than gc_matrix_plan_workspace_bytes");
     return GC_OK;
 }
 
