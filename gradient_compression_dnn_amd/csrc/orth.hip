@@ -810,8 +810,12 @@ __device__ __forceinline__ const uint32_t *block_of(const uint32_t *words, uint3
     return words + (2 * ib + (jb ^ ib)) * kBlockWords;
 }
 
-// g += Y Y^T for the wave's 64 x 64, Y's first 32 n columns in `words`.
-__device__ __forceinline__ void add_square(const uint32_t *words, uint32_t wr, uint32_t wc, uint32_t n, f32x4 (&g)[4][4]) {
+// g += Y Y^T for the wave's 64 x 64, Y's first 32 n columns in `words`. Y has m
+// rows: 16-row tiles behind them are neither read nor multiplied, their operands
+// stay zero and so do their sums (29 x 1600, 5 steps: 95 us instead of 101).
+__device__ __forceinline__ void add_square(const uint32_t *words, uint32_t wr, uint32_t wc, uint32_t n, uint32_t m,
+                                           f32x4 (&g)[4][4]) {
+    const uint32_t ra = m - 64 * wr, rb = m - 64 * wc;
     for (uint32_t s = 0; s < n; ++s) {
         auto operand = [&](uint32_t ib, uint32_t t, h8 &hi, h8 &lo) {  // rows 16 t + lane % 16 of row block ib
             const uint32_t *b = block_of(words, ib, s >> 1);
@@ -831,11 +835,13 @@ __device__ __forceinline__ void add_square(const uint32_t *words, uint32_t wr, u
             hi = __builtin_bit_cast(h8, h);
             lo = __builtin_bit_cast(h8, l);
         };
-        h8 qh[4], ql[4];
+        h8 qh[4] = {}, ql[4] = {};
 #pragma unroll
-        for (int b = 0; b < 4; ++b) operand(wc, b, qh[b], ql[b]);
+        for (int b = 0; b < 4; ++b)
+            if (16u * b < rb) operand(wc, b, qh[b], ql[b]);
 #pragma unroll
         for (int a = 0; a < 4; ++a) {
+            if (16u * a >= ra) break;
             h8 ph, pl;
             operand(wr, a, ph, pl);
 #pragma unroll
@@ -939,7 +945,7 @@ __global__ __launch_bounds__(kBlock) void orth_slab_kernel(GemmArgs g, FirstArgs
             lds_barrier();
         }
         if (active) write_columns<1>(g.Tn + M.x, M.mp, block, pr, j0 + qr);
-        if (squares) add_square(words, wr, wc, 4, sums);
+        if (squares) add_square(words, wr, wc, 4, M.m, sums);
     }
     if (kSlabKind == kLast || !squares) return;
     f32x4 *p = reinterpret_cast<f32x4 *>(g.partial + static_cast<uint64_t>(it.slot) * kNarrow * kNarrow) + w * (16 * kWave) + lane_id();
@@ -995,7 +1001,7 @@ __global__ __launch_bounds__(kBlock) void orth_small_kernel(GemmArgs g, float sq
     for (int a = 0; a < 4; ++a)
 #pragma unroll
         for (int b = 0; b < 4; ++b) A2[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    if (active) add_square(words, wr, wc, (M.m + 31) / 32, A2);
+    if (active) add_square(words, wr, wc, (M.m + 31) / 32, M.m, A2);
     lds_barrier();  // every wave has read A
     if (!active) return;
 #pragma unroll
