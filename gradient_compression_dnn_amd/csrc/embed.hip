@@ -102,7 +102,9 @@ __device__ __forceinline__ uint32_t token_key(const Tok *tokens, uint64_t i, uin
 // ------------------------------------------------------------------ lookup
 // A flat grid over the groups of kLookupCols columns of all tokens: kLookupVecs per
 // thread, a workgroup's stride apart, all loads issued before the first
-// store.
+// store.  Memory bounds it: 32,768 tokens by 4,096 columns to bf16 take 92 us,
+// 4.9 TB/s over the distinct rows read and y written, a large copy's rate.  At 700 tokens
+// by 1,500 columns 4 us, a launch's own time.
 constexpr int kLookupVecs = 4;
 template <class T>
 constexpr int kLookupCols = 16 / int(sizeof(typename T::Store));  // 16 bytes of y
@@ -162,8 +164,10 @@ struct Lists {
 // Workgroup x ranks tokens [64 x, 64 x + 64) inside their tile; workgroups
 // from `nrank` on clear the dense gradient meanwhile (nfill > 0), 16 x 1024
 // elements each.  A row that has tokens is written again by the sum, one
-// launch later.
-template <class Tok, uint32_t kTile>
+// launch later.  kSet is the tokens ranked together.  LDS reads bound it, one
+// of 16 bytes for 4 comparisons of a wave's 64 tokens: 8 us at 32,000 tokens
+// in tiles of kTile; with the clearing of 15 M elements 12 us, 5.1 TB/s.
+template <class Tok, uint32_t kSet>
 __global__ __launch_bounds__(kRankThreads) void embed_rank_kernel(const Tok *__restrict__ tokens, uint32_t n,
                                                                   uint32_t rows, uint32_t *__restrict__ key_out,
                                                                   uint32_t *__restrict__ pos_out, uint32_t *list_count,
@@ -178,11 +182,11 @@ __global__ __launch_bounds__(kRankThreads) void embed_rank_kernel(const Tok *__r
         return;
     }
     if (blockIdx.x == 0 && threadIdx.x < 2) list_count[threadIdx.x] = 0;
-    __shared__ uint32_t keys[kTile];
+    __shared__ uint32_t keys[kSet];
     __shared__ uint32_t part[kRankWaves][kWave];
     const uint32_t i0 = blockIdx.x * kWave;
-    const uint32_t t0 = i0 / kTile * kTile;
-    const uint32_t cnt = min(n - t0, kTile);
+    const uint32_t t0 = i0 / kSet * kSet;
+    const uint32_t cnt = min(n - t0, kSet);
     const uint32_t cnt4 = (cnt + 3u) & ~3u;
     for (uint32_t j = threadIdx.x; j < cnt4; j += kRankThreads)
         keys[j] = j < cnt ? token_key(tokens, t0 + j, rows) : 0xFFFFFFFFu;  // above every key
@@ -237,7 +241,7 @@ __global__ __launch_bounds__(kRankThreads) void embed_rank_kernel(const Tok *__r
 // range to a 64th, and each element's 16 searches are spread over 4 threads.
 // (The code is kept short for the same reason: with the 16 runs unrolled it
 // took 20 to 24 us at 16,000 to 32,000 tokens, most of them instruction
-// fetches.)
+// fetches; as it stands 9 to 11.)
 constexpr int kMergeThreads = 1024;
 constexpr uint32_t kMergeElems = 256;
 constexpr uint32_t kMergeKeys = 512;  // keys of one other run held in LDS
@@ -354,7 +358,8 @@ __global__ __launch_bounds__(kHeadThreads) void embed_heads_kernel(const uint32_
 }
 
 // Workgroup x places tile x (tile_heads null: it counts the heads in front
-// of its tile first); the last one writes the message's offsets.
+// of its tile first, which spares a launch); the last one writes the message's
+// offsets.  Latency bounds it: 16,383 tokens take 5 to 6 us.
 __global__ __launch_bounds__(kHeadThreads) void embed_rows_kernel(const uint32_t *__restrict__ key, uint32_t n,
                                                                   uint32_t rows, uint32_t cols,
                                                                   const uint32_t *__restrict__ tile_heads,
@@ -439,6 +444,8 @@ __device__ __forceinline__ void put_row(const SumOut &o, uint32_t row, uint32_t 
 // w + waves, ... and adds each one's rows in order.  part[2 b] holds the sum of
 // a run that comes from the block before, part[2 b + 1] of one that begins
 // here and goes on; the latter is listed for the join.
+// Memory bounds it: 32,000 rows of 1,500 fp16 columns added to g take 37 us, of
+// 32 that the bytes of dy and g need at a large copy's rate.
 // The body is one short loop: unrolled over the 16 positions it ran 3 times
 // longer at 20 tokens and 4 times at 32,000, for its instruction fetches.
 // Each lane has 4 columns in every type: the sums leave in fp32, 16 bytes a
@@ -448,9 +455,9 @@ constexpr uint32_t kJoinWaves = 16;
 constexpr int kLaneCols = 4;
 constexpr uint32_t kSlab = kWave * kLaneCols;
 
-// Two rows ahead: one took 43 us at 32,000 tokens by 1,500 fp16 columns where
-// two take 37, eight 40 (most pieces are a row or two).
-// acc += rows dy[pos[l]] for lanes l in [from, to) of the wave's lpos.
+// acc += rows dy[pos[l]] for lanes l in [from, to) of the wave's lpos.  Two
+// rows ahead: one took 43 us at 32,000 tokens by 1,500 fp16 columns where two
+// take 37, eight 40 (most pieces are a row or two).
 template <class T>
 __device__ __forceinline__ void add_rows(const typename T::Store *__restrict__ dy, uint64_t stride, uint32_t lpos,
                                          uint32_t from, uint32_t to, uint32_t c, uint32_t cols,
@@ -522,7 +529,9 @@ __global__ __launch_bounds__(1024) void embed_sum_kernel(const typename T::Store
 // waves ranks the batch for itself in LDS; workgroup (group g of 16 runs, slab)
 // sums a run per wave, block by block of 16 sorted positions as the other
 // path's partial sums (at most 16 blocks, so they are added in order); the
-// workgroups behind them clear the rows that have no token (dense).
+// workgroups behind them clear the rows that have no token (dense).  Latency
+// bounds it: 20 tokens by 1,500 columns take 5 us, where the other path's four
+// launches took 13.
 constexpr uint32_t kSmall = 256;
 constexpr int kSmallThreads = 1024;
 constexpr uint32_t kSmallWaves = kSmallThreads / kWave;
@@ -639,7 +648,8 @@ __global__ __launch_bounds__(kSmallThreads) void embed_small_kernel(const typena
 // The partial sums of the listed runs: part[2 b + 1], then part[2 (b + i)].
 // Runs of at most kJoinWaves partials take a wave each and are added in
 // order; for longer ones wave w of a workgroup adds partials w, w + 16, ...,
-// and then the 16 sums are added in wave order.
+// and then the 16 sums are added in wave order.  Latency bounds it, of the
+// longest run's partials: 11 us at 32,000 tokens by 1,500 columns, 4 at 700.
 constexpr int kJoinThreads = kJoinWaves * kWave;
 
 __device__ __forceinline__ uint32_t run_blocks(const uint32_t *__restrict__ key, uint32_t n, uint32_t b, uint32_t k) {

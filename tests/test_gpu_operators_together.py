@@ -1,0 +1,158 @@
+"""The embedding's calls and the matrix updates as a training step uses them
+together: one after the other, captured, and with workspaces in turn.  The
+single calls are checked against 64 bits elsewhere; here every run has to give
+the bits of the same calls made one by one."""
+import numpy as np
+import pytest
+import torch
+
+from gradient_compression_dnn_amd import binding as B
+from gradient_compression_dnn_amd import workloads as W
+from tests.gpu_util import dev, say
+
+pytestmark = pytest.mark.gpu
+
+
+class Learner:
+    """A flat model of an embedding, matrices and a vector; one step is
+    lookup, the embedding's message, its decode into the dense gradient, the
+    matrices' Muon step, and the embedding's own gradient added elsewhere."""
+
+    def __init__(self, rows, cols, shapes, n, seed):
+        rng = np.random.default_rng(seed)
+        lens = [rows * cols] + [r * c for r, c in shapes] + [9]
+        self.rows, self.cols, self.n = rows, cols, n
+        self.plan = B.Plan(W.make_table(lens, [1] * len(lens)))
+        self.mplan = B.MatrixPlan(self.plan, [0] + [r for r, _ in shapes] + [0])
+        self.plan.upload()
+        self.mplan.upload()
+        N = self.plan.n_total
+        self.G = torch.from_numpy(rng.normal(0, 1e-3, N).astype(np.float32)).to(dev())
+        self.w0 = torch.from_numpy(rng.normal(0, 1, N).astype(np.float32)).to(dev())
+        self.tokens = torch.from_numpy(rng.integers(-1, rows + 1, n)).to(dev())
+        self.dy = torch.from_numpy(rng.normal(0, 1, (n, cols)).astype(np.float32)).to(dev())
+        self.opt = B.muon_options(0.9, 0.02, weight_decay=0.01)
+        self.need = max(self.mplan.workspace_bytes(), B.gc_embed_workspace_bytes(self.plan, 0, rows, n))
+
+    def state(self):
+        N = self.plan.n_total
+        z = lambda *s: torch.zeros(*s, device=dev())
+        return dict(y=z(self.n, self.cols), w=self.w0.clone(), U=z(N), dense=z(N), added=z(N),
+                    msg=B.Sparse.empty(self.plan, B.gc_embed_message_cap(self.plan, 0, self.rows, self.n), dev()),
+                    dws=self.plan.workspace(B.GC_OP_DECODE, dev()))
+
+    def step(self, s, ws):
+        B.gc_embed_lookup(self.plan, 0, self.rows, s["w"], self.tokens, 0.5, s["y"])
+        B.gc_embed_message(self.plan, 0, self.rows, self.dy, self.tokens, 0.25, s["msg"], ws)
+        s["dense"].copy_(self.G)
+        B.gc_decompress_accumulate(self.plan, [s["msg"]], s["dense"], B.GC_SUM, True, s["dws"])
+        B.gc_muon_step(self.mplan, s["dense"], s["U"], s["w"], self.opt, ws)
+        B.gc_embed_grad(self.plan, 0, self.rows, self.dy, self.tokens, 0.25, s["added"], True, ws)
+        # the embedding's own step, so that the next lookup differs
+        s["w"][:self.rows * self.cols] -= 0.1 * s["dense"][:self.rows * self.cols]
+
+
+def same(a, b):
+    for k in ("y", "w", "U", "dense", "added"):
+        assert torch.equal(a[k], b[k]), k
+    for p, q in zip(a["msg"].host()[:3], b["msg"].host()[:3]):
+        assert np.array_equal(p, q)
+
+
+LEARNERS = [
+    (50, 12, [(29, 300), (100, 70), (1, 1)], 200),        # one launch a message, matrices of few rows
+    (300, 40, [(700, 1200), (1200, 700)], 3000),          # sorted tokens, two steps at a time
+    (40, 257, [(200, 333), (20, 5)], 7000),               # merged runs, one step at a time
+]
+
+
+def test_two_graphs_that_share_a_workspace():
+    ls = [Learner(*a, seed=31 + k) for k, a in enumerate(LEARNERS)]
+    ws = torch.full((max(l.need for l in ls),), 0xFF, dtype=torch.uint8, device=dev())
+    states, graphs = [l.state() for l in ls], []
+    eager, own = [l.state() for l in ls], [torch.full((l.need,), 0xFF, dtype=torch.uint8, device=dev()) for l in ls]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for k, (l, s) in enumerate(zip(ls, states)):
+        say(f"capture of learner {k}")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            l.step(s, ws)
+        graphs.append(graph)
+    for t in range(4):
+        for k, graph in enumerate(graphs):
+            say(f"replay {t} of learner {k}")
+            graph.replay()
+        torch.cuda.synchronize()
+        for l, s, w in zip(ls, eager, own):
+            l.step(s, w)
+        torch.cuda.synchronize()
+        for a, b in zip(states, eager):
+            same(a, b)
+            assert bool(torch.isfinite(a["w"]).all())
+
+
+def test_learners_on_their_own_streams():
+    ls = [Learner(*a, seed=41 + k) for k, a in enumerate(LEARNERS)]
+    spaces = [torch.full((l.need,), 0xFF, dtype=torch.uint8, device=dev()) for l in ls]
+    alone, states = [l.state() for l in ls], [l.state() for l in ls]
+    torch.cuda.synchronize()
+    for l, s, w in zip(ls, alone, spaces):
+        for _ in range(3):
+            l.step(s, w)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ls]
+    say("three learners at once")
+    for _ in range(3):
+        for l, s, w, st in zip(ls, states, spaces, streams):
+            with torch.cuda.stream(st):
+                l.step(s, w)
+    torch.cuda.synchronize()
+    for a, b in zip(alone, states):
+        same(a, b)
+
+
+@pytest.mark.parametrize("shapes", [[(600, 900)] * 3, [(200, 500)] * 3, [(600, 900), (16, 20), (700, 640)]])
+def test_a_matrix_that_is_not_finite_leaves_the_others_alone(shapes):
+    """Its workspace is full of NaN afterwards, and the next call is right."""
+    rng = np.random.default_rng(51)
+    plan = B.Plan(W.make_table([r * c for r, c in shapes], [1] * len(shapes)))
+    m = B.MatrixPlan(plan, [r for r, _ in shapes])
+    x = torch.from_numpy(rng.normal(size=plan.n_total).astype(np.float32)).to(dev())
+    want, got = torch.zeros_like(x), torch.zeros_like(x)
+    ws = m.workspace(dev())
+    B.gc_orthogonalize(m, x, want, B.orth_options(), ws)
+    offs = np.cumsum([0] + [r * c for r, c in shapes])
+    for bad, value in ((0, float("nan")), (1, float("inf")), (2, -float("inf"))):
+        y = x.clone()
+        y[int(offs[bad + 1]) - 1] = value
+        say(f"{shapes} with {value} in matrix {bad}")
+        B.gc_orthogonalize(m, y, got, B.orth_options(), ws)
+        for k in range(3):
+            a, b = (t[int(offs[k]):int(offs[k + 1])] for t in (got, want))
+            assert bool(torch.isnan(a).all()) if k == bad else torch.equal(a, b)
+        B.gc_orthogonalize(m, x, got, B.orth_options(), ws)
+        assert torch.equal(got, want)
+
+
+def test_one_token_again_and_again():
+    """Every position the same row: one run over all blocks, at lengths around
+    the partial sums of a join and the ranked tiles."""
+    rows, cols = 5, 6
+    plan = B.Plan(W.make_table([rows * cols], [1]))
+    for n in (1, 2, 15, 16, 17, 255, 256, 257, 272, 273, 2048, 6144, 6145, 32768, 32769, 40000):
+        tokens = torch.full((n,), 4, dtype=torch.int32, device=dev())
+        dy = torch.ones(n, cols, device=dev())
+        g = torch.full((plan.n_total,), 7.0, device=dev())
+        ws = torch.empty(B.gc_embed_workspace_bytes(plan, 0, rows, n), dtype=torch.uint8, device=dev())
+        say(f"one row {n} times")
+        B.gc_embed_grad(plan, 0, rows, dy, tokens, 0.5, g, False, ws)
+        want = torch.zeros(rows, cols, device=dev())
+        want[4] = 0.5 * n  # whole numbers below 2^24: exact in any order
+        assert torch.equal(g.view(rows, cols), want)
+        B.gc_embed_grad(plan, 0, rows, dy, tokens, 0.5, g, True, ws)
+        assert torch.equal(g.view(rows, cols), 2 * want)
+        msg = B.Sparse.empty(plan, B.gc_embed_message_cap(plan, 0, rows, n), dev())
+        B.gc_embed_message(plan, 0, rows, dy, tokens, 0.5, msg, ws)
+        idx, val, off, _ = msg.host()
+        assert np.array_equal(idx, np.arange(4 * cols, 5 * cols)) and (val == 0.5 * n).all() and off[1] == cols
