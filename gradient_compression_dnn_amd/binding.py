@@ -227,14 +227,17 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
 
 
+_Tensor = torch.Tensor
+
+
 # The C ABI trusts the sizes it is given; these checks make every pointer the
 # binding passes down a contiguous CUDA tensor of the right type holding at
 # least the elements the call may touch.
 def _dev(t, dtype, n: int, name: str):
-    if not torch.is_tensor(t) or t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
         raise ValueError(f"{name}: need a contiguous CUDA {str(dtype).replace('torch.', '')} tensor "
                          f"of >= {n} elements")
-    return _ptr(t)
+    return t.data_ptr()
 
 
 def _f32(t: torch.Tensor, n: int, name: str):
@@ -339,11 +342,10 @@ class Sparse:
     def checked(self, plan: "Plan", name: str = "message") -> gc_sparse:
         """The struct, after checking that the tensors hold cap entries and
         the plan's per-segment arrays."""
-        _dev(self.idx, torch.int32, self.cap, f"{name}.idx")
-        _dev(self.val, torch.float32, self.cap, f"{name}.val")
-        _dev(self.seg_off, torch.int32, plan.nseg + 1, f"{name}.seg_off")
-        _dev(self.seg_scale, torch.float32, max(plan.nseg, 1), f"{name}.seg_scale")
-        return self.struct()
+        i32, f32, nseg = torch.int32, torch.float32, plan.nseg
+        return gc_sparse(_dev(self.idx, i32, self.cap, name + ".idx"), _dev(self.val, f32, self.cap, name + ".val"),
+                         _dev(self.seg_off, i32, nseg + 1, name + ".seg_off"),
+                         _dev(self.seg_scale, f32, nseg or 1, name + ".seg_scale"), self.cap)
 
     def count(self) -> int:
         return int(self.seg_off[-1].item())
@@ -496,7 +498,7 @@ def gc_dcd_decode(scales: torch.Tensor, codes: torch.Tensor, x_hat, bits: int, b
 def gc_dcd_mix(replicas, weights, grad, lr: float, x_half):
     n = x_half.numel()
     K = len(replicas)
-    reps = (ctypes.c_void_p * max(K, 1))(*[_f32(r, n, "replica").value for r in replicas])
+    reps = (ctypes.c_void_p * max(K, 1))(*[_f32(r, n, "replica") for r in replicas])
     w = (ctypes.c_float * max(K, 1))(*[float(v) for v in weights])
     _check(load().gc_dcd_mix(reps, w, K, _f32(grad, n, "grad"), float(lr), _f32(x_half, n, "x_half"), n,
                              _stream(x_half)))
@@ -577,7 +579,7 @@ def _batch(plan: Plan, seg: int, rows: int, tokens, t, name: str):
     columns of segment seg, read as rows x columns, appended."""
     if not 0 <= seg < plan.nseg or rows < 1 or plan.lengths[seg] % rows:
         raise ValueError("seg must be a segment of the plan and rows divide its length")
-    if not torch.is_tensor(tokens) or not torch.is_tensor(t) or not tokens.is_contiguous():
+    if not isinstance(tokens, _Tensor) or not isinstance(t, _Tensor) or not tokens.is_contiguous():
         raise ValueError(f"tokens, {name}: need tensors, tokens contiguous")
     cols, token_type, kind = plan.lengths[seg] // rows, _TOKEN_TYPES.get(tokens.dtype), _FLOAT_TYPES.get(t.dtype)
     if token_type is None:
@@ -588,9 +590,11 @@ def _batch(plan: Plan, seg: int, rows: int, tokens, t, name: str):
     return (t.data_ptr(), kind, stride), (tokens.data_ptr(), token_type, tokens.numel())
 
 
-# the raw handle without a Stream object around it (about 1 us less per call)
+# the raw handle without a Stream object around it (about 1 us less per call),
+# and the device without the check that CUDA is initialised, which its tensors show
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _call(fn: str, tensors, *args):
@@ -600,8 +604,8 @@ def _call(fn: str, tensors, *args):
     for t in tensors:
         if t.get_device() != index or index < 0:
             raise ValueError("need CUDA tensors on one device")
-    if torch.cuda.current_device() == index:
-        status = getattr(load(), fn)(*args, _raw_stream(index))
+    if _device() == index:
+        status = getattr(_lib or load(), fn)(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
             status = getattr(load(), fn)(*args, _raw_stream(index))
