@@ -100,8 +100,8 @@ struct OrthDev {
 struct gc_matrix_plan {
     uint64_t n_total = 0;
     uint64_t xhalves = 0, ahalves = 0;  // halves of one X (or T) array and of one A (or B) array
-    uint32_t slots = 0;                 // parts of split tiles held at once
-    bool large = false;                 // tiles of 256 x 256
+    uint64_t partial = 0;               // floats of split tiles' parts held at once
+    bool large[gc::kLists] = {};        // products: tiles of 256 x 256
     bool pairs = false;                 // two steps at a time
     bool narrow = false;                // every matrix has at most kNarrow rows
     std::vector<gc::MatDev> mat;
@@ -238,10 +238,13 @@ bool orth_scales(const gc_orth_options &o, Scales *s) {
 // --------------------------------------------------------------- tile shapes
 // kTile x kTile per workgroup by kWR x kWC waves, two stages of 32 columns of
 // both planes in LDS; kUnits workgroups at once on 256 compute units.  The
-// large tile reads half as much per product (the LSTM's four matrices: 2.45 ms
-// against 2.62), the small one fits small matrices and writes out while its
-// neighbour multiplies (ResNet-50's: 1.33 ms against 1.40; with four stages and
-// a unit to itself 1.43).
+// large tile reads half as much per product, the small one fits small matrices
+// and writes out while its neighbour multiplies; the plan's model picks one for
+// each kind of product.  Measured, large against small: B A of four matrices of
+// 1500 rows 65 us and 76, B X of 4096 x 4096 318 and 353, of ResNet-50's 54
+// matrices 112 and 123; their X X^T 75 and 66, their A A^T 55 and 40, X X^T of 28
+// matrices of 800 to 2400 rows 655 and 628.  (A small tile with four stages and
+// a unit to itself: 1.43 ms for ResNet-50's update where two stages took 1.33.)
 struct Large {
     static constexpr uint32_t kUnits = 256;
     static constexpr int kTile = 256, kWR = 2, kWC = 4;
@@ -271,8 +274,7 @@ OrthWs orth_ws(void *ws, const gc_matrix_plan *p) {
     w.S = c.take<_Float16>(p->pairs ? p->ahalves : 0);
     w.sums = c.take<double>(p->list[kChunks].size());
     w.inv = c.take<double>(p->mat.size());
-    const uint64_t tile = p->large ? Large::kTile : Small::kTile;
-    w.partial = c.take<float>(p->slots * tile * tile);
+    w.partial = c.take<float>(p->partial);
     w.bytes = c.used + 256;  // room to round the base up to 256 bytes
     return w;
 }
@@ -444,6 +446,18 @@ struct Shape : T {
     static_assert(kWaves * 64 * 64 * 4 <= kLds, "a block of results per wave");
     static_assert(kWaveCols == 64 && kWaveRows % 64 == 0, "the epilogue's blocks");
 };
+
+// Whether the wave at (pr, qr) of a tile lies above the diagonal of a symmetric
+// result's diagonal tile; the waves below it write its mirror image.
+template <class C>
+__device__ __forceinline__ bool above(uint32_t pr, uint32_t qr) {
+    return qr >= pr + C::kWaveRows;
+}
+// Whether the block at (r, c) of tile `it` has to write its mirror image.
+template <class C>
+__device__ __forceinline__ bool mirrors(const Item &it, uint32_t r, uint32_t c) {
+    return it.i != it.j || above<C>(c / C::kWaveRows * C::kWaveRows, r);
+}
 
 typedef __attribute__((address_space(1))) const char GlobalChar;
 typedef __attribute__((address_space(3))) char LdsChar;
@@ -735,7 +749,7 @@ __global__ __launch_bounds__(C::kThreads) void orth_gemm_kernel(GemmArgs g) {
         // with half its rows or columns costs half
         const uint32_t wr = w / C::kWC, wc = (w + wr * (C::kWC / 2)) % C::kWC;
         const uint32_t pr = wr * C::kWaveRows, qr = wc * C::kWaveCols;
-        const bool active = pr < rows_p && qr < rows_q;
+        const bool active = pr < rows_p && qr < rows_q && !(kKind == kSym && it.i == it.j && above<C>(pr, qr));
         f32x4 acc[C::kRA][C::kRB];
 #pragma unroll
         for (int a = 0; a < C::kRA; ++a)
@@ -767,7 +781,7 @@ __global__ __launch_bounds__(C::kThreads) void orth_gemm_kernel(GemmArgs g) {
 #pragma unroll
                 for (int b = 0; b < C::kRB; ++b)
                     put_tile(block, a, b, acc[4 * h + a][b]);
-            write_block<kKind, 1>(g, M, block, i0 + pr + 64 * h, j0 + qr, it.i != it.j);
+            write_block<kKind, 1>(g, M, block, i0 + pr + 64 * h, j0 + qr, mirrors<C>(it, pr + 64 * h, qr));
         }
     }
 }
@@ -783,8 +797,10 @@ __global__ __launch_bounds__(kBlock) void orth_join_kernel(GemmArgs g) {
     const MatDev M = g.mats[it.mat];
     const uint32_t part = blockIdx.x % kBlocks, w = part / (C::kRA / 4), h = part % (C::kRA / 4);
     const uint32_t wr = w / C::kWC, wc = (w + wr * (C::kWC / 2)) % C::kWC;
-    const uint32_t i0 = it.i * C::kTile + wr * C::kWaveRows + 64 * h, j0 = it.j * C::kTile + wc * C::kWaveCols;
+    const uint32_t pr = wr * C::kWaveRows, qr = wc * C::kWaveCols;
+    const uint32_t i0 = it.i * C::kTile + pr + 64 * h, j0 = it.j * C::kTile + qr;
     if (i0 >= M.mp || j0 >= (kKind == kSym ? M.mp : M.np)) return;
+    if (kKind == kSym && it.i == it.j && above<C>(pr, qr)) return;
     // tiles 4 a + b of the block: a is this wave's
     const uint32_t a = wave_id();
     const f32x4 *p = reinterpret_cast<const f32x4 *>(g.partial + static_cast<uint64_t>(it.slot) * C::kTile * C::kTile) +
@@ -800,7 +816,7 @@ __global__ __launch_bounds__(kBlock) void orth_join_kernel(GemmArgs g) {
 #pragma unroll
     for (int b = 0; b < C::kRB; ++b) put_tile(block, a, b, v[b]);
     __syncthreads();
-    write_block<kKind, kWaves>(g, M, block, i0, j0, it.i != it.j);
+    write_block<kKind, kWaves>(g, M, block, i0, j0, mirrors<C>(it, pr + 64 * h, qr));
 }
 
 // ----------------------------------------------------- matrices of few rows
@@ -1068,7 +1084,7 @@ void product_of(const char *name, const gc_matrix_plan *p, const OrthDev &d, Lis
 
 template <Kind kKind>
 void product(const char *name, const gc_matrix_plan *p, const OrthDev &d, List l, const GemmArgs &g, hipStream_t stream) {
-    if (p->large) product_of<kKind, Shape<Large>>(name, p, d, l, g, stream);
+    if (p->large[l]) product_of<kKind, Shape<Large>>(name, p, d, l, g, stream);
     else product_of<kKind, Shape<Small>>(name, p, d, l, g, stream);
 }
 
@@ -1213,6 +1229,9 @@ struct Tile {
 
 // us of a stage of a whole tile, of an item (first loads, writing out), of a
 // part's sums written and read again, on the memory's account, and of a join.
+// Fitted to the 24 products of four plans (ResNet-50's matrices, four of 1500 x
+// 6000, 28 of 800 to 2400 rows, one of 4096 x 4096) in both tiles, whose times
+// they give to 7 %.
 struct Costs {
     uint32_t units;
     double stage, item, part, join;
@@ -1328,15 +1347,17 @@ constexpr uint64_t kMaxParts = 16;
 void plan_narrow(gc_matrix_plan *p) {
     p->narrow = true;
     uint64_t slabs = 0;
+    uint32_t slots = 0;
     for (const MatDev &M : p->mat) slabs += M.np / kNarrow;
     for (uint32_t id = 0; id < p->mat.size(); ++id) {
         const uint32_t n = p->mat[id].np / kNarrow;
         const uint32_t per = static_cast<uint32_t>(std::max(ceil_div(n, kMaxParts), ceil_div(slabs, Small::kUnits)));
         const uint32_t parts = static_cast<uint32_t>(ceil_div(n, per));
-        p->list[kSmalls].push_back({id, 0, 0, 0, parts, p->slots});
+        p->list[kSmalls].push_back({id, 0, 0, 0, parts, slots});
         for (uint32_t q = 0; q < parts; ++q)
-            p->list[kSlabs].push_back({id, 0, 0, q * per, std::min((q + 1) * per, n), p->slots++});
+            p->list[kSlabs].push_back({id, 0, 0, q * per, std::min((q + 1) * per, n), slots++});
     }
+    p->partial = static_cast<uint64_t>(slots) * kNarrow * kNarrow;
 }
 
 // The tables of every matrix.
@@ -1380,24 +1401,22 @@ void fill_plan(gc_matrix_plan *p, const gc_plan *plan, const uint32_t *rows) {
         plan_narrow(p);
         return;
     }
-    // the tile shape and the schedules that the model finds fastest for one step
-    const Costs costs[2] = {{Small::kUnits, 1.3, 10.0, 0.03, 10.0}, {Large::kUnits, 2.25, 16.0, 0.12, 12.0}};  // us: Small, Large
+    // per product the tile shape and schedule that the model finds fastest
+    const Costs costs[2] = {{Small::kUnits, 1.18, 17.5, 0.02, 5.5}, {Large::kUnits, 2.33, 14.0, 0.04, 8.0}};
     constexpr List kProducts[3] = {kGram, kSquare, kApply};
     Schedule best[3];
-    for (int large = 0; large < 2; ++large) {
-        Schedule s[3];
-        double time = 0.0, before = 0.0;
-        for (int q = 0; q < 3; ++q) {
-            s[q] = schedule(tiles_of(p->mat, large ? Large::kTile : Small::kTile, kProducts[q]), costs[large]);
-            time += s[q].time;
-            before += best[q].time;
+    for (int q = 0; q < 3; ++q) {
+        const List l = kProducts[q];
+        best[q] = schedule(tiles_of(p->mat, Small::kTile, l), costs[0]);
+        Schedule s = schedule(tiles_of(p->mat, Large::kTile, l), costs[1]);
+        if (s.time < best[q].time) {
+            p->large[l] = true;
+            best[q] = std::move(s);
         }
-        if (large == 0 || time < before) {
-            p->large = large;
-            p->pairs = least >= kPairRows && s[0].time + s[2].time > 3.0 * s[1].time;
-            for (int q = 0; q < 3; ++q) best[q] = std::move(s[q]);
-        }
+        const uint64_t tile = p->large[l] ? Large::kTile : Small::kTile;
+        p->partial = std::max(p->partial, best[q].slots * tile * tile);
     }
+    p->pairs = least >= kPairRows && best[0].time + best[2].time > 3.0 * best[1].time;
     for (int q = 0; q < 3; ++q) {
         // workgroup b runs on XCD b % 8; units next to each other, with tiles next to
         // each other, share an XCD and its L2
@@ -1411,7 +1430,6 @@ void fill_plan(gc_matrix_plan *p, const gc_plan *plan, const uint32_t *rows) {
         }
         first.push_back(static_cast<uint32_t>(items.size()));
         p->list[kProducts[q] + 1] = std::move(best[q].joins);
-        p->slots = std::max(p->slots, best[q].slots);
     }
 }
 
