@@ -104,6 +104,7 @@ struct gc_matrix_plan {
     bool large[gc::kLists] = {};        // products: tiles of 256 x 256
     bool pairs = false;                 // two steps at a time
     bool narrow = false;                // every matrix has at most kNarrow rows
+    bool fused = false;                 // and the slabs' workgroups make B themselves
     std::vector<gc::MatDev> mat;
     std::vector<gc::Item> list[gc::kLists];
     std::vector<uint32_t> first[gc::kLists];  // products only
@@ -636,26 +637,36 @@ __device__ __forceinline__ void split_block(const GemmArgs &g, const MatDev &M, 
     }
 }
 
-// Eight split values, consecutive in a split row, to p (hi) and p + 32 (lo).
+// Eight split values' hi and lo.
+__device__ __forceinline__ void unsplit(const uint32_t (&v)[8], h8 &hi, h8 &lo) {
+    uint4 h, l;
+    h.x = __builtin_amdgcn_perm(v[1], v[0], 0x05040100u);
+    h.y = __builtin_amdgcn_perm(v[3], v[2], 0x05040100u);
+    h.z = __builtin_amdgcn_perm(v[5], v[4], 0x05040100u);
+    h.w = __builtin_amdgcn_perm(v[7], v[6], 0x05040100u);
+    l.x = __builtin_amdgcn_perm(v[1], v[0], 0x07060302u);
+    l.y = __builtin_amdgcn_perm(v[3], v[2], 0x07060302u);
+    l.z = __builtin_amdgcn_perm(v[5], v[4], 0x07060302u);
+    l.w = __builtin_amdgcn_perm(v[7], v[6], 0x07060302u);
+    hi = __builtin_bit_cast(h8, h);
+    lo = __builtin_bit_cast(h8, l);
+}
+
+// Consecutive in a split row, to p (hi) and p + 32 (lo).
 __device__ __forceinline__ void put_split(_Float16 *p, const uint32_t (&v)[8]) {
-    uint4 hi, lo;
-    hi.x = __builtin_amdgcn_perm(v[1], v[0], 0x05040100u);
-    hi.y = __builtin_amdgcn_perm(v[3], v[2], 0x05040100u);
-    hi.z = __builtin_amdgcn_perm(v[5], v[4], 0x05040100u);
-    hi.w = __builtin_amdgcn_perm(v[7], v[6], 0x05040100u);
-    lo.x = __builtin_amdgcn_perm(v[1], v[0], 0x07060302u);
-    lo.y = __builtin_amdgcn_perm(v[3], v[2], 0x07060302u);
-    lo.z = __builtin_amdgcn_perm(v[5], v[4], 0x07060302u);
-    lo.w = __builtin_amdgcn_perm(v[7], v[6], 0x07060302u);
-    *reinterpret_cast<uint4 *>(p) = hi;
-    *reinterpret_cast<uint4 *>(p + 32) = lo;
+    h8 hi, lo;
+    unsplit(v, hi, lo);
+    *reinterpret_cast<h8 *>(p) = hi;
+    *reinterpret_cast<h8 *>(p + 32) = lo;
 }
 
 // A block of split values along its columns: row j of the split matrix at `to`
-// with columns i, from (j0, i0) on.  8 lanes by 8 values of a split row.
+// with `cols` columns i, from (j0, i0) on.  8 lanes by 8 values of a split row.
 template <int kTeam>
-__device__ __forceinline__ void write_columns(_Float16 *to, uint32_t ld, const uint32_t *block, uint32_t i0, uint32_t j0) {
+__device__ __forceinline__ void write_columns(_Float16 *to, uint32_t ld, const uint32_t *block, uint32_t i0, uint32_t j0,
+                                              uint32_t cols = 64) {
     const uint32_t k = lane_id() & 7, r = lane_id() >> 3;
+    if (8 * k >= cols) return;
     to += static_cast<uint64_t>(j0 + r) * ld * 2 + split_at(i0 + 8 * k);
 #pragma unroll 2
     for (uint32_t t = kTeam > 1 ? wave_id() : 0; t < 8; t += kTeam) {
@@ -826,9 +837,14 @@ __global__ __launch_bounds__(kBlock) void orth_join_kernel(GemmArgs g) {
 //   slab   X' = B X for its slabs of 128 columns, T' written (X itself is not
 //          needed), and the sum of X' X'^T over them, left as a part
 //   small  per matrix: the parts added in order, A, and B = a I + b A + c A^2
-// after a first slab launch that makes X_0 from D.  (29 x 1600, 5 steps: 12
-// launches instead of 23.)  Latency bounds both, of operands loaded, multiplied
-// and written out once: 9 us a slab launch there and 8 us a small one.
+// after a first slab launch that makes X_0 from D.  Latency bounds both, of
+// operands loaded, multiplied and written out once, and of the instructions
+// fetched for it: what a matrix has no rows for is skipped tile by tile (95 us
+// at 29 x 1600 and 5 steps, then 84).  Where every matrix has at most 64 rows
+// and the slabs are at most kFusedSlabs, each slab's workgroup makes its B
+// itself and a step is one launch: 72 us for 29 x 1600 against 84, 83 against 88
+// for 16 of them (208 slabs), 203 against 205 for 8 of 64 x 4096 (256 slabs); 141
+// against 108 for 507 slabs, and 326 against 315 for 8 of 128 x 4096.
 constexpr uint32_t kNarrow = 128;
 enum Slab { kFirst, kMiddle, kLast };
 
@@ -837,30 +853,50 @@ __device__ __forceinline__ const uint32_t *block_of(const uint32_t *words, uint3
     return words + (2 * ib + (jb ^ ib)) * kBlockWords;
 }
 
+// A word of split value x.
+__device__ __forceinline__ uint32_t split_word(float x) {
+    _Float16 h, l;
+    split(x, h, l);
+    return __builtin_bit_cast(uint16_t, h) | (static_cast<uint32_t>(__builtin_bit_cast(uint16_t, l)) << 16);
+}
+
+__device__ __forceinline__ float joined(uint32_t word) {
+    return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(word))) +
+           static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(word >> 16)));
+}
+
+// put_tile of the split values.
+__device__ __forceinline__ void put_split_tile(uint32_t *block, uint32_t a, uint32_t b, f32x4 v) {
+    *reinterpret_cast<uint4 *>(block + block_at(16 * b + (lane_id() & 15), 4 * a + (lane_id() >> 4))) =
+        make_uint4(split_word(v[0]), split_word(v[1]), split_word(v[2]), split_word(v[3]));
+}
+
+// Rows j .. j + 7 of a block's column.
+__device__ __forceinline__ void column_of(const uint32_t *block, uint32_t col, uint32_t j, h8 &hi, h8 &lo) {
+    const uint4 x = *reinterpret_cast<const uint4 *>(block + block_at(col, j >> 2));
+    const uint4 y = *reinterpret_cast<const uint4 *>(block + block_at(col, (j >> 2) + 1));
+    unsplit({x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w}, hi, lo);
+}
+
 // g += Y Y^T for the wave's 64 x 64, Y's first 32 n columns in `words`. Y has m
 // rows: 16-row tiles behind them are neither read nor multiplied, their operands
-// stay zero and so do their sums (29 x 1600, 5 steps: 95 us instead of 101).
+// stay zero and so do their sums.
+template <bool kSymmetric>
 __device__ __forceinline__ void add_square(const uint32_t *words, uint32_t wr, uint32_t wc, uint32_t n, uint32_t m,
                                            f32x4 (&g)[4][4]) {
     const uint32_t ra = m - 64 * wr, rb = m - 64 * wc;
     for (uint32_t s = 0; s < n; ++s) {
         auto operand = [&](uint32_t ib, uint32_t t, h8 &hi, h8 &lo) {  // rows 16 t + lane % 16 of row block ib
-            const uint32_t *b = block_of(words, ib, s >> 1);
             const uint32_t r = 16 * t + (lane_id() & 15), j = 32 * (s & 1) + 8 * (lane_id() >> 4);
+            if (kSymmetric) {  // column r's rows, which stand together
+                column_of(block_of(words, s >> 1, ib), r, j, hi, lo);
+                return;
+            }
+            const uint32_t *b = block_of(words, ib, s >> 1);
             uint32_t v[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) v[u] = b[block_at(j + u, r >> 2) + (r & 3)];
-            uint4 h, l;
-            h.x = __builtin_amdgcn_perm(v[1], v[0], 0x05040100u);
-            h.y = __builtin_amdgcn_perm(v[3], v[2], 0x05040100u);
-            h.z = __builtin_amdgcn_perm(v[5], v[4], 0x05040100u);
-            h.w = __builtin_amdgcn_perm(v[7], v[6], 0x05040100u);
-            l.x = __builtin_amdgcn_perm(v[1], v[0], 0x07060302u);
-            l.y = __builtin_amdgcn_perm(v[3], v[2], 0x07060302u);
-            l.z = __builtin_amdgcn_perm(v[5], v[4], 0x07060302u);
-            l.w = __builtin_amdgcn_perm(v[7], v[6], 0x07060302u);
-            hi = __builtin_bit_cast(h8, h);
-            lo = __builtin_bit_cast(h8, l);
+            unsplit(v, hi, lo);
         };
         h8 qh[4] = {}, ql[4] = {};
 #pragma unroll
@@ -886,13 +922,6 @@ struct FirstArgs {
     const double *sums;
     float eps, pow2;
 };
-
-// A word of split value x.
-__device__ __forceinline__ uint32_t split_word(float x) {
-    _Float16 h, l;
-    split(x, h, l);
-    return __builtin_bit_cast(uint16_t, h) | (static_cast<uint32_t>(__builtin_bit_cast(uint16_t, l)) << 16);
-}
 
 // X_0's columns j0 .. j0 + 127 into `words`, zeros outside the matrix.
 __device__ __forceinline__ void first_slab(const MatDev &M, const FirstArgs &f, double scale, uint32_t j0, uint32_t *words) {
@@ -922,11 +951,136 @@ __device__ __forceinline__ void first_slab(const MatDev &M, const FirstArgs &f, 
     lds_barrier();
 }
 
-// Slabs [it.k0, it.k1) of a matrix.
-template <Slab kSlabKind>
-__global__ __launch_bounds__(kBlock) void orth_slab_kernel(GemmArgs g, FirstArgs f) {
+// B^T = diag I + add A + square A^2 of one matrix, split, as four blocks in
+// `words`, where A = acc * (the parts from `p` on, in order).  All waves of the
+// workgroup; ends with every block written but not yet visible to all.
+struct SmallArgs {
+    const float *partial;
+    float acc, add, square, diag;
+};
+
+// Every wave adds its 16 rows of each of the kBlocks blocks, those that exist;
+// one block's (kBlocks == 1) only as far as there are m rows.
+template <int kBlocks>
+__device__ __forceinline__ void sum_parts(const SmallArgs &g, uint32_t slot, uint32_t parts, uint32_t m, uint32_t *words) {
+    constexpr uint32_t kStep = kNarrow * kNarrow / 4;
+    const uint32_t w = __builtin_amdgcn_readfirstlane(wave_id());
+    const f32x4 *p = reinterpret_cast<const f32x4 *>(g.partial + static_cast<uint64_t>(slot) * kNarrow * kNarrow) +
+                     w * (4 * kWave) + lane_id();
+    f32x4 v[kBlocks][4];
+    const auto add = [&](int b0, int b1) {
+#pragma unroll
+        for (int q = 0; q < kBlocks; ++q)
+#pragma unroll
+            for (int b = b0; b < b1; ++b) v[q][b] = p[q * (16 * kWave) + b * kWave];
+#pragma unroll(kBlocks == 1 ? 4 : 2)
+        for (uint32_t s = 1; s < parts; ++s)
+#pragma unroll
+            for (int q = 0; q < kBlocks; ++q)
+#pragma unroll
+                for (int b = b0; b < b1; ++b) v[q][b] = v[q][b] + p[s * kStep + q * (16 * kWave) + b * kWave];
+    };
+#pragma unroll
+    for (int q = 0; q < kBlocks; ++q)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) v[q][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (kBlocks > 1) {
+        add(0, 4);
+    } else if (16 * w < m) {
+        if (m > 32) add(0, 4);
+        else add(0, 2);
+    }
+#pragma unroll
+    for (int q = 0; q < kBlocks; ++q)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) put_split_tile(words + q * kBlockWords, w, b, v[q][b] * g.acc);
+}
+
+template <int kBlocks>
+__device__ __forceinline__ void small_poly(const SmallArgs &g, const MatDev &M, uint32_t slot, uint32_t parts, uint32_t *words) {
+    const uint32_t w = __builtin_amdgcn_readfirstlane(wave_id());
+    const uint32_t wr = w / 2, wc = (w ^ wr) & 1;
+    const bool active = 64 * wr < M.m && 64 * wc < M.m;
+    sum_parts<kBlocks>(g, slot, parts, M.m, words);
+    lds_barrier();
+    f32x4 A2[4][4];
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) A2[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (active) add_square<true>(words, wr, wc, (M.m + 31) / 32, M.m, A2);
+    lds_barrier();  // every wave has read A
+    if (!active) return;
+    uint32_t *block = words + w * kBlockWords;
+    const uint32_t c = lane_id() & 15, r = 4 * (lane_id() >> 4);
+    const bool diagonal = wr == wc;
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            if (64 * wr + 16 * a >= M.m || 64 * wc + 16 * b >= M.m) continue;  // zeros, as A's
+            const uint4 v = *reinterpret_cast<const uint4 *>(block + block_at(16 * b + c, 4 * a + (lane_id() >> 4)));
+            f32x4 x{joined(v.x), joined(v.y), joined(v.z), joined(v.w)};
+#pragma unroll
+            for (uint32_t u = 0; u < 4; ++u) {
+                x[u] = A2[a][b][u] * g.square + g.add * x[u];
+                if (a == b && diagonal && r + u == c && 64 * wr + 16 * a + c < M.m) x[u] = x[u] + g.diag;
+            }
+            put_split_tile(block, a, b, x);
+        }
+}
+
+// All columns of the slab's 128 rows of T into LDS, stage by stage as load_stage
+// has them.
+__device__ __forceinline__ void load_slab(const _Float16 *T, uint32_t stages, char *__restrict__ lds) {
+    const uint32_t lane = lane_id(), row = __builtin_amdgcn_readfirstlane(wave_id()) * 32;
+    const uint32_t part = (lane & 7) ^ (lane >> 4);
+    const int32_t odd = part & 4 ? -64 : 64;
+    const char *from = reinterpret_cast<const char *>(T + static_cast<uint64_t>(row + (lane >> 3)) * (2 * kNarrow)) + part * 16;
+    for (uint32_t s = 0; s < stages; ++s)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            __builtin_amdgcn_global_load_lds((GlobalChar *)(from + s * 128 + q * (32 * kNarrow) + (q & 1 ? odd : 0)),
+                                             (LdsChar *)(lds + s * (128 * kNarrow) + row * 128 + q * 1024), 16, 0, 0);
+}
+
+// acc += B X for the wave's 64 x 64, of m rows: B^T's blocks in `words`, the
+// slab of T as load_slab left it.
+__device__ __forceinline__ void slab_product(const uint32_t *__restrict__ words, const char *__restrict__ lds, uint32_t m,
+                                             uint32_t pr, uint32_t qr, f32x4 (&acc)[4][4]) {
+    const uint32_t stages = (m + 31) / 32;
+    const uint32_t row = lane_id() & 15, part = lane_id() >> 4;
+    const uint32_t hi = row * 128 + ((part ^ ((row >> 1) & 7)) << 4), lo = hi ^ 64;
+    for (uint32_t s = 0; s < stages; ++s) {
+        const char *q = lds + s * (128 * kNarrow) + qr * 128;
+        const uint32_t *block = block_of(words, s >> 1, pr >> 6);
+        h8 qh[4], ql[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            qh[b] = *reinterpret_cast<const h8 *>(q + b * 2048 + hi);
+            ql[b] = *reinterpret_cast<const h8 *>(q + b * 2048 + lo);
+        }
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+            if (pr + 16 * a >= m) break;
+            h8 ph, pl;
+            column_of(block, 16 * a + row, 32 * (s & 1) + 8 * part, ph, pl);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ph, ql[b], acc[a][b], 0, 0, 0);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(pl, qh[b], acc[a][b], 0, 0, 0);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ph, qh[b], acc[a][b], 0, 0, 0);
+        }
+    }
+}
+
+// Slabs [it.k0, it.k1) of a matrix.  kFused: B comes from the it.j parts from
+// it.i on instead of g.P.
+template <Slab kSlabKind, bool kFused>
+__global__ __launch_bounds__(kBlock, kFused ? 1 : 2) void orth_slab_kernel(GemmArgs g, FirstArgs f, SmallArgs small) {
     using C = Shape<Small>;
-    __shared__ __attribute__((aligned(128))) char lds[C::kLds];
+    __shared__ __attribute__((aligned(128))) char lds[C::kLds + (kFused ? 4 * kBlockWords : 0)];
     uint32_t *words = reinterpret_cast<uint32_t *>(lds);
     const Item it = g.items[blockIdx.x];
     const MatDev M = g.mats[it.mat];
@@ -939,6 +1093,12 @@ __global__ __launch_bounds__(kBlock) void orth_slab_kernel(GemmArgs g, FirstArgs
         double sum = 0.0;
         for (uint32_t c = threadIdx.x; c < M.nchunk; c += kBlock) sum += f.sums[M.chunk0 + c];
         scale = norm_scale(block_tree_sum(sum), f.eps) * static_cast<double>(f.pow2);
+    }
+    const uint32_t read = (M.m + 31) & ~31u;  // columns of T that a product reads
+    uint32_t *bwords = words + 4 * kBlockWords;
+    if (kFused) {
+        load_slab(g.Q + M.x + static_cast<uint64_t>(it.k0) * kNarrow * M.mp * 2, (M.m + 31) / 32, lds);
+        small_poly<1>(small, M, it.i, it.j, bwords);
     }
     f32x4 sums[4][4];
 #pragma unroll
@@ -957,22 +1117,29 @@ __global__ __launch_bounds__(kBlock) void orth_slab_kernel(GemmArgs g, FirstArgs
 #pragma unroll
                 for (int b = 0; b < 4; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             const uint32_t all = (M.m + 31) / 32;
-            all_stages<C>(lds, g.P + M.a, M.mp, kNarrow, g.Q + M.x + static_cast<uint64_t>(j0) * M.mp * 2, M.mp, kNarrow,
-                          Stages{all, 0, all}, active, pr, qr, acc);
+            const _Float16 *T = g.Q + M.x + static_cast<uint64_t>(j0) * M.mp * 2;
+            if (kFused) {
+                if (s > it.k0) load_slab(T, all, lds);
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the slab has landed
+                lds_barrier();
+                if (active) slab_product(bwords, lds, M.m, pr, qr, acc);
+            } else all_stages<C>(lds, g.P + M.a, M.mp, kNarrow, T, M.mp, kNarrow, Stages{all, 0, all}, active, pr, qr, acc);
             lds_barrier();
             if (active) {
 #pragma unroll
-                for (int a = 0; a < 4; ++a)
+                for (int a = 0; a < 4; ++a) {
+                    if (pr + 16 * a >= read) break;
 #pragma unroll
                     for (int b = 0; b < 4; ++b) put_tile(block, a, b, acc[a][b]);
+                }
                 if (kSlabKind == kLast) write_block<kOut, 1>(g, M, block, pr, j0 + qr, false);
                 else split_block<kNext, 1>(g, M, block, pr, j0 + qr);
             }
             if (kSlabKind == kLast) continue;
             lds_barrier();
         }
-        if (active) write_columns<1>(g.Tn + M.x, M.mp, block, pr, j0 + qr);
-        if (squares) add_square(words, wr, wc, 4, M.m, sums);
+        if (active) write_columns<1>(g.Tn + M.x, M.mp, block, pr, j0 + qr, read - pr);
+        if (squares) add_square<false>(words, wr, wc, 4, M.m, sums);
     }
     if (kSlabKind == kLast || !squares) return;
     f32x4 *p = reinterpret_cast<f32x4 *>(g.partial + static_cast<uint64_t>(it.slot) * kNarrow * kNarrow) + w * (16 * kWave) + lane_id();
@@ -982,70 +1149,16 @@ __global__ __launch_bounds__(kBlock) void orth_slab_kernel(GemmArgs g, FirstArgs
         for (int b = 0; b < 4; ++b) p[(a * 4 + b) * kWave] = sums[a][b];
 }
 
-// Per matrix: A = acc * (the it.k1 parts from it.slot on, in order), and
-// B = diag I + add A + square A^2 into g.S.
-__global__ __launch_bounds__(kBlock) void orth_small_kernel(GemmArgs g, float square) {
+// Per matrix: B into g.S.
+__global__ __launch_bounds__(kBlock) void orth_small_kernel(GemmArgs g, SmallArgs a) {
     __shared__ __attribute__((aligned(128))) uint32_t words[4 * kBlockWords];
     const Item it = g.items[blockIdx.x];
     const MatDev M = g.mats[it.mat];
     const uint32_t w = __builtin_amdgcn_readfirstlane(wave_id());
     const uint32_t wr = w / 2, wc = (w ^ wr) & 1;
-    const bool active = 64 * wr < M.m && 64 * wc < M.m;
-    constexpr uint32_t kStep = kNarrow * kNarrow / 4;
-    // every wave adds a quarter of each block that exists
-    for (uint32_t q = 0; q < 4; ++q) {
-        if (64 * (q / 2) >= M.m || 64 * ((q ^ (q / 2)) & 1) >= M.m) continue;
-        const f32x4 *p = reinterpret_cast<const f32x4 *>(g.partial + static_cast<uint64_t>(it.slot) * kNarrow * kNarrow) +
-                         q * (16 * kWave) + w * (4 * kWave) + lane_id();
-        f32x4 v[4];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) v[b] = p[b * kWave];
-#pragma unroll 4
-        for (uint32_t s = 1; s < it.k1; ++s)
-#pragma unroll
-            for (int b = 0; b < 4; ++b) v[b] = v[b] + p[s * kStep + b * kWave];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) put_tile(words + q * kBlockWords, w, b, v[b] * g.acc);
-    }
-    lds_barrier();
-    uint32_t *block = words + w * kBlockWords;
-    auto place = [&](int a, int b) { return block + block_at(16 * b + (lane_id() & 15), 4 * a + (lane_id() >> 4)); };
-    f32x4 A[4][4];
-    if (active) {
-#pragma unroll
-        for (int a = 0; a < 4; ++a)
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                uint32_t *at = place(a, b);
-                A[a][b] = *reinterpret_cast<const f32x4 *>(at);
-                *reinterpret_cast<uint4 *>(at) = make_uint4(split_word(A[a][b][0]), split_word(A[a][b][1]),
-                                                            split_word(A[a][b][2]), split_word(A[a][b][3]));
-            }
-    }
-    lds_barrier();
-    f32x4 A2[4][4];
-#pragma unroll
-    for (int a = 0; a < 4; ++a)
-#pragma unroll
-        for (int b = 0; b < 4; ++b) A2[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    if (active) add_square(words, wr, wc, (M.m + 31) / 32, M.m, A2);
-    lds_barrier();  // every wave has read A
-    if (!active) return;
-#pragma unroll
-    for (int a = 0; a < 4; ++a)
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const uint32_t i = 64 * wr + 16 * a + 4 * (lane_id() >> 4), j = 64 * wc + 16 * b + (lane_id() & 15);
-            uint32_t y[4];
-#pragma unroll
-            for (uint32_t u = 0; u < 4; ++u) {
-                float x = A2[a][b][u] * square + g.add * A[a][b][u];
-                if (i + u == j && j < M.m) x = x + g.diag;
-                y[u] = split_word(x);
-            }
-            *reinterpret_cast<uint4 *>(place(a, b)) = make_uint4(y[0], y[1], y[2], y[3]);
-        }
-    write_columns<1>(g.S + M.a, M.mp, block, 64 * wr, 64 * wc);
+    if (M.m <= 64) small_poly<1>(a, M, it.slot, it.k1, words);
+    else small_poly<4>(a, M, it.slot, it.k1, words);
+    if (64 * wr < M.m && 64 * wc < M.m) write_columns<1>(g.S + M.a, M.mp, words + w * kBlockWords, 64 * wr, 64 * wc);
 }
 
 // --------------------------------------------------------------- host side
@@ -1105,26 +1218,30 @@ gc_status narrow_steps(const char *fn, const gc_matrix_plan *p, const OrthDev &d
     g.lr = lr;
     g.shape = shape;
     FirstArgs f{src, w.sums, o.eps, pow2(1.0, sc[0].ex)};
+    // a fused step reads the parts of the step before while it writes its own
+    float *const parts[2] = {w.partial, w.partial + (p->fused ? p->partial / 2 : 0)};
     int cur = 0;
     g.items = d.list[kSlabs];
     g.Tn = w.T[0];
-    GC_LAUNCH("orth_slab", stream, orth_slab_kernel<kFirst><<<slabs, kBlock, 0, stream>>>(g, f));
+    GC_LAUNCH("orth_slab", stream, orth_slab_kernel<kFirst, false><<<slabs, kBlock, 0, stream>>>(g, f, SmallArgs{}));
     for (int k = 0; k < o.steps; ++k) {
         const Scales &s = sc[k];
-        g.items = d.list[kSmalls];
-        g.acc = pow2(1.0, s.ea - 2 * s.ex);
-        g.add = pow2(o.coef[k][1], s.eb - s.ea);
-        g.diag = pow2(o.coef[k][0], s.eb);
-        GC_LAUNCH("orth_small", stream,
-                  orth_small_kernel<<<smalls, kBlock, 0, stream>>>(g, pow2(o.coef[k][2], s.eb - 2 * s.ea)));
+        const SmallArgs b{parts[cur], pow2(1.0, s.ea - 2 * s.ex), pow2(o.coef[k][1], s.eb - s.ea),
+                          pow2(o.coef[k][2], s.eb - 2 * s.ea), pow2(o.coef[k][0], s.eb)};
+        if (!p->fused) {
+            g.items = d.list[kSmalls];
+            GC_LAUNCH("orth_small", stream, orth_small_kernel<<<smalls, kBlock, 0, stream>>>(g, b));
+        }
         const bool last = k + 1 == o.steps;
         g.items = d.list[kSlabs];
         g.acc = pow2(1.0, (last ? 0 : sc[k + 1].ex) - s.eb - s.ex);
         g.Q = w.T[cur];
-        g.Tn = w.T[cur ^ 1];
         cur ^= 1;
-        if (last) GC_LAUNCH("orth_slab", stream, orth_slab_kernel<kLast><<<slabs, kBlock, 0, stream>>>(g, f));
-        else GC_LAUNCH("orth_slab", stream, orth_slab_kernel<kMiddle><<<slabs, kBlock, 0, stream>>>(g, f));
+        g.Tn = w.T[cur];
+        g.partial = parts[cur];
+        const auto kernel = p->fused ? (last ? orth_slab_kernel<kLast, true> : orth_slab_kernel<kMiddle, true>)
+                                     : (last ? orth_slab_kernel<kLast, false> : orth_slab_kernel<kMiddle, false>);
+        GC_LAUNCH("orth_slab", stream, kernel<<<slabs, kBlock, 0, stream>>>(g, f, b));
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return hip_error(e, fn);
@@ -1343,8 +1460,11 @@ constexpr uint32_t kPairRows = 512;
 // Matrices of few rows: slabs per workgroup so that they fill the units once
 // and no matrix has more than kMaxParts parts, which one workgroup adds.
 constexpr uint64_t kMaxParts = 16;
+// Up to here, and with 64 rows at most, a slab's workgroup makes its B itself
+// (times at the slab kernel's section).
+constexpr uint64_t kFusedSlabs = 256;
 
-void plan_narrow(gc_matrix_plan *p) {
+void plan_narrow(gc_matrix_plan *p, uint32_t most) {
     p->narrow = true;
     uint64_t slabs = 0;
     uint32_t slots = 0;
@@ -1353,11 +1473,13 @@ void plan_narrow(gc_matrix_plan *p) {
         const uint32_t n = p->mat[id].np / kNarrow;
         const uint32_t per = static_cast<uint32_t>(std::max(ceil_div(n, kMaxParts), ceil_div(slabs, Small::kUnits)));
         const uint32_t parts = static_cast<uint32_t>(ceil_div(n, per));
-        p->list[kSmalls].push_back({id, 0, 0, 0, parts, slots});
+        const uint32_t slot = slots;
+        p->list[kSmalls].push_back({id, 0, 0, 0, parts, slot});
         for (uint32_t q = 0; q < parts; ++q)
-            p->list[kSlabs].push_back({id, 0, 0, q * per, std::min((q + 1) * per, n), slots++});
+            p->list[kSlabs].push_back({id, slot, parts, q * per, std::min((q + 1) * per, n), slots++});
     }
-    p->partial = static_cast<uint64_t>(slots) * kNarrow * kNarrow;
+    p->fused = most <= 64 && slabs <= kFusedSlabs;
+    p->partial = static_cast<uint64_t>(slots) * kNarrow * kNarrow * (p->fused ? 2 : 1);
 }
 
 // The tables of every matrix.
@@ -1398,7 +1520,7 @@ void fill_plan(gc_matrix_plan *p, const gc_plan *plan, const uint32_t *rows) {
         most = std::max(most, M.m);
     }
     if (most <= kNarrow) {
-        plan_narrow(p);
+        plan_narrow(p, most);
         return;
     }
     // per product the tile shape and schedule that the model finds fastest

@@ -9,6 +9,7 @@ import torch
 from gradient_compression_dnn_amd import binding as B
 from gradient_compression_dnn_amd import workloads as W
 from tests.gpu_util import dev, say
+from tests.test_gpu_orth import Mats, check, matrix, to_dev
 
 pytestmark = pytest.mark.gpu
 
@@ -156,3 +157,23 @@ def test_one_token_again_and_again():
         B.gc_embed_message(plan, 0, rows, dy, tokens, 0.5, msg, ws)
         idx, val, off, _ = msg.host()
         assert np.array_equal(idx, np.arange(4 * cols, 5 * cols)) and (val == 0.5 * n).all() and off[1] == cols
+
+
+@pytest.mark.parametrize("shapes", [
+    [(1, 1)], [(16, 17)], [(33, 129)], [(64, 64)],          # one slab, whole and part tiles of 16 rows
+    [(5, 6000)], [(2100, 64)], [(17, 2049)],                # several slabs a workgroup, 16 parts
+    [(40, 2100)] * 20, [(64, 300), (3, 70)] * 90,           # more slabs than compute units
+    [(64, 700), (65, 200)],                                 # a row more than a block has
+])
+@pytest.mark.parametrize("steps", [1, 2, 5])
+def test_few_rows(shapes, steps):
+    rng = np.random.default_rng(61)
+    ms = Mats(shapes)
+    mats = [matrix(rng, *s, ("gauss", "heavy")[k % 2]) for k, s in enumerate(shapes)]
+    O = torch.full((ms.n,), 5.0, device=dev())
+    say(f"few rows {shapes[:2]} x {len(shapes)} steps {steps}")
+    B.gc_orthogonalize(ms.m, to_dev(ms.flat(mats, rng)), O, B.orth_options(steps), ms.ws())
+    got = O.cpu().numpy()
+    for o, D in zip(ms.parts(got), mats):
+        check(o, D, steps)
+    assert (ms.outside(got) == 5.0).all()
