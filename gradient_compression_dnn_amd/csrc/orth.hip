@@ -748,11 +748,18 @@ template <Kind kKind, class C>
 __global__ __launch_bounds__(C::kThreads) void orth_gemm_kernel(GemmArgs g) {
     __shared__ __attribute__((aligned(128))) char lds[C::kLds];
     const uint32_t w = __builtin_amdgcn_readfirstlane(wave_id()), lane = lane_id();
-    const uint32_t end = g.first[blockIdx.x + 1];
-    for (uint32_t at = g.first[blockIdx.x]; at < end; ++at) {
-        const Item it = g.items[at];
-        const MatDev M = g.mats[it.mat];
+    const uint32_t begin = g.first[blockIdx.x], end = g.first[blockIdx.x + 1];
+    if (begin == end) return;
+    Item next = g.items[begin];
+    MatDev next_mat = g.mats[next.mat];
+    for (uint32_t at = begin; at < end; ++at) {
+        const Item it = next;
+        const MatDev M = next_mat;
         lds_barrier();  // every wave is done with the LDS of the item before
+        if (at + 1 < end) {  // read while this one is multiplied
+            next = g.items[at + 1];
+            next_mat = g.mats[next.mat];
+        }
         const uint32_t i0 = it.i * C::kTile, j0 = it.j * C::kTile;
         // rows of this tile that exist (multiples of 128)
         const uint32_t rows_p = min(uint32_t(C::kTile), M.mp - i0), rows_q = min(uint32_t(C::kTile), (kKind == kSym ? M.mp : M.np) - j0);
