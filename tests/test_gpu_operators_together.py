@@ -177,3 +177,27 @@ def test_few_rows(shapes, steps):
     for o, D in zip(ms.parts(got), mats):
         check(o, D, steps)
     assert (ms.outside(got) == 5.0).all()
+
+
+@pytest.mark.parametrize("rows,cols,n", [
+    (3000, 30, 257), (3000, 30, 1024), (3000, 30, 1025),  # clearing halved between two launches, and not
+    (7, 9001, 700), (20000, 3, 1000), (40000, 1, 300),    # rows longer than a workgroup clears, and many in one
+    (33, 513, 900), (1, 32768, 400), (2, 16384, 400),
+])
+def test_rows_without_tokens_are_cleared(rows, cols, n):
+    """Every element of a used buffer is written; nothing beside the segment is."""
+    rng = np.random.default_rng(rows + n)
+    plan = B.Plan(W.make_table([5, rows * cols, 6], [1] * 3))
+    for share in (1.0, 0.02):  # of the rows have tokens
+        keys = rng.integers(0, max(1, int(rows * share)), n)
+        keys[::7] = -1
+        dy = rng.integers(-8, 9, (n, cols)).astype(np.float32)  # whole numbers: exact in any order
+        want = np.zeros((rows, cols), np.float32)
+        np.add.at(want, keys[keys >= 0], dy[keys >= 0])
+        g = torch.full((plan.n_total,), 7.0, device=dev())
+        ws = torch.full((B.gc_embed_workspace_bytes(plan, 1, rows, n),), 0xFF, dtype=torch.uint8, device=dev())
+        say(f"clear {rows} x {cols}, {n} tokens, share {share}")
+        B.gc_embed_grad(plan, 1, rows, to_dev(dy), torch.from_numpy(keys).to(dev()), 1.0, g, False, ws)
+        got = g.cpu().numpy()
+        assert np.array_equal(got[5:-6].reshape(rows, cols), want)
+        assert (got[:5] == 7).all() and (got[-6:] == 7).all()
