@@ -72,7 +72,8 @@ struct MatDev {
 
 // A workgroup's work: a matrix and a tile (norm: a chunk); products: its
 // stages [k0, k1) of 32 columns of the common index, and where a part of a
-// split tile goes; joins: k1 parts from `slot` on.
+// split tile goes; joins: k1 parts from `slot` on; slabs: [k0, k1) of a matrix,
+// whose j parts begin at slot i, and the slot of their own.
 struct Item {
     uint32_t mat, i, j, k0, k1, slot;
 };
@@ -87,7 +88,6 @@ enum List { kChunks, kTiles, kGram, kGramJoin, kSquare, kSquareJoin, kApply, kAp
 
 // Products are planned for the workgroups that 256 compute units hold; unit u
 // has items [first[u], first[u + 1]) of its list.
-
 struct OrthDev {
     const MatDev *mat;
     const Item *list[kLists];
@@ -958,9 +958,10 @@ __device__ __forceinline__ void first_slab(const MatDev &M, const FirstArgs &f, 
     lds_barrier();
 }
 
-// B^T = diag I + add A + square A^2 of one matrix, split, as four blocks in
-// `words`, where A = acc * (the parts from `p` on, in order).  All waves of the
-// workgroup; ends with every block written but not yet visible to all.
+// B^T = diag I + add A + square A^2 of one matrix, split, as kBlocks blocks in
+// `words`, where A = acc * (the `parts` parts from `slot` on, in order).  All
+// waves of the workgroup; ends with every block written but not yet visible to
+// all.
 struct SmallArgs {
     const float *partial;
     float acc, add, square, diag;
