@@ -170,11 +170,13 @@ struct Lists {
 };
 
 // Workgroup x ranks tokens [64 x, 64 x + 64) inside their tile; workgroups
-// from `nrank` on clear the dense gradient's first nfill elements meanwhile, 16 x
-// 1024 each.  A row that has tokens is written again by the sum, one
+// from `nrank` on clear the dense gradient meanwhile (nfill > 0), 16 x 1024
+// elements each.  A row that has tokens is written again by the sum, one
 // launch later.  kSet is the tokens ranked together.  LDS reads bound it, one
 // of 16 bytes for 4 comparisons of a wave's 64 tokens: 8 us at 32,000 tokens
-// in tiles of kTile.
+// in tiles of kTile; with the clearing of 15 M elements 11 us.  (Half of the
+// clearing beside the sum instead, with the rows that have a token left out:
+// 19.6 us against 18.7 at 700 tokens into 10,000 x 1,500, 29 against 24 at 3,000.)
 template <class Tok, uint32_t kSet>
 __global__ __launch_bounds__(kRankThreads) void embed_rank_kernel(const Tok *__restrict__ tokens, uint32_t n,
                                                                   uint32_t rows, uint32_t *__restrict__ key_out,
@@ -450,8 +452,7 @@ __device__ __forceinline__ void put_row(const SumOut &o, uint32_t row, uint32_t 
 // piece is a run's part of the block: wave w takes the block's pieces w,
 // w + waves, ... and adds each one's rows in order.  part[2 b] holds the sum of
 // a run that comes from the block before, part[2 b + 1] of one that begins
-// here and goes on; the latter is listed for the join.  Workgroups from nsum on
-// clear the rows without a token among elements [cut, fill).
+// here and goes on; the latter is listed for the join.
 // Memory bounds it: 32,000 rows of 1,500 fp16 columns added to g take 37 us, of
 // 32 that the bytes of dy and g need at a large copy's rate.
 // The body is one short loop: unrolled over the 16 positions it ran 3 times
@@ -462,49 +463,6 @@ __device__ __forceinline__ void put_row(const SumOut &o, uint32_t row, uint32_t 
 constexpr uint32_t kJoinWaves = 16;
 constexpr int kLaneCols = 4;
 constexpr uint32_t kSlab = kWave * kLaneCols;
-
-// Clears the workgroup's 16 elements per thread from `base` on, below `end`, of
-// rows without a token: of the batch's n keys, those in reach are marked in
-// LDS.
-constexpr uint32_t kFill = 1024 * 16;  // elements cleared per workgroup of 1024 threads, the largest
-
-// Batches of at most kHalves tokens clear half of the gradient beside the sum:
-// 18.6 us instead of 20.6 at 700 tokens and 10,000 x 1,500, 44 instead of 51 at
-// 1,000 and 50,000 x 1,024; at 2,000 tokens and 100,000 x 64 it would be 19.1
-// instead of 16.7, at 4,000 and 50,000 x 256 25.8 instead of 22.
-constexpr uint32_t kHalves = 1024;
-
-template <class Key>
-__device__ __forceinline__ void clear_free(float *__restrict__ g, uint64_t base, uint64_t end, uint32_t cols, uint32_t n,
-                                           uint32_t rows, Key key) {
-    __shared__ uint32_t held[kFill / 32 + 1];
-    __shared__ uint32_t any;
-    const uint32_t t = threadIdx.x, threads = blockDim.x;
-    const uint32_t cnt = static_cast<uint32_t>(umin64(end - base, 16 * threads));
-    const BufRsrc r = chunk_buf(g + base, cnt);
-    const uint32_t r0 = static_cast<uint32_t>(base / cols), rem = static_cast<uint32_t>(base - static_cast<uint64_t>(r0) * cols);
-    const uint32_t span = (rem + cnt - 1) / cols + 1;  // rows, at most kFill + 1
-    for (uint32_t i = t; i <= kFill / 32; i += threads) held[i] = 0;
-    if (t == 0) any = 0;
-    __syncthreads();
-    for (uint32_t i = t; i < n; i += threads) {
-        const uint32_t k = key(i);
-        if (k < rows && k - r0 < span) {
-            atomicOr(&held[(k - r0) / 32], 1u << ((k - r0) % 32));
-            any = 1;
-        }
-    }
-    __syncthreads();
-    if (!any) {
-#pragma unroll
-        for (uint32_t j = 0; j < 4; ++j) clear4(r, (j * threads + t) * 4);
-        return;
-    }
-    for (uint32_t x = t; x < cnt; x += threads) {
-        const uint32_t row = (rem + x) / cols;
-        if (!(held[row / 32] >> (row % 32) & 1)) g[base + x] = 0.0f;
-    }
-}
 
 // acc += rows dy[pos[l]] for lanes l in [from, to) of the wave's lpos.  Two
 // rows ahead: one took 43 us at 32,000 tokens by 1,500 fp16 columns where two
@@ -534,14 +492,8 @@ __global__ __launch_bounds__(1024) void embed_sum_kernel(const typename T::Store
                                                          const uint32_t *__restrict__ key,
                                                          const uint32_t *__restrict__ pos, uint32_t n, uint32_t rows,
                                                          uint32_t cols, uint32_t slabs, float scale, SumOut out,
-                                                         float *__restrict__ part, uint32_t ldpart, Lists lists,
-                                                         uint32_t nsum, uint64_t cut, uint64_t fill) {
+                                                         float *__restrict__ part, uint32_t ldpart, Lists lists) {
     constexpr int N = kLaneCols;
-    if (blockIdx.x >= nsum) {
-        clear_free(out.g, cut + static_cast<uint64_t>(blockIdx.x - nsum) * (16 * blockDim.x), fill, cols, n, rows,
-                   [&](uint32_t i) { return key[i]; });
-        return;
-    }
     const uint32_t waves = blockDim.x / kWave, w = __builtin_amdgcn_readfirstlane(wave_id());
     const uint32_t b = blockIdx.x / slabs, slab = blockIdx.x - b * slabs;
     const uint32_t c = (slab * kWave + lane_id()) * N;
@@ -592,6 +544,8 @@ __global__ __launch_bounds__(1024) void embed_sum_kernel(const typename T::Store
 constexpr uint32_t kSmall = 256;
 constexpr int kSmallThreads = 1024;
 constexpr uint32_t kSmallWaves = kSmallThreads / kWave;
+constexpr uint32_t kFill = kSmallThreads * 16;  // elements cleared per workgroup
+static_assert(kFill / 32 < kSmallThreads, "a thread per word of held rows");
 static_assert(kSmall <= kSpan * kJoinWaves, "a run of a small batch has at most kJoinWaves partial sums");
 
 template <class T, class Tok>
@@ -606,8 +560,35 @@ __global__ __launch_bounds__(kSmallThreads) void embed_small_kernel(const typena
     __shared__ uint32_t raw[kSmall], key[kSmall + 1], pos[kSmall], part[kParts][kSmall], run_at[kSmall + 1], nruns, live;
     const uint32_t t = threadIdx.x, e = t % kSmall, q = t / kSmall;
     if (blockIdx.x >= nsum) {
-        clear_free(out.g, static_cast<uint64_t>(blockIdx.x - nsum) * kFill, fill, cols, n, rows,
-                   [&](uint32_t i) { return token_key(tokens, i, rows); });
+        // 16 elements per thread of rows without a token; `held` marks those
+        // with one among the rows of this workgroup's elements
+        const uint64_t base = static_cast<uint64_t>(blockIdx.x - nsum) * kFill;
+        const uint32_t cnt = static_cast<uint32_t>(umin64(fill - base, kFill));
+        const BufRsrc r = chunk_buf(out.g + base, cnt);
+        const uint32_t r0 = static_cast<uint32_t>(base / cols), rem = static_cast<uint32_t>(base - static_cast<uint64_t>(r0) * cols);
+        const uint32_t span = (rem + cnt - 1) / cols + 1;  // rows, at most kFill + 1
+        __shared__ uint32_t held[kFill / 32 + 1];
+        __shared__ uint32_t any;
+        if (t <= kFill / 32) held[t] = 0;
+        if (t == 0) any = 0;
+        __syncthreads();
+        if (t < n) {
+            const uint32_t k = token_key(tokens, t, rows);
+            if (k < rows && k - r0 < span) {
+                atomicOr(&held[(k - r0) / 32], 1u << ((k - r0) % 32));
+                any = 1;
+            }
+        }
+        __syncthreads();
+        if (!any) {
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j) clear4(r, (j * kSmallThreads + t) * 4);
+            return;
+        }
+        for (uint32_t x = t; x < cnt; x += kSmallThreads) {
+            const uint32_t row = (rem + x) / cols;
+            if (!(held[row / 32] >> (row % 32) & 1)) out.g[base + x] = 0.0f;
+        }
         return;
     }
     if (t < kSmall) raw[t] = t < n ? token_key(tokens, t, rows) : 0xFFFFFFFFu;
@@ -848,20 +829,14 @@ gc_status embed_backward(const char *fn, const gc_plan *plan, int seg, uint32_t 
                          SumOut out, uint64_t fill, uint32_t *seg_off, void *ws, hipStream_t stream) {
     const uint32_t n = static_cast<uint32_t>(n64);
     EmbedWs w = embed_ws(align256(ws), n64, cols);
-    // clearing in the rank's launch; a short batch, which ranks and sums in less time, halves it between the two
-    const uint64_t cut = n > kHalves ? fill : fill / 2 / kFill * kFill;
-    const uint64_t nrank = ceil_div(n, kWave), nclear = ceil_div(cut, kFill);
+    const uint64_t nfill = ceil_div(fill, kRankThreads * 16), nrank = ceil_div(n, kWave);
     const uint32_t blocks = static_cast<uint32_t>(ceil_div(n, kSpan));
     const uint32_t slabs = static_cast<uint32_t>(ceil_div(cols, kSlab));
     const uint64_t sums = static_cast<uint64_t>(blocks) * slabs;
-    // one piece per wave while the chip holds them all at once, else 4 waves a block
-    const uint32_t threads = sums <= 512 ? 1024 : kBlock;
-    const uint64_t nfree = ceil_div(fill - cut, 16 * threads);
-    if (nrank + nclear > max_grid(kRankThreads) || sums + nfree > max_grid(threads))
+    if (nrank + nfill > max_grid(kRankThreads) || sums > max_grid(kBlock))
         return set_error(GC_ERANGE, std::string(fn) + ": more workgroups than a launch has");
     if (n <= kSmall) {
         const uint32_t nsum = static_cast<uint32_t>(ceil_div(n, kSmallWaves)) * slabs;
-        const uint64_t nfill = ceil_div(fill, kFill);
         with_type(type, [&](auto t) {
             with_tokens(token_type, [&](auto tok) {
                 using T = decltype(t);
@@ -880,9 +855,9 @@ gc_status embed_backward(const char *fn, const gc_plan *plan, int seg, uint32_t 
         using Tok = decltype(tok);
         const auto kernel = n <= kOneTile ? embed_rank_kernel<Tok, kOneTile> : embed_rank_kernel<Tok, kTile>;
         GC_LAUNCH("embed_rank", stream,
-                  kernel<<<static_cast<unsigned>(nrank + nclear), kRankThreads, 0, stream>>>(
+                  kernel<<<static_cast<unsigned>(nrank + nfill), kRankThreads, 0, stream>>>(
                       static_cast<const Tok *>(tokens), n, rows, w.key[0], w.pos[0], w.lists.count,
-                      static_cast<uint32_t>(nrank), out.g, cut));
+                      static_cast<uint32_t>(nrank), out.g, fill));
     });
     int cur = 0;
     for (uint64_t run = n <= kOneTile ? kOneTile : kTile; run < n; run *= kWays) {
@@ -902,12 +877,14 @@ gc_status embed_backward(const char *fn, const gc_plan *plan, int seg, uint32_t 
                                                                       w.heads_before, seg_off, plan->nseg, seg));
         out.heads_before = w.heads_before;
     }
+    // one piece per wave while the chip holds them all at once, else 4 waves a block
+    const int threads = sums <= 512 ? 1024 : 256;
     with_type(type, [&](auto t) {
         using T = decltype(t);
         GC_LAUNCH("embed_sum", stream,
-                  embed_sum_kernel<T><<<static_cast<unsigned>(sums + nfree), threads, 0, stream>>>(
+                  embed_sum_kernel<T><<<static_cast<unsigned>(sums), threads, 0, stream>>>(
                       static_cast<const typename T::Store *>(dy), stride, w.key[cur], w.pos[cur], n, rows, cols, slabs,
-                      scale, out, w.part, w.ldpart, w.lists, static_cast<uint32_t>(sums), cut, fill));
+                      scale, out, w.part, w.ldpart, w.lists));
     });
     {
         const unsigned grid = static_cast<unsigned>(umin64(ceil_div(static_cast<uint64_t>(blocks - 1) * slabs, 2), 512));
