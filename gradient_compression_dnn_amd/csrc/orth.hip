@@ -349,58 +349,6 @@ __global__ __launch_bounds__(kBlock) void orth_scale_kernel(const MatDev *__rest
     if (threadIdx.x == 0) inv[blockIdx.x] = norm_scale(sum, eps);
 }
 
-// A 64 x 64 tile of X_0, split, into X and T; the padding becomes zeros.
-// Memory bounds it: 36 M elements with Nesterov's D formed again from U and G
-// take 135 us, 4.3 TB/s; D kept by orth_norm would be 4 more bytes written for
-// 4 fewer read.
-__global__ __launch_bounds__(kBlock) void orth_split_kernel(const Item *__restrict__ items, const MatDev *__restrict__ mats,
-                                                            Source s, const double *__restrict__ inv, float pow2,
-                                                            _Float16 *__restrict__ X, _Float16 *__restrict__ T) {
-    const Item it = items[blockIdx.x];
-    const MatDev M = mats[it.mat];
-    __shared__ float tile[kSplitTile][kSplitTile + 1];  // [i][j] of X
-    const double scale = inv[it.mat] * static_cast<double>(pow2);
-    const uint32_t i0 = it.i * kSplitTile, j0 = it.j * kSplitTile;
-    // D is read along its rows: lanes run over j, or over i where X = D^T
-    const uint32_t l = threadIdx.x & 63, r0 = threadIdx.x >> 6;
-    for (uint32_t r = r0; r < kSplitTile; r += kWaves) {
-        const uint32_t i = M.flip ? i0 + l : i0 + r, j = M.flip ? j0 + r : j0 + l;
-        float v = 0.0f;
-        if (i < M.m && j < M.n) {
-            const uint64_t at = M.off + (M.flip ? static_cast<uint64_t>(j) * M.C + i : static_cast<uint64_t>(i) * M.C + j);
-            const float g = s.G[at];
-            const float d = s.U ? direction(s, s.U[at], g) : g;
-            v = static_cast<float>(static_cast<double>(d) * scale);
-        }
-        tile[M.flip ? l : r][M.flip ? r : l] = v;
-    }
-    __syncthreads();
-    for (uint32_t e = threadIdx.x; e < kSplitTile * kSplitTile / 4; e += kBlock) {
-        const uint32_t r = e / (kSplitTile / 4), c = e % (kSplitTile / 4) * 4;
-        h4 hi, lo;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            _Float16 a, b;
-            split(tile[r][c + u], a, b);
-            hi[u] = a;
-            lo[u] = b;
-        }
-        _Float16 *p = X + M.x + static_cast<uint64_t>(i0 + r) * M.np * 2 + split_at(j0 + c);
-        *reinterpret_cast<h4 *>(p) = hi;
-        *reinterpret_cast<h4 *>(p + 32) = lo;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            _Float16 a, b;
-            split(tile[c + u][r], a, b);
-            hi[u] = a;
-            lo[u] = b;
-        }
-        p = T + M.x + static_cast<uint64_t>(j0 + r) * M.mp * 2 + split_at(i0 + c);
-        *reinterpret_cast<h4 *>(p) = hi;
-        *reinterpret_cast<h4 *>(p + 32) = lo;
-    }
-}
-
 // ---------------------------------------------------------------- products
 // One product of the chain: P Q^T for every tile of an item list.
 //   kSym    P, Q symmetric or equal: the result is symmetric, tiles on and
@@ -587,6 +535,13 @@ __device__ __forceinline__ void put_out(const GemmArgs &g, uint64_t at, uint32_t
         }
 }
 
+// A word of split value x.
+__device__ __forceinline__ uint32_t split_word(float x) {
+    _Float16 h, l;
+    split(x, h, l);
+    return __builtin_bit_cast(uint16_t, h) | (static_cast<uint32_t>(__builtin_bit_cast(uint16_t, l)) << 16);
+}
+
 // A block of 64 x 64 results in LDS, [column][row], a word each: fp32 (kOut),
 // or hi and lo in its halves.  The 16 parts of 4 rows of a column are permuted
 // so that a matrix-core tile's lanes (a column's 4 rows), lanes along a column
@@ -690,6 +645,53 @@ __device__ __forceinline__ void write_rows(_Float16 *to, uint32_t ld, const uint
         for (int u = 0; u < 8; ++u) v[u] = block[block_at(8 * k + u, ii >> 2) + (ii & 3)];
         put_split(to + static_cast<uint64_t>(8 * t) * ld * 2, v);
     }
+}
+
+// A 64 x 64 tile of X_0, split, into X and T; the padding becomes zeros.
+// Memory bounds it: 36 M elements with Nesterov's D formed again from U and G
+// take 128 us, 4.5 TB/s (135 with 8-byte stores, and 58 against 44 for 16 M
+// elements without momentum); D kept by orth_norm would be 4 more bytes
+// written for 4 fewer read.
+__global__ __launch_bounds__(kBlock) void orth_split_kernel(const Item *__restrict__ items, const MatDev *__restrict__ mats,
+                                                            Source s, const double *__restrict__ inv, float pow2,
+                                                            _Float16 *__restrict__ X, _Float16 *__restrict__ T) {
+    const Item it = items[blockIdx.x];
+    const MatDev M = mats[it.mat];
+    __shared__ __attribute__((aligned(16))) uint32_t block[kBlockWords];
+    const double scale = inv[it.mat] * static_cast<double>(pow2);
+    const uint32_t i0 = it.i * kSplitTile, j0 = it.j * kSplitTile;
+    // D is read along its rows: lanes run over j, or over i where X = D^T; a
+    // thread has 16 of D's rows r0 + 4 (k % 4) + 16 (k / 4), 4 next to each other
+    const uint32_t l = lane_id(), r0 = wave_id() * 4;
+    const uint32_t rows = M.flip ? M.n - min(M.n, j0) : M.m - min(M.m, i0), cols = M.flip ? M.m - min(M.m, i0) : M.n - min(M.n, j0);
+    const uint64_t at = M.off + (M.flip ? static_cast<uint64_t>(j0) * M.C + i0 : static_cast<uint64_t>(i0) * M.C + j0) + l;
+    float d[16];
+#pragma unroll
+    for (uint32_t k = 0; k < 16; ++k) {
+        const uint32_t r = 16 * (k / 4) + r0 + k % 4;
+        d[k] = 0.0f;
+        if (r < rows && l < cols) {
+            const uint64_t e = at + static_cast<uint64_t>(r) * M.C;
+            const float g = s.G[e];
+            d[k] = s.U ? direction(s, s.U[e], g) : g;
+        }
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < 16; k += 4) {
+        const uint32_t r = 4 * k + r0;
+        uint32_t v[4];
+#pragma unroll
+        for (uint32_t u = 0; u < 4; ++u) v[u] = split_word(static_cast<float>(static_cast<double>(d[k + u]) * scale));
+        if (M.flip) {
+#pragma unroll
+            for (uint32_t u = 0; u < 4; ++u) block[block_at(r + u, l >> 2) + (l & 3)] = v[u];
+        } else {
+            *reinterpret_cast<uint4 *>(block + block_at(l, r >> 2)) = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+    }
+    __syncthreads();
+    write_columns<kWaves>(T + M.x, M.mp, block, i0, j0);
+    write_rows<kWaves>(X + M.x, M.np, block, i0, j0);
 }
 
 // Writes a block of sums out, by one wave or a team of kTeam: along its columns
@@ -858,13 +860,6 @@ enum Slab { kFirst, kMiddle, kLast };
 // 128 x 128 split values as four blocks, block wave 2 (i / 64) + (j / 64 ^ i / 64).
 __device__ __forceinline__ const uint32_t *block_of(const uint32_t *words, uint32_t ib, uint32_t jb) {
     return words + (2 * ib + (jb ^ ib)) * kBlockWords;
-}
-
-// A word of split value x.
-__device__ __forceinline__ uint32_t split_word(float x) {
-    _Float16 h, l;
-    split(x, h, l);
-    return __builtin_bit_cast(uint16_t, h) | (static_cast<uint32_t>(__builtin_bit_cast(uint16_t, l)) << 16);
 }
 
 __device__ __forceinline__ float joined(uint32_t word) {
