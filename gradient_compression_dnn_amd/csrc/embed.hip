@@ -92,9 +92,9 @@ __device__ __forceinline__ void store_cols(typename T::Store *row, uint32_t c, u
     }
 }
 
-// Zeros to elements [e0, e0 + 4) of a chunk.  Stored in the cache: 26 us at 205 MB
-// (a plain fill's time) where non-temporal stores took 36, 103 at 600 MB where
-// they took 110.
+// Zeros to elements [e0, e0 + 4) of a chunk.  Stored in the cache: with a batch
+// of 200 tokens 27 us at 205 MB, a plain fill's time, where non-temporal stores
+// took 37; 106 at 600 MB where they took 110.
 __device__ __forceinline__ void clear4(BufRsrc r, uint32_t e0) {
     typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
     __builtin_amdgcn_raw_buffer_store_b128(u32x4{0, 0, 0, 0}, r, static_cast<int>(e0 * 4u), 0, 0);
