@@ -126,7 +126,7 @@ __global__ __launch_bounds__(kBlock) void embed_lookup_kernel(const float *__res
     const uint64_t first = static_cast<uint64_t>(blockIdx.x) * (kBlock * kLookupVecs);
     const uint64_t tok0 = first / vecs;
     const uint32_t rem0 = static_cast<uint32_t>(first - tok0 * vecs);
-    float v[kLookupVecs][N];
+    float v[kLookupVecs][N], s[kLookupVecs];  // padding: +0 times +0, whatever the scale's sign
     uint64_t at[kLookupVecs];
     uint32_t col[kLookupVecs];
 #pragma unroll
@@ -137,8 +137,10 @@ __global__ __launch_bounds__(kBlock) void embed_lookup_kernel(const float *__res
         col[j] = (r - dt * vecs) * N;
 #pragma unroll
         for (int u = 0; u < N; ++u) v[j][u] = 0.0f;
+        s[j] = 0.0f;
         if (at[j] < ntok) {
             const uint32_t key = token_key(tokens, at[j], rows);
+            s[j] = key < rows ? scale : 0.0f;
             if (key < rows) load_cols<F32, N>(w + static_cast<uint64_t>(key) * cols, col[j], cols, v[j]);
         }
     }
@@ -146,7 +148,7 @@ __global__ __launch_bounds__(kBlock) void embed_lookup_kernel(const float *__res
     for (int j = 0; j < kLookupVecs; ++j) {
         if (at[j] < ntok) {
 #pragma unroll
-            for (int u = 0; u < N; ++u) v[j][u] = scale * v[j][u];
+            for (int u = 0; u < N; ++u) v[j][u] = s[j] * v[j][u];
             store_cols<T, N>(y + at[j] * ystride, col[j], cols, v[j]);
         }
     }

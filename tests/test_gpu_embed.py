@@ -368,3 +368,24 @@ def test_a_table_past_two_gigabytes():
     B.gc_embed_grad(plan, 0, rows, torch.ones_like(y), tokens, 1.0, w, False, ws)
     assert bool((v.sum(1)[[0, 131_072, 130_944, rows - 1]] == torch.tensor([1, 1, 1, 2], device=dev()) * cols).all())
     assert v.sum(dtype=torch.float64).item() == 5 * cols
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("scale", [-1.0, -0.37, -0.0, 0.0, 0.37])
+def test_lookup_bits_of_padding(dtype, scale):
+    """Padding's row is +0 whatever the scale's sign, and a row of zeros has
+    the sign of the product: compared bit by bit."""
+    bits = {torch.float32: torch.int32, torch.bfloat16: torch.int16, torch.float16: torch.int16}[DTYPES[dtype]]
+    for rows, cols, n in ((1, 1, 3), (40, 33, 70), (90, 512, 300)):
+        b = Batch(rows, cols, n, dtype)
+        b.w[b.lead] = 0.0
+        b.tokens[0], b.tokens[n - 1] = 0, rows
+        ok = (b.tokens >= 0) & (b.tokens < rows)
+        y = torch.full((n, cols), 7.0, dtype=DTYPES[dtype], device=dev())
+        say(f"lookup {rows}x{cols} n={n} {dtype} scale={scale}")
+        B.gc_embed_lookup(b.plan, b.seg, rows, b.w, b.tokens, scale, y)
+        table = b.w[b.lead:b.lead + rows * cols].view(rows, cols).cpu()
+        want = torch.zeros(n, cols)
+        want[ok.cpu()] = table[b.tokens[ok].cpu()] * torch.tensor(scale, dtype=torch.float32)
+        assert torch.equal(y.cpu().view(bits), want.to(DTYPES[dtype]).view(bits))
+        assert not y[~ok].view(bits).any()
