@@ -389,3 +389,48 @@ def test_lookup_bits_of_padding(dtype, scale):
         want[ok.cpu()] = table[b.tokens[ok].cpu()] * torch.tensor(scale, dtype=torch.float32)
         assert torch.equal(y.cpu().view(bits), want.to(DTYPES[dtype]).view(bits))
         assert not y[~ok].view(bits).any()
+
+
+def banded_tokens(rows, n, rng):
+    """Tiles of 2,048 tokens that are alternately spread over all rows and
+    packed into a narrow band, so that between two neighbours of a spread run
+    stand hundreds of a packed one's tokens, and a twentieth padding."""
+    tile = np.arange(n) // 2048
+    spread = rng.integers(0, rows, n)
+    band = (tile * 37) % rows + rng.integers(0, max(1, rows // 64), n)
+    keys = np.where(tile % 2 == 0, spread, band % rows)
+    keys[rng.random(n) < 0.05] = -1
+    return keys
+
+
+# two rounds of merging: at one token more than a round's 16 tiles, at odd
+# lengths, and with all 16 runs of the second round; then three rounds
+@pytest.mark.parametrize("n", [32_768, 32_769, 70_001, 16 * 32_768, 16 * 32_768 + 4_097])
+@pytest.mark.parametrize("rows", [64, 5000])
+def test_gradient_order_of_long_batches(rows, n):
+    """The order of every sum after more than one round of merging, by the bits
+    of sums whose order matters."""
+    cols = 3
+    rng = np.random.default_rng(n + rows)
+    keys = banded_tokens(rows, n, rng)
+    plan = B.Plan(W.make_table([rows * cols], [1]))
+    dy = (rng.normal(size=(n, cols)) * np.exp(2 * rng.normal(size=(n, 1)))).astype(np.float32)
+    sums = ordered_sums(keys, dy, rows)
+    backwards = ordered_sums(keys[::-1], dy[::-1], rows)
+    assert any((sums[r] != backwards[r]).any() for r in sums)  # the order shows in the bits
+    want = np.zeros((rows, cols), np.float32)
+    for r, v in sums.items():
+        want[r] = np.float32(0.5) * v
+    tokens, d = torch.from_numpy(keys).to(dev()), torch.from_numpy(dy).to(dev())
+    ws = torch.full((B.gc_embed_workspace_bytes(plan, 0, rows, n),), 0xA5, dtype=torch.uint8, device=dev())
+    say(f"order of {n} tokens in {rows} rows")
+    g = torch.full((rows * cols,), 7.0, device=dev())
+    B.gc_embed_grad(plan, 0, rows, d, tokens, 0.5, g, False, ws)
+    got = f32(g)
+    assert same_bits(got, want.reshape(-1)), ulp_report(got, want.reshape(-1))
+    msg = B.Sparse.empty(plan, B.gc_embed_message_cap(plan, 0, rows, n), dev())
+    B.gc_embed_message(plan, 0, rows, d, tokens, 0.5, msg, ws)
+    idx, val, off, _ = msg.host()
+    held = sorted(sums)
+    assert off[1] == len(held) * cols and np.array_equal(idx.reshape(-1, cols)[:, 0], np.array(held) * cols)
+    assert same_bits(val, want[held].reshape(-1)), ulp_report(val, want[held].reshape(-1))
