@@ -835,10 +835,12 @@ gc_status embed_backward(const char *fn, const gc_plan *plan, int seg, uint32_t 
     const uint32_t blocks = static_cast<uint32_t>(ceil_div(n, kSpan));
     const uint32_t slabs = static_cast<uint32_t>(ceil_div(cols, kSlab));
     const uint64_t sums = static_cast<uint64_t>(blocks) * slabs;
-    if (nrank + nfill > max_grid(kRankThreads) || sums > max_grid(kBlock))
+    const uint64_t nsum64 = ceil_div(n, kSmallWaves) * slabs;  // of a short batch
+    if (n <= kSmall ? nsum64 + nfill > max_grid(kSmallThreads)
+                    : nrank + nfill > max_grid(kRankThreads) || sums > max_grid(kBlock))
         return set_error(GC_ERANGE, std::string(fn) + ": more workgroups than a launch has");
     if (n <= kSmall) {
-        const uint32_t nsum = static_cast<uint32_t>(ceil_div(n, kSmallWaves)) * slabs;
+        const uint32_t nsum = static_cast<uint32_t>(nsum64);
         with_type(type, [&](auto t) {
             with_tokens(token_type, [&](auto tok) {
                 using T = decltype(t);

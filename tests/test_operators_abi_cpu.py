@@ -215,3 +215,26 @@ def test_option_structs_match_the_header():
     o = B.orth_options(steps=2, coef=((1, 2, 3), (4, 5, 6)), eps=0.5)
     assert list(o.coef[1]) == [4, 5, 6] and o.steps == 2 and o.eps == 0.5
     assert np.allclose(list(B.orth_options(steps=3).coef[2]), (3.4445, -4.7750, 2.0315))
+
+
+@pytest.mark.parametrize("op,cols,n", [
+    ("message", (1 << 30) + 1, 1), ("message", 1_100_000_000, 16), ("message", (1 << 26) + 1, 256),
+    ("add", (1 << 30) + 1, 16), ("add", 1 << 27, 256), ("dense", 1 << 30, 16),
+    # the sums alone fit a launch, with the clearing beside them they do not
+    ("dense", 1_062_400_000, 1),
+])
+def test_short_batches_of_more_columns_than_a_launch_has_threads(op, cols, n):
+    """A workgroup of 1,024 threads for every 256 columns of every 16 tokens,
+    and for every 16,384 elements that are cleared: 2^32 threads or more are
+    refused before anything is enqueued."""
+    groups = -(-n // 16) * -(-cols // 256) + (-(-cols // 16384) if op == "dense" else 0)
+    assert groups * 1024 >= 1 << 32 and n * cols <= 1 << 35
+    p = B.Plan(W.make_table([cols], [1]))
+    need = B.gc_embed_workspace_bytes(p, 0, 1, n)
+    lib = B.load()
+    if op == "message":
+        msg = B.gc_sparse(FAKE.value, FAKE.value, FAKE.value, None, cols)
+        code = lib.gc_embed_message(p.handle, 0, 1, FAKE, 0, cols, FAKE, 0, n, 1.0, ctypes.byref(msg), FAKE, need, None)
+    else:
+        code = lib.gc_embed_grad(p.handle, 0, 1, FAKE, 0, cols, FAKE, 0, n, 1.0, FAKE, int(op == "add"), FAKE, need, None)
+    assert code == B.GC_ERANGE, B.gc_last_error()
