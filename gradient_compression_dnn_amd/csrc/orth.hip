@@ -195,31 +195,44 @@ struct Scales {
 // The largest exponent that keeps |v| <= bound below 60000 in fp16.
 int exponent_for(double bound) { return static_cast<int>(std::floor(std::log2(60000.0 / bound))); }
 
-// Bounds of the singular values of X, A and B at every step, from the
-// polynomial on [0, top]: sampled at 1024 points, with what it can rise
-// between two of them (a derivative's bound times half a spacing) and 1/64
-// for rounding.  s[k] is step k's, s[steps] the result's.
+// The largest |q(y)| and |x q(x^2)| for y = x^2, x in [0, top], with q(y) = a +
+// b y + c y^2: at an end of the range, or where the derivative vanishes.
+void largest(double a, double b, double c, double top, double *of_q, double *of_p) {
+    const double t2 = top * top;
+    auto q = [&](double y) { return std::fabs(a + (b + c * y) * y); };
+    auto inside = [&](double y) { return y > 0.0 && y < t2; };  // false for NaN
+    *of_q = std::max(q(0.0), q(t2));
+    *of_p = top * q(t2);
+    const double vertex = -b / (2.0 * c);
+    if (inside(vertex)) *of_q = std::max(*of_q, q(vertex));
+    const double square = 9.0 * b * b - 20.0 * a * c;  // of a + 3 b y + 5 c y^2 = 0
+    if (!(square >= 0.0)) return;
+    const double w = -0.5 * (3.0 * b + std::copysign(std::sqrt(square), b));
+    for (double y : {w / (5.0 * c), a / w})
+        if (inside(y)) *of_p = std::max(*of_p, std::sqrt(y) * q(y));
+}
+
+// Bounds of the singular values of X, A and B at every step: the largest value
+// of the polynomial on [0, top], and kRounding of the sizes of its terms for
+// the step's own roundings (an operand is off by up to 2^-23, A by 2^-21, c A^2
+// by 2^-19 of itself).  No more than that: where a schedule is steep at the
+// top of its range, what is added at one step comes back 10 to 20 times as
+// large at the next.  s[k] is step k's, s[steps] the result's.
 // The bounds are worst cases; what a matrix really holds may be smaller by
 // as much as the bounds are loose, and where that reaches fp16's subnormals
 // the lo parts lose bits (a schedule whose bound rose to 24 and then 3e6 gave
 // 5.2e-6 where fp32 gives 2.7e-7).  So false, a refusal, if X's bound passes 8
 // before the last step, B's 2^14, the result's 1e12, or one vanishes.
 bool orth_scales(const gc_orth_options &o, Scales *s) {
-    double top = 1.0 + 1.0 / 64, before = 0.0;
+    constexpr double kRounding = 1.0 / (1 << 19);
+    double top = 1.0 + kRounding, before = 0.0;
     for (int k = 0; k <= o.steps; ++k) {
         s[k].ex = exponent_for(top);
         if (k == o.steps) break;
         const double a = o.coef[k][0], b = o.coef[k][1], c = o.coef[k][2];
-        constexpr int kPoints = 1024;
-        double px = 0.0, pb = 0.0;
-        for (int i = 0; i <= kPoints; ++i) {
-            const double x = top * i / kPoints, q = (b + c * x * x) * x * x;
-            pb = std::max(pb, std::fabs(a + q));
-            px = std::max(px, std::fabs((a + q) * x));
-        }
-        const double t2 = top * top, half = 0.5 * top / kPoints;
-        pb += half * (2 * std::fabs(b) * top + 4 * std::fabs(c) * t2 * top);
-        px += half * (std::fabs(a) + 3 * std::fabs(b) * t2 + 5 * std::fabs(c) * t2 * t2);
+        const double t2 = top * top;
+        double px, pb;
+        largest(a, b, c, top, &pb, &px);
         s[k].ea = exponent_for(t2 * (1.0 + 1.0 / 64));
         s[k].eb = exponent_for(std::max(pb, 1e-12) * (1.0 + 1.0 / 64));
         // S = B A has values s |p(s)|, Q = B' B at most the product of the two bounds
@@ -230,7 +243,7 @@ bool orth_scales(const gc_orth_options &o, Scales *s) {
             s[k - 1].pair = before * pb <= 16384.0;
         }
         before = pb;
-        top = px * (1.0 + 1.0 / 64);
+        top = px + kRounding * (std::fabs(a) + (std::fabs(b) + std::fabs(c) * t2) * t2) * top;
         if (!(top <= (k + 1 == o.steps ? 1e12 : 8.0)) || !(pb <= 16384.0) || !(top > 1e-12)) return false;
     }
     return true;

@@ -700,7 +700,8 @@ size_t    gc_matrix_plan_workspace_bytes(const gc_matrix_plan *mplan);
  * Errors: GC_EINVAL (null, steps, eps negative or not finite, reserved not 0,
  *         coefficients that are not finite, or with which singular values
  *         of at most 1 at the start may pass 8 before the last step (1e12
- *         after it), those of a I + b A + c A^2 2^14, or all fall below 1e-12;
+ *         after it), those of a I + b A + c A^2 2^14, or all fall below 1e-12,
+ *         where a step may be off by 2^-19 of the sizes of its terms;
  *         overlapping buffers), GC_ECAPACITY (ws).
  */
 #define GC_MAX_ORTH_STEPS  16

@@ -15,6 +15,7 @@ import torch
 from gradient_compression_dnn_amd import binding as B
 from gradient_compression_dnn_amd import workloads as W
 from tests.gpu_util import dev, same_bits, say, ulp_report
+from tests.test_operators_abi_cpu import DIVIDED, FIVE, LAST, SIX
 
 pytestmark = pytest.mark.gpu
 
@@ -384,3 +385,52 @@ def test_refused_calls_touch_nothing():
         B.gc_orthogonalize(ms.m, x[:-1], O, B.orth_options(), ms.ws())
     torch.cuda.synchronize()
     assert bool((O == 3.0).all())
+
+
+STEEP = [SIX[:3], SIX, DIVIDED, DIVIDED + (LAST,) * 2, FIVE, ((7.9, 0.0, 0.0), (0.1, 0.0, 0.0))]
+
+
+@pytest.mark.parametrize("coef", STEEP)
+def test_steep_schedules(coef):
+    """Schedules whose polynomials are steep where the singular values are
+    largest.  The matrices have many singular values, which share the error."""
+    rng = np.random.default_rng(28)
+    for shape, kind in (((40, 130), "gauss"), ((90, 200), "gauss"), ((200, 90), "ortho"), ((29, 1600), "gauss"),
+                        ((300, 520), "gauss"), ((520, 300), "sparse"), ((600, 640), "gauss")):
+        D = matrix(rng, *shape, kind).astype(np.float32)
+        ms = Mats([shape])
+        O = torch.zeros(ms.n, device=dev())
+        say(f"steep schedule of {len(coef)} steps {shape} {kind}")
+        B.gc_orthogonalize(ms.m, to_dev(ms.flat([D], rng)), O, B.orth_options(len(coef), coef), ms.ws())
+        check(ms.parts(O.cpu().numpy())[0], D, len(coef), coef)
+
+
+@pytest.mark.parametrize("coef", STEEP + [(COEF,) * 5])
+def test_a_vector_runs_through_the_polynomials(coef):
+    """The one singular value of a vector is 1 at the start and then p(1),
+    p(p(1)), ...  X_0 is off by 2^-22 of itself.  A step is off by its
+    roundings, 2^-19 of the sizes of its terms (an operand by 2^-23, A by 2^-21,
+    c A^2 by 2^-19) and as much again for up to 32 additions of a sum, 2^-24
+    each; and by what it was off before times the slope at its value, or p(s) / s,
+    whichever is larger.  Half as much again for the second order, which is below
+    that while the error is below 0.01."""
+    rng = np.random.default_rng(29)
+    s, err = 1.0, 2.0 ** -22
+    for a, b, c in coef:
+        slope = max(abs(a + 3 * b * s ** 2 + 5 * c * s ** 4), abs(a + b * s ** 2 + c * s ** 4))
+        err = slope * err + 2.0 ** -18 * (abs(a) * s + abs(b) * s ** 3 + abs(c) * s ** 5)
+        s = abs(a * s + b * s ** 3 + c * s ** 5)
+    for shape in ((1, 1), (1, 7), (9, 1), (1, 1000), (1000, 1)):
+        D = rng.normal(0, 1e-2, shape).astype(np.float32)
+        ms = Mats([shape])
+        O = torch.zeros(ms.n, device=dev())
+        say(f"vector {shape} of {len(coef)} steps")
+        B.gc_orthogonalize(ms.m, to_dev(ms.flat([D], rng)), O, B.orth_options(len(coef), coef, eps=0.0), ms.ws())
+        got = ms.parts(O.cpu().numpy())[0]
+        assert np.isfinite(got).all()
+        want = recurrence(D, len(coef), coef, 0.0, torch.float64)
+        assert abs(np.linalg.norm(want) - s) <= 1e-6 * s  # the coefficients in fp32 and in 64 bits
+        if err < 0.01 * s:
+            assert np.linalg.norm(got - want) <= 1.5 * err
+        else:  # no digits are left; the bounds the call chose its exponents by still hold
+            assert np.linalg.norm(got) <= 8.0

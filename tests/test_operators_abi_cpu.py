@@ -238,3 +238,40 @@ def test_short_batches_of_more_columns_than_a_launch_has_threads(op, cols, n):
     else:
         code = lib.gc_embed_grad(p.handle, 0, 1, FAKE, 0, cols, FAKE, 0, n, 1.0, FAKE, int(op == "add"), FAKE, need, None)
     assert code == B.GC_ERANGE, B.gc_last_error()
+
+
+# Schedules that are steep at the top of their range: singular values of at
+# most 1 stay below 2 at every step.  Published for six steps and more, as they
+# are and with their arguments divided by 1.01, and one of five steps.
+SIX = ((8.28721, -23.59589, 17.30039), (4.10706, -2.94785, 0.54484), (3.94869, -2.90890, 0.55182),
+       (3.31842, -2.48849, 0.51005), (2.30065, -1.66890, 0.41881), (1.89130, -1.26800, 0.37680))
+DIVIDED = tuple((a / 1.01, b / 1.01 ** 3, c / 1.01 ** 5) for a, b, c in SIX)
+FIVE = ((8.1566, -22.4833, 15.8788), (4.0429, -2.8089, 0.5000), (3.8917, -2.7725, 0.5061), (3.2858, -2.3681, 0.4645),
+        (2.3465, -1.6998, 0.4232))
+LAST = (1.875, -1.25, 0.375)
+
+
+@pytest.mark.parametrize("coef,code", [
+    (SIX[:3], B.GC_ECAPACITY), (SIX, B.GC_ECAPACITY), (DIVIDED[:4], B.GC_ECAPACITY), (DIVIDED, B.GC_ECAPACITY),
+    (DIVIDED + (LAST,) * 10, B.GC_ECAPACITY), (FIVE, B.GC_ECAPACITY), (FIVE + (LAST,), B.GC_ECAPACITY),
+    # on either side of the largest X, B and result
+    (((7.99, 0, 0), (1, 0, 0)), B.GC_ECAPACITY), (((8.01, 0, 0), (1, 0, 0)), B.GC_EINVAL),
+    (((1, 0, 0), (16380, 0, 0)), B.GC_ECAPACITY), (((1, 0, 0), (16390, 0, 0)), B.GC_EINVAL),
+    (((0, 0, 7.99), (1, 0, 0)), B.GC_ECAPACITY), (((0, 0, -8.01), (1, 0, 0)), B.GC_EINVAL),
+    (((0, 7.99, 0), (0.125, 0, 0)), B.GC_ECAPACITY), (((0, -8.01, 0), (0.125, 0, 0)), B.GC_EINVAL),
+    # the largest value inside the range: 8.08 and 7.97 at about 1/2
+    (((23.9, -31.0, 0), (0.125, 0, 0)), B.GC_EINVAL), (((23.5, -30.3, 0), (0.125, 0, 0)), B.GC_ECAPACITY),
+])
+def test_schedules_at_the_edge_of_the_range(coef, code):
+    """Refused only where singular values of at most 1 really pass 8 before the
+    last step: a short workspace is what an accepted call is refused for."""
+    x = np.linspace(0, 1, 20001)
+    most = []
+    for a, b, c in coef:
+        x = np.abs(a * x + b * x ** 3 + c * x ** 5)
+        most.append(x.max())
+    p = _plan()
+    m = B.MatrixPlan(p, [0, 10, 6])
+    o = B.orth_options(len(coef), coef)
+    lib = B.load()
+    assert lib.gc_orthogonalize(m.handle, FAKE, FAKE, ctypes.byref(o), FAKE, m.workspace_bytes() - 1, None) == code, most
