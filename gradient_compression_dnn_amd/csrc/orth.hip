@@ -226,13 +226,15 @@ void largest(double a, double b, double c, double top, double *of_q, double *of_
 bool orth_scales(const gc_orth_options &o, Scales *s) {
     constexpr double kRounding = 1.0 / (1 << 19);
     double top = 1.0 + kRounding, before = 0.0;
-    for (int k = 0; k <= o.steps; ++k) {
-        s[k].ex = exponent_for(top);
-        if (k == o.steps) break;
+    s[0].ex = exponent_for(top);
+    for (int k = 0; k < o.steps; ++k) {
         const double a = o.coef[k][0], b = o.coef[k][1], c = o.coef[k][2];
         const double t2 = top * top;
         double px, pb;
         largest(a, b, c, top, &pb, &px);
+        const double next = px + kRounding * (std::fabs(a) + (std::fabs(b) + std::fabs(c) * t2) * t2) * top;
+        // before an exponent is formed, which needs bounds that are finite
+        if (!(next <= (k + 1 == o.steps ? 1e12 : 8.0)) || !(pb <= 16384.0) || !(next > 1e-12)) return false;
         s[k].ea = exponent_for(t2 * (1.0 + 1.0 / 64));
         s[k].eb = exponent_for(std::max(pb, 1e-12) * (1.0 + 1.0 / 64));
         // S = B A has values s |p(s)|, Q = B' B at most the product of the two bounds
@@ -243,8 +245,8 @@ bool orth_scales(const gc_orth_options &o, Scales *s) {
             s[k - 1].pair = before * pb <= 16384.0;
         }
         before = pb;
-        top = px + kRounding * (std::fabs(a) + (std::fabs(b) + std::fabs(c) * t2) * t2) * top;
-        if (!(top <= (k + 1 == o.steps ? 1e12 : 8.0)) || !(pb <= 16384.0) || !(top > 1e-12)) return false;
+        top = next;
+        s[k + 1].ex = exponent_for(top);
     }
     return true;
 }

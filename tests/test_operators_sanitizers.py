@@ -98,3 +98,60 @@ def test_operator_entry_points_under_asan_ubsan_and_lsan(tmp_path):
     r = subprocess.run([exe], capture_output=True, text=True, timeout=300, env=env)
     assert r.returncode == 0, r.stdout[-4000:] + r.stderr[-4000:]
     assert r.stdout.strip().endswith("ok")
+
+
+SCHEDULES = r"""
+#include <math.h>
+#include <stdio.h>
+#include <string.h>
+#include "gradcomp.h"
+
+/* Coefficients that are not finite, overflow, or let X vanish: each is an
+   error, and none a number that an int cannot hold on the way there. */
+int main(void) {
+    static const float coef[][3] = {{0, 0, 0}, {NAN, 0, 0}, {1, NAN, 0}, {1, 0, NAN}, {1, 0, INFINITY}, {-INFINITY, INFINITY, 0},
+                                    {3e38f, 3e38f, 3e38f}, {-3e38f, 3e38f, 0}, {1e-30f, 0, 0}, {0, 1e-38f, 0}, {0, 0, 1e-45f}};
+    static float buf[4096];
+    gc_segment seg = {0, 120, 1, 1, 0};
+    uint32_t rows = 10;
+    gc_plan *p = NULL;
+    gc_matrix_plan *m = NULL;
+    if (gc_plan_create(&seg, 1, 120, &p) != GC_OK || gc_matrix_plan_create(p, &rows, &m) != GC_OK) return 1;
+    for (unsigned i = 0; i < sizeof coef / sizeof coef[0]; ++i)
+        for (int at = 0; at < GC_MAX_ORTH_STEPS; ++at)
+            for (int steps = at + 1; steps <= GC_MAX_ORTH_STEPS; steps += 5) {
+                gc_orth_options o;
+                memset(&o, 0, sizeof o);
+                o.steps = steps;
+                for (int k = 0; k < steps; ++k) { o.coef[k][0] = 1.5f; o.coef[k][1] = -0.5f; }
+                memcpy(o.coef[at], coef[i], sizeof coef[i]);
+                if (gc_orthogonalize(m, buf, buf, &o, buf, 16, NULL) != GC_EINVAL) {
+                    printf("coefficients %u in step %d of %d\n", i, at, steps);
+                    return 1;
+                }
+            }
+    gc_matrix_plan_destroy(m);
+    gc_plan_destroy(p);
+    printf("ok\n");
+    return 0;
+}
+"""
+
+
+@pytest.mark.skipif(not (os.path.exists(S.CLANG) and os.path.exists(S.hip_build.HIPCC)),
+                    reason="needs the ROCm toolchain")
+def test_refused_schedules_under_asan_and_ubsan(tmp_path):
+    out = str(tmp_path)
+    S.build_host_library(out)
+    src, exe = os.path.join(out, "schedules.c"), os.path.join(out, "schedules")
+    with open(src, "w") as f:
+        f.write(SCHEDULES)
+    r = subprocess.run([S.CLANG, "-std=c99", "-g", "-Wall", "-Werror", "-fsanitize=address,undefined",
+                        "-fno-sanitize-recover=all", "-fno-omit-frame-pointer", "-D__HIP_PLATFORM_AMD__",
+                        "-I", os.path.join(S.ROOT, "include"), "-I", "/opt/rocm/include", src, "-o", exe,
+                        "-L", out, "-lgradcomp", f"-Wl,-rpath,{out}"], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout + r.stderr
+    env = dict(os.environ, ASAN_OPTIONS="detect_leaks=1:halt_on_error=1", UBSAN_OPTIONS="halt_on_error=1:print_stacktrace=1")
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=300, env=env)
+    assert r.returncode == 0, r.stdout[-4000:] + r.stderr[-4000:]
+    assert r.stdout.strip().endswith("ok")
