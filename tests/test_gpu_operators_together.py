@@ -62,8 +62,8 @@ def same(a, b):
 
 LEARNERS = [
     (50, 12, [(29, 300), (100, 70), (1, 1)], 200),        # one launch a message, matrices of few rows
-    (300, 40, [(700, 1200), (1200, 700)], 3000),          # sorted tokens, two steps at a time
-    (40, 257, [(200, 333), (20, 5)], 7000),               # merged runs, one step at a time
+    (300, 40, [(700, 1200), (1200, 700)], 3000),          # sorted tokens, matrices of many rows
+    (40, 257, [(200, 333), (20, 5)], 7000),               # merged runs, few rows beside more
 ]
 
 
@@ -180,7 +180,7 @@ def test_few_rows(shapes, steps):
 
 
 @pytest.mark.parametrize("rows,cols,n", [
-    (3000, 30, 257), (3000, 30, 1024), (3000, 30, 1025),  # clearing halved between two launches, and not
+    (3000, 30, 257), (3000, 30, 1024), (3000, 30, 1025),  # cleared beside the ranking
     (7, 9001, 700), (20000, 3, 1000), (40000, 1, 300),    # rows longer than a workgroup clears, and many in one
     (33, 513, 900), (1, 32768, 400), (2, 16384, 400),
 ])

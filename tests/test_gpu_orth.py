@@ -300,9 +300,9 @@ def test_decoded_update_of_learners_into_weights():
 
 
 @pytest.mark.parametrize("shapes", [
-    [(1100, 1500)],                      # two steps at a time, tiles cut to fill the units
+    [(1100, 1500)],                      # tiles cut to fill the units
     [(2600, 600)], [(513, 2000)] * 3,    # the same, transposed and several at once
-    [(1030, 1030)], [(511, 1800)],       # one step at a time: square, and too few rows for pairs
+    [(1030, 1030)], [(511, 1800)],       # square, and fewer rows than steps in pairs need
     [(700, 900), (30, 40), (129, 3001)],  # few rows beside many
     [(128, 9000)], [(5, 6000), (100, 100), (1, 3)],  # few rows only: several slabs a workgroup and parts
 ])
