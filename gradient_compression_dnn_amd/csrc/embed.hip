@@ -789,6 +789,8 @@ gc_status check_table(const char *fn, const gc_plan *plan, int seg, uint32_t row
     return GC_OK;
 }
 
+bool aligned4(const void *p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
+
 size_t type_bytes(int type) { return type == GC_F32 ? 4 : 2; }
 
 gc_status check_batch(const char *fn, const void *tokens, int token_type, uint64_t n, const void *x, int type,
@@ -925,6 +927,7 @@ extern "C" gc_status gc_embed_lookup(const gc_plan *plan, int seg, uint32_t rows
     if (st != GC_OK) return st;
     if (n_tokens == 0) return GC_OK;
     if (!w) return set_error(GC_EINVAL, "gc_embed_lookup: buffers must be non-null");
+    if (!aligned4(w)) return set_error(GC_EINVAL, "gc_embed_lookup: buffers must be aligned to their elements");
     const uint32_t vecs = static_cast<uint32_t>(ceil_div(cols, y_type == GC_F32 ? kLookupCols<F32> : kLookupCols<BF16>));
     const uint64_t grid = ceil_div(n_tokens * vecs, kBlock * kLookupVecs);
     if (grid > max_grid(kBlock)) return set_error(GC_ERANGE, "gc_embed_lookup: more workgroups than a launch has");
@@ -969,6 +972,7 @@ extern "C" gc_status gc_embed_grad(const gc_plan *plan, int seg, uint32_t rows, 
     st = check_batch("gc_embed_grad", tokens, token_type, n_tokens, dy, dy_type, dy_stride, cols, scale);
     if (st != GC_OK) return st;
     if (!g) return set_error(GC_EINVAL, "gc_embed_grad: g must be non-null");
+    if (!aligned4(g)) return set_error(GC_EINVAL, "gc_embed_grad: buffers must be aligned to their elements");
     if (n_tokens && !ws) return set_error(GC_EINVAL, "gc_embed_grad: ws must be non-null");
     if (n_tokens && ws_bytes < embed_ws(nullptr, n_tokens, cols).bytes)
         return set_error(GC_ECAPACITY, "gc_embed_grad: workspace smaller than gc_embed_workspace_bytes");
@@ -1000,6 +1004,8 @@ extern "C" gc_status gc_embed_message(const gc_plan *plan, int seg, uint32_t row
     if (st != GC_OK) return st;
     if (!msg || !msg->seg_off || (n_tokens && (!msg->idx || !msg->val)))
         return set_error(GC_EINVAL, "gc_embed_message: out and its idx, val, seg_off must be non-null");
+    if (!aligned4(msg->idx) || !aligned4(msg->val) || !aligned4(msg->seg_off))
+        return set_error(GC_EINVAL, "gc_embed_message: buffers must be aligned to their elements");
     if (n_tokens && !ws) return set_error(GC_EINVAL, "gc_embed_message: ws must be non-null");
     if (msg->cap < umin64(n_tokens, rows) * cols)
         return set_error(GC_ECAPACITY, "gc_embed_message: out->cap smaller than gc_embed_message_cap");

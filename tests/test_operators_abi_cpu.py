@@ -275,3 +275,22 @@ def test_schedules_at_the_edge_of_the_range(coef, code):
     o = B.orth_options(len(coef), coef)
     lib = B.load()
     assert lib.gc_orthogonalize(m.handle, FAKE, FAKE, ctypes.byref(o), FAKE, m.workspace_bytes() - 1, None) == code, most
+
+
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_misaligned_embedding_and_message_buffers(off):
+    """Every buffer of a call, not only the batch's."""
+    p = _plan()
+    lib = B.load()
+    bad = ctypes.c_void_p(FAKE.value + off)
+    need = B.gc_embed_workspace_bytes(p, 1, 10, 5)
+    assert _lookup(p, w=bad) == B.GC_EINVAL
+    for acc in (0, 1):
+        assert lib.gc_embed_grad(p.handle, 1, 10, FAKE, 0, 12, FAKE, 0, 5, 1.0, bad, acc, FAKE, need, None) == B.GC_EINVAL
+        # an empty batch still clears
+        assert lib.gc_embed_grad(p.handle, 1, 10, None, 0, 12, None, 0, 0, 1.0, bad, acc, None, 0, None) == B.GC_EINVAL
+    for k in range(3):
+        at = [bad.value if i == k else FAKE.value for i in range(3)]
+        msg = B.gc_sparse(at[0], at[1], at[2], None, 60)
+        assert lib.gc_embed_message(p.handle, 1, 10, FAKE, 0, 12, FAKE, 0, 5, 1.0, ctypes.byref(msg), FAKE, need,
+                                    None) == B.GC_EINVAL
