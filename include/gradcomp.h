@@ -698,12 +698,12 @@ size_t    gc_matrix_plan_workspace_bytes(const gc_matrix_plan *mplan);
  * random matrices against 64 bits, five of these steps end 0.2 to 1.4 times as
  * far off as with fp32 products (0.6e-6 to 3e-6 of the result); one or two
  * steps, or gentle coefficients such as (1.5, -0.5, 0), up to 5 times as far, at
- * 5e-7 of the result or less.  (Where one or a few singular values make up the
- * matrix, theirs are single chains of roundings, 2^-19 of a step's terms at most,
- * times the slopes of the later steps.  Entries of X_0 below 2^-18, where ||D|| is far below eps,
- * keep an absolute 2^-40 instead.)  Unlike the other calls' results it is no
- * fixed sequence of IEEE operations, but the same call on the same device gives
- * the same bits.
+ * 5e-7 of the result or less.  Where one or a few singular values make up the
+ * matrix, theirs are single chains of roundings: about 2^-19 of a step's terms
+ * at most, times the slopes of the later steps.  (Entries of X_0 below 2^-18,
+ * where ||D|| is far below eps, keep an absolute 2^-40 instead.)  Unlike the
+ * other calls' results it is no fixed sequence of IEEE operations, but the same
+ * call on the same device gives the same bits.
  * D = 0 gives O = +-0.  A matrix with a NaN or Inf becomes NaN altogether and
  * leaves the others alone.
  *   D [n_total] in, O [n_total] out; O may be D, or must not overlap it.
