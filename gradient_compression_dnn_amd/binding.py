@@ -29,6 +29,10 @@ GC_TOKENS_I32, GC_TOKENS_I64 = 0, 1
 GC_MUON_SCALE_NONE, GC_MUON_SCALE_SHAPE, GC_MUON_SCALE_RMS = 0, 1, 2
 GC_MAX_MATRIX_DIM = 1 << 20
 GC_MAX_ORTH_STEPS = 16
+GC_ACT_NONE, GC_ACT_RELU, GC_ACT_GELU, GC_ACT_GELU_TANH, GC_ACT_SILU = 0, 1, 2, 3, 4
+GC_MAX_VOCAB = 1 << 20
+GC_MAX_TOP_LOGITS = 1024
+GC_DISTILL_TOP, GC_DISTILL_REST = 0, 1
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgradcomp.so")
 
@@ -73,6 +77,16 @@ class gc_muon_options(ctypes.Structure):
     _fields_ = [("orth", gc_orth_options), ("momentum", ctypes.c_float), ("lr", ctypes.c_float),
                 ("weight_decay", ctypes.c_float), ("momentum_kind", ctypes.c_int), ("scale", ctypes.c_int),
                 ("reserved", ctypes.c_uint32)]
+
+
+class gc_linear(ctypes.Structure):
+    _fields_ = [("seg", ctypes.c_int), ("rows", ctypes.c_uint32), ("bias_seg", ctypes.c_int), ("type", ctypes.c_int),
+                ("reserved", ctypes.c_uint32 * 2)]
+
+
+class gc_distill_options(ctypes.Structure):
+    _fields_ = [("temperature", ctypes.c_float), ("kd_weight", ctypes.c_float), ("ce_weight", ctypes.c_float),
+                ("grad_scale", ctypes.c_float), ("mode", ctypes.c_int), ("reserved", ctypes.c_uint32 * 3)]
 
 
 _lib = None
@@ -139,6 +153,22 @@ _SIGS = {
     "gc_matrix_plan_workspace_bytes": (ctypes.c_size_t, [_P]),
     "gc_orthogonalize": (ctypes.c_int, [_P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "gc_muon_step": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "gc_linear_workspace_bytes": (ctypes.c_size_t, [_P, _P, ctypes.c_uint64]),
+    "gc_linear_forward": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_int, _P,
+                                         ctypes.c_uint64, _P, ctypes.c_uint64, _P, ctypes.c_uint64, _P, ctypes.c_size_t,
+                                         _P]),
+    "gc_act_grad": (ctypes.c_int, [_P, ctypes.c_uint64, _P, ctypes.c_uint64, ctypes.c_int, ctypes.c_int, ctypes.c_uint64,
+                                   ctypes.c_uint64, _P, ctypes.c_uint64, _P]),
+    "gc_linear_grad_input": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_uint64, ctypes.c_uint64, _P, ctypes.c_uint64,
+                                            ctypes.c_int, _P, ctypes.c_uint64, _P, ctypes.c_uint64, _P, ctypes.c_uint64,
+                                            _P, ctypes.c_size_t, _P]),
+    "gc_linear_grad_weight": (ctypes.c_int, [_P, _P, _P, ctypes.c_uint64, _P, ctypes.c_uint64, ctypes.c_uint64, _P,
+                                             ctypes.c_int, _P, ctypes.c_size_t, _P]),
+    "gc_top_logits": (ctypes.c_int, [_P, ctypes.c_int, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_uint32, ctypes.c_uint32,
+                                     ctypes.c_float, _P, _P, _P, _P]),
+    "gc_distill_loss": (ctypes.c_int, [_P, ctypes.c_int, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_uint32, _P,
+                                       ctypes.c_int, ctypes.c_uint64, _P, ctypes.c_int, ctypes.c_uint64, ctypes.c_uint32,
+                                       _P, _P, _P, _P, _P, _P, ctypes.c_uint64, _P]),
     "gc_timing_enable": (ctypes.c_int, [ctypes.c_char_p]),
     "gc_timing_take": (ctypes.c_int, [ctypes.c_char_p, _P, _P]),
     "gc_stream_probe": (ctypes.c_int, [_P, _P, _P, _P, _P, ctypes.c_uint64, _P]),
@@ -152,7 +182,7 @@ KERNELS = ("dgc_norm", "dgc_prep", "dgc_prepare", "dgc_sample", "dgc_bound", "dg
            "dcd_decode", "dcd_mix", "ecd_compress", "ecd_update", "slimdp_values", "stream_probe",
            "embed_lookup", "embed_rank", "embed_merge", "embed_heads", "embed_rows", "embed_sum", "embed_join",
            "embed_small", "embed_empty", "orth_norm", "orth_scale", "orth_split", "orth_gram", "orth_poly", "orth_pair", "orth_apply", "orth_join",
-           "orth_slab", "orth_small")
+           "orth_slab", "orth_small", "linear_product", "linear_join", "act_grad", "top_logits", "distill")
 
 
 def gc_timing_enable(kernels) -> None:
@@ -710,3 +740,140 @@ def gc_muon_step(mplan: MatrixPlan, G, U, W, opt: gc_muon_options, ws: torch.Ten
     n = mplan.n_total
     args = _f32(G, n, "G"), _f32(U, n, "U"), _f32(W, n, "W"), ctypes.byref(opt), *_ws(ws)
     _call("gc_muon_step", (W, G, U, ws), mplan.handle, *args)
+
+
+# ------------------------------------------------------- layer products
+def linear_layer(seg: int, rows: int, dtype=torch.float32, bias_seg: int = -1) -> gc_linear:
+    """The layer whose weights are segment seg, read as rows x columns, with
+    activations (and the copy of the flat model) in dtype."""
+    if dtype not in _FLOAT_TYPES:
+        raise ValueError("dtype: need torch.float32, bfloat16 or float16")
+    return gc_linear(int(seg), int(rows), int(bias_seg), _FLOAT_TYPES[dtype])
+
+
+_DTYPES = {v: k for k, v in _FLOAT_TYPES.items()}
+_ABSENT = (None, 0)
+
+
+def _layer_cols(plan: Plan, layer: gc_linear) -> int:
+    if not 0 <= layer.seg < plan.nseg or layer.rows < 1 or plan.lengths[layer.seg] % layer.rows:
+        raise ValueError("seg must be a segment of the plan and rows divide its length")
+    if layer.type not in _DTYPES:
+        raise ValueError("type: need GC_F32, GC_BF16 or GC_F16")
+    return plan.lengths[layer.seg] // layer.rows
+
+
+def _acts(t, dtype, shape, name: str):
+    """(pointer, row stride) of activations of the given shape, rows one stride apart."""
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name}: need a {str(dtype).replace('torch.', '')} tensor of shape {tuple(shape)}")
+    return t.data_ptr(), shape[-1] if t.is_contiguous() else _row_stride(t, name)
+
+
+def gc_linear_workspace_bytes(plan: Plan, layer: gc_linear, n_tokens: int) -> int:
+    return int(load().gc_linear_workspace_bytes(plan.handle, ctypes.byref(layer), int(n_tokens)))
+
+
+def gc_linear_forward(plan: Plan, layer: gc_linear, w, x: torch.Tensor, y: torch.Tensor, ws: torch.Tensor,
+                      act: int = GC_ACT_NONE, r=None, z=None):
+    """y = act(z) + r, z = x W^T + b: w is the flat model in the layer's type;
+    x [..., columns], y, r and z [..., rows] of that type."""
+    cols, dtype = _layer_cols(plan, layer), _DTYPES[layer.type]
+    if not isinstance(x, _Tensor) or x.dim() < 1:
+        raise ValueError("x: need a tensor of rows")
+    lead = x.shape[:-1]
+    wide = (*lead, layer.rows)
+    xs, ys = _acts(x, dtype, (*lead, cols), "x"), _acts(y, dtype, wide, "y")
+    rs = _ABSENT if r is None else _acts(r, dtype, wide, "r")
+    zs = _ABSENT if z is None else _acts(z, dtype, wide, "z")
+    args = _dev(w, dtype, plan.n_total, "w"), *xs, x.numel() // cols, int(act), *rs, *zs, *ys, *_ws(ws)
+    _call("gc_linear_forward", [t for t in (y, x, w, ws, r, z) if t is not None], plan.handle, ctypes.byref(layer), *args)
+
+
+def gc_act_grad(dy: torch.Tensor, z: torch.Tensor, act: int, dz: torch.Tensor):
+    """dz = dy act'(z), elementwise; dz may be dy or z."""
+    if not isinstance(dy, _Tensor) or dy.dtype not in _FLOAT_TYPES or dy.dim() < 1:
+        raise ValueError("dy: need an fp32, bf16 or fp16 tensor of rows")
+    shape = tuple(dy.shape)
+    cols = shape[-1]
+    ys, zs, ds = (_acts(t, dy.dtype, shape, name) for t, name in ((dy, "dy"), (z, "z"), (dz, "dz")))
+    _call("gc_act_grad", (dz, dy, z), *ys, *zs, int(act), _FLOAT_TYPES[dy.dtype], dy.numel() // cols if cols else 0, cols, *ds)
+
+
+def gc_linear_grad_input(plan: Plan, layer: gc_linear, w, dz: torch.Tensor, dx, ws: torch.Tensor, a=None,
+                         act: int = GC_ACT_NONE, z=None, dzx=None):
+    """dx = dz W + a, and dzx = (dz W + a) act'(z); dx or dzx may be None."""
+    cols, dtype = _layer_cols(plan, layer), _DTYPES[layer.type]
+    if not isinstance(dz, _Tensor) or dz.dim() < 1:
+        raise ValueError("dz: need a tensor of rows")
+    lead = dz.shape[:-1]
+    narrow = (*lead, cols)
+    ds = _acts(dz, dtype, (*lead, layer.rows), "dz")
+    als, zs, xs, gs = (_ABSENT if t is None else _acts(t, dtype, narrow, name)
+                       for t, name in ((a, "a"), (z, "z"), (dx, "dx"), (dzx, "dzx")))
+    args = _dev(w, dtype, plan.n_total, "w"), *ds, dz.numel() // layer.rows, *als, int(act), *zs, *xs, *gs, *_ws(ws)
+    _call("gc_linear_grad_input", [t for t in (dz, w, ws, a, z, dx, dzx) if t is not None], plan.handle,
+          ctypes.byref(layer), *args)
+
+
+def gc_linear_grad_weight(plan: Plan, layer: gc_linear, dz: torch.Tensor, x: torch.Tensor, g, accumulate: bool,
+                          ws: torch.Tensor):
+    """dz^T x over (accumulate False) or added to the layer's segment of the
+    flat fp32 g, and the sum of dz's rows to its bias' segment."""
+    cols, dtype = _layer_cols(plan, layer), _DTYPES[layer.type]
+    if not isinstance(x, _Tensor) or x.dim() < 1:
+        raise ValueError("x: need a tensor of rows")
+    lead = x.shape[:-1]
+    ds, xs = _acts(dz, dtype, (*lead, layer.rows), "dz"), _acts(x, dtype, (*lead, cols), "x")
+    args = *ds, *xs, x.numel() // cols, _f32(g, plan.n_total, "g"), int(bool(accumulate)), *_ws(ws)
+    _call("gc_linear_grad_weight", (g, dz, x, ws), plan.handle, ctypes.byref(layer), *args)
+
+
+# ---------------------------------------------------------- distillation
+def _logits(t, name: str):
+    """(pointer, GC_* type, row stride, rows, columns) of logits [..., columns]."""
+    if not isinstance(t, _Tensor) or t.dtype not in _FLOAT_TYPES or t.dim() < 1 or t.shape[-1] < 1:
+        raise ValueError(f"{name}: need an fp32, bf16 or fp16 tensor of rows")
+    v = t.shape[-1]
+    return t.data_ptr(), _FLOAT_TYPES[t.dtype], v if t.is_contiguous() else _row_stride(t, name), t.numel() // v, v
+
+
+def gc_top_logits(logits: torch.Tensor, idx: torch.Tensor, val, lse=None, temperature: float = 1.0):
+    """The idx.shape[-1] first logits of every row, by value and then by
+    column: int32 columns and fp32 values; lse: the rows' log-sum-exp at 1 /
+    temperature, fp32."""
+    ptr, kind, stride, n, vocab = _logits(logits, "logits")
+    k = idx.shape[-1] if isinstance(idx, _Tensor) and idx.dim() else 0
+    if k < 1 or tuple(idx.shape[:-1]) != tuple(logits.shape[:-1]) or not isinstance(val, _Tensor) or val.shape != idx.shape:
+        raise ValueError("idx, val: need the logits' rows by k columns")
+    ip, vp = _dev(idx, torch.int32, n * k, "idx"), _f32(val, n * k, "val")
+    lp = None if lse is None else _f32(lse, n, "lse")
+    _call("gc_top_logits", [t for t in (logits, idx, val, lse) if t is not None], ptr, kind, stride, n, vocab, k,
+          float(temperature), ip, vp, lp)
+
+
+def distill_options(temperature: float = 1.0, kd_weight: float = 1.0, ce_weight: float = 0.0, grad_scale: float = 1.0,
+                    tail: bool = False) -> gc_distill_options:
+    """tail: the teacher's mass outside its entries is held too (GC_DISTILL_REST)."""
+    return gc_distill_options(float(temperature), float(kd_weight), float(ce_weight), float(grad_scale),
+                              GC_DISTILL_REST if tail else GC_DISTILL_TOP)
+
+
+def gc_distill_loss(logits: torch.Tensor, idx: torch.Tensor, t: torch.Tensor, opt: gc_distill_options, loss,
+                    dlogits=None, t_lse=None, labels=None, weights=None):
+    """The rows' losses against the teacher's entries (idx, t) [..., k], and the
+    gradient of their sum times opt.grad_scale; dlogits may be logits."""
+    ptr, kind, stride, n, vocab = _logits(logits, "logits")
+    lead = tuple(logits.shape[:-1])
+    if not isinstance(idx, _Tensor) or not isinstance(t, _Tensor) or idx.dim() < 1 or tuple(idx.shape[:-1]) != lead or t.shape != idx.shape:
+        raise ValueError("idx, t: need the logits' rows by k columns")
+    id_type, t_type, k = _TOKEN_TYPES.get(idx.dtype), _FLOAT_TYPES.get(t.dtype), idx.shape[-1]
+    if id_type is None or t_type is None:
+        raise ValueError("idx, t: need int32 or int64, and fp32, bf16 or fp16")
+    istride, tstride = (k if u.is_contiguous() else _row_stride(u, "idx, t") for u in (idx, t))
+    dp, ds = _ABSENT if dlogits is None else _acts(dlogits, logits.dtype, logits.shape, "dlogits")
+    tl, wp = (None if u is None else _f32(u, n, name) for u, name in ((t_lse, "t_lse"), (weights, "weights")))
+    lp = None if labels is None else _dev(labels, idx.dtype, n, "labels")
+    _call("gc_distill_loss", [u for u in (logits, idx, t, loss, dlogits, t_lse, labels, weights) if u is not None], ptr, kind,
+          stride, n, vocab, idx.data_ptr(), id_type, istride, t.data_ptr(), t_type, tstride, k, tl, lp, wp,
+          ctypes.byref(opt), _f32(loss, n, "loss"), dp, ds)

@@ -27,36 +27,6 @@ namespace gc {
 
 namespace {
 
-// N elements with the alignment of one: the hardware's unaligned mode takes
-// 8 or 16 bytes as one access, so odd offsets and strides need no variant.
-template <class S, int N>
-struct __attribute__((packed, aligned(sizeof(S)))) Pack {
-    S v[N];
-};
-
-// Storage types.
-struct F32 {
-    using Store = float;
-    static __device__ __forceinline__ float to_f32(float x) { return x; }
-    static __device__ __forceinline__ float from_f32(float x) { return x; }
-};
-struct BF16 {
-    using Store = uint16_t;
-    static __device__ __forceinline__ float to_f32(uint16_t x) { return dev_u2f(uint32_t(x) << 16); }
-    static __device__ __forceinline__ uint16_t from_f32(float x) {
-        return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x));
-    }
-};
-struct F16 {
-    using Store = uint16_t;
-    static __device__ __forceinline__ float to_f32(uint16_t x) {
-        return static_cast<float>(__builtin_bit_cast(_Float16, x));
-    }
-    static __device__ __forceinline__ uint16_t from_f32(float x) {
-        return __builtin_bit_cast(uint16_t, static_cast<_Float16>(x));
-    }
-};
-
 // N columns of a row from column c on; those at or past cols are 0 / dropped.
 // A vector access needs all of them, so a row's last lane goes by elements.
 template <class T, int N>

@@ -192,6 +192,37 @@ __device__ __forceinline__ float dev_u2f(uint32_t u) { return __builtin_bit_cast
 __device__ __forceinline__ int lane_id() { return threadIdx.x & (kWave - 1); }
 __device__ __forceinline__ int wave_id() { return threadIdx.x / kWave; }
 
+// N elements with the alignment of one: the hardware's unaligned mode takes
+// 8 or 16 bytes as one access, so odd offsets and strides need no variant.
+template <class S, int N>
+struct __attribute__((packed, aligned(sizeof(S)))) Pack {
+    S v[N];
+};
+
+// Storage types of activations: their values in fp32, and back with one rounding to
+// nearest, ties to even.
+struct F32 {
+    using Store = float;
+    static __device__ __forceinline__ float to_f32(float x) { return x; }
+    static __device__ __forceinline__ float from_f32(float x) { return x; }
+};
+struct BF16 {
+    using Store = uint16_t;
+    static __device__ __forceinline__ float to_f32(uint16_t x) { return dev_u2f(uint32_t(x) << 16); }
+    static __device__ __forceinline__ uint16_t from_f32(float x) {
+        return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x));
+    }
+};
+struct F16 {
+    using Store = uint16_t;
+    static __device__ __forceinline__ float to_f32(uint16_t x) {
+        return static_cast<float>(__builtin_bit_cast(_Float16, x));
+    }
+    static __device__ __forceinline__ uint16_t from_f32(float x) {
+        return __builtin_bit_cast(uint16_t, static_cast<_Float16>(x));
+    }
+};
+
 // Number of set bits of a wave mask below this lane.
 __device__ __forceinline__ uint32_t lane_rank(uint64_t mask) {
     return __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(mask >> 32),

@@ -18,8 +18,9 @@
  *             and the experimental setup (Quant-DP baseline: random
  *             quantization with buckets of 512).
  *   The embedding's lookup and gradient and the orthogonalised matrix update
- *   (Newton-Schulz products, as the Muon optimiser applies them) come from no
- *   page: they are given by their formulas at each call.
+ *   (Newton-Schulz products, as the Muon optimiser applies them), the layers'
+ *   products, the top logits and the distillation loss come from no page: they
+ *   are given by their formulas at each call.
  *
  * Conventions shared by every call
  * --------------------------------
@@ -759,6 +760,174 @@ typedef struct gc_muon_options {
 gc_status gc_muon_step(const gc_matrix_plan *mplan, const float *G, float *U, float *W,
                        const gc_muon_options *opt, void *ws, size_t ws_bytes, hipStream_t stream);
 
+/* ------------------------------------------------------- layer products */
+/*
+ * A layer of the model: segment `seg` of the plan is its weight matrix W, rows
+ * x cols, row-major (cols = length / rows), segment `bias_seg` its bias b of
+ * `rows` elements (-1: none).  A batch is n_tokens rows of activations; every
+ * such array has elements of `type` and its own stride, in elements, from one
+ * row to the next (at least the row's length; the elements between are neither
+ * read nor written).  w is the flat model in that type: the fp32 buffer itself,
+ * or a copy of it in bf16 or fp16 with the same offsets.
+ * Sums are fp32 over exact products for bf16 and fp16, of fp32 products for
+ * fp32; each output is rounded once.  The order of a sum is fixed by the
+ * shapes, so the same call gives the same bits.  NaN and Inf go where the
+ * formulas take them; no row or column reaches another's results.
+ *
+ * Activations: act(z) is z (GC_ACT_NONE), max(z, 0) (RELU; NaN stays),
+ * z Phi(z) (GELU; Phi the normal distribution), z s(2 u) with
+ * u = sqrt(2 / pi) (z + 0.044715 z^3) (GELU_TANH; s(v) = 1 / (1 + exp(-v))),
+ * z s(z) (SILU).  RELU's slope at 0 is 0.
+ */
+#define GC_ACT_NONE       0
+#define GC_ACT_RELU       1
+#define GC_ACT_GELU       2
+#define GC_ACT_GELU_TANH  3
+#define GC_ACT_SILU       4
+typedef struct gc_linear {
+    int      seg;
+    uint32_t rows;          /* outputs; must divide the segment's length        */
+    int      bias_seg;      /* a segment of `rows` elements, or -1: no bias     */
+    int      type;          /* GC_F32, GC_BF16 or GC_F16                        */
+    uint32_t reserved[2];   /* must be 0                                        */
+} gc_linear;
+
+/* Device workspace bytes of the three calls below for up to n_tokens rows (0
+ * on an argument error).  Calls that run one after the other can share one. */
+size_t gc_linear_workspace_bytes(const gc_plan *plan, const gc_linear *layer, uint64_t n_tokens);
+
+/*
+ * z = x W^T + b;  y = act(z) + r.
+ *   w [n_total] in; x [n_tokens][cols] in; y [n_tokens][rows] out.
+ *   r [n_tokens][rows] in, or NULL: nothing is added.  r may be y (with its stride).
+ *   z [n_tokens][rows] out, or NULL: z (rounded to the type; y is formed
+ *     before that rounding), which gc_act_grad and gc_linear_grad_input take.
+ * n_tokens == 0 enqueues nothing.
+ * Errors: GC_EINVAL (null, seg, rows or bias_seg that do not fit the plan,
+ *         unknown type or act, reserved not 0, a stride below its row, buffers
+ *         not aligned to their elements, an output that is another buffer of
+ *         the call), GC_ERANGE (n_tokens >= 2^28, n_tokens * max(rows, cols) >
+ *         2^35, n_tokens * a stride > 2^48, more workgroups than a launch has),
+ *         GC_ECAPACITY (ws).
+ */
+gc_status gc_linear_forward(const gc_plan *plan, const gc_linear *layer, const void *w, const void *x,
+                            uint64_t x_stride, uint64_t n_tokens, int act, const void *r, uint64_t r_stride,
+                            void *z, uint64_t z_stride, void *y, uint64_t y_stride, void *ws, size_t ws_bytes,
+                            hipStream_t stream);
+
+/*
+ * dz = dy act'(z), the first step of the way back where no other call's
+ * epilogue does it; n_rows x cols elements of `type`.  dz may be dy or z (with
+ * its stride).
+ * Errors: GC_EINVAL (null, unknown type or act, strides, misaligned buffers),
+ *         GC_ERANGE (as above).
+ */
+gc_status gc_act_grad(const void *dy, uint64_t dy_stride, const void *z, uint64_t z_stride, int act, int type,
+                      uint64_t n_rows, uint64_t cols, void *dz, uint64_t dz_stride, hipStream_t stream);
+
+/*
+ * The gradient of the layer's input, and of what the layer before it
+ * activated: g = dz W + a;  dx = g;  dzx = g act'(z), where x = act(z) (+ a
+ * residual) and a is the gradient that reaches x another way.
+ *   dz [n_tokens][rows] in; w as above.
+ *   a [n_tokens][cols] in, or NULL.  a may be dx or dzx (with its stride).
+ *   dx, dzx [n_tokens][cols] out; either may be NULL, not both.  dzx is formed
+ *     from g before its rounding to dx.
+ *   z [n_tokens][cols] in; needed with dzx unless act is GC_ACT_NONE.
+ * Errors: as gc_linear_forward.
+ */
+gc_status gc_linear_grad_input(const gc_plan *plan, const gc_linear *layer, const void *w, const void *dz,
+                               uint64_t dz_stride, uint64_t n_tokens, const void *a, uint64_t a_stride, int act,
+                               const void *z, uint64_t z_stride, void *dx, uint64_t dx_stride, void *dzx,
+                               uint64_t dzx_stride, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * The gradient of the layer's weights, in the flat gradient that the
+ * compression calls and gc_muon_step take: segment seg of g becomes dz^T x
+ * and segment bias_seg (if any) the sum of dz's rows (accumulate == 0), or
+ * fl32(g + that) (accumulate != 0).  Always fp32.
+ *   dz [n_tokens][rows], x [n_tokens][cols] in; g [n_total] out (in/out).
+ * n_tokens == 0 clears the segments, or with accumulate enqueues nothing.
+ * Errors: as gc_linear_forward.
+ */
+gc_status gc_linear_grad_weight(const gc_plan *plan, const gc_linear *layer, const void *dz, uint64_t dz_stride,
+                                const void *x, uint64_t x_stride, uint64_t n_tokens, float *g, int accumulate,
+                                void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------- distillation */
+/*
+ * Logits: n_rows rows of `vocab` elements of `type`, `stride` elements apart.
+ * A logit of -Inf is a masked column.
+ */
+#define GC_MAX_VOCAB       (1u << 20)
+#define GC_MAX_TOP_LOGITS  1024
+
+/*
+ * The top logits of every row, as a teacher sends them: the k entries first in
+ * the order (value descending, index ascending) among the logits that are
+ * neither NaN nor -Inf (+0 equals -0; exact, ties included).
+ *   idx [n_rows][k] out: int32 columns; -1 behind a row's last entry.
+ *   val [n_rows][k] out: the logits in fp32 (exact); -Inf there.
+ *   lse [n_rows] out, or NULL: log sum_j exp(z_j / temperature) over the whole
+ *     row (-Inf where every column is masked, NaN where one is NaN).
+ * n_rows == 0 enqueues nothing.
+ * Errors: GC_EINVAL (null, unknown type, k = 0, stride < vocab, vocab = 0,
+ *         temperature not positive and finite, misaligned buffers), GC_ENOTSUP
+ *         (vocab > GC_MAX_VOCAB, k > GC_MAX_TOP_LOGITS), GC_ERANGE (n_rows >=
+ *         2^22, n_rows * stride > 2^48).
+ */
+gc_status gc_top_logits(const void *logits, int type, uint64_t stride, uint64_t n_rows, uint32_t vocab,
+                        uint32_t k, float temperature, int32_t *idx, float *val, float *lse,
+                        hipStream_t stream);
+
+/*
+ * The loss of a student's rows z against a teacher's top logits t_k at columns
+ * c_k, and its gradient.  T = temperature, p = softmax(z / T).
+ *   GC_DISTILL_TOP : q_k = exp(t_k / T) / sum of those (renormalised), q_r = 0
+ *   GC_DISTILL_REST: q_k = exp(t_k / T - t_lse), q_r = max(0, 1 - sum_k q_k),
+ *                    the mass of all columns that no entry names (p_r in the
+ *                    student); where those are all masked, q_r = 0
+ *   KL = sum_k q_k (log q_k - log p_{c_k}) + q_r (log q_r - log p_r)
+ *        (a term with q = 0 is 0)
+ *   loss = weight (kd_weight T^2 KL + ce_weight (log sum exp(z) - z_label))
+ *   dlogits = grad_scale d loss / d z
+ * An entry whose column lies outside [0, vocab), or whose t_k is -Inf, is no
+ * entry; without any, or with kd_weight 0, there is no KL term.  Without a
+ * label in [0, vocab), or with ce_weight 0, there is no label's term.  A row with neither, or with weight 0, has loss 0 and a
+ * gradient of +0, whatever its logits are.  A column that several entries name
+ * takes each of them.  A NaN or +Inf in a row that counts makes its loss and its
+ * gradient NaN; a masked column's gradient is +-0 unless the teacher or the
+ * label names it.
+ *   idx [n_rows][idx_stride]: k int32 or int64 (idx_type GC_TOKENS_*); t
+ *   [n_rows][t_stride]: k values of t_type; t_lse [n_rows] fp32 for
+ *   GC_DISTILL_REST (gc_top_logits writes it, for the same T); labels [n_rows]
+ *   of idx_type, or NULL; weights [n_rows] fp32, or NULL: 1.
+ *   loss [n_rows] fp32 out.
+ *   dlogits [n_rows][dstride] of `type` out, or NULL: the loss alone.  dlogits
+ *     may be logits (with its stride).
+ * k == 0 leaves the labels' term alone.  n_rows == 0 enqueues nothing.
+ * Sums are fp32 (over the teacher's entries in double) in an order that the
+ * sizes fix.
+ * Errors: as gc_top_logits; GC_EINVAL also for unknown types, a mode,
+ *         kd_weight, ce_weight or grad_scale not finite, t_lse missing,
+ *         reserved not 0.
+ */
+#define GC_DISTILL_TOP   0
+#define GC_DISTILL_REST  1
+typedef struct gc_distill_options {
+    float    temperature;   /* > 0                */
+    float    kd_weight;
+    float    ce_weight;
+    float    grad_scale;
+    int      mode;          /* GC_DISTILL_*       */
+    uint32_t reserved[3];   /* must be 0          */
+} gc_distill_options;
+gc_status gc_distill_loss(const void *logits, int type, uint64_t stride, uint64_t n_rows, uint32_t vocab,
+                          const void *idx, int idx_type, uint64_t idx_stride, const void *t, int t_type,
+                          uint64_t t_stride, uint32_t k, const float *t_lse, const void *labels,
+                          const float *weights, const gc_distill_options *opt, float *loss, void *dlogits,
+                          uint64_t dstride, hipStream_t stream);
+
 /* ----------------------------------------------------------- measurement */
 /*
  * Kernel timing for measurement tools (off by default).  While enabled, each
@@ -778,7 +947,8 @@ gc_status gc_muon_step(const gc_matrix_plan *mplan, const float *G, float *U, fl
  *             embed_heads, embed_rows, embed_sum, embed_join, embed_small,
  *             embed_empty,
  *             orth_norm, orth_scale, orth_split, orth_gram, orth_poly,
- *             orth_pair, orth_apply, orth_join, orth_slab, orth_small.
+ *             orth_pair, orth_apply, orth_join, orth_slab, orth_small,
+ *             linear_product, linear_join, act_grad, top_logits, distill.
  * gc_timing_take waits for the recorded events of one kernel and returns the
  * summed duration in milliseconds and the number of launches, then forgets
  * them.  Host-thread safe; not for use while a stream is being captured.

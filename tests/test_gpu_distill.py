@@ -1,0 +1,287 @@
+"""The top logits of a row, exactly, and the distillation loss with its gradient
+against 64 bits: ties, masks, empty rows, every mode, odd sizes and strides.
+
+Bounds of the loss: an exponential of d = (z - max) / T costs at most
+(|d| + 4) 2^-23 of itself (d's two roundings, its scaling, the function, the
+sum's rounding), a fixed sum of at most 2^20 terms in blocks (no chain is
+longer than 2^10 / 2 + 40) 600 2^-24 of itself, a logarithm 4 steps.  So a
+probability is off by (|d| + 1000) 2^-23 of itself, and log p by 1000 2^-23 +
+|d| 2^-22."""
+import math
+
+import pytest
+import torch
+
+from gradient_compression_dnn_amd import binding as B
+from tests.gpu_util import say
+from tests.layer_util import DTYPES, U32, Rows, half_step
+
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+
+
+def logits(n, vocab, dtype, kind, pitch=0, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed * 7919 + n + vocab)
+    z = 3.0 * torch.randn(n, vocab, generator=g, device="cuda")
+    if kind == "ties":      # few distinct values, +0 and -0 among them
+        z = torch.round(z / 3.0) * torch.where(torch.rand(z.shape, generator=g, device="cuda") < 0.5, 1.0, -1.0)
+    elif kind == "equal":
+        z = torch.full_like(z, -2.5)
+    elif kind == "masked":  # columns out, whole rows out, one column left
+        z[torch.rand(z.shape, generator=g, device="cuda") < 0.4] = -INF
+        z[::3] = -INF
+        if n > 1:
+            z[1, :] = -INF
+            z[1, vocab // 2] = 0.25
+    elif kind == "special":
+        z[torch.rand(z.shape, generator=g, device="cuda") < 0.1] = float("nan")
+        z[torch.rand(z.shape, generator=g, device="cuda") < 0.1] = INF
+        z[torch.rand(z.shape, generator=g, device="cuda") < 0.1] = torch.finfo(DTYPES[dtype]).min
+    elif kind == "wide":    # far below the maximum, the type's lowest value as a mask
+        z = z * 30.0
+        z[:, ::5] = torch.finfo(DTYPES[dtype]).min
+    elif kind == "rising":
+        z = torch.arange(vocab, device="cuda").float().repeat(n, 1) / vocab
+    return Rows(n, vocab, DTYPES[dtype], pitch, z)
+
+
+SIZES = [(1, 1, 1), (2, 2, 1), (3, 65, 65), (5, 1000, 8), (2, 4097, 64), (3, 8192, 1000), (2, 20001, 1024), (70, 515, 3),
+         (2, 65536, 256), (1, 131071, 64), (1, 262145, 17)]
+KINDS = ["normal", "ties", "equal", "masked", "special", "rising"]
+
+
+@pytest.mark.parametrize("n,vocab,k", SIZES)
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_top_logits_exactly(n, vocab, k, dtype):
+    for i, kind in enumerate(KINDS):
+        say(f"top {n}x{vocab} k={k} {dtype} {kind}")
+        z = logits(n, vocab, dtype, kind, (0, 5, 8)[i % 3], i)
+        idx = torch.full((n, k), -7, dtype=torch.int32, device="cuda")
+        val, lse = torch.full((n, k), 7.0, device="cuda"), torch.full((n,), 7.0, device="cuda")
+        B.gc_top_logits(z.t, idx, val, lse, temperature=2.0)
+        v = z.f64() + 0.0
+        v = torch.where(torch.isnan(v), torch.full_like(v, -INF), v)
+        s, j = torch.sort(v, dim=1, descending=True, stable=True)
+        want = torch.where(s[:, :k] > -INF, j[:, :k], -1).int()
+        assert torch.equal(idx, want)
+        exact = torch.where(want >= 0, torch.gather(z.f64(), 1, want.clamp(min=0).long()), torch.tensor(-INF, dtype=torch.float64, device="cuda"))
+        assert torch.equal(val.double(), exact)
+        l64 = torch.logsumexp(z.f64() / 2.0, 1)
+        fine = torch.isfinite(l64)
+        assert torch.equal(torch.isnan(l64), torch.isnan(lse)) and torch.equal(l64[~fine & ~torch.isnan(l64)].float(), lse[~fine & ~torch.isnan(l64)])
+        assert bool(((lse.double() - l64).abs()[fine] <= (1000 * 2 ** -23 + 4 * U32 * l64.abs())[fine]).all())
+        # without the sums, and the same bits again
+        idx2, val2 = torch.empty_like(idx), torch.empty_like(val)
+        B.gc_top_logits(z.t, idx2, val2)
+        assert torch.equal(idx, idx2) and torch.equal(val, val2) and z.guards_kept()
+
+
+def reference(z, idx, t, T, kd, ce, scale, rest, tlse, labels, weights):
+    """The loss and its gradient in 64 bits, a row at a time from the definition."""
+    n, V = z.shape
+    loss, grad = torch.zeros(n, dtype=torch.float64, device=z.device), torch.zeros_like(z)
+    for r in range(n):
+        w = 1.0 if weights is None else float(weights[r])
+        there = (idx[r] >= 0) & (idx[r] < V) & (t[r] > -INF)
+        c, tt = idx[r][there].long(), t[r][there]
+        lab = int(labels[r]) if labels is not None and ce else -1
+        some, labelled = bool(there.any()) and kd != 0, 0 <= lab < V
+        if w == 0 or not (some or labelled):
+            continue
+        L = torch.zeros((), dtype=torch.float64, device=z.device)
+        if some:
+            logp = torch.log_softmax(z[r] / T, 0)
+            q = torch.exp(tt / T - float(tlse[r])) if rest else torch.softmax(tt / T, 0)
+            kl = torch.special.xlogy(q, q).sum() - torch.where(q > 0, q * logp[c], 0.0 * q).sum()
+            mask = torch.ones(V, dtype=torch.bool, device=z.device)
+            mask[c] = False
+            lr = torch.where(mask, logp, torch.full_like(logp, -INF))
+            held = max(0.0, 1.0 - float(q.sum())) if rest and bool((lr > -INF).any()) else 0.0
+            g = (q.sum() + held) * torch.exp(logp)
+            g.index_add_(0, c, -q)
+            if held > 0:
+                l_r = torch.logsumexp(lr, 0)
+                kl = kl + held * (math.log(held) - l_r)
+                g = g - held * torch.exp(lr - l_r)
+            L = L + kd * T * T * kl
+            grad[r] += kd * T * g
+        if labelled:
+            log1 = torch.log_softmax(z[r], 0)
+            L = L - ce * log1[lab]
+            grad[r] += ce * torch.exp(log1)
+            grad[r, lab] -= ce
+        loss[r], grad[r] = w * L, w * scale * grad[r]
+    return loss, grad
+
+
+class Case:
+    def __init__(self, n, vocab, k, dtype, kind, T, seed, ids=torch.int32, ttype="f32", pitch=0, dup=False):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.z = logits(n, vocab, dtype, kind, pitch, seed)
+        t = torch.where(torch.isfinite(self.z.t.float()), self.z.t.float(), -9.0) + torch.randn(n, vocab, generator=g, device="cuda")
+        t = t.clamp(-60, 60)
+        v, i = torch.topk(t, k, dim=1)
+        if dup and k > 2:  # a column named twice, entries that are none, an entry masked
+            i[:, k - 1] = i[:, 0]
+            i[::2, 1] = -1
+            i[1::2, 1] = vocab
+            v[:, 2] = -INF
+        if n > 2:
+            i[2] = -1     # a row without a teacher
+        self.idx = Rows(n, k, ids, 3, i.to(ids))
+        self.t = Rows(n, k, DTYPES[ttype], 1, v)
+        self.tlse = torch.logsumexp(t / T, 1)
+        self.labels = torch.randint(-1, vocab + 1, (n,), generator=g, device="cuda").to(ids)
+        self.labels[0] = i[0, 0].to(ids)
+        self.weights = torch.rand(n, generator=g, device="cuda") + 0.25
+        if n > 4:
+            self.weights[4] = 0.0
+
+
+LOSS_SIZES = [(1, 1, 1), (3, 2, 2), (5, 65, 64), (7, 1000, 8), (6, 4097, 33), (3, 20001, 1000), (2, 65536, 64), (2, 131071, 256), (1, 262145, 5)]
+
+
+@pytest.mark.parametrize("n,vocab,k", LOSS_SIZES)
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_loss_and_gradient(n, vocab, k, dtype):
+    D = DTYPES[dtype]
+    settings = [("normal", 1.0, False, 0.0, torch.int32, "f32", 0, False), ("normal", 2.0, False, 0.5, torch.int64, "bf16", 5, True),
+                ("normal", 3.0, True, 0.0, torch.int32, "f32", 8, False), ("ties", 2.0, True, 0.7, torch.int64, "f16", 1, True),
+                ("wide", 4.0, True, 0.5, torch.int32, "f32", 0, False), ("equal", 1.0, True, 0.3, torch.int32, "f32", 0, True)]
+    for i, (kind, T, rest, ce, ids, ttype, pitch, dup) in enumerate(settings):
+        say(f"distill {n}x{vocab} k={k} {dtype} {kind} T={T} rest={rest} ce={ce}")
+        c = Case(n, vocab, k, dtype, kind, T, 10 + i, ids, ttype, pitch, dup)
+        kd, scale = 0.8, 64.0
+        labels, weights, tlse = c.labels if ce else None, c.weights if i % 2 else None, c.tlse if rest else None
+        opt = B.distill_options(T, kd, ce, scale, tail=rest)
+        loss, dz = torch.full((n,), 7.0, device="cuda"), Rows(n, vocab, D, pitch)
+        B.gc_distill_loss(c.z.t, c.idx.t, c.t.t, opt, loss, dz.t, t_lse=tlse, labels=labels, weights=weights)
+        want_l, want_g = reference(c.z.f64(), c.idx.t, c.t.f64(), T, kd, ce, scale, rest, tlse, labels, weights)
+        w = torch.ones(n, dtype=torch.float64, device="cuda") if weights is None else weights.double()
+        zf = c.z.f64()
+        d = torch.where(torch.isfinite(zf), zf.amax(1, keepdim=True) - zf, torch.zeros_like(zf))
+        # q: its own exponential of at most |t / T - lse| <= 130; entries of a row add up to at most k of them
+        eq = (130 + 1000) * 2.0 ** -23
+        deepest = torch.gather(d, 1, c.idx.t.long().clamp(0, vocab - 1)).amax(1)
+        lab_d = torch.gather(d, 1, c.labels.long().clamp(0, vocab - 1)[:, None])[:, 0]
+        elog = 1000 * 2.0 ** -23
+        mass = max(1.0, k / 1.0 if dup else 1.0) + 1.0
+        # |KL's terms| <= mass (|log q| + |log p|); q_r is off by eq in all, where log q_r may be as large as 17
+        room_l = w * (kd * T * T * (mass * ((eq + elog) * (130 + deepest / T + 40) + deepest / T * 2.0 ** -21)) + ce * (elog + lab_d * 2.0 ** -21)) + 8 * U32 * want_l.abs()
+        assert bool(((loss.double() - want_l).abs() <= room_l).all()), (loss, want_l, room_l)
+        # gradient: each of its terms to its own relative error, q (and with it q_r) to eq
+        p_t, p_1 = torch.softmax(zf / T, 1), torch.softmax(zf, 1)
+        ep = lambda x: (x + 1000) * 2.0 ** -23
+        room = kd * T * ((mass * p_t) * (ep(d / T) + 2 * eq)) + ce * (p_1 * ep(d))
+        named = torch.zeros_like(zf).scatter_add_(1, c.idx.t.long().clamp(0, vocab - 1), torch.ones_like(c.t.f64()))
+        room = room + kd * T * named * 2 * eq + ce * 4 * U32
+        if rest:  # softmax over the rest: q_r of at most 1, relative to its own maximum
+            lr = torch.where(named > 0, torch.full_like(zf, -INF), zf / T)
+            top = lr.amax(1, keepdim=True)
+            pr = torch.where(torch.isfinite(top), torch.softmax(lr, 1), torch.zeros_like(zf))
+            room = room + kd * T * pr * (ep(torch.where(torch.isfinite(lr), top - lr, torch.zeros_like(lr)) + d.amax(1, keepdim=True) / T * 0) + 2 * eq)
+        room = (w * scale)[:, None] * room
+        tiny = torch.finfo(D).smallest_normal * torch.finfo(D).eps
+        off = (dz.f64() - want_g).abs()
+        lim = room + half_step(D) * (want_g.abs() + room) + tiny
+        assert bool((off <= lim).all()), (float((off / lim).max()), int((off > lim).sum()))
+        assert dz.guards_kept() and c.z.guards_kept() and c.idx.t.shape == (n, k)
+        # the loss alone, and in place of the logits: the same bits
+        loss2 = torch.zeros_like(loss)
+        B.gc_distill_loss(c.z.t, c.idx.t, c.t.t, opt, loss2, None, t_lse=tlse, labels=labels, weights=weights)
+        assert torch.equal(loss, loss2)
+        B.gc_distill_loss(c.z.t, c.idx.t, c.t.t, opt, loss2, c.z.t, t_lse=tlse, labels=labels, weights=weights)
+        assert torch.equal(c.z.t, dz.t) and torch.equal(loss, loss2) and c.z.guards_kept()
+
+
+@pytest.mark.parametrize("rest", [False, True])
+def test_gradient_against_differences(rest):
+    """Along a direction u the loss changes by its gradient's product with u:
+    central differences of the kernel's losses with h = 1/16."""
+    n, V, k, T, ce = 6, 300, 16, 2.0, 0.5
+    c = Case(n, V, k, "f32", "normal", T, 77)
+    opt = B.distill_options(T, 1.0, ce, 1.0, tail=rest)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    u = torch.rand(n, V, generator=g, device="cuda") * 2 - 1
+    h = 1.0 / 16
+    kw = dict(t_lse=c.tlse if rest else None, labels=c.labels, weights=c.weights)
+
+    def loss(z, dz=None):
+        out = torch.zeros(n, device="cuda")
+        B.gc_distill_loss(z, c.idx.t, c.t.t, opt, out, dz, **kw)
+        return out.double()
+
+    dz = torch.zeros(n, V, device="cuda")
+    loss(c.z.t, dz)
+    diff = (loss(c.z.t + h * u) - loss(c.z.t - h * u)) / (2 * h)
+    # a log-sum-exp along |u| <= 1 has a third derivative of at most 2 (T = 1), 2 / T^3; KL holds two of them, times T^2
+    room = c.weights.double() * (h * h / 6 * (T * T * 2 * 2 / T ** 3 + ce * 2) + (T * T + ce) * 2000 * 2.0 ** -23 * 10 / h)
+    assert bool(((diff - (dz.double() * u.double()).sum(1)).abs() <= room).all())
+
+
+def test_rows_that_count_for_nothing():
+    """No teacher and no label, or weight 0: loss 0 and a gradient of +0,
+    whatever the logits are; masked columns get 0."""
+    V, k = 5000, 4
+    z = torch.randn(6, V, device="cuda").to(torch.bfloat16)
+    z[0], z[1, 7], z[2, 3] = float("nan"), INF, float("nan")
+    z[3:, 100:] = -INF
+    idx = torch.arange(k, device="cuda").repeat(6, 1)
+    t = torch.randn(6, k, device="cuda")
+    idx[0], t[1] = -5, -INF
+    w = torch.tensor([1.0, 1.0, 0.0, 1.0, 1.0, 1.0], device="cuda")
+    for rest in (False, True):
+        loss, dz = torch.full((6,), 9.0, device="cuda"), torch.full_like(z, 9.0)
+        B.gc_distill_loss(z, idx, t, B.distill_options(2.0, 1.0, 0.5, tail=rest), loss, dz, t_lse=torch.logsumexp(t / 2, 1) + 0.1, weights=w)
+        assert bool((loss[:3] == 0).all()) and bool((dz[:3] == 0).all()) and not bool(torch.signbit(dz[:3]).any())
+        assert bool((dz[3:, 100:] == 0).all()) and bool(torch.isfinite(dz).all()) and bool((loss[3:] > 0).all())
+    # a row that counts: NaN in the loss and the gradient of that row alone
+    w[2] = 1.0
+    B.gc_distill_loss(z, idx, t, B.distill_options(2.0), loss, dz, weights=w)
+    assert bool(torch.isnan(loss[2])) and bool(torch.isnan(dz[2]).any()) and bool(torch.isfinite(loss[3:]).all())
+    # a teacher's column that is masked in the student: no finite loss, and a finite gradient that pulls it up
+    z[4, 2] = -INF
+    B.gc_distill_loss(z, idx, t, B.distill_options(2.0), loss, dz, weights=w)
+    assert float(loss[4]) == INF and bool(torch.isfinite(dz[4]).all()) and float(dz[4, 2]) < 0
+
+
+def test_rest_of_a_sure_student():
+    """The student's mass outside the entries far below 2^-24 keeps its
+    logarithm and its gradient: nothing is formed as 1 - p."""
+    V, T = 1000, 1.0
+    z = torch.full((1, V), -60.0, device="cuda")
+    z[0, :2] = torch.tensor([3.0, 2.0])
+    z[0, 2:] += torch.arange(V - 2, device="cuda") % 7
+    idx = torch.tensor([[0, 1]], dtype=torch.int32, device="cuda")
+    t, tlse = torch.tensor([[1.0, 0.5]], device="cuda"), torch.tensor([2.0], device="cuda")
+    loss, dz = torch.zeros(1, device="cuda"), torch.zeros_like(z)
+    B.gc_distill_loss(z, idx, t, B.distill_options(T, tail=True), loss, dz, t_lse=tlse)
+    want_l, want_g = reference(z.double(), idx, t.double(), T, 1.0, 0.0, 1.0, True, tlse, None, None)
+    assert abs(float(loss) - float(want_l)) < 2000 * 2.0 ** -23 * 70
+    assert bool(((dz.double() - want_g).abs() <= 1200 * 2.0 ** -23 * want_g.abs() + 4 * 1100 * 2.0 ** -23 * (want_g.abs() > 0.05)).all())
+
+
+def test_all_columns_named():
+    V = 33
+    z = torch.randn(2, V, device="cuda")
+    idx = torch.arange(V, device="cuda", dtype=torch.int32).repeat(2, 1)
+    t = torch.randn(2, V, device="cuda")
+    tlse = torch.logsumexp(t, 1) + 0.25  # mass is missing, but no column is left to take it
+    loss, dz = torch.zeros(2, device="cuda"), torch.zeros_like(z)
+    B.gc_distill_loss(z, idx, t, B.distill_options(1.0, tail=True), loss, dz, t_lse=tlse)
+    want_l, want_g = reference(z.double(), idx, t.double(), 1.0, 1.0, 0.0, 1.0, True, tlse, None, None)
+    assert bool(((loss.double() - want_l).abs() < 1e-3).all()) and bool(((dz.double() - want_g).abs() < 3000 * 2.0 ** -23).all())
+
+
+def test_no_rows_and_labels_alone():
+    e = torch.empty(0, 50, device="cuda")
+    none = torch.empty(0, 3, dtype=torch.int32, device="cuda")
+    B.gc_top_logits(e, none, torch.empty(0, 3, device="cuda"))
+    B.gc_distill_loss(e, none, torch.empty(0, 3, device="cuda"), B.distill_options(), torch.empty(0, device="cuda"), e)
+    z, lab = torch.randn(9, 777, device="cuda"), torch.arange(9, device="cuda") * 80 + 50
+    idx, t = torch.empty(9, 0, dtype=torch.int64, device="cuda"), torch.empty(9, 0, device="cuda")
+    loss, dz = torch.zeros(9, device="cuda"), torch.zeros_like(z)
+    B.gc_distill_loss(z, idx, t, B.distill_options(2.0, 1.0, 1.0), loss, dz, labels=lab)
+    want_l, want_g = reference(z.double(), idx, t.double(), 2.0, 1.0, 1.0, 1.0, False, None, lab, None)
+    assert bool(((loss.double() - want_l).abs() <= 1100 * 2.0 ** -23).all()) and bool(((dz.double() - want_g).abs() <= 1100 * 2.0 ** -23 * want_g.abs() + 4 * U32).all())

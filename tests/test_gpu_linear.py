@@ -1,0 +1,277 @@
+"""A layer's product and its gradients on the GPU against 64 bits: odd sizes,
+strides, offsets, types, masks and empty batches.
+
+Bounds: a product's sum of k terms in fp32 is off by at most (2 k + 8) 2^-24
+times the sum of the terms' magnitudes (each term and each addition rounds
+once), and each output by half a step of its type on top."""
+import pytest
+import torch
+
+from gradient_compression_dnn_amd import binding as B
+from tests.gpu_util import say
+from tests.layer_util import ACTS, DTYPES, GUARD, U32, Layer, Rows, act64, act_error, half_step
+
+pytestmark = pytest.mark.gpu
+
+# tokens, rows, columns
+SIZES = [(1, 1, 1), (1, 7, 300), (2, 130, 64), (3, 5, 7), (15, 64, 33), (16, 100, 128), (17, 257, 129), (33, 48, 513),
+         (64, 128, 64), (100, 300, 40), (129, 127, 100), (255, 33, 1000), (300, 513, 72)]
+
+
+def normal(n, cols, seed, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(n, cols, generator=g, device="cuda") * scale
+
+
+def within(got, want, bound, dtype, what):
+    """|got - want| <= bound + one rounding of the type (of a value within bound of want)."""
+    got, bound = got.double(), torch.as_tensor(bound, device=want.device)
+    room = bound + half_step(dtype) * (want.abs() + bound) + torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps
+    off = (got - want).abs()
+    bad = ~(off <= room)
+    assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.numel()} off, by up to {float((off / room)[bad].max())} of the bound"
+
+
+def sum_bound(a, b, k):
+    """(2 k + 8) 2^-24 sum |a| |b| for a @ b."""
+    return (2 * k + 8) * U32 * (a.abs() @ b.abs())
+
+
+@pytest.mark.parametrize("n,rows,cols", SIZES)
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_forward(n, rows, cols, dtype):
+    D = DTYPES[dtype]
+    for i, (act, lead, pitch, bias, res, keep) in enumerate((("none", 0, 0, False, False, False), ("gelu", 3, 5, True, True, True),
+                                                             ("silu", 8, 8, True, False, True), ("gelu_tanh", 1, 0, False, True, False),
+                                                             ("relu", 0, 1, True, False, False))):
+        say(f"forward {n}x{rows}x{cols} {dtype} {act} lead={lead} pitch={pitch}")
+        L = Layer(rows, cols, dtype, lead, bias, i)
+        x = Rows(n, cols, D, pitch, normal(n, cols, i))
+        r = Rows(n, rows, D, pitch, normal(n, rows, i + 50)) if res else None
+        z = Rows(n, rows, D, pitch) if keep else None
+        y = Rows(n, rows, D, pitch)
+        B.gc_linear_forward(L.plan, L.layer, L.w, x.t, y.t, L.ws(n), act=ACTS[act], r=r.t if res else None, z=z.t if keep else None)
+        w64 = L.weights().double()
+        z64 = x.f64() @ w64.T
+        bound = sum_bound(x.f64(), w64.T, cols)
+        if bias:
+            z64 = z64 + L.bias().double()
+            bound = bound + U32 * (z64.abs() + bound)
+        if keep:
+            within(z.t, z64, bound, D, "z")
+            assert z.guards_kept()
+        want, _ = act64(z64, act)
+        bound = 1.2 * bound + act_error(z64, act)  # no slope here is above 1.13
+        if res:
+            want = want + r.f64()
+            bound = bound + U32 * (want.abs() + bound)
+        within(y.t, want, bound, D, "y")
+        assert y.guards_kept() and x.guards_kept()
+
+
+@pytest.mark.parametrize("n,rows,cols", SIZES)
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_grad_input(n, rows, cols, dtype):
+    D = DTYPES[dtype]
+    for i, (act, lead, pitch, extra, want_dx, want_dzx) in enumerate((("none", 0, 0, False, True, False), ("gelu", 3, 5, True, True, True),
+                                                                       ("silu", 8, 8, False, False, True), ("gelu_tanh", 1, 0, True, True, True),
+                                                                       ("relu", 0, 1, False, True, True), ("none", 3, 0, True, True, True))):
+        say(f"input {n}x{rows}x{cols} {dtype} {act} lead={lead} pitch={pitch}")
+        L = Layer(rows, cols, dtype, lead, False, i, scale=rows ** -0.5)
+        dz = Rows(n, rows, D, pitch, normal(n, rows, i))
+        a = Rows(n, cols, D, pitch, normal(n, cols, i + 50)) if extra else None
+        z = Rows(n, cols, D, pitch, normal(n, cols, i + 60, 2.0))
+        dx, dzx = (Rows(n, cols, D, pitch) for _ in range(2))
+        B.gc_linear_grad_input(L.plan, L.layer, L.w, dz.t, dx.t if want_dx else None, L.ws(n), a=a.t if extra else None, act=ACTS[act],
+                               z=None if act == "none" else z.t, dzx=dzx.t if want_dzx else None)
+        w64 = L.weights().double()
+        g = dz.f64() @ w64
+        bound = sum_bound(dz.f64(), w64, rows)
+        if extra:
+            g = g + a.f64()
+            bound = bound + U32 * (g.abs() + bound)
+        if want_dx:
+            within(dx.t, g, bound, D, "dx")
+        if want_dzx:
+            slope = act64(z.f64(), act)[1]
+            err = act_error(z.f64(), act)
+            within(dzx.t, g * slope, bound * (slope.abs() + err) + g.abs() * err + 2 * U32 * (g * slope).abs(), D, "dzx")
+        assert dx.guards_kept() and dzx.guards_kept()
+        assert want_dx or bool((dx.t == GUARD).all())
+        assert want_dzx or bool((dzx.t == GUARD).all())
+
+
+@pytest.mark.parametrize("n,rows,cols", SIZES)
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_grad_weight(n, rows, cols, dtype):
+    D = DTYPES[dtype]
+    for i, (lead, pitch, bias, add) in enumerate(((0, 0, False, False), (3, 5, True, True), (8, 8, True, False), (1, 0, False, True))):
+        say(f"weight {n}x{rows}x{cols} {dtype} lead={lead} pitch={pitch} add={add}")
+        L = Layer(rows, cols, dtype, lead, bias, i)
+        dz, x = Rows(n, rows, D, pitch, normal(n, rows, i)), Rows(n, cols, D, pitch, normal(n, cols, i + 50))
+        g0 = normal(1, L.plan.n_total, i + 70)[0]
+        g = g0.clone()
+        B.gc_linear_grad_weight(L.plan, L.layer, dz.t, x.t, g, add, L.ws(n))
+        base = g0.double() if add else 0.0 * g0.double()
+        for part, want, bound in ((L.weights(g), dz.f64().T @ x.f64(), sum_bound(dz.f64().T, x.f64(), n)),
+                                  (L.bias(g), dz.f64().sum(0), (2 * n + 8) * U32 * dz.f64().abs().sum(0))):
+            if part is None:
+                continue
+            old = L.weights(base) if part.dim() == 2 else L.bias(base)
+            within(part, old + want, bound, torch.float32, "g")
+        assert torch.equal(L.outside(g), L.outside(g0))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("act", list(ACTS))
+def test_act_grad(dtype, act):
+    D = DTYPES[dtype]
+    z = torch.cat([torch.linspace(-14, 14, 2001), torch.tensor([0.0, -0.0, 1e-30, -1e-30, 60.0, -60.0, 200.0, -200.0, 6e4, -6e4])])
+    for n, cols, pitch in ((1, z.numel(), 0), (3, 13, 5), (257, 1, 1), (5, 1024, 8), (1, 1, 0)):
+        say(f"act_grad {n}x{cols} {dtype} {act}")
+        zr = Rows(n, cols, D, pitch, z.repeat(1 + n * cols // z.numel())[:n * cols].view(n, cols))
+        dy, dz = Rows(n, cols, D, pitch, normal(n, cols, 3)), Rows(n, cols, D, pitch)
+        B.gc_act_grad(dy.t, zr.t, ACTS[act], dz.t)
+        want = dy.f64() * act64(zr.f64(), act)[1]
+        bound = dy.f64().abs() * act_error(torch.clamp(zr.f64(), -16, 16), act) + U32 * want.abs()
+        within(dz.t, want, bound, D, "dz")
+        assert dz.guards_kept()
+        kept = dz.t.clone()
+        for place in (dy, zr):  # in place of either input
+            d2, z2 = Rows(n, cols, D, pitch, dy.t), Rows(n, cols, D, pitch, zr.t)
+            out = d2 if place is dy else z2
+            B.gc_act_grad(d2.t, z2.t, ACTS[act], out.t)
+            assert torch.equal(out.t, kept) and out.guards_kept()
+
+
+@pytest.mark.parametrize("act", list(ACTS))
+def test_slopes_against_differences(act):
+    """act' is the difference quotient of act: by the formulas in 64 bits, and of
+    the kernel's own fp32 values."""
+    z = torch.linspace(-6.03, 6.02, 1024, dtype=torch.float64, device="cuda:0").view(8, 128)
+    h = 2.0 ** -5
+    slope = act64(z, act)[1]
+    if act == "relu":
+        keep = z.abs() > h
+    else:
+        keep = torch.ones_like(z, dtype=torch.bool)
+    near = (act64(z + 1e-5, act)[0] - act64(z - 1e-5, act)[0]) / 2e-5
+    assert float((near - slope)[keep].abs().max()) < 1e-8  # h^2 / 6 |act'''| and 2^-53 |act| / h
+    # through a layer whose matrix is the identity: y = act(x)
+    L = Layer(128, 128, "f32", 0, False)
+    L.weights().copy_(torch.eye(128))
+    x, ys = z.float(), []
+    for d in (h, -h):
+        y = torch.empty_like(x)
+        B.gc_linear_forward(L.plan, L.layer, L.w, x + d, y, L.ws(8), act=ACTS[act])
+        ys.append(y.double())
+    dz = torch.empty_like(x)
+    B.gc_act_grad(torch.ones_like(x), x, ACTS[act], dz)
+    # |act'''| <= 2 for all of them; values of at most 6.1 are off by 32 steps of it
+    room = h * h / 6 * 2 + 2 * 33 * U32 * 6.1 / (2 * h) + 64 * U32
+    assert float(((ys[0] - ys[1]) / (2 * h) - dz.double())[keep].abs().max()) < room
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gradients_against_differences(dtype):
+    """L = sum(c y) with y = x W^T + b: linear in x, W and b, so a difference
+    of L over any step is the gradient's product with it."""
+    D = DTYPES[dtype]
+    n, rows, cols = 37, 61, 83
+    L = Layer(rows, cols, dtype, 3, True)
+    x, c = normal(n, cols, 1).to(D), normal(n, rows, 2).to(D)
+    dx, g = torch.empty_like(x), torch.zeros(L.plan.n_total, device="cuda:0")
+    B.gc_linear_grad_input(L.plan, L.layer, L.w, c, dx, L.ws(n))
+    B.gc_linear_grad_weight(L.plan, L.layer, c, x, g, False, L.ws(n))
+
+    def loss(xx, ww):
+        y = torch.empty(n, rows, dtype=D, device="cuda:0")
+        B.gc_linear_forward(L.plan, L.layer, ww, xx, y, L.ws(n))
+        return float((y.double() * c.double()).sum())
+
+    room_y = float((c.double().abs() * half_step(D) * 1.1 * ((x.double().abs() @ L.weights().double().abs().T) + 1)).sum())
+    for step_x, step_w in ((normal(n, cols, 5), None), (None, normal(1, L.plan.n_total, 6)[0])):
+        x2 = x if step_x is None else (x.double() + step_x).to(D)
+        w2 = L.w if step_w is None else (L.w.double() + 0.1 * step_w).to(D)
+        if step_x is not None:
+            want = float(((x2.double() - x.double()) * dx.double()).sum())
+            room = float(((x2.double() - x.double()).abs() * (half_step(D) * dx.double().abs() + 2 ** -14 * dx.double().abs().max())).sum())
+        else:
+            d = w2.double() - L.w.double()
+            d[:L.lead] = 0
+            want, room = float((d * g.double()).sum()), float((d.abs() * 2 ** -14 * g.double().abs().max()).sum())
+        diff = loss(x2, w2) - loss(x, L.w)
+        assert abs(diff - want) <= room + 8 * room_y, (diff, want, room, room_y)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_special_values_stay_in_their_row_and_column(dtype):
+    D = DTYPES[dtype]
+    n, rows, cols = 70, 90, 45
+    L = Layer(rows, cols, dtype, 0, True)
+    x = normal(n, cols, 1).to(D)
+    y0, y1 = (torch.empty(n, rows, dtype=D, device="cuda:0") for _ in range(2))
+    B.gc_linear_forward(L.plan, L.layer, L.w, x, y0, L.ws(n))
+    x[13, 44], x[69, 0] = float("nan"), float("inf")
+    L.weights()[7, 3] = float("-inf")
+    L.weights()[89, 44] = float("nan")
+    B.gc_linear_forward(L.plan, L.layer, L.w, x, y1, L.ws(n))
+    hit = torch.zeros(n, rows, dtype=torch.bool, device="cuda:0")
+    hit[[13, 69], :] = True
+    hit[:, [7, 89]] = True
+    assert torch.equal(y0[~hit], y1[~hit]) and not bool(torch.isfinite(y1[hit]).any())
+    # the same for the gradients
+    dz = normal(n, rows, 2).to(D)
+    dx, g = torch.empty(n, cols, dtype=D, device="cuda:0"), torch.zeros(L.plan.n_total, device="cuda:0")
+    B.gc_linear_grad_input(L.plan, L.layer, L.w, dz, dx, L.ws(n))
+    assert not bool(torch.isfinite(dx[:, [3, 44]]).any()) and bool(torch.isfinite(dx[:, 4:44]).all())
+    B.gc_linear_grad_weight(L.plan, L.layer, dz, x, g, False, L.ws(n))
+    dw = L.weights(g)
+    assert not bool(torch.isfinite(dw[:, [44, 0]]).any()) and bool(torch.isfinite(dw[:, 1:44]).all())
+    assert bool(torch.isfinite(L.bias(g)).all())
+
+
+def test_subnormal_operands_count():
+    """Products of the types' smallest values are not taken as 0."""
+    for dtype, tiny in (("f16", 2.0 ** -24), ("bf16", 2.0 ** -133), ("f32", 2.0 ** -140)):
+        L = Layer(4, 64, dtype, 0, False)
+        L.weights().fill_(tiny)
+        x = torch.full((3, 64), 1024.0, dtype=DTYPES[dtype], device="cuda:0")
+        y = torch.empty(3, 4, dtype=DTYPES[dtype], device="cuda:0")
+        B.gc_linear_forward(L.plan, L.layer, L.w, x, y, L.ws(3))
+        assert bool((y.double() == 64 * 1024 * tiny).all()), dtype
+
+
+def test_empty_batches():
+    L = Layer(6, 10, "bf16", 3, True)
+    e = lambda c: torch.empty(0, c, dtype=torch.bfloat16, device="cuda:0")
+    B.gc_linear_forward(L.plan, L.layer, L.w, e(10), e(6), L.ws(0))
+    B.gc_linear_grad_input(L.plan, L.layer, L.w, e(6), e(10), L.ws(0))
+    B.gc_act_grad(e(6), e(6), B.GC_ACT_GELU, e(6))
+    g0 = torch.randn(L.plan.n_total, device="cuda:0")
+    g = g0.clone()
+    B.gc_linear_grad_weight(L.plan, L.layer, e(6), e(10), g, True, L.ws(0))
+    assert torch.equal(g, g0)
+    B.gc_linear_grad_weight(L.plan, L.layer, e(6), e(10), g, False, L.ws(0))
+    assert bool((L.weights(g) == 0).all()) and bool((L.bias(g) == 0).all()) and torch.equal(L.outside(g), L.outside(g0))
+
+
+def test_residual_in_place_and_batches_of_more_dimensions():
+    L = Layer(130, 70, "bf16", 0, True)
+    x = normal(6 * 35, 70, 1).to(torch.bfloat16).view(6, 35, 70)
+    r = normal(6 * 35, 130, 2).to(torch.bfloat16).view(6, 35, 130)
+    y, y2 = torch.empty_like(r), r.clone()
+    B.gc_linear_forward(L.plan, L.layer, L.w, x, y, L.ws(210), act=B.GC_ACT_SILU, r=r)
+    B.gc_linear_forward(L.plan, L.layer, L.w, x, y2, L.ws(210), act=B.GC_ACT_SILU, r=y2)
+    assert torch.equal(y, y2)
+    # a = dx and a = dzx
+    a = normal(210, 70, 3).to(torch.bfloat16).view(6, 35, 70)
+    z = normal(210, 70, 4).to(torch.bfloat16).view(6, 35, 70)
+    outs = []
+    for place in (None, "dx", "dzx"):
+        dx, dzx = (a.clone() if place == "dx" else torch.empty_like(a)), (a.clone() if place == "dzx" else torch.empty_like(a))
+        B.gc_linear_grad_input(L.plan, L.layer, L.w, r, dx, L.ws(210), a=dx if place == "dx" else dzx if place == "dzx" else a,
+                               act=B.GC_ACT_GELU, z=z, dzx=dzx)
+        outs.append((dx, dzx))
+    for o in outs[1:]:
+        assert torch.equal(o[0], outs[0][0]) and torch.equal(o[1], outs[0][1])
