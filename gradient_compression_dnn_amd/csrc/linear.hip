@@ -1,353 +1,37 @@
 // The product of a layer's weight matrix with a batch and its gradients
 // (gc_linear_forward, gc_linear_grad_input, gc_linear_grad_weight), and the
-// slope of an activation (gc_act_grad).
-//
-//   forward  z = x W^T + b, y = act(z) + r
-//   input    g = dz W + a,  dx = g, dzx = g act'(z)
-//   weight   G[W] (+)= dz^T x, G[b] (+)= column sums of dz
-//
-// All three are D[m][n] = sum_k A[m][k] B[n][k] with D row-major; what differs
-// is which of an operand's two indices is contiguous in memory:
-//            m        n      k       A           B
-//   forward  tokens   rows   cols    x, k        W, k
-//   input    tokens   cols   rows    dz, k       W, n
-//   weight   rows     cols   tokens  dz, m       x, n
+// slope of an activation (gc_act_grad): the calls, their checks, and how a
+// product is spread over the chip.  The kernels are in linear_kernels.hpp.
 #include <algorithm>
 #include <string>
 
-#include "gc_internal.hpp"
+#include "activations.hpp"
+#include "linear.hpp"
 
 namespace gc {
 
 namespace {
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-
-// ------------------------------------------------------------- activations
-__device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
-// 2 sqrt(2 / pi) (z + 0.044715 z^3), whose sigmoid is gelu_tanh's factor
-constexpr float kTanh2 = 1.5957691216057308f, kCubic = 0.044715f;
-constexpr float kSqrtHalf = 0.70710678118654752f, kInvSqrt2Pi = 0.39894228040143268f;
-
-__device__ __forceinline__ float act_value(int act, float z) {
-    switch (act) {
-        case GC_ACT_RELU: return z < 0.0f ? 0.0f : z;
-        case GC_ACT_GELU: return z * (0.5f * erfcf(-z * kSqrtHalf));
-        case GC_ACT_GELU_TANH: return z * sigmoid(kTanh2 * (z + kCubic * z * z * z));
-        case GC_ACT_SILU: return z * sigmoid(z);
-        default: return z;
-    }
-}
-// Beyond +-kFar every slope here is 0 or 1 in fp32, and z^2 could overflow.
-constexpr float kFar = 128.0f;
-__device__ __forceinline__ float act_slope(int act, float z) {
-    if (act == GC_ACT_NONE) return 1.0f;
-    if (act == GC_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
-    if (fabsf(z) > kFar) return z > 0.0f ? 1.0f : 0.0f;
-    switch (act) {
-        case GC_ACT_GELU: return 0.5f * erfcf(-z * kSqrtHalf) + z * (kInvSqrt2Pi * expf(-0.5f * z * z));
-        case GC_ACT_GELU_TANH: {
-            const float s = sigmoid(kTanh2 * (z + kCubic * z * z * z));
-            return s + z * (s * (1.0f - s)) * (kTanh2 * (1.0f + 3.0f * kCubic * z * z));
-        }
-        default: {
-            const float s = sigmoid(z);
-            return s * (1.0f + z * (1.0f - s));
-        }
-    }
-}
-
-// Up to 4 elements of a row.
-template <class T>
-__device__ __forceinline__ void get4(const void *base, uint64_t at, uint32_t n, float (&v)[4]) {
-    const auto *p = static_cast<const typename T::Store *>(base) + at;
-    if (n >= 4) {
-        const auto t = *reinterpret_cast<const Pack<typename T::Store, 4> *>(p);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) v[u] = T::to_f32(t.v[u]);
-        return;
-    }
-#pragma unroll
-    for (uint32_t u = 0; u < 4; ++u) v[u] = u < n ? T::to_f32(p[u]) : 0.0f;
-}
-template <class T>
-__device__ __forceinline__ void put4(void *base, uint64_t at, uint32_t n, const float (&v)[4]) {
-    auto *p = static_cast<typename T::Store *>(base) + at;
-    if (n >= 4) {
-        Pack<typename T::Store, 4> t;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) t.v[u] = T::from_f32(v[u]);
-        *reinterpret_cast<Pack<typename T::Store, 4> *>(p) = t;
-        return;
-    }
-#pragma unroll
-    for (uint32_t u = 0; u < 4; ++u)
-        if (u < n) p[u] = T::from_f32(v[u]);
-}
-
-// --------------------------------------------------------------- products
-enum Kind { kForward, kInput, kWeight };
-
-struct Product {
-    const void *A, *B;
-    uint64_t lda, ldb;
-    uint32_t M, N, K;
-    const void *bias;           // forward: [N], or null; weight: null or not, whether column sums go to gbias
-    const void *add;            // forward: r; input: a
-    const void *z;              // input: the argument of the activation
-    void *zout;                 // forward
-    void *out, *out2;           // forward: y; input: dx, dzx; weight: the segment of g
-    uint64_t ldadd, ldz, ldout, ldout2;
-    float *gbias;               // weight: the bias' segment of g
-    int act;
-    int accumulate;             // weight
-};
-
-// A stage of an operand: kTile rows by 128 bytes of k (64 elements of 16 bits,
-// 32 of fp32), kTile * 8 parts of 16 bytes in LDS.
-//   k contiguous: [row][128 bytes], part c of a row at c ^ ((row >> 1) & 7), so
-//     that the 16 rows a matrix operand reads at once lie in different banks
-//   k slow: [k][kTile elements]; 16 elements stay together, at u ^ spread(k)
-template <class T, bool kSlow, int kTile>
-struct Operand {
-    using Store = typename T::Store;
-    static constexpr int kElems = 16 / int(sizeof(Store)), kStage = 128 / int(sizeof(Store));
-    static constexpr int kUnits = kTile / 16, kRowBytes = kTile * int(sizeof(Store)), kUnitBytes = 16 * int(sizeof(Store));
-    static constexpr uint32_t kParts = kTile * 8, kRowParts = kRowBytes / 16;
-
-    static __device__ __forceinline__ uint32_t spread(uint32_t k) {
-        return (sizeof(Store) == 2 ? ((k & 3) | ((k >> 1) & 4)) : ((k >> 2) & 3)) & (kUnits - 1);
-    }
-    // where a part stands, and which row (k contiguous) or k (slow) and which piece of it that is
-    static __device__ __forceinline__ uint32_t place(uint32_t part, uint32_t &line, uint32_t &piece) {
-        if (!kSlow) {
-            line = part >> 3;
-            piece = part & 7;
-            return line * 128 + ((piece ^ ((line >> 1) & 7)) << 4);
-        }
-        line = part / kRowParts;
-        piece = part % kRowParts;
-        constexpr uint32_t kUnitParts = kUnitBytes / 16;
-        return line * kRowBytes + ((piece / kUnitParts) ^ spread(line)) * kUnitBytes + (piece % kUnitParts) * 16;
-    }
-    // a part from memory; what lies past the last k is 0, past the last row anything
-    static __device__ __forceinline__ u32x4 fetch(const void *base, uint64_t ld, uint32_t row0, uint32_t rows,
-                                                  uint32_t k0, uint32_t K, uint32_t line, uint32_t piece) {
-        const uint32_t r = kSlow ? row0 + piece * kElems : min(row0 + line, rows - 1);
-        const uint32_t k = kSlow ? k0 + line : k0 + piece * kElems;
-        const Store *p = static_cast<const Store *>(base) + (kSlow ? k * ld + r : r * ld + k);
-        const uint32_t at = kSlow ? r : k, end = kSlow ? rows : K;
-        if (kSlow && k >= K) return u32x4{0, 0, 0, 0};
-        if (at + kElems <= end) return __builtin_bit_cast(u32x4, *reinterpret_cast<const Pack<Store, kElems> *>(p));
-        Pack<Store, kElems> t;
-#pragma unroll
-        for (uint32_t u = 0; u < kElems; ++u) t.v[u] = at + u < end ? p[u] : Store(0);
-        return __builtin_bit_cast(u32x4, t);
-    }
-    // rows row0 .. row0 + 15, 16 bytes of k a lane: row lane % 16, k from ((lane / 16) + 4 half) * kElems
-    static __device__ __forceinline__ u32x4 read(const char *lds, uint32_t row0, int half) {
-        const uint32_t lane = lane_id(), part = (lane >> 4) + 4 * half;
-        if (!kSlow) {
-            const uint32_t row = row0 + (lane & 15);
-            return *reinterpret_cast<const u32x4 *>(lds + row * 128 + ((part ^ ((row >> 1) & 7)) << 4));
-        }
-        const uint32_t k = part * kElems;
-        if constexpr (sizeof(Store) == 2) {
-            // a transposing read: of 16 lanes, lane l fetches 4 rows of k + l / 4 and gets 4 k of row l
-            typedef __attribute__((address_space(3))) s16x4 LdsS4;
-            u32x4 v;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t line = k + 4 * h + ((lane & 15) >> 2);
-                const char *p = lds + line * kRowBytes + ((row0 >> 4) ^ spread(line)) * kUnitBytes + (lane & 3) * 8;
-                const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsS4 *)(p));
-                const uint2 w = __builtin_bit_cast(uint2, t);
-                v[2 * h] = w.x;
-                v[2 * h + 1] = w.y;
-            }
-            return v;
-        } else {
-            u32x4 v;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                v[e] = *reinterpret_cast<const uint32_t *>(lds + (k + e) * kRowBytes + ((row0 >> 4) ^ spread(k + e)) * kUnitBytes + (lane & 15) * 4);
-            return v;
-        }
-    }
-};
-
-// d[i][j] += sum over 16 bytes of k of a[i] b[j]
-template <class T>
-__device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 d) {
-    if constexpr (sizeof(typename T::Store) == 4) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) d = __builtin_amdgcn_mfma_f32_16x16x4f32(dev_u2f(a[e]), dev_u2f(b[e]), d, 0, 0, 0);
-        return d;
-    } else if constexpr (std::is_same<T, BF16>::value) {
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), d, 0, 0, 0);
-    } else {
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), d, 0, 0, 0);
-    }
-}
-
-template <class T>
-__device__ __forceinline__ u32x4 ones() {
-    const uint32_t w = sizeof(typename T::Store) == 4 ? 0x3F800000u : std::is_same<T, BF16>::value ? 0x3F803F80u : 0x3C003C00u;
-    return u32x4{w, w, w, w};
-}
-
-// What becomes of 4 sums of row m, columns n on.
-template <class T, Kind kKind>
-__device__ __forceinline__ void finish(const Product &p, uint32_t m, uint32_t n, f32x4 sum) {
-    const uint32_t cnt = min(p.N - n, 4u);
-    float v[4], t[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) v[u] = sum[u];
-    if constexpr (kKind == kWeight) {
-        const uint64_t at = m * p.ldout + n;
-        if (p.accumulate) {
-            get4<F32>(p.out, at, cnt, t);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) v[u] = t[u] + v[u];
-        }
-        put4<F32>(p.out, at, cnt, v);
-    } else if constexpr (kKind == kForward) {
-        if (p.bias) {
-            get4<T>(p.bias, n, cnt, t);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) v[u] = v[u] + t[u];
-        }
-        if (p.zout) put4<T>(p.zout, m * p.ldz + n, cnt, v);
-        if (p.act != GC_ACT_NONE)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) v[u] = act_value(p.act, v[u]);
-        if (p.add) {
-            get4<T>(p.add, m * p.ldadd + n, cnt, t);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) v[u] = v[u] + t[u];
-        }
-        put4<T>(p.out, m * p.ldout + n, cnt, v);
-    } else {
-        if (p.add) {
-            get4<T>(p.add, m * p.ldadd + n, cnt, t);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) v[u] = v[u] + t[u];
-        }
-        if (p.out) put4<T>(p.out, m * p.ldout + n, cnt, v);
-        if (p.out2) {
-            if (p.act != GC_ACT_NONE) {
-                get4<T>(p.z, m * p.ldz + n, cnt, t);
-#pragma unroll
-                for (int u = 0; u < 4; ++u) v[u] = v[u] * act_slope(p.act, t[u]);
-            }
-            put4<T>(p.out2, m * p.ldout2 + n, cnt, v);
-        }
-    }
-}
-
-// A workgroup of kWR x kWC waves per tile of kTileM x kTileN, stages of 128
-// bytes of k through registers into one of two LDS buffers.
-template <class T, Kind kKind, int kTileM, int kTileN, int kWR, int kWC>
-__global__ __launch_bounds__(kWR *kWC *kWave) void linear_kernel(Product p, uint32_t tiles_m) {
-    constexpr int kThreads = kWR * kWC * kWave;
-    using OpA = Operand<T, kKind == kWeight, kTileM>;
-    using OpB = Operand<T, kKind != kForward, kTileN>;
-    constexpr int kLoadsA = OpA::kParts / kThreads, kLoadsB = OpB::kParts / kThreads;
-    constexpr int kRA = kTileM / kWR / 16, kRB = kTileN / kWC / 16;
-    constexpr int kBytesA = kTileM * 128, kBytes = kBytesA + kTileN * 128;
-    __shared__ __attribute__((aligned(128))) char lds[2 * kBytes];
-    const uint32_t m0 = blockIdx.x % tiles_m * kTileM, n0 = blockIdx.x / tiles_m * kTileN;
-    const uint32_t w = __builtin_amdgcn_readfirstlane(wave_id()), lane = lane_id();
-    const uint32_t wm = w / kWC * (kTileM / kWR), wn = w % kWC * (kTileN / kWC);
-    u32x4 ra[kLoadsA], rb[kLoadsB];
-    auto fetch = [&](uint32_t k0) {
-#pragma unroll
-        for (int i = 0; i < kLoadsA; ++i) {
-            uint32_t line, piece;
-            (void)OpA::place(i * kThreads + threadIdx.x, line, piece);
-            ra[i] = OpA::fetch(p.A, p.lda, m0, p.M, k0, p.K, line, piece);
-        }
-#pragma unroll
-        for (int i = 0; i < kLoadsB; ++i) {
-            uint32_t line, piece;
-            (void)OpB::place(i * kThreads + threadIdx.x, line, piece);
-            rb[i] = OpB::fetch(p.B, p.ldb, n0, p.N, k0, p.K, line, piece);
-        }
-    };
-    auto stash = [&](char *to) {
-        uint32_t line, piece;
-#pragma unroll
-        for (int i = 0; i < kLoadsA; ++i)
-            *reinterpret_cast<u32x4 *>(to + OpA::place(i * kThreads + threadIdx.x, line, piece)) = ra[i];
-#pragma unroll
-        for (int i = 0; i < kLoadsB; ++i)
-            *reinterpret_cast<u32x4 *>(to + kBytesA + OpB::place(i * kThreads + threadIdx.x, line, piece)) = rb[i];
-    };
-    f32x4 acc[kRA][kRB], colsum[kRA];
-#pragma unroll
-    for (int a = 0; a < kRA; ++a) {
-        colsum[a] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int b = 0; b < kRB; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    }
-    // the sums of A over k, for the bias: a product with ones in the first column of tiles
-    const bool sums = kKind == kWeight && p.gbias && n0 == 0 && wn == 0;
-    const uint32_t stages = static_cast<uint32_t>(ceil_div(p.K, OpA::kStage));
-    if (stages) {
-        fetch(0);
-        stash(lds);
-    }
-    for (uint32_t s = 0; s < stages; ++s) {
-        __syncthreads();
-        const char *cur = lds + (s & 1) * kBytes;
-        if (s + 1 < stages) fetch((s + 1) * OpA::kStage);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            u32x4 fb[kRB];
-#pragma unroll
-            for (int b = 0; b < kRB; ++b) fb[b] = OpB::read(cur + kBytesA, wn + 16 * b, h);
-#pragma unroll
-            for (int a = 0; a < kRA; ++a) {
-                const u32x4 fa = OpA::read(cur, wm + 16 * a, h);
-#pragma unroll
-                for (int b = 0; b < kRB; ++b) acc[a][b] = mma<T>(fb[b], fa, acc[a][b]);
-                if (sums) colsum[a] = mma<T>(ones<T>(), fa, colsum[a]);
-            }
-        }
-        if (s + 1 < stages) stash(lds + ((s + 1) & 1) * kBytes);
-    }
-    // a lane holds 4 columns of row lane % 16 of each block of 16 x 16
-#pragma unroll
-    for (int a = 0; a < kRA; ++a) {
-        const uint32_t m = m0 + wm + 16 * a + (lane & 15);
-        if (m >= p.M) continue;
-        if (sums && lane < 16) p.gbias[m] = p.accumulate ? p.gbias[m] + colsum[a][0] : colsum[a][0];
-#pragma unroll
-        for (int b = 0; b < kRB; ++b) {
-            const uint32_t n = n0 + wn + 16 * b + 4 * (lane >> 4);
-            if (n < p.N) finish<T, kKind>(p, m, n, acc[a][b]);
-        }
-    }
-}
-
-// dz = dy act'(z): 4 elements a thread.
+// dz = dy act'(z): 8 elements a thread.  Memory bounds it.
+constexpr int kActCols = 8;
 template <class T>
 __global__ __launch_bounds__(kBlock) void act_grad_kernel(const void *dy, uint64_t ldy, const void *z, uint64_t ldz, int act,
                                                           uint64_t n, uint64_t cols, void *dz, uint64_t ldd) {
-    const uint64_t vecs = ceil_div(cols, 4);
+    const uint64_t vecs = ceil_div(cols, kActCols);
     const uint64_t i = static_cast<uint64_t>(blockIdx.x) * kBlock + threadIdx.x;
-    const uint64_t row = i / vecs, c = (i - row * vecs) * 4;
+    const uint64_t row = i / vecs, c = (i - row * vecs) * kActCols;
     if (row >= n) return;
-    const uint32_t cnt = static_cast<uint32_t>(umin64(cols - c, 4));
-    float g[4], t[4];
-    get4<T>(dy, row * ldy + c, cnt, g);
-    get4<T>(z, row * ldz + c, cnt, t);
+    const uint32_t cnt = static_cast<uint32_t>(umin64(cols - c, kActCols));
+    Cols<T, kActCols> g, at;
+    g.load(dy, row * ldy + c, cnt);
+    at.load(z, row * ldz + c, cnt);
+    float t[kActCols];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) g[u] = g[u] * act_slope(act, t[u]);
-    put4<T>(dz, row * ldd + c, cnt, g);
+    for (uint32_t u = 0; u < kActCols; ++u) t[u] = at.at(u);
+    act_slopes<sizeof(typename T::Store) == 2>(act, t);
+#pragma unroll
+    for (uint32_t u = 0; u < kActCols; ++u) t[u] = g.at(u) * t[u];
+    put_cols<T>(dz, row * ldd + c, cnt, t);
 }
 
 // --------------------------------------------------------------- host side
@@ -388,26 +72,98 @@ gc_status check_rows(const char *fn, const void *p, uint64_t stride, uint64_t n,
     return GC_OK;
 }
 
-constexpr int kTM = 128, kTN = 128, kWR = 2, kWC = 2;
+// ------------------------------------------------------------- the cut
+// A product is cut into tiles, and where they do not fill the chip, into parts
+// of the common index as well; the choice is the least of a model of the time.
+struct ShapeModel {
+    TileShape shape;
+    uint32_t tm, tn, slots;   // workgroups that run at once
+    double stage16, stage32;  // us a stage of 128 bytes of k, with every slot busy
+};
+constexpr ShapeModel kShapes[] = {
+    {kBig, Big::kTM, Big::kTN, 256, 2.0, 8.5},
+    {kMid, Mid::kTM, Mid::kTN, 512, 1.3, 4.5},
+    {kThin, Thin::kTM, Thin::kTN, 1024, 1.3, 3.0},
+};
+constexpr double kTileUs = 3.0, kJoinUs = 4.0, kPartialBytesPerUs = 4e6;
+constexpr uint32_t kMaxParts = 32, kThinTokens = 64;
 
-template <Kind kKind>
-gc_status launch(const char *fn, int type, const Product &p, hipStream_t stream) {
-    const uint64_t tiles_m = ceil_div(p.M, kTM), tiles = tiles_m * ceil_div(p.N, kTN);
-    if (tiles > max_grid(kWR * kWC * kWave)) return fail(fn, GC_ERANGE, "more workgroups than a launch has");
-    auto go = [&](auto t) {
-        using T = decltype(t);
-        GC_LAUNCH("linear_product", stream,
-                  linear_kernel<T, kKind, kTM, kTN, kWR, kWC><<<static_cast<unsigned>(tiles), kWR * kWC * kWave, 0, stream>>>(
-                      p, static_cast<uint32_t>(tiles_m)));
-    };
-    if (type == GC_F32) go(F32{});
-    else if (type == GC_BF16) go(BF16{});
-    else go(F16{});
-    const hipError_t e = hipGetLastError();
-    return e == hipSuccess ? GC_OK : hip_error(e, fn);
+Cut plan_cut(Kind kind, int type, uint32_t M, uint32_t N, uint32_t K, bool any) {
+    Cut best{};
+    double least = 0.0;
+    const uint32_t stages = static_cast<uint32_t>(ceil_div(K, 128 / type_bytes(type)));
+    for (const ShapeModel &s : kShapes) {
+        if (s.shape != kMid && any) continue;
+        if (s.shape == kThin && (kind == kWeight || M > kThinTokens)) continue;
+        const uint64_t tm = ceil_div(M, s.tm), tn = ceil_div(N, s.tn), tiles = tm * tn;
+        for (uint32_t parts = 1; parts <= std::min(kMaxParts, std::max(stages, 1u)); ++parts) {
+            if (parts > 1 && tiles * parts > s.slots) break;
+            const uint32_t per = static_cast<uint32_t>(ceil_div(stages, parts));
+            if (parts > 1 && static_cast<uint64_t>(per) * (parts - 1) >= stages) continue;  // a part without stages
+            double us = static_cast<double>(ceil_div(tiles * parts, s.slots)) * (per * (type == GC_F32 ? s.stage32 : s.stage16) + kTileUs);
+            if (parts > 1) us += kJoinUs + 2.0 * static_cast<double>(tiles * parts) * s.tm * s.tn * 4 / kPartialBytesPerUs;
+            if (best.per == 0 || us < least) {
+                least = us;
+                best.shape = s.shape;
+                best.tiles_m = static_cast<uint32_t>(tm);
+                best.tiles_n = static_cast<uint32_t>(tn);
+                best.parts = parts;
+                best.stages = stages;
+                best.per = std::max(per, 1u);
+            }
+        }
+    }
+    return best;
 }
 
-size_t workspace_bytes(const gc_linear *, uint32_t, uint64_t) { return 256; }
+const ShapeModel &model_of(const Cut &c) { return kShapes[c.shape == kBig ? 0 : c.shape == kMid ? 1 : 2]; }
+
+// Lays the parts' sums out in the workspace; the bytes it needs.
+size_t cut_ws(Cut &c, void *ws) {
+    const ShapeModel &s = model_of(c);
+    WsCursor at(ws);
+    if (c.parts > 1) {
+        c.partial = at.take<float>(static_cast<size_t>(c.tiles_m) * c.tiles_n * c.parts * s.tm * s.tn);
+        c.colsums = at.take<float>(static_cast<size_t>(c.parts) * c.tiles_m * s.tm);
+    }
+    return at.used + 256;  // room to round the base up to 256 bytes
+}
+
+size_t workspace_bytes(const gc_linear *l, uint32_t cols, uint64_t n) {
+    const uint32_t n32 = static_cast<uint32_t>(n);
+    size_t most = 256;
+    if (!n) return most;
+    for (bool any : {false, true})
+        for (Cut c : {plan_cut(kForward, l->type, n32, l->rows, cols, any), plan_cut(kInput, l->type, n32, cols, l->rows, any),
+                      plan_cut(kWeight, l->type, l->rows, cols, n32, any)})
+            most = std::max(most, cut_ws(c, nullptr));
+    return most;
+}
+
+void *align256(void *p) {
+    return reinterpret_cast<void *>((reinterpret_cast<uintptr_t>(p) + 255) & ~uintptr_t(255));
+}
+
+// How an operand gets into LDS: straight where its 16-byte pieces start on 16
+// bytes and, where k is slow, none crosses the end of a row; through registers
+// where a row (k slow) or a sum has a piece at least and a stage's offsets fit 31 bits.
+Mode mode_of(const void *p, uint64_t ld, bool slow, uint32_t extent, uint32_t K, int type) {
+    const uint64_t size = type_bytes(type), piece = 16 / size;
+    if ((slow ? extent : K) < piece || ld * size >= (uint64_t(1) << 31) / 256) return kAny;
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * size % 16 == 0 && (!slow || extent * size % 16 == 0) ? kDirect : kHeld;
+}
+
+gc_status launch(const char *fn, Kind kind, int type, const Product &p, void *ws, hipStream_t stream) {
+    const Mode mode = std::max(mode_of(p.A, p.lda, kind == kWeight, p.M, p.K, type), mode_of(p.B, p.ldb, kind != kForward, p.N, p.K, type));
+    Cut c = plan_cut(kind, type, p.M, p.N, p.K, mode == kAny);
+    c.mode = mode;
+    const ShapeModel &s = model_of(c);
+    if (ceil_div(p.M, s.tm) * ceil_div(p.N, s.tn) > max_grid(512)) return fail(fn, GC_ERANGE, "more workgroups than a launch has");
+    (void)cut_ws(c, align256(ws));
+    if (type == GC_F32) return linear_launch<F32>(fn, kind, p, c, stream);
+    if (type == GC_BF16) return linear_launch<BF16>(fn, kind, p, c, stream);
+    return linear_launch<F16>(fn, kind, p, c, stream);
+}
 
 const void *at_element(const void *base, uint64_t elem, int type) { return static_cast<const char *>(base) + elem * type_bytes(type); }
 
@@ -471,7 +227,7 @@ extern "C" gc_status gc_linear_forward(const gc_plan *plan, const gc_linear *lay
     p.out = y;
     p.ldout = y_stride;
     p.act = act;
-    return launch<kForward>(fn, type, p, stream);
+    return launch(fn, kForward, type, p, ws, stream);
 }
 
 extern "C" gc_status gc_act_grad(const void *dy, uint64_t dy_stride, const void *z, uint64_t z_stride, int act, int type,
@@ -488,7 +244,7 @@ extern "C" gc_status gc_act_grad(const void *dy, uint64_t dy_stride, const void 
     GC_TRY(check_rows(fn, dz, dz_stride, n_rows, cols, type, true));
     if ((dz == dy && dz_stride != dy_stride) || (dz == z && dz_stride != z_stride))
         return fail(fn, GC_EINVAL, "dz in place of another array must have its stride");
-    const uint64_t grid = ceil_div(n_rows * ceil_div(cols, 4), kBlock);
+    const uint64_t grid = ceil_div(n_rows * ceil_div(cols, kActCols), kBlock);
     if (grid > max_grid(kBlock)) return fail(fn, GC_ERANGE, "more workgroups than a launch has");
     auto go = [&](auto t) {
         GC_LAUNCH("act_grad", stream,
@@ -536,14 +292,14 @@ extern "C" gc_status gc_linear_grad_input(const gc_plan *plan, const gc_linear *
     p.K = rows;
     p.add = a;
     p.ldadd = a_stride;
-    p.z = z;
+    p.z = dzx && act != GC_ACT_NONE ? z : nullptr;
     p.ldz = z_stride;
     p.out = dx;
     p.ldout = dx_stride;
     p.out2 = dzx;
     p.ldout2 = dzx_stride;
     p.act = act;
-    return launch<kInput>(fn, type, p, stream);
+    return launch(fn, kInput, type, p, ws, stream);
 }
 
 extern "C" gc_status gc_linear_grad_weight(const gc_plan *plan, const gc_linear *layer, const void *dz, uint64_t dz_stride,
@@ -576,5 +332,5 @@ extern "C" gc_status gc_linear_grad_weight(const gc_plan *plan, const gc_linear 
     p.ldout = cols;
     p.gbias = layer->bias_seg >= 0 ? g + plan->seg[layer->bias_seg].off : nullptr;
     p.accumulate = accumulate ? 1 : 0;
-    return launch<kWeight>(fn, type, p, stream);
+    return launch(fn, kWeight, type, p, ws, stream);
 }
