@@ -2,6 +2,7 @@
 // (gc_top_logits), and the loss of a student's rows with its gradient
 // (gc_distill_loss).  One workgroup a row.
 #include <string>
+#include <type_traits>
 
 #include "gc_internal.hpp"
 
@@ -9,9 +10,12 @@ namespace gc {
 
 namespace {
 
-constexpr int kThreads = 1024;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr uint32_t kNone = 0xFFFFFFFFu;
+
+// 16 bytes of a row are one vector of it.
+template <class T>
+constexpr int kVec = 16 / int(sizeof(typename T::Store));
 
 // N elements of a row from c on; those at or past `cols` are -Inf.
 template <class T, int N>
@@ -26,34 +30,84 @@ __device__ __forceinline__ void load_logits(const typename T::Store *row, uint32
     }
 }
 
-template <class T>
-constexpr int kVec = 16 / int(sizeof(typename T::Store));  // 16 bytes
+__device__ __forceinline__ float across(float x, int d) { return __shfl_xor(x, d, kWave); }
+__device__ __forceinline__ double across(double x, int d) { return __shfl_xor(x, d, kWave); }
 
-// The workgroup's maximum (NaNs left out) and sums, in every thread.
+// op over the values of the workgroup's threads, in every thread: a tree over
+// a wave's lanes, then over the waves.
+template <int NT, class V, class Op>
+__device__ __forceinline__ V block_reduce(V x, V *lds, Op op) {
+    constexpr int kCount = NT / kWave;
+    static_assert((kCount & (kCount - 1)) == 0 && kCount <= kWave, "a lane per wave");
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) x = op(x, across(x, d));
+    __syncthreads();
+    if (lane_id() == 0) lds[wave_id()] = x;
+    __syncthreads();
+    x = lds[lane_id() & (kCount - 1)];
+#pragma unroll
+    for (int d = 1; d < kCount; d <<= 1) x = op(x, across(x, d));
+    return x;
+}
+
+// The maximum leaves NaNs out.
+template <int NT>
 __device__ __forceinline__ float block_max(float x, float *lds) {
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) x = fmaxf(x, __shfl_xor(x, d, kWave));
-    __syncthreads();
-    if (lane_id() == 0) lds[wave_id()] = x;
-    __syncthreads();
-    x = lds[0];
-    for (uint32_t w = 1; w < blockDim.x / kWave; ++w) x = fmaxf(x, lds[w]);
-    return x;
+    return block_reduce<NT>(x, lds, [](float a, float b) { return fmaxf(a, b); });
 }
-template <class V>
+template <int NT, class V>
 __device__ __forceinline__ V block_sum(V x, V *lds) {
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) x = x + __shfl_xor(x, d, kWave);
-    __syncthreads();
-    if (lane_id() == 0) lds[wave_id()] = x;
-    __syncthreads();
-    x = lds[0];
-    for (uint32_t w = 1; w < blockDim.x / kWave; ++w) x = x + lds[w];
-    return x;
+    return block_reduce<NT>(x, lds, [](V a, V b) { return a + b; });
 }
 
-// A maximum to subtract: 0 where every value was -Inf.
-__device__ __forceinline__ float finite_max(float m) { return m == -INFINITY ? 0.0f : m; }
+// exp2 of the hardware (within a step; results below 2^-126 are 0).
+__device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// A sum of exp((x_j - r) / T), r an element near the largest: differences first, so that neither
+// a large common part of the logits nor a row of the type's lowest value costs anything.  c is
+// log2(e) / T throughout.
+struct Sum {
+    float r, s;
+};
+constexpr Sum kNoTerms{-INFINITY, 0.0f};
+__device__ __forceinline__ float term(float x, float r, float c) { return exp2_of((x - r) * c); }
+__device__ __forceinline__ Sum join(Sum a, Sum b, float c) {
+    const float r = fmaxf(a.r, b.r);
+    // an empty side has r = -Inf; its s is 0, or NaN where a NaN was its only term
+    const float fa = a.r == r ? 1.0f : term(a.r, r, c), fb = b.r == r ? 1.0f : term(b.r, r, c);
+    return Sum{r, a.s * fa + b.s * fb};
+}
+__device__ __forceinline__ Sum across(Sum x, int d) { return Sum{__shfl_xor(x.r, d, kWave), __shfl_xor(x.s, d, kWave)}; }
+template <int NT>
+__device__ __forceinline__ Sum block_join(Sum x, float c, Sum *lds) {
+    return block_reduce<NT>(x, lds, [c](Sum a, Sum b) { return join(a, b, c); });
+}
+
+// An element to subtract: 0 where there is none.
+__device__ __forceinline__ float base(Sum a) { return a.r == -INFINITY ? 0.0f : a.r; }
+
+// Adds a vector's terms.  `top` is its largest value (NaNs left out).  The
+// reference moves only where a term could pass 2^kRoom.
+constexpr float kRoom = 32.0f;
+template <int N>
+__device__ __forceinline__ void add_terms(Sum &a, float c, const float (&v)[N], float top) {
+    if (!((top - a.r) * c <= kRoom) && top > -INFINITY) {
+        a.s = a.r == -INFINITY ? a.s : a.s * term(a.r, top, c);
+        a.r = top;
+    }
+    const float r = base(a);
+#pragma unroll
+    for (int u = 0; u < N; ++u) a.s = a.s + term(v[u], r, c);
+    asm volatile("" : "+v"(a.s));  // now: the terms of all vectors, kept for later, do not fit the registers
+}
+
+template <int N>
+__device__ __forceinline__ float largest(const float (&v)[N]) {
+    float m = v[0];
+#pragma unroll
+    for (int u = 1; u < N; ++u) m = fmaxf(m, v[u]);
+    return m;
+}
 
 // ------------------------------------------------------------------- top k
 // Logits in the order of their values as unsigned keys; -0 as +0, and 0 for
@@ -67,113 +121,186 @@ __device__ __forceinline__ float key_value(uint32_t key) {
     return dev_u2f(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
 
-// Three passes of 11, 11 and 10 bits find the key of the k-th candidate; all
-// above it are taken, and of those equal to it the first by index.
-template <class T>
-__global__ __launch_bounds__(kThreads) void top_kernel(const typename T::Store *__restrict__ logits, uint64_t stride,
-                                                       uint32_t vocab, uint32_t k, float scale, int32_t *__restrict__ idx,
-                                                       float *__restrict__ val, float *__restrict__ lse) {
+// The order of entries as one number: the key above, and below it 2^20 - 1 - column.
+constexpr int kColBits = 20;
+static_assert(GC_MAX_VOCAB <= 1u << kColBits, "columns fit");
+__device__ __forceinline__ uint64_t entry_of(uint32_t key, uint32_t col) {
+    return (static_cast<uint64_t>(key) << kColBits) | ((1u << kColBits) - 1 - col);
+}
+
+// The digits of an entry, from the highest: 11, 11, 10 bits of the key, 10, 10 of the column.
+struct Digit {
+    int shift, bits;
+};
+__device__ __forceinline__ Digit digit_of(int pass) {
+    return pass == 0 ? Digit{41, 11} : pass == 1 ? Digit{30, 11} : pass == 2 ? Digit{20, 10} : pass == 3 ? Digit{10, 10} : Digit{0, 10};
+}
+
+// The `want` largest of the entries that each(f) calls f for (by all threads alike): every entry with
+// (entry & known) > prefix is taken, and every one with (entry & known) == prefix.
+template <int NT, class Each>
+__device__ __forceinline__ void select_entries(uint32_t want, Each each, uint32_t *hist, uint64_t *known_out, uint64_t *prefix_out) {
+    uint64_t known = 0, prefix = 0;
+    uint32_t need = want;
+    for (int pass = 0; pass < 5; ++pass) {
+        const Digit d = digit_of(pass);
+        const uint64_t mask = ((1ull << d.bits) - 1) << d.shift;
+        for (uint32_t i = threadIdx.x; i < 2048; i += NT) hist[i] = 0;
+        __syncthreads();
+        each([&](uint64_t e) {
+            if ((e & known) == prefix) atomicAdd(&hist[(e & mask) >> d.shift], 1u);
+        });
+        __syncthreads();
+        uint32_t above;
+        const uint32_t b = block_find_bucket<2048, NT>(need, [&](int i) { return hist[i]; }, &above);
+        need -= above;
+        prefix |= static_cast<uint64_t>(b) << d.shift;
+        known |= mask;
+        const bool all = hist[b] == need;  // the whole bucket is taken
+        __syncthreads();
+        if (all) break;
+    }
+    *known_out = known;
+    *prefix_out = prefix;
+}
+
+// The top k of a row.  A bound under the k-th largest comes from a sample: the maxima of kSample vectors a
+// thread, spread over the row; k of those are above it.  One pass then lists what is above the bound, with the
+// sums beside it, and the list's top k are found digit by digit and ranked by counting.  A row that fills the
+// list (many ties, a sample that misses the large ones) is read again, digit by digit.  Memory bounds
+// the pass.
+constexpr uint32_t kListEntries = 4096;
+
+template <class T, int NT>
+__global__ __launch_bounds__(NT) void top_kernel(const typename T::Store *__restrict__ logits, uint64_t stride, uint32_t vocab,
+                                                 uint32_t k, float scale, int32_t *__restrict__ idx, float *__restrict__ val,
+                                                 float *__restrict__ lse) {
     constexpr int N = kVec<T>;
+    constexpr uint32_t kSample = 4, kAhead = 4;
     __shared__ uint32_t hist[2048];
-    __shared__ uint32_t keys[GC_MAX_TOP_LOGITS], cols[GC_MAX_TOP_LOGITS];
-    __shared__ float red[kThreads / kWave];
-    __shared__ uint32_t taken;
+    __shared__ uint64_t list[kListEntries], best[GC_MAX_TOP_LOGITS];
+    __shared__ float red[NT / kWave];
+    __shared__ Sum sums[NT / kWave];
+    __shared__ uint32_t listed, taken;
     const uint64_t r = blockIdx.x;
     const typename T::Store *row = logits + r * stride;
-    const uint32_t t = threadIdx.x;
-    // statistics, and the number of candidates
-    float m = -INFINITY;
-    uint32_t cand = 0;
-    for (uint32_t c = t * N; c < vocab; c += kThreads * N) {
-        float v[N];
-        load_logits<T>(row, c, vocab, v);
+    const uint32_t t = threadIdx.x, vecs = static_cast<uint32_t>(ceil_div(vocab, N));
+    // The sample.
+    const uint32_t most = (vecs + NT - 1) / NT, ns = min(min(kSample, (4 * k + NT - 1) / NT), most);
+    float top[kSample], high = -INFINITY, low = INFINITY;
 #pragma unroll
-        for (int u = 0; u < N; ++u) {
-            m = fmaxf(m, v[u]);
-            cand += v[u] > -INFINITY;
+    for (uint32_t i = 0; i < kSample; ++i) {
+        top[i] = -INFINITY;
+        const uint32_t g = i * NT + t;  // group g of ns NT, or of all vectors where those are fewer
+        if (i < ns && g < vecs) {
+            const uint32_t at = vecs <= ns * NT ? g : static_cast<uint32_t>(static_cast<uint64_t>(g) * vecs / (ns * NT));
+            float v[N];
+            load_logits<T>(row, at * N, vocab, v);
+            top[i] = largest(v);
+            high = fmaxf(high, top[i]);
+            if (top[i] > -INFINITY) low = fminf(low, top[i]);
         }
     }
-    m = finite_max(block_max(m, red));
-    if (lse) {
-        float s = 0.0f;
-        for (uint32_t c = t * N; c < vocab; c += kThreads * N) {
-            float v[N];
-            load_logits<T>(row, c, vocab, v);
+    if (t == 0) listed = taken = 0;
+    for (uint32_t i = t; i < 2048; i += NT) hist[i] = 0;
+    high = block_max<NT>(high, red);
+    low = -block_max<NT>(-low, red);
+    // bins of the distance from the largest; its order is the values' reversed
+    const float per = 2047.0f / (high - low);
+    const bool usable = high < INFINITY && per > 0.0f && per < INFINITY;
+    float limit = INFINITY;  // listed is what has (high - x) per < limit
+    if (usable) {
+        uint32_t mine = 0;
 #pragma unroll
-            for (int u = 0; u < N; ++u) s = s + (v[u] == m ? 1.0f : expf((v[u] - m) * scale));
+        for (uint32_t i = 0; i < kSample; ++i)
+            if (top[i] > -INFINITY) {
+                atomicAdd(&hist[2047 - static_cast<uint32_t>((high - top[i]) * per)], 1u);
+                ++mine;
+            }
+        uint32_t groups;
+        (void)block_exclusive_scan<uint32_t, NT>(mine, &groups);
+        if (groups >= k) {
+            uint32_t above;
+            limit = static_cast<float>(2048 - block_find_bucket<2048, NT>(k, [&](int b) { return hist[b]; }, &above));
         }
-        s = block_sum(s, red);
-        if (t == 0) lse[r] = m * scale + logf(s);
+    }
+    const float from = usable ? high : 0.0f, by = usable ? per : 0.0f;
+    // (x - 0) 0 is NaN for an infinite x, which has no place below the limit
+    __syncthreads();
+    const float c2 = scale * kLog2e;
+    Sum sum = kNoTerms;
+    uint32_t cand = 0;
+    for (uint32_t b = 0; b < vecs; b += NT * kAhead) {
+        float v[kAhead][N];
+#pragma unroll
+        for (uint32_t i = 0; i < kAhead; ++i) {
+            const uint32_t at = b + i * NT + t;
+            if (at < vecs) load_logits<T>(row, at * N, vocab, v[i]);
+            else
+#pragma unroll
+                for (int u = 0; u < N; ++u) v[i][u] = -INFINITY;
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < kAhead; ++i) {
+            const float m = largest(v[i]);
+            if (m > -INFINITY && !((from - m) * by >= limit)) {
+#pragma unroll
+                for (uint32_t u = 0; u < N; ++u)
+                    if (v[i][u] > -INFINITY && !((from - v[i][u]) * by >= limit)) {
+                        const uint32_t p = atomicAdd(&listed, 1u);
+                        if (p < kListEntries) list[p] = entry_of(order_key(v[i][u]), (b + i * NT + t) * N + u);
+                    }
+            }
+            if (lse) add_terms(sum, c2, v[i], m);
+#pragma unroll
+            for (int u = 0; u < N; ++u) cand += v[i][u] > -INFINITY;
+        }
+    }
+    if (lse) {
+        sum = block_join<NT>(sum, c2, sums);
+        if (t == 0) lse[r] = base(sum) * scale + logf(sum.s);
     }
     uint32_t total;
-    (void)block_exclusive_scan<uint32_t, kThreads>(cand, &total);
-    const uint32_t want = min(k, total);
-    uint32_t prefix = 0, known = 0, need = want;  // keys with these top bits hold the `need`-th of the rest
+    (void)block_exclusive_scan<uint32_t, NT>(cand, &total);
+    const uint32_t want = min(k, total), n = listed;
     if (want) {
-        for (int pass = 0; pass < 3; ++pass) {
-            const int bits = pass < 2 ? 11 : 10, low = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-            for (uint32_t i = t; i < 2048; i += kThreads) hist[i] = 0;
-            __syncthreads();
-            for (uint32_t c = t * N; c < vocab; c += kThreads * N) {
-                float v[N];
-                load_logits<T>(row, c, vocab, v);
+        uint64_t known, prefix;
+        auto take = [&](uint64_t e) {
+            if ((e & known) >= prefix) best[atomicAdd(&taken, 1u)] = e;  // in any order: ranked below
+        };
+        if (n >= want && n <= kListEntries) {
+            auto each = [&](auto f) {
+                for (uint32_t i = t; i < n; i += NT) f(list[i]);
+            };
+            select_entries<NT>(want, each, hist, &known, &prefix);
+            each(take);
+        } else {
+            auto each = [&](auto f) {
+                for (uint32_t at = t; at < vecs; at += NT) {
+                    float v[N];
+                    load_logits<T>(row, at * N, vocab, v);
 #pragma unroll
-                for (int u = 0; u < N; ++u) {
-                    const uint32_t key = order_key(v[u]);
-                    if (key && (key & known) == prefix) atomicAdd(&hist[(key >> low) & ((1u << bits) - 1)], 1u);
-                }
-            }
-            __syncthreads();
-            uint32_t above;
-            const uint32_t d = block_find_bucket<2048, kThreads>(need, [&](int b) { return hist[b]; }, &above);
-            need -= above;
-            prefix |= d << low;
-            known |= ((1u << bits) - 1) << low;
-        }
-        if (t == 0) taken = 0;
-        __syncthreads();
-        const uint32_t over = want - need;  // keys above the threshold
-        uint32_t equal = 0;                 // equal ones in front of this part of the row
-        for (uint32_t c0 = 0; c0 < vocab; c0 += kThreads * N) {
-            float v[N];
-            load_logits<T>(row, c0 + t * N, vocab, v);
-            uint32_t mine = 0;
-#pragma unroll
-            for (int u = 0; u < N; ++u) {
-                const uint32_t key = order_key(v[u]);
-                if (key > prefix) {
-                    const uint32_t at = atomicAdd(&taken, 1u);  // any order: ranked below
-                    keys[at] = key;
-                    cols[at] = c0 + t * N + u;
-                }
-                mine += key == prefix;
-            }
-            uint32_t here;
-            uint32_t at = equal + block_exclusive_scan<uint32_t, kThreads>(mine, &here);
-            if (mine)
-#pragma unroll
-                for (int u = 0; u < N; ++u)
-                    if (order_key(v[u]) == prefix) {
-                        if (at < need) {
-                            keys[over + at] = prefix;
-                            cols[over + at] = c0 + t * N + u;
-                        }
-                        ++at;
+                    for (uint32_t u = 0; u < N; ++u) {
+                        const uint32_t key = order_key(v[u]);
+                        if (key) f(entry_of(key, at * N + u));
                     }
-            equal += here;
+                }
+            };
+            select_entries<NT>(want, each, hist, &known, &prefix);
+            each(take);
         }
         __syncthreads();
     }
-    if (t < k) {
-        if (t < want) {
-            const uint32_t key = keys[t], col = cols[t];
+    for (uint32_t i = t; i < k; i += NT) {
+        if (i < want) {
+            const uint64_t e = best[i];
             uint32_t rank = 0;
-            for (uint32_t j = 0; j < want; ++j) rank += keys[j] > key || (keys[j] == key && cols[j] < col);
-            idx[r * k + rank] = static_cast<int32_t>(col);
-            val[r * k + rank] = key_value(key);
+            for (uint32_t j = 0; j < want; ++j) rank += best[j] > e;
+            idx[r * k + rank] = static_cast<int32_t>((1u << kColBits) - 1 - (e & ((1u << kColBits) - 1)));
+            val[r * k + rank] = key_value(static_cast<uint32_t>(e >> kColBits));
         } else {
-            idx[r * k + t] = -1;
-            val[r * k + t] = -INFINITY;
+            idx[r * k + i] = -1;
+            val[r * k + i] = -INFINITY;
         }
     }
 }
@@ -186,209 +313,252 @@ struct Distill {
     void *dlogits;
     uint64_t stride, idx_stride, t_stride, dstride;
     uint32_t vocab, k;
-    int t_type, rest;
+    int id_type, t_type, rest;
     float inv_t, kd, kd_slope, ce, grad;  // 1 / T; kd T^2 and kd T
 };
 
-// The largest value so far and the sums of exp relative to it, at 1 / T and at 1.
-struct Stats {
-    float m, st, s1;
-};
-__device__ __forceinline__ Stats join(const Stats &a, const Stats &b, float ct) {
-    Stats o;
-    o.m = fmaxf(a.m, b.m);
-    const float m = finite_max(o.m);
-    // an empty side has m = -Inf and sums of 0
-    const float fa = (finite_max(a.m) - m) * kLog2e, fb = (finite_max(b.m) - m) * kLog2e;
-    const bool ea = a.m == -INFINITY, eb = b.m == -INFINITY;
-    o.st = (ea ? a.st : a.st * exp2f(fa * ct)) + (eb ? b.st : b.st * exp2f(fb * ct));
-    o.s1 = (ea ? a.s1 : a.s1 * exp2f(fa)) + (eb ? b.s1 : b.s1 * exp2f(fb));
-    return o;
+__device__ __forceinline__ int64_t id_at(const void *ids, int type, uint64_t at) {
+    return type == GC_TOKENS_I32 ? static_cast<const int32_t *>(ids)[at] : static_cast<const int64_t *>(ids)[at];
 }
-
 __device__ __forceinline__ float teacher_value(const Distill &d, uint64_t at) {
     if (d.t_type == GC_F32) return static_cast<const float *>(d.t)[at];
     const uint16_t x = static_cast<const uint16_t *>(d.t)[at];
     return d.t_type == GC_BF16 ? BF16::to_f32(x) : F16::to_f32(x);
 }
 
-// LDS: columns, q and student logits of the entries, then a bit per column
-// (GC_DISTILL_REST) of those that an entry names.
-template <class T, class Ids>
-__global__ __launch_bounds__(kThreads) void distill_kernel(Distill d) {
+// A row of logits: C vectors a thread, held in registers from the first sweep to the last (the row is read once),
+// or, C = 0, read by each sweep.
+template <class T, int NT, int C>
+struct Row {
+    static constexpr int N = kVec<T>;
+    using Store = typename T::Store;
+    const Store *row;
+    uint32_t vocab;
+    u32x4 raw[C ? C : 1];
+
+    // The vector that ends with the row stands for the one that crosses its end, and for those past it.
+    __device__ __forceinline__ uint32_t column(int i, uint32_t t) const { return min((i * NT + t) * N, vocab - N); }
+    __device__ __forceinline__ void load() {
+#pragma unroll
+        for (int i = 0; i < C; ++i) raw[i] = __builtin_bit_cast(u32x4, *reinterpret_cast<const Pack<Store, N> *>(row + column(i, threadIdx.x)));
+    }
+    // f(column, values, count): columns that another call has already are -Inf for kOnce; count of them exist.
+    template <bool kOnce, class F>
+    __device__ __forceinline__ void each(F f) const {
+        float v[N];
+        if constexpr (C > 0) {
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                // a vector at a time, neither its values in fp32 nor its place kept for another sweep: else they do
+                // not fit the registers
+                u32x4 w = raw[i];
+                uint32_t t = threadIdx.x;
+                asm volatile("" : "+v"(w), "+v"(t));
+                const uint32_t c = column(i, t), own = (i * NT + t) * N;
+                const auto x = __builtin_bit_cast(Pack<Store, N>, w);
+#pragma unroll
+                for (int u = 0; u < N; ++u) v[u] = T::to_f32(x.v[u]);
+                if (kOnce && (i + 1) * NT * N > static_cast<int>(vocab))
+#pragma unroll
+                    for (uint32_t u = 0; u < N; ++u) v[u] = c + u < own ? -INFINITY : v[u];
+                if (kOnce || own < vocab) f(c, v, uint32_t(N));
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        } else {
+            for (uint32_t c = threadIdx.x * N; c < vocab; c += NT * N) {
+                load_logits<T>(row, c, vocab, v);
+                f(c, v, min(vocab - c, uint32_t(N)));
+            }
+        }
+    }
+};
+
+// LDS: columns, q, q summed over a column's entries, and student logits of the entries, and
+// (GC_DISTILL_REST) a bit per column that an entry names.
+// The row's exponentials and its two trips over HBM bound it.  kTwo: the labels' softmax has another
+// temperature than the teacher's.
+template <class T, int NT, int C, bool kTwo>
+__global__ __launch_bounds__(NT) void distill_kernel(Distill d) {
     constexpr int N = kVec<T>;
     using Store = typename T::Store;
     extern __shared__ __attribute__((aligned(16))) uint32_t dyn[];
-    __shared__ float red[kThreads / kWave];
-    __shared__ double redd[kThreads / kWave];
-    __shared__ Stats reds[kThreads / kWave];
+    __shared__ float red[NT / kWave];
+    __shared__ double redd[NT / kWave];
+    __shared__ Sum reds[NT / kWave];
+    const uint32_t t = threadIdx.x, V = d.vocab, K = d.k, K4 = (K + 3) & ~3u;
     uint32_t *col = dyn;
-    float *q = reinterpret_cast<float *>(dyn + d.k), *zk = q + d.k;
-    uint32_t *named = dyn + 3 * d.k;
+    float *q = reinterpret_cast<float *>(dyn + K4), *qs = q + K4, *zk = qs + K4;
+    uint32_t *named = dyn + 4 * K4;
     const uint64_t r = blockIdx.x;
-    const uint32_t t = threadIdx.x, V = d.vocab, K = d.k;
     const Store *row = static_cast<const Store *>(d.logits) + r * d.stride;
     Store *out = d.dlogits ? static_cast<Store *>(d.dlogits) + r * d.dstride : nullptr;
 
     const float weight = d.weights ? d.weights[r] : 1.0f;
     uint32_t label = kNone;
     if (d.labels && d.ce != 0.0f) {
-        const int64_t l = static_cast<const Ids *>(d.labels)[r];
+        const int64_t l = id_at(d.labels, d.id_type, r);
         if (l >= 0 && l < static_cast<int64_t>(V)) label = static_cast<uint32_t>(l);
     }
     // the teacher's entries
     float tmax = -INFINITY;
     uint32_t count = 0;
     if (d.kd != 0.0f)
-        for (uint32_t e = t; e < K; e += kThreads) {
-            const int64_t c = static_cast<const Ids *>(d.idx)[r * d.idx_stride + e];
+        for (uint32_t e = t; e < K; e += NT) {
+            const int64_t c = id_at(d.idx, d.id_type, r * d.idx_stride + e);
             const float v = teacher_value(d, r * d.t_stride + e);
             const bool there = c >= 0 && c < static_cast<int64_t>(V) && v != -INFINITY;
             col[e] = there ? static_cast<uint32_t>(c) : kNone;
             q[e] = v;
-            zk[e] = there ? T::to_f32(row[c]) : 0.0f;
             tmax = there ? fmaxf(tmax, v) : tmax;
             count += there;
         }
     uint32_t entries;
-    (void)block_exclusive_scan<uint32_t, kThreads>(count, &entries);
+    (void)block_exclusive_scan<uint32_t, NT>(count, &entries);
     if (weight == 0.0f || (entries == 0 && label == kNone)) {
         if (t == 0) d.loss[r] = 0.0f;
         if (out)
-            for (uint32_t c = t; c < V; c += kThreads) out[c] = Store(0);
+            for (uint32_t c = t * N; c < V; c += NT * N) {
+                if (c + N <= V) *reinterpret_cast<Pack<Store, N> *>(out + c) = Pack<Store, N>{};
+                else
+                    for (uint32_t u = c; u < V; ++u) out[u] = Store(0);
+            }
         return;
     }
+    // the row is on its way while the teacher is looked at
+    Row<T, NT, C> z{row, V};
+    z.load();
+    const float zl = label != kNone ? T::to_f32(row[label]) : 0.0f;
     const bool rest = d.rest && entries;
-    if (rest) {
-        for (uint32_t i = t; i < (V + 31) / 32; i += kThreads) named[i] = 0;
-        __syncthreads();
-        for (uint32_t e = t; e < K; e += kThreads)
-            if (col[e] != kNone) atomicOr(&named[col[e] / 32], 1u << (col[e] % 32));
-    }
-    tmax = finite_max(block_max(tmax, red));
-    const float tlse = d.rest ? (d.t_lse ? d.t_lse[r] : 0.0f) : tmax * d.inv_t;
+    if (rest)
+        for (uint32_t i = t; i < (V + 31) / 32 + 1; i += NT) named[i] = 0;
     double qsum = 0.0;
-    if (entries)
-        for (uint32_t e = t; e < K; e += kThreads) {
-            q[e] = col[e] == kNone ? 0.0f : expf((d.rest ? q[e] * d.inv_t - tlse : (q[e] - tmax) * d.inv_t));
-            qsum += q[e];
+    if (entries) {
+        for (uint32_t e = t; e < K4; e += NT) {
+            if (e >= K) col[e] = kNone;
+            else if (col[e] != kNone) zk[e] = T::to_f32(row[col[e]]);
         }
-    qsum = block_sum(qsum, redd);
-    if (entries && !d.rest) {
-        const float inv = static_cast<float>(1.0 / qsum);
-        for (uint32_t e = t; e < K; e += kThreads) q[e] = q[e] * inv;
-        qsum = 1.0;
+        tmax = block_max<NT>(tmax, red);
+        tmax = tmax == -INFINITY ? 0.0f : tmax;
+        const float tlse = d.rest ? d.t_lse[r] : 0.0f;
+        for (uint32_t e = t; e < K; e += NT) {
+            const bool there = col[e] != kNone;
+            q[e] = there ? expf(d.rest ? q[e] * d.inv_t - tlse : (q[e] - tmax) * d.inv_t) : 0.0f;
+            qsum += q[e];
+            if (rest && there) atomicOr(&named[col[e] / 32], 1u << (col[e] % 32));
+        }
+        qsum = block_sum<NT>(qsum, redd);
+        const float inv = d.rest ? 1.0f : static_cast<float>(1.0 / qsum);
+        qsum = d.rest ? qsum : 1.0;
+        for (uint32_t e = t; e < K; e += NT) q[e] = q[e] * inv;
+        __syncthreads();
+        // a column's first entry holds the sum of all of them, the others a negative number
+        for (uint32_t e = t; e < K; e += NT) {
+            const uint32_t c = col[e];
+            float sum = 0.0f;
+            bool first = c != kNone;
+            if (first)
+                for (uint32_t j = 0; j < K4; j += 4) {
+                    const uint4 o = *reinterpret_cast<const uint4 *>(col + j);
+                    if (o.x == c || o.y == c || o.z == c || o.w == c)
+#pragma unroll
+                        for (uint32_t u = 0; u < 4; ++u)
+                            if ((u == 0 ? o.x : u == 1 ? o.y : u == 2 ? o.z : o.w) == c) {
+                                first = first && j + u >= e;
+                                sum = sum + q[j + u];
+                            }
+                }
+            qs[e] = first ? sum : -1.0f;
+        }
     }
     __syncthreads();
 
-    // the row, or the rest of it
-    const float ct = d.inv_t, c1 = kLog2e, c2 = d.inv_t * kLog2e;
-    Stats s{-INFINITY, 0.0f, 0.0f};
-    for (uint32_t c = t * N; c < V; c += kThreads * N) {
-        float v[N];
-        load_logits<T>(row, c, V, v);
+    // the row, or the rest of it: sums of exp at 1 / T and, for another softmax of the labels, at 1
+    const float c2 = d.inv_t * kLog2e, c1 = kTwo ? kLog2e : c2;
+    Sum s2 = kNoTerms, s1 = kNoTerms;
+    z.template each<true>([&](uint32_t c, float(&v)[N], uint32_t) {
         if (rest) {
-            const uint32_t bits = named[c / 32] >> (c % 32);
+            const uint32_t w = c / 32;
+            const uint32_t bits = __builtin_amdgcn_alignbit(named[w + 1], named[w], c % 32);
+            if (bits & ((1u << N) - 1))
 #pragma unroll
-            for (int u = 0; u < N; ++u) v[u] = bits >> u & 1 ? -INFINITY : v[u];
+                for (int u = 0; u < N; ++u) v[u] = bits >> u & 1 ? -INFINITY : v[u];
         }
-        Stats p{v[0], 0.0f, 0.0f};
-#pragma unroll
-        for (int u = 1; u < N; ++u) p.m = fmaxf(p.m, v[u]);
-        const float m = finite_max(p.m);
-#pragma unroll
-        for (int u = 0; u < N; ++u) {
-            p.st = p.st + exp2f((v[u] - m) * c2);
-            p.s1 = p.s1 + exp2f((v[u] - m) * c1);
-        }
-        s = join(s, p, ct);
-    }
-#pragma unroll
-    for (int x = 1; x < kWave; x <<= 1)
-        s = join(s, Stats{__shfl_xor(s.m, x, kWave), __shfl_xor(s.st, x, kWave), __shfl_xor(s.s1, x, kWave)}, ct);
-    if (lane_id() == 0) reds[wave_id()] = s;
-    __syncthreads();
-    s = reds[0];
-    for (int w = 1; w < kThreads / kWave; ++w) s = join(s, reds[w], ct);
-    const Stats of_rest = s;
-    // the entries that were left out, each column once
-    Stats all = s;
-    if (rest) {
-        Stats mine{-INFINITY, 0.0f, 0.0f};
-        for (uint32_t e = t; e < K; e += kThreads) {
-            bool first = col[e] != kNone;
-            for (uint32_t j = 0; first && j < e; ++j) first = col[j] != col[e];
-            if (first) {
-                const float z = zk[e], m = finite_max(z);
-                mine = join(mine, Stats{z, exp2f((z - m) * c2), exp2f((z - m) * c1)}, ct);
+        const float top = largest(v);
+        add_terms(s2, c2, v, top);
+        if (kTwo) add_terms(s1, c1, v, top);
+    });
+    const Sum rest2 = block_join<NT>(s2, c2, reds);
+    Sum all2 = rest2, all1 = rest2;
+    if (kTwo) all1 = block_join<NT>(s1, c1, reds);
+    if (rest) {  // the entries that were left out, each column once
+        s2 = s1 = kNoTerms;
+        for (uint32_t e = t; e < K; e += NT)
+            if (qs[e] >= 0.0f || qs[e] != qs[e]) {
+                const float v[1] = {zk[e]};
+                add_terms(s2, c2, v, v[0]);
+                if (kTwo) add_terms(s1, c1, v, v[0]);
             }
-        }
-#pragma unroll
-        for (int x = 1; x < kWave; x <<= 1)
-            mine = join(mine, Stats{__shfl_xor(mine.m, x, kWave), __shfl_xor(mine.st, x, kWave), __shfl_xor(mine.s1, x, kWave)}, ct);
-        __syncthreads();
-        if (lane_id() == 0) reds[wave_id()] = mine;
-        __syncthreads();
-        for (int w = 0; w < kThreads / kWave; ++w) all = join(all, reds[w], ct);
+        all2 = join(rest2, block_join<NT>(s2, c2, reds), c2);
+        all1 = kTwo ? join(all1, block_join<NT>(s1, c1, reds), c1) : all2;
     }
-    const float m = finite_max(all.m), mr = finite_max(of_rest.m);
-    const float logst = logf(all.st), logs1 = logf(all.s1);
-    const float held = rest && of_rest.st != 0.0f ? fmaxf(static_cast<float>(1.0 - qsum), 0.0f) : 0.0f;
+    const float r2 = base(all2), r1 = base(all1), rr = base(rest2);
+    const float log2s = logf(all2.s);
+    const float held = rest && rest2.s != 0.0f ? fmaxf(static_cast<float>(1.0 - qsum), 0.0f) : 0.0f;
     const float mass = entries ? static_cast<float>(qsum) + held : 0.0f;
     // the loss
     double kl = 0.0;
-    if (entries)
-        for (uint32_t e = t; e < K; e += kThreads)
-            if (q[e] != 0.0f) kl += q[e] * (logf(q[e]) - ((zk[e] - m) * ct - logst));
-    kl = block_sum(kl, redd);
-    if (held > 0.0f) kl += held * (logf(held) - ((mr - m) * ct + logf(of_rest.st) - logst));
-    const float zl = label != kNone ? T::to_f32(row[label]) : 0.0f;
+    if (entries) {
+        for (uint32_t e = t; e < K; e += NT)
+            if (q[e] != 0.0f) kl += q[e] * (logf(q[e]) - ((zk[e] - r2) * d.inv_t - log2s));
+        kl = block_sum<NT>(kl, redd);
+        if (held > 0.0f) kl += held * (logf(held) - ((rr - r2) * d.inv_t + logf(rest2.s) - log2s));
+    }
     if (t == 0) {
         float loss = entries ? d.kd * static_cast<float>(kl) : 0.0f;
-        if (label != kNone) loss = loss + d.ce * (logs1 - (zl - m));
+        if (label != kNone) loss = loss + d.ce * (logf(all1.s) - (kTwo ? zl - r1 : (zl - r1) * d.inv_t));
         d.loss[r] = weight * loss;
     }
     if (!out) return;
     // the gradient: kd T (mass p_j - held p_j / p_r - q_j) + ce (softmax_j - [j = label])
     const float f = weight * d.grad;
     const float kt = entries ? f * d.kd_slope : 0.0f, kc = label != kNone ? f * d.ce : 0.0f;
-    const float pt = mass * exp2f((mr - m) * c2);  // mass p_j = pt exp((z - mr) / T) / st
-    const float at = kt * (pt / all.st - (held > 0.0f ? held / of_rest.st : 0.0f));
-    const float a1 = kc * (exp2f((mr - m) * c1) / all.s1);
-    __syncthreads();  // row[label], which may lie in out, has been read
-    for (uint32_t c = t * N; c < V; c += kThreads * N) {
-        float v[N];
-        load_logits<T>(row, c, V, v);
+    const float back = term(rr, r2, c2);  // p_j = back term(z_j, rr) / all2.s
+    float g2 = kt * (mass * back / all2.s - (held > 0.0f ? held / rest2.s : 0.0f));
+    const float g1 = kc / all1.s;
+    if (!kTwo) g2 = g2 + g1 * back;
+    __syncthreads();  // zk and zl, whose places may be out's, have been read
+    z.template each<false>([&](uint32_t c, float(&v)[N], uint32_t cnt) {
+        Pack<Store, N> g;
 #pragma unroll
-        for (uint32_t u = 0; u < N; ++u) {
-            float g = 0.0f;
-            if (v[u] != -INFINITY) g = at * exp2f((v[u] - mr) * c2) + a1 * exp2f((v[u] - mr) * c1);
-            if (c + u < V) out[c + u] = T::from_f32(g);
+        for (int u = 0; u < N; ++u) {
+            float x = g2 * term(v[u], rr, c2);
+            if (kTwo) x = x + g1 * term(v[u], r1, c1);
+            g.v[u] = T::from_f32(x);
         }
-    }
+        if (cnt == N) *reinterpret_cast<Pack<Store, N> *>(out + c) = g;
+        else
+#pragma unroll
+            for (uint32_t u = 0; u < N; ++u)
+                if (u < cnt) out[c + u] = g.v[u];
+    });
     __syncthreads();
     // columns that an entry or the label names
-    for (uint32_t e = t; e < K + 1; e += kThreads) {
-        const uint32_t c = e < K ? (entries ? col[e] : kNone) : label;
-        if (c == kNone) continue;
-        bool first = true;
-        float qs = 0.0f;
-        if (entries)
-            for (uint32_t j = 0; j < K; ++j)
-                if (col[j] == c) {
-                    first = first && j >= e;
-                    qs = qs + q[j];
-                }
-        if (!first) continue;
-        const float z = e < K ? zk[e] : zl;
-        float g = kt * (mass * (exp2f((z - m) * c2) / all.st) - qs) + kc * (exp2f((z - m) * c1) / all.s1 - (c == label ? 1.0f : 0.0f));
-        if (e == K && held > 0.0f) g = g - kt * held * (exp2f((z - mr) * c2) / of_rest.st);  // a label of the rest
+    bool own_label = label != kNone;  // no entry names it
+    if (entries && label != kNone)
+        for (uint32_t j = 0; j < K; ++j) own_label = own_label && col[j] != label;
+    for (uint32_t e = t; e < K + 1; e += NT) {
+        if (e < K ? !entries || col[e] == kNone || qs[e] < 0.0f : !own_label) continue;
+        const uint32_t c = e < K ? col[e] : label;
+        const float x = e < K ? zk[e] : zl, p = term(x, r2, c2) / all2.s;
+        float g = kt * (mass * p - (e < K ? qs[e] : 0.0f)) + kc * (term(x, r1, c1) / all1.s - (c == label ? 1.0f : 0.0f));
+        if (e == K && held > 0.0f) g = g - kt * held * (term(x, rr, c2) / rest2.s);  // a label of the rest
         out[c] = T::from_f32(g);
     }
 }
 
 // --------------------------------------------------------------- host side
 constexpr uint64_t kMaxRows = uint64_t(1) << 22;
+constexpr uint64_t kShortVecs = 2048;  // rows of at most so many 16-byte vectors take 256 threads
 
 size_t type_bytes(int type) { return type == GC_F32 ? 4 : 2; }
 bool known_type(int type) { return type == GC_F32 || type == GC_BF16 || type == GC_F16; }
@@ -440,9 +610,14 @@ extern "C" gc_status gc_top_logits(const void *logits, int type, uint64_t stride
     if (misaligned(lse, 4)) return fail(fn, GC_EINVAL, "buffers must be aligned to their elements");
     auto go = [&](auto t) {
         using T = decltype(t);
-        GC_LAUNCH("top_logits", stream,
-                  top_kernel<T><<<static_cast<unsigned>(n_rows), kThreads, 0, stream>>>(
-                      static_cast<const typename T::Store *>(logits), stride, vocab, k, 1.0f / temperature, idx, val, lse));
+        auto with = [&](auto threads) {
+            constexpr int NT = decltype(threads)::value;
+            GC_LAUNCH("top_logits", stream,
+                      top_kernel<T, NT><<<static_cast<unsigned>(n_rows), NT, 0, stream>>>(
+                          static_cast<const typename T::Store *>(logits), stride, vocab, k, 1.0f / temperature, idx, val, lse));
+        };
+        if (ceil_div(vocab, kVec<T>) <= kShortVecs) with(std::integral_constant<int, 256>{});
+        else with(std::integral_constant<int, 1024>{});
     };
     if (type == GC_F32) go(F32{});
     else if (type == GC_BF16) go(BF16{});
@@ -484,25 +659,37 @@ extern "C" gc_status gc_distill_loss(const void *logits, int type, uint64_t stri
         if (dlogits == logits && dstride != stride)
             return fail(fn, GC_EINVAL, "dlogits in place of logits must have their stride");
     }
-    Distill d{logits, idx,       t,        labels,  t_lse, weights, loss, dlogits, stride, idx_stride, t_stride, dstride, vocab, k, t_type,
+    Distill d{logits, idx, t, labels, t_lse, weights, loss, dlogits, stride, idx_stride, t_stride, dstride, vocab, k, idx_type, t_type,
               opt->mode == GC_DISTILL_REST, 1.0f / T, kd, opt->kd_weight * T, opt->ce_weight, opt->grad_scale};
     if (!k) d.kd = 0.0f;
-    const size_t lds = 12 * size_t(k) + (d.rest ? 4 * ((size_t(vocab) + 31) / 32) : 0);
+    const size_t lds = 16 * ((size_t(k) + 3) & ~size_t(3)) + (d.rest ? 4 * ((size_t(vocab) + 31) / 32 + 1) : 0);
+    const bool two = labels && opt->ce_weight != 0.0f && T != 1.0f;
     hipError_t e = hipSuccess;
-    auto go = [&](auto type_tag, auto id_tag) {
-        const auto kernel = distill_kernel<decltype(type_tag), decltype(id_tag)>;
+    auto go = [&](auto kernel, int threads) {
         if (lds > 48 * 1024)
             e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
         if (e != hipSuccess) return;
-        GC_LAUNCH("distill", stream, kernel<<<static_cast<unsigned>(n_rows), kThreads, lds, stream>>>(d));
+        GC_LAUNCH("distill", stream, kernel<<<static_cast<unsigned>(n_rows), threads, lds, stream>>>(d));
     };
-    auto ids = [&](auto type_tag) {
-        if (idx_type == GC_TOKENS_I32) go(type_tag, int32_t{});
-        else go(type_tag, int64_t{});
+    auto with = [&](auto type_tag, auto is_two) {
+        using Tp = decltype(type_tag);
+        constexpr bool kTwo = decltype(is_two)::value;
+        const uint64_t vecs = ceil_div(vocab, kVec<Tp>);
+        if (vecs < 2) go(distill_kernel<Tp, 256, 0, kTwo>, 256);
+        else if (vecs <= 256 * 4) go(distill_kernel<Tp, 256, 4, kTwo>, 256);
+        else if (vecs <= 256 * 8) go(distill_kernel<Tp, 256, 8, kTwo>, 256);
+        else if (vecs <= 1024 * 4) go(distill_kernel<Tp, 1024, 4, kTwo>, 1024);
+        else if (vecs <= 1024 * 8) go(distill_kernel<Tp, 1024, 8, kTwo>, 1024);
+        else if (vecs <= 1024 * 16) go(distill_kernel<Tp, 1024, 16, kTwo>, 1024);
+        else go(distill_kernel<Tp, 1024, 0, kTwo>, 1024);
     };
-    if (type == GC_F32) ids(F32{});
-    else if (type == GC_BF16) ids(BF16{});
-    else ids(F16{});
+    auto of = [&](auto type_tag) {
+        if (two) with(type_tag, std::true_type{});
+        else with(type_tag, std::false_type{});
+    };
+    if (type == GC_F32) of(F32{});
+    else if (type == GC_BF16) of(BF16{});
+    else of(F16{});
     if (e == hipSuccess) e = hipGetLastError();
     return e == hipSuccess ? GC_OK : hip_error(e, fn);
 }
