@@ -91,9 +91,10 @@ __device__ __forceinline__ float base(Sum a) { return a.r == -INFINITY ? 0.0f : 
 constexpr float kRoom = 32.0f;
 template <int N>
 __device__ __forceinline__ void add_terms(Sum &a, float c, const float (&v)[N], float top) {
-    if (!((top - a.r) * c <= kRoom) && top > -INFINITY) {
-        a.s = a.r == -INFINITY ? a.s : a.s * term(a.r, top, c);
-        a.r = top;
+    const bool move = !((top - a.r) * c <= kRoom) && top > -INFINITY;
+    if (__builtin_expect(__ballot(move) != 0, 0)) {  // a branch of the wave: as selects its arithmetic ran every time
+        a.s = !move || a.r == -INFINITY ? a.s : a.s * term(a.r, top, c);
+        a.r = move ? top : a.r;
     }
     const float r = base(a);
 #pragma unroll
@@ -229,7 +230,6 @@ __global__ __launch_bounds__(NT) void top_kernel(const typename T::Store *__rest
     __syncthreads();
     const float c2 = scale * kLog2e;
     Sum sum = kNoTerms;
-    uint32_t cand = 0;
     for (uint32_t b = 0; b < vecs; b += NT * kAhead) {
         float v[kAhead][N];
 #pragma unroll
@@ -252,23 +252,21 @@ __global__ __launch_bounds__(NT) void top_kernel(const typename T::Store *__rest
                     }
             }
             if (lse) add_terms(sum, c2, v[i], m);
-#pragma unroll
-            for (int u = 0; u < N; ++u) cand += v[i][u] > -INFINITY;
         }
     }
     if (lse) {
         sum = block_join<NT>(sum, c2, sums);
         if (t == 0) lse[r] = base(sum) * scale + logf(sum.s);
     }
-    uint32_t total;
-    (void)block_exclusive_scan<uint32_t, NT>(cand, &total);
-    const uint32_t want = min(k, total), n = listed;
+    __syncthreads();
+    // a list of fewer than k holds every candidate: a bound has k above it
+    const uint32_t n = listed, want = min(k, n);
     if (want) {
         uint64_t known, prefix;
         auto take = [&](uint64_t e) {
             if ((e & known) >= prefix) best[atomicAdd(&taken, 1u)] = e;  // in any order: ranked below
         };
-        if (n >= want && n <= kListEntries) {
+        if (n <= kListEntries) {
             auto each = [&](auto f) {
                 for (uint32_t i = t; i < n; i += NT) f(list[i]);
             };
@@ -312,6 +310,7 @@ struct Distill {
     float *loss;
     void *dlogits;
     uint64_t stride, idx_stride, t_stride, dstride;
+    uint64_t rows;
     uint32_t vocab, k;
     int id_type, t_type, rest;
     float inv_t, kd, kd_slope, ce, grad;  // 1 / T; kd T^2 and kd T
@@ -339,29 +338,32 @@ struct Row {
     // The vector that ends with the row stands for the one that crosses its end, and for those past it.
     __device__ __forceinline__ uint32_t column(int i, uint32_t t) const { return min((i * NT + t) * N, vocab - N); }
     __device__ __forceinline__ void load() {
+        uint32_t t = threadIdx.x;
+        asm volatile("" : "+v"(t));
 #pragma unroll
-        for (int i = 0; i < C; ++i) raw[i] = __builtin_bit_cast(u32x4, *reinterpret_cast<const Pack<Store, N> *>(row + column(i, threadIdx.x)));
+        for (int i = 0; i < C; ++i) raw[i] = __builtin_bit_cast(u32x4, *reinterpret_cast<const Pack<Store, N> *>(row + column(i, t)));
     }
     // f(column, values, count): columns that another call has already are -Inf for kOnce; count of them exist.
+    // `next`: the row whose vectors take the places of this one's as they are done with, or null.
     template <bool kOnce, class F>
-    __device__ __forceinline__ void each(F f) const {
+    __device__ __forceinline__ void each(F f, const Store *next = nullptr) {
         float v[N];
         if constexpr (C > 0) {
 #pragma unroll
             for (int i = 0; i < C; ++i) {
                 // a vector at a time, neither its values in fp32 nor its place kept for another sweep: else they do
                 // not fit the registers
-                u32x4 w = raw[i];
                 uint32_t t = threadIdx.x;
-                asm volatile("" : "+v"(w), "+v"(t));
+                asm volatile("" : "+v"(raw[i]), "+v"(t));
                 const uint32_t c = column(i, t), own = (i * NT + t) * N;
-                const auto x = __builtin_bit_cast(Pack<Store, N>, w);
+                const auto x = __builtin_bit_cast(Pack<Store, N>, raw[i]);
 #pragma unroll
                 for (int u = 0; u < N; ++u) v[u] = T::to_f32(x.v[u]);
                 if (kOnce && (i + 1) * NT * N > static_cast<int>(vocab))
 #pragma unroll
                     for (uint32_t u = 0; u < N; ++u) v[u] = c + u < own ? -INFINITY : v[u];
-                if (kOnce || own < vocab) f(c, v, uint32_t(N));
+                f(c, v, kOnce || own < vocab ? uint32_t(N) : 0u);
+                if (!kOnce) raw[i] = __builtin_bit_cast(u32x4, *reinterpret_cast<const Pack<Store, N> *>(next + c));
                 __builtin_amdgcn_sched_barrier(0);
             }
         } else {
@@ -385,12 +387,19 @@ __global__ __launch_bounds__(NT) void distill_kernel(Distill d) {
     __shared__ float red[NT / kWave];
     __shared__ double redd[NT / kWave];
     __shared__ Sum reds[NT / kWave];
-    const uint32_t t = threadIdx.x, V = d.vocab, K = d.k, K4 = (K + 3) & ~3u;
+    const uint32_t V = d.vocab, K = d.k, K4 = (K + 3) & ~3u;
     uint32_t *col = dyn;
     float *q = reinterpret_cast<float *>(dyn + K4), *qs = q + K4, *zk = qs + K4;
     uint32_t *named = dyn + 4 * K4;
-    const uint64_t r = blockIdx.x;
+    Row<T, NT, C> z{static_cast<const Store *>(d.logits) + blockIdx.x * d.stride, V};
+    z.load();
+    for (uint64_t r = blockIdx.x; r < d.rows; r += gridDim.x) {
     const Store *row = static_cast<const Store *>(d.logits) + r * d.stride;
+    const Store *next = r + gridDim.x < d.rows ? row + gridDim.x * d.stride : row;
+    z.row = row;
+    uint32_t t = threadIdx.x;
+    asm volatile("" : "+v"(t));  // places are formed anew for every row: kept, they take the row's registers
+    __syncthreads();  // the LDS of the row before has been read
     Store *out = d.dlogits ? static_cast<Store *>(d.dlogits) + r * d.dstride : nullptr;
 
     const float weight = d.weights ? d.weights[r] : 1.0f;
@@ -422,11 +431,10 @@ __global__ __launch_bounds__(NT) void distill_kernel(Distill d) {
                 else
                     for (uint32_t u = c; u < V; ++u) out[u] = Store(0);
             }
-        return;
+        z.row = next;
+        z.load();
+        continue;
     }
-    // the row is on its way while the teacher is looked at
-    Row<T, NT, C> z{row, V};
-    z.load();
     const float zl = label != kNone ? T::to_f32(row[label]) : 0.0f;
     const bool rest = d.rest && entries;
     if (rest)
@@ -518,7 +526,11 @@ __global__ __launch_bounds__(NT) void distill_kernel(Distill d) {
         if (label != kNone) loss = loss + d.ce * (logf(all1.s) - (kTwo ? zl - r1 : (zl - r1) * d.inv_t));
         d.loss[r] = weight * loss;
     }
-    if (!out) return;
+    if (!out) {
+        z.row = next;
+        z.load();
+        continue;
+    }
     // the gradient: kd T (mass p_j - held p_j / p_r - q_j) + ce (softmax_j - [j = label])
     const float f = weight * d.grad;
     const float kt = entries ? f * d.kd_slope : 0.0f, kc = label != kNone ? f * d.ce : 0.0f;
@@ -540,7 +552,7 @@ __global__ __launch_bounds__(NT) void distill_kernel(Distill d) {
 #pragma unroll
             for (uint32_t u = 0; u < N; ++u)
                 if (u < cnt) out[c + u] = g.v[u];
-    });
+    }, next);
     __syncthreads();
     // columns that an entry or the label names
     bool own_label = label != kNone;  // no entry names it
@@ -553,6 +565,7 @@ __global__ __launch_bounds__(NT) void distill_kernel(Distill d) {
         float g = kt * (mass * p - (e < K ? qs[e] : 0.0f)) + kc * (term(x, r1, c1) / all1.s - (c == label ? 1.0f : 0.0f));
         if (e == K && held > 0.0f) g = g - kt * held * (term(x, rr, c2) / rest2.s);  // a label of the rest
         out[c] = T::from_f32(g);
+    }
     }
 }
 
@@ -659,29 +672,30 @@ extern "C" gc_status gc_distill_loss(const void *logits, int type, uint64_t stri
         if (dlogits == logits && dstride != stride)
             return fail(fn, GC_EINVAL, "dlogits in place of logits must have their stride");
     }
-    Distill d{logits, idx, t, labels, t_lse, weights, loss, dlogits, stride, idx_stride, t_stride, dstride, vocab, k, idx_type, t_type,
+    Distill d{logits, idx, t, labels, t_lse, weights, loss, dlogits, stride, idx_stride, t_stride, dstride, n_rows, vocab, k, idx_type, t_type,
               opt->mode == GC_DISTILL_REST, 1.0f / T, kd, opt->kd_weight * T, opt->ce_weight, opt->grad_scale};
     if (!k) d.kd = 0.0f;
     const size_t lds = 16 * ((size_t(k) + 3) & ~size_t(3)) + (d.rest ? 4 * ((size_t(vocab) + 31) / 32 + 1) : 0);
     const bool two = labels && opt->ce_weight != 0.0f && T != 1.0f;
     hipError_t e = hipSuccess;
-    auto go = [&](auto kernel, int threads) {
+    auto go = [&](auto kernel, int threads, uint64_t most) {
         if (lds > 48 * 1024)
             e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
         if (e != hipSuccess) return;
-        GC_LAUNCH("distill", stream, kernel<<<static_cast<unsigned>(n_rows), threads, lds, stream>>>(d));
+        GC_LAUNCH("distill", stream, kernel<<<static_cast<unsigned>(umin64(n_rows, most)), threads, lds, stream>>>(d));
     };
     auto with = [&](auto type_tag, auto is_two) {
         using Tp = decltype(type_tag);
         constexpr bool kTwo = decltype(is_two)::value;
         const uint64_t vecs = ceil_div(vocab, kVec<Tp>);
-        if (vecs < 2) go(distill_kernel<Tp, 256, 0, kTwo>, 256);
-        else if (vecs <= 256 * 4) go(distill_kernel<Tp, 256, 4, kTwo>, 256);
-        else if (vecs <= 256 * 8) go(distill_kernel<Tp, 256, 8, kTwo>, 256);
-        else if (vecs <= 1024 * 4) go(distill_kernel<Tp, 1024, 4, kTwo>, 1024);
-        else if (vecs <= 1024 * 8) go(distill_kernel<Tp, 1024, 8, kTwo>, 1024);
-        else if (vecs <= 1024 * 16) go(distill_kernel<Tp, 1024, 16, kTwo>, 1024);
-        else go(distill_kernel<Tp, 1024, 0, kTwo>, 1024);
+        constexpr uint64_t kAll = kMaxRows;
+        if (vecs < 2) go(distill_kernel<Tp, 256, 0, kTwo>, 256, kAll);
+        else if (vecs <= 256 * 4) go(distill_kernel<Tp, 256, 4, kTwo>, 256, kAll);
+        else if (vecs <= 256 * 8) go(distill_kernel<Tp, 256, 8, kTwo>, 256, kAll);
+        else if (vecs <= 256 * 16) go(distill_kernel<Tp, 256, 16, kTwo>, 256, kAll);
+        else if (vecs <= 1024 * 8) go(distill_kernel<Tp, 1024, 8, kTwo>, 1024, 256);
+        else if (vecs <= 1024 * 16) go(distill_kernel<Tp, 1024, 16, kTwo>, 1024, 256);
+        else go(distill_kernel<Tp, 1024, 0, kTwo>, 1024, kAll);
     };
     auto of = [&](auto type_tag) {
         if (two) with(type_tag, std::true_type{});

@@ -87,9 +87,21 @@ constexpr ShapeModel kShapes[] = {
 };
 constexpr double kTileUs = 3.0, kJoinUs = 4.0, kPartialBytesPerUs = 4e6;
 constexpr uint32_t kMaxParts = 32, kThinTokens = 64;
+constexpr uint64_t kFewOutputs = 1 << 16;
 
 Cut plan_cut(Kind kind, int type, uint32_t M, uint32_t N, uint32_t K, bool any) {
     Cut best{};
+    // Few tokens: every 16 rows of W read all of x, so a longer batch over many rows goes by tiles (us, few and
+    // tiles: 1 x 16384 rows x 4096 columns 26 and 29, 16 x 4096 x 4096 10.0 and 11.7, 16 x 16384 x 4096 35 and 29).
+    if (kind == kForward && M <= 16 && (M <= 4 || static_cast<uint64_t>(M) * N <= kFewOutputs)) {
+        const uint64_t chunks = ceil_div(static_cast<uint64_t>(K) * type_bytes(type), 256);
+        best.shape = kFew;
+        best.tiles_m = 1;
+        best.tiles_n = static_cast<uint32_t>(ceil_div(N, 16));
+        best.parts = 1;  // waves: 16 (26 us; 8 take 29, 4 take 30), or as many as have a chunk
+        while (best.parts < 16 && best.parts < chunks) best.parts *= 2;
+        return best;
+    }
     double least = 0.0;
     const uint32_t stages = static_cast<uint32_t>(ceil_div(K, 128 / type_bytes(type)));
     for (const ShapeModel &s : kShapes) {
@@ -122,7 +134,7 @@ const ShapeModel &model_of(const Cut &c) { return kShapes[c.shape == kBig ? 0 : 
 size_t cut_ws(Cut &c, void *ws) {
     const ShapeModel &s = model_of(c);
     WsCursor at(ws);
-    if (c.parts > 1) {
+    if (c.parts > 1 && c.shape != kFew) {
         c.partial = at.take<float>(static_cast<size_t>(c.tiles_m) * c.tiles_n * c.parts * s.tm * s.tn);
         c.colsums = at.take<float>(static_cast<size_t>(c.parts) * c.tiles_m * s.tm);
     }
@@ -157,8 +169,8 @@ gc_status launch(const char *fn, Kind kind, int type, const Product &p, void *ws
     const Mode mode = std::max(mode_of(p.A, p.lda, kind == kWeight, p.M, p.K, type), mode_of(p.B, p.ldb, kind != kForward, p.N, p.K, type));
     Cut c = plan_cut(kind, type, p.M, p.N, p.K, mode == kAny);
     c.mode = mode;
-    const ShapeModel &s = model_of(c);
-    if (ceil_div(p.M, s.tm) * ceil_div(p.N, s.tn) > max_grid(512)) return fail(fn, GC_ERANGE, "more workgroups than a launch has");
+    const uint64_t groups = c.shape == kFew ? c.tiles_n : ceil_div(p.M, model_of(c).tm) * ceil_div(p.N, model_of(c).tn);
+    if (groups > max_grid(1024)) return fail(fn, GC_ERANGE, "more workgroups than a launch has");
     (void)cut_ws(c, align256(ws));
     if (type == GC_F32) return linear_launch<F32>(fn, kind, p, c, stream);
     if (type == GC_BF16) return linear_launch<BF16>(fn, kind, p, c, stream);

@@ -33,7 +33,7 @@ struct Mid {
 struct Thin {
     static constexpr int kTM = 32, kTN = 128, kWR = 1, kWC = 4, kWavesPerSimd = 4;
 };
-enum TileShape { kBig, kMid, kThin };
+enum TileShape { kBig, kMid, kThin, kFew };  // kFew: 16 rows of W, no tile
 
 // How the operands get into LDS.
 //   kDirect  16-byte pieces go straight there; a stage with the last k inside goes through registers
@@ -45,7 +45,7 @@ enum Mode { kDirect, kHeld, kAny };
 // (stages of 128 bytes of it) whose sums linear_join_kernel adds.
 struct Cut {
     TileShape shape;
-    uint32_t tiles_m, tiles_n, parts, stages, per;  // per: stages of a part
+    uint32_t tiles_m, tiles_n, parts, stages, per;  // per: stages of a part; kFew: parts are waves
     Mode mode;
     float *partial;                                 // parts > 1: sums in register order, a tile after the other
     float *colsums;                                 // and [parts][tiles_m * kTM] of the bias

@@ -322,31 +322,35 @@ struct Run {
     using Acc = f32x4[C::kRA][C::kRB];
     using Sums = float[C::kRA];  // a lane's part of the sums of A's rows over k
 
-    // acc += a stage's product; blocks of A one ahead, and no further: hoisted, they do not fit the registers
+    // acc += a stage's product; blocks of A one ahead, and no further: hoisted, they do not fit the registers.
+    // Where registers hold the next stage meanwhile, half of this one's k at a time.
     template <bool kSums>
     static __device__ __forceinline__ void multiply(const char *__restrict__ lds, uint32_t wm, uint32_t wn, Acc &acc, Sums &sums) {
+        constexpr int kTogether = kMode == kDirect ? 2 : 1;
         const char *la = lds, *lb = lds + C::kBytesA;
-        u32x4 fb[2][C::kRB];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h0 = 0; h0 < 2; h0 += kTogether) {
+            u32x4 fb[kTogether][C::kRB], fa[kTogether], na[kTogether];
 #pragma unroll
-            for (int b = 0; b < C::kRB; ++b) fb[h][b] = OpB::read(lb, wn + 16 * b, h);
-        u32x4 fa[2] = {OpA::read(la, wm, 0), OpA::read(la, wm, 1)};
+            for (int h = 0; h < kTogether; ++h) {
 #pragma unroll
-        for (int a = 0; a < C::kRA; ++a) {
-            u32x4 na[2] = {fa[0], fa[1]};
-            if (a + 1 < C::kRA)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) na[h] = OpA::read(la, wm + 16 * (a + 1), h);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                for (int b = 0; b < C::kRB; ++b) acc[a][b] = mma<T>(fb[h][b], fa[h], acc[a][b]);
-                if (kSums) sums[a] = add_all<T>(fa[h], sums[a]);
+                for (int b = 0; b < C::kRB; ++b) fb[h][b] = OpB::read(lb, wn + 16 * b, h0 + h);
+                fa[h] = OpA::read(la, wm, h0 + h);
             }
-            fa[0] = na[0];
-            fa[1] = na[1];
-            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int a = 0; a < C::kRA; ++a) {
+#pragma unroll
+                for (int h = 0; h < kTogether; ++h) na[h] = a + 1 < C::kRA ? OpA::read(la, wm + 16 * (a + 1), h0 + h) : fa[h];
+#pragma unroll
+                for (int h = 0; h < kTogether; ++h) {
+#pragma unroll
+                    for (int b = 0; b < C::kRB; ++b) acc[a][b] = mma<T>(fb[h][b], fa[h], acc[a][b]);
+                    if (kSums) sums[a] = add_all<T>(fa[h], sums[a]);
+                }
+#pragma unroll
+                for (int h = 0; h < kTogether; ++h) fa[h] = na[h];
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
     }
 
@@ -444,26 +448,25 @@ struct Run {
             }
         }
     }
-    // The same straight from the registers: a lane holds 4 columns of row lane % 16 of each block.  For fp32
-    // results alone, where those are 16 bytes.
+    // The same straight from the registers, for fp32 results of whole blocks: a lane holds 16 bytes of row
+    // lane % 16 of each.
     static __device__ __forceinline__ void write_blocks(const Product &p, uint32_t m0, uint32_t n0, const Acc &acc) {
-        const uint32_t lane = lane_id();
+        constexpr int kAhead = C::kRA < 4 ? C::kRA : 4;  // rows of blocks whose old values are on their way at once
+        const uint32_t m = m0 + (lane_id() & 15), n = n0 + 4 * (lane_id() >> 4);
 #pragma unroll
-        for (int a = 0; a < C::kRA; ++a) {
-            const uint32_t m = m0 + 16 * a + (lane & 15);
-            if (m >= p.M) continue;
-            Beside<T, kKind, 4> beside[C::kRB];
+        for (int a0 = 0; a0 < C::kRA; a0 += kAhead) {
+            Beside<T, kKind, 4> beside[kAhead][C::kRB];
 #pragma unroll
-            for (int b = 0; b < C::kRB; ++b) {
-                const uint32_t n = n0 + 16 * b + 4 * (lane >> 4);
-                if (n < p.N) beside[b].load(p, m, n, min(p.N - n, 4u));
-            }
+            for (int a = 0; a < kAhead; ++a)
 #pragma unroll
-            for (int b = 0; b < C::kRB; ++b) {
-                const uint32_t n = n0 + 16 * b + 4 * (lane >> 4);
-                float v[4] = {acc[a][b][0], acc[a][b][1], acc[a][b][2], acc[a][b][3]};
-                if (n < p.N) finish<T, kKind, 4>(p, beside[b], m, n, min(p.N - n, 4u), v);
-            }
+                for (int b = 0; b < C::kRB; ++b) beside[a][b].load(p, m + 16 * (a0 + a), n + 16 * b, 4);
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a)
+#pragma unroll
+                for (int b = 0; b < C::kRB; ++b) {
+                    float v[4] = {acc[a0 + a][b][0], acc[a0 + a][b][1], acc[a0 + a][b][2], acc[a0 + a][b][3]};
+                    finish<T, kKind, 4>(p, beside[a][b], m + 16 * (a0 + a), n + 16 * b, 4, v);
+                }
         }
     }
 };
@@ -539,12 +542,14 @@ __global__ __launch_bounds__(Shape<S>::kThreads, S::kWavesPerSimd) void linear_k
             const uint32_t m = m0 + wm + 16 * a + lane;
             if (m < p.M) p.gbias[m] = p.accumulate ? p.gbias[m] + sums[a] : sums[a];
         }
-    if constexpr (kKind == kWeight) {
-        if (active) R::write_blocks(p, m0 + wm, n0 + wn, acc);
-        return;
-    }
     __syncthreads();  // the last stage has been read
-    if (active) R::write_out(p, lds + w * R::kWaveBytes, m0 + wm, n0 + wn, acc);
+    if (!active) return;
+    if constexpr (kKind == kWeight)
+        if (m0 + wm + C::kRA * 16 <= p.M && n0 + wn + C::kRB * 16 <= p.N) {
+            R::write_blocks(p, m0 + wm, n0 + wn, acc);
+            return;
+        }
+    R::write_out(p, lds + w * R::kWaveBytes, m0 + wm, n0 + wn, acc);
 }
 
 // The parts' sums added in order: a workgroup per 4 blocks of 16 x 16 of a tile.
@@ -580,6 +585,65 @@ __global__ __launch_bounds__(kBlock) void linear_join_kernel(Product p, Cut c) {
     finish<T, kKind, 4>(p, beside, m, n, min(p.N - n, 4u), x);
 }
 
+// Up to 16 tokens: a workgroup has 16 rows of W, its waves take chunks of 256 bytes of k in turn, straight from
+// memory into matrix operands, the next chunk on its way meanwhile, and their sums are added in order.  W is
+// read once, at memory's rate, and nothing is launched behind it.
+template <class T>
+__global__ __launch_bounds__(16 * kWave) void linear_few_kernel(Product p) {
+    using Store = typename T::Store;
+    constexpr uint32_t kElems = 16 / sizeof(Store), kStep = 4 * kElems, kSteps = 4, kChunk = kSteps * kStep;  // elements of k
+    extern __shared__ __attribute__((aligned(16))) f32x4 sums[];  // [waves][64]
+    const uint32_t lane = lane_id(), w = __builtin_amdgcn_readfirstlane(wave_id()), waves = blockDim.x / kWave;
+    const uint32_t n0 = blockIdx.x * 16, at = (lane >> 4) * kElems;
+    const Store *wrow = static_cast<const Store *>(p.B) + min(n0 + (lane & 15), p.N - 1) * p.ldb;
+    const Store *xrow = static_cast<const Store *>(p.A) + min(lane & 15, p.M - 1) * p.lda;
+    auto whole = [](const Store *q) { return __builtin_bit_cast(u32x4, *reinterpret_cast<const Pack<Store, int(kElems)> *>(q)); };
+    auto part = [&](const Store *q, uint32_t k) {
+        Pack<Store, int(kElems)> t;
+#pragma unroll
+        for (uint32_t u = 0; u < kElems; ++u) t.v[u] = k + u < p.K ? q[k + u] : Store(0);
+        return __builtin_bit_cast(u32x4, t);
+    };
+    const uint32_t chunks = p.K / kChunk;
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    u32x4 fw[kSteps], fx[kSteps], nw[kSteps], nx[kSteps];
+    auto fetch = [&](uint32_t c, u32x4(&a)[kSteps], u32x4(&b)[kSteps]) {
+        const uint32_t k = c * kChunk + at;
+#pragma unroll
+        for (uint32_t s = 0; s < kSteps; ++s) a[s] = whole(wrow + k + s * kStep);
+#pragma unroll
+        for (uint32_t s = 0; s < kSteps; ++s) b[s] = whole(xrow + k + s * kStep);
+    };
+    if (w < chunks) fetch(w, fw, fx);
+    for (uint32_t c = w; c < chunks; c += waves) {
+        fetch(c + waves < chunks ? c + waves : c, nw, nx);
+#pragma unroll
+        for (uint32_t s = 0; s < kSteps; ++s) acc = mma<T>(fw[s], fx[s], acc);
+#pragma unroll
+        for (uint32_t s = 0; s < kSteps; ++s) {
+            fw[s] = nw[s];
+            fx[s] = nx[s];
+        }
+    }
+    if (chunks % waves == w)  // the chunk with the last k, element by element
+        for (uint32_t k = chunks * kChunk; k < p.K; k += kStep) acc = mma<T>(part(wrow, k + at), part(xrow, k + at), acc);
+    sums[w * kWave + lane] = acc;
+    __syncthreads();
+    // a lane's 4 sums: columns n0 + 4 (lane / 16) on of token lane % 16
+    const uint32_t m = lane & 15, n = n0 + 4 * (lane >> 4);
+    if (w || m >= p.M || n >= p.N) return;
+    const uint32_t cnt = min(p.N - n, 4u);
+    Beside<T, kForward, 4> beside;
+    beside.load(p, m, n, cnt);
+    for (uint32_t x = 1; x < waves; ++x) {
+        const f32x4 t = sums[x * kWave + lane];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) acc[u] = acc[u] + t[u];
+    }
+    float y[4] = {acc[0], acc[1], acc[2], acc[3]};
+    finish<T, kForward, 4>(p, beside, m, n, cnt, y);
+}
+
 template <class T, Kind kKind, class S>
 gc_status launch_shape(const char *fn, const Product &p, const Cut &c, hipStream_t stream) {
     using C = Shape<S>;
@@ -605,6 +669,12 @@ gc_status linear_launch(const char *fn, Kind kind, const Product &p, const Cut &
         if (kind == kInput) return launch_shape<T, kInput, S>(fn, p, c, stream);
         return launch_shape<T, kWeight, S>(fn, p, c, stream);
     };
+    if (c.shape == kFew) {
+        GC_LAUNCH("linear_few", stream,
+                  linear_few_kernel<T><<<c.tiles_n, c.parts * kWave, c.parts * kWave * sizeof(f32x4), stream>>>(p));
+        const hipError_t e = hipGetLastError();
+        return e == hipSuccess ? GC_OK : hip_error(e, fn);
+    }
     if (c.shape == kBig) return of(Big{});
     if (c.shape == kMid || kind == kWeight) return of(Mid{});
     if (kind == kForward) return launch_shape<T, kForward, Thin>(fn, p, c, stream);

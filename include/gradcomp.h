@@ -948,7 +948,7 @@ gc_status gc_distill_loss(const void *logits, int type, uint64_t stride, uint64_
  *             embed_empty,
  *             orth_norm, orth_scale, orth_split, orth_gram, orth_poly,
  *             orth_pair, orth_apply, orth_join, orth_slab, orth_small,
- *             linear_product, linear_join, act_grad, top_logits, distill.
+ *             linear_product, linear_few, linear_join, act_grad, top_logits, distill.
  * gc_timing_take waits for the recorded events of one kernel and returns the
  * summed duration in milliseconds and the number of launches, then forgets
  * them.  Host-thread safe; not for use while a stream is being captured.
