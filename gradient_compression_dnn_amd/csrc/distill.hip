@@ -310,7 +310,6 @@ struct Distill {
     float *loss;
     void *dlogits;
     uint64_t stride, idx_stride, t_stride, dstride;
-    uint64_t rows;
     uint32_t vocab, k;
     int id_type, t_type, rest;
     float inv_t, kd, kd_slope, ce, grad;  // 1 / T; kd T^2 and kd T
@@ -325,49 +324,66 @@ __device__ __forceinline__ float teacher_value(const Distill &d, uint64_t at) {
     return d.t_type == GC_BF16 ? BF16::to_f32(x) : F16::to_f32(x);
 }
 
-// A row of logits: C vectors a thread, held in registers from the first sweep to the last (the row is read once),
-// or, C = 0, read by each sweep.
-template <class T, int NT, int C>
+// A row of logits: C vectors a thread, held in registers from the sums to the gradient, so that they
+// are read once.  kMore: the row goes on behind them, and that part is read by each sweep.
+template <class T, int NT, int C, bool kMore>
 struct Row {
     static constexpr int N = kVec<T>;
+    static constexpr uint32_t kStep = NT * N;
     using Store = typename T::Store;
     const Store *row;
     uint32_t vocab;
     u32x4 raw[C ? C : 1];
 
     // The vector that ends with the row stands for the one that crosses its end, and for those past it.
-    __device__ __forceinline__ uint32_t column(int i, uint32_t t) const { return min((i * NT + t) * N, vocab - N); }
+    __device__ __forceinline__ uint32_t column(int i, uint32_t t) const {
+        const uint32_t c = i * kStep + t * N;
+        return kMore ? c : min(c, vocab - N);
+    }
+    __device__ __forceinline__ u32x4 vector_at(uint32_t c) const {
+        return __builtin_bit_cast(u32x4, *reinterpret_cast<const Pack<Store, N> *>(row + c));
+    }
     __device__ __forceinline__ void load() {
-        uint32_t t = threadIdx.x;
-        asm volatile("" : "+v"(t));
 #pragma unroll
-        for (int i = 0; i < C; ++i) raw[i] = __builtin_bit_cast(u32x4, *reinterpret_cast<const Pack<Store, N> *>(row + column(i, t)));
+        for (int i = 0; i < C; ++i) raw[i] = vector_at(column(i, threadIdx.x));
     }
     // f(column, values, count): columns that another call has already are -Inf for kOnce; count of them exist.
-    // `next`: the row whose vectors take the places of this one's as they are done with, or null.
     template <bool kOnce, class F>
-    __device__ __forceinline__ void each(F f, const Store *next = nullptr) {
+    __device__ __forceinline__ void each(F f) {
         float v[N];
-        if constexpr (C > 0) {
+        auto values = [&](u32x4 w) {
+            const auto x = __builtin_bit_cast(Pack<Store, N>, w);
 #pragma unroll
-            for (int i = 0; i < C; ++i) {
-                // a vector at a time, neither its values in fp32 nor its place kept for another sweep: else they do
-                // not fit the registers
-                uint32_t t = threadIdx.x;
-                asm volatile("" : "+v"(raw[i]), "+v"(t));
-                const uint32_t c = column(i, t), own = (i * NT + t) * N;
-                const auto x = __builtin_bit_cast(Pack<Store, N>, raw[i]);
+            for (int u = 0; u < N; ++u) v[u] = T::to_f32(x.v[u]);
+        };
 #pragma unroll
-                for (int u = 0; u < N; ++u) v[u] = T::to_f32(x.v[u]);
-                if (kOnce && (i + 1) * NT * N > static_cast<int>(vocab))
+        for (int i = 0; i < C; ++i) {
+            // a vector at a time, neither its values in fp32 nor its place kept for another sweep: else they do
+            // not fit the registers
+            uint32_t t = threadIdx.x;
+            asm volatile("" : "+v"(raw[i]), "+v"(t));
+            const uint32_t c = column(i, t), own = i * kStep + t * N;
+            values(raw[i]);
+            if (!kMore && kOnce && (i + 1) * kStep > vocab)
 #pragma unroll
-                    for (uint32_t u = 0; u < N; ++u) v[u] = c + u < own ? -INFINITY : v[u];
-                f(c, v, kOnce || own < vocab ? uint32_t(N) : 0u);
-                if (!kOnce) raw[i] = __builtin_bit_cast(u32x4, *reinterpret_cast<const Pack<Store, N> *>(next + c));
-                __builtin_amdgcn_sched_barrier(0);
+                for (uint32_t u = 0; u < N; ++u) v[u] = c + u < own ? -INFINITY : v[u];
+            if (kMore || kOnce || own < vocab) f(c, v, uint32_t(N));
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (kMore) {
+            constexpr int kAhead = 4;
+            uint32_t c = C * kStep + threadIdx.x * N;
+            for (; c + (kAhead - 1) * kStep + N <= vocab; c += kAhead * kStep) {
+                u32x4 w[kAhead];
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) w[i] = vector_at(c + i * kStep);
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    values(w[i]);
+                    f(c + i * kStep, v, uint32_t(N));
+                }
             }
-        } else {
-            for (uint32_t c = threadIdx.x * N; c < vocab; c += NT * N) {
+            for (; c < vocab; c += kStep) {
                 load_logits<T>(row, c, vocab, v);
                 f(c, v, min(vocab - c, uint32_t(N)));
             }
@@ -375,11 +391,11 @@ struct Row {
     }
 };
 
-// LDS: columns, q, q summed over a column's entries, and student logits of the entries, and
-// (GC_DISTILL_REST) a bit per column that an entry names.
-// The row's exponentials and its two trips over HBM bound it.  kTwo: the labels' softmax has another
-// temperature than the teacher's.
-template <class T, int NT, int C, bool kTwo>
+// A workgroup a row; several rows share a unit, so that one's sums and exponentials run while
+// others are on their way.  LDS: columns, q, q summed over a column's entries, and student logits of the
+// entries, and (GC_DISTILL_REST) a bit per column that an entry names.
+// kTwo: the labels' softmax has another temperature than the teacher's.
+template <class T, int NT, int C, bool kMore, bool kTwo>
 __global__ __launch_bounds__(NT) void distill_kernel(Distill d) {
     constexpr int N = kVec<T>;
     using Store = typename T::Store;
@@ -387,43 +403,55 @@ __global__ __launch_bounds__(NT) void distill_kernel(Distill d) {
     __shared__ float red[NT / kWave];
     __shared__ double redd[NT / kWave];
     __shared__ Sum reds[NT / kWave];
-    const uint32_t V = d.vocab, K = d.k, K4 = (K + 3) & ~3u;
+    const uint32_t t = threadIdx.x, V = d.vocab, K = d.k, K4 = (K + 3) & ~3u;
     uint32_t *col = dyn;
     float *q = reinterpret_cast<float *>(dyn + K4), *qs = q + K4, *zk = qs + K4;
     uint32_t *named = dyn + 4 * K4;
-    Row<T, NT, C> z{static_cast<const Store *>(d.logits) + blockIdx.x * d.stride, V};
-    z.load();
-    for (uint64_t r = blockIdx.x; r < d.rows; r += gridDim.x) {
+    const uint64_t r = blockIdx.x;
     const Store *row = static_cast<const Store *>(d.logits) + r * d.stride;
-    const Store *next = r + gridDim.x < d.rows ? row + gridDim.x * d.stride : row;
-    z.row = row;
-    uint32_t t = threadIdx.x;
-    asm volatile("" : "+v"(t));  // places are formed anew for every row: kept, they take the row's registers
-    __syncthreads();  // the LDS of the row before has been read
     Store *out = d.dlogits ? static_cast<Store *>(d.dlogits) + r * d.dstride : nullptr;
+    // entry e: its column, or kNone, and the teacher's logit
+    auto entry = [&](uint32_t e, uint32_t &c, float &v) {
+        c = kNone;
+        v = -INFINITY;
+        if (e >= K || d.kd == 0.0f) return;
+        const int64_t id = id_at(d.idx, d.id_type, r * d.idx_stride + e);
+        v = teacher_value(d, r * d.t_stride + e);
+        if (id >= 0 && id < static_cast<int64_t>(V) && v != -INFINITY) c = static_cast<uint32_t>(id);
+    };
+    auto student = [&](uint32_t c) { return c != kNone ? T::to_f32(row[c]) : 0.0f; };
 
-    const float weight = d.weights ? d.weights[r] : 1.0f;
-    uint32_t label = kNone;
+    // This thread's entry and the label come first, then the row, then the logits of the former: memory answers in order.
+    uint32_t my_col, label = kNone;
+    float my_t;
+    entry(t, my_col, my_t);
     if (d.labels && d.ce != 0.0f) {
         const int64_t l = id_at(d.labels, d.id_type, r);
         if (l >= 0 && l < static_cast<int64_t>(V)) label = static_cast<uint32_t>(l);
     }
-    // the teacher's entries
-    float tmax = -INFINITY;
-    uint32_t count = 0;
-    if (d.kd != 0.0f)
-        for (uint32_t e = t; e < K; e += NT) {
-            const int64_t c = id_at(d.idx, d.id_type, r * d.idx_stride + e);
-            const float v = teacher_value(d, r * d.t_stride + e);
-            const bool there = c >= 0 && c < static_cast<int64_t>(V) && v != -INFINITY;
-            col[e] = there ? static_cast<uint32_t>(c) : kNone;
-            q[e] = v;
-            tmax = there ? fmaxf(tmax, v) : tmax;
-            count += there;
-        }
-    uint32_t entries;
-    (void)block_exclusive_scan<uint32_t, NT>(count, &entries);
-    if (weight == 0.0f || (entries == 0 && label == kNone)) {
+    Row<T, NT, C, kMore> z{row, V};
+    z.load();
+    const float my_z = student(my_col), zl = student(label);
+    const float weight = d.weights ? d.weights[r] : 1.0f;
+    // the teacher's distribution
+    float tmax = my_col != kNone ? my_t : -INFINITY;
+    bool there = my_col != kNone;
+    if (t < K4) {
+        col[t] = my_col;
+        q[t] = my_t;
+    }
+    for (uint32_t e = t + NT; e < K4; e += NT) {
+        uint32_t c;
+        float v;
+        entry(e, c, v);
+        col[e] = c;
+        q[e] = v;
+        zk[e] = student(c);
+        there = there || c != kNone;
+        tmax = c != kNone ? fmaxf(tmax, v) : tmax;
+    }
+    const bool entries = __syncthreads_or(there);
+    if (weight == 0.0f || !(entries || label != kNone)) {  // the row counts for nothing
         if (t == 0) d.loss[r] = 0.0f;
         if (out)
             for (uint32_t c = t * N; c < V; c += NT * N) {
@@ -431,28 +459,22 @@ __global__ __launch_bounds__(NT) void distill_kernel(Distill d) {
                 else
                     for (uint32_t u = c; u < V; ++u) out[u] = Store(0);
             }
-        z.row = next;
-        z.load();
-        continue;
+        return;
     }
-    const float zl = label != kNone ? T::to_f32(row[label]) : 0.0f;
     const bool rest = d.rest && entries;
-    if (rest)
-        for (uint32_t i = t; i < (V + 31) / 32 + 1; i += NT) named[i] = 0;
     double qsum = 0.0;
     if (entries) {
-        for (uint32_t e = t; e < K4; e += NT) {
-            if (e >= K) col[e] = kNone;
-            else if (col[e] != kNone) zk[e] = T::to_f32(row[col[e]]);
-        }
-        tmax = block_max<NT>(tmax, red);
+        if (rest)
+            for (uint32_t i = t; i < (V + 31) / 32 + 1; i += NT) named[i] = 0;
+        if (!d.rest) tmax = block_max<NT>(tmax, red);
+        else __syncthreads();
         tmax = tmax == -INFINITY ? 0.0f : tmax;
         const float tlse = d.rest ? d.t_lse[r] : 0.0f;
         for (uint32_t e = t; e < K; e += NT) {
-            const bool there = col[e] != kNone;
-            q[e] = there ? expf(d.rest ? q[e] * d.inv_t - tlse : (q[e] - tmax) * d.inv_t) : 0.0f;
+            const uint32_t c = col[e];
+            q[e] = c != kNone ? expf(d.rest ? q[e] * d.inv_t - tlse : (q[e] - tmax) * d.inv_t) : 0.0f;
             qsum += q[e];
-            if (rest && there) atomicOr(&named[col[e] / 32], 1u << (col[e] % 32));
+            if (rest && c != kNone) atomicOr(&named[c / 32], 1u << (c % 32));
         }
         qsum = block_sum<NT>(qsum, redd);
         const float inv = d.rest ? 1.0f : static_cast<float>(1.0 / qsum);
@@ -477,9 +499,12 @@ __global__ __launch_bounds__(NT) void distill_kernel(Distill d) {
                 }
             qs[e] = first ? sum : -1.0f;
         }
+        __syncthreads();
     }
-    __syncthreads();
-
+    auto each_own = [&](auto f) {  // f(entry, its student's logit)
+        if (t < K) f(t, my_z);
+        for (uint32_t e = t + NT; e < K; e += NT) f(e, zk[e]);
+    };
     // the row, or the rest of it: sums of exp at 1 / T and, for another softmax of the labels, at 1
     const float c2 = d.inv_t * kLog2e, c1 = kTwo ? kLog2e : c2;
     Sum s2 = kNoTerms, s1 = kNoTerms;
@@ -496,77 +521,77 @@ __global__ __launch_bounds__(NT) void distill_kernel(Distill d) {
         if (kTwo) add_terms(s1, c1, v, top);
     });
     const Sum rest2 = block_join<NT>(s2, c2, reds);
-    Sum all2 = rest2, all1 = rest2;
-    if (kTwo) all1 = block_join<NT>(s1, c1, reds);
+    Sum all2 = rest2, all1 = kTwo ? block_join<NT>(s1, c1, reds) : rest2;
     if (rest) {  // the entries that were left out, each column once
         s2 = s1 = kNoTerms;
-        for (uint32_t e = t; e < K; e += NT)
+        each_own([&](uint32_t e, float x) {
             if (qs[e] >= 0.0f || qs[e] != qs[e]) {
-                const float v[1] = {zk[e]};
-                add_terms(s2, c2, v, v[0]);
-                if (kTwo) add_terms(s1, c1, v, v[0]);
+                const float v[1] = {x};
+                add_terms(s2, c2, v, x);
+                if (kTwo) add_terms(s1, c1, v, x);
             }
+        });
         all2 = join(rest2, block_join<NT>(s2, c2, reds), c2);
         all1 = kTwo ? join(all1, block_join<NT>(s1, c1, reds), c1) : all2;
     }
     const float r2 = base(all2), r1 = base(all1), rr = base(rest2);
-    const float log2s = logf(all2.s);
     const float held = rest && rest2.s != 0.0f ? fmaxf(static_cast<float>(1.0 - qsum), 0.0f) : 0.0f;
-    const float mass = entries ? static_cast<float>(qsum) + held : 0.0f;
-    // the loss
-    double kl = 0.0;
+    if (out) {
+        // the gradient: kd T (mass p_j - held p_j / p_r - q_j) + ce (softmax_j - [j = label])
+        const float mass = entries ? static_cast<float>(qsum) + held : 0.0f, f = weight * d.grad;
+        const float kt = entries ? f * d.kd_slope : 0.0f, kc = label != kNone ? f * d.ce : 0.0f;
+        const float back = term(rr, r2, c2);  // p_j = back term(z_j, rr) / all2.s
+        float g2 = kt * (mass * back / all2.s - (held > 0.0f ? held / rest2.s : 0.0f));
+        const float g1 = kc / all1.s;
+        if (!kTwo) g2 = g2 + g1 * back;
+        __syncthreads();  // the entries' logits, whose places may be out's, have been read
+        z.template each<false>([&](uint32_t c, float(&v)[N], uint32_t cnt) {
+            Pack<Store, N> g;
+#pragma unroll
+            for (int u = 0; u < N; ++u) {
+                float x = g2 * term(v[u], rr, c2);
+                if (kTwo) x = x + g1 * term(v[u], r1, c1);
+                g.v[u] = T::from_f32(x);
+            }
+            if (cnt == N) *reinterpret_cast<Pack<Store, N> *>(out + c) = g;
+            else
+#pragma unroll
+                for (uint32_t u = 0; u < N; ++u)
+                    if (u < cnt) out[c + u] = g.v[u];
+        });
+        __syncthreads();
+        // columns that an entry or the label names
+        auto set = [&](uint32_t c, float x, float sum, bool of_rest) {
+            const float p = term(x, r2, c2) / all2.s;
+            float g = kt * (mass * p - sum) + kc * (term(x, r1, c1) / all1.s - (c == label ? 1.0f : 0.0f));
+            if (of_rest && held > 0.0f) g = g - kt * held * (term(x, rr, c2) / rest2.s);
+            out[c] = T::from_f32(g);
+        };
+        if (entries)
+            each_own([&](uint32_t e, float x) {
+                if (col[e] != kNone && !(qs[e] < 0.0f)) set(col[e], x, qs[e], false);
+            });
+        if (label != kNone && t == NT - 1) {
+            bool own = true;  // no entry names it
+            if (entries)
+                for (uint32_t j = 0; j < K; ++j) own = own && col[j] != label;
+            if (own) set(label, zl, 0.0f, true);
+        }
+    }
+    // the loss, while the gradient is on its way
+    float loss = 0.0f;
+    const float log2s = logf(all2.s);
     if (entries) {
-        for (uint32_t e = t; e < K; e += NT)
-            if (q[e] != 0.0f) kl += q[e] * (logf(q[e]) - ((zk[e] - r2) * d.inv_t - log2s));
+        double kl = 0.0;
+        each_own([&](uint32_t e, float x) {
+            if (q[e] != 0.0f) kl += q[e] * (logf(q[e]) - ((x - r2) * d.inv_t - log2s));
+        });
         kl = block_sum<NT>(kl, redd);
         if (held > 0.0f) kl += held * (logf(held) - ((rr - r2) * d.inv_t + logf(rest2.s) - log2s));
+        loss = d.kd * static_cast<float>(kl);
     }
-    if (t == 0) {
-        float loss = entries ? d.kd * static_cast<float>(kl) : 0.0f;
-        if (label != kNone) loss = loss + d.ce * (logf(all1.s) - (kTwo ? zl - r1 : (zl - r1) * d.inv_t));
-        d.loss[r] = weight * loss;
-    }
-    if (!out) {
-        z.row = next;
-        z.load();
-        continue;
-    }
-    // the gradient: kd T (mass p_j - held p_j / p_r - q_j) + ce (softmax_j - [j = label])
-    const float f = weight * d.grad;
-    const float kt = entries ? f * d.kd_slope : 0.0f, kc = label != kNone ? f * d.ce : 0.0f;
-    const float back = term(rr, r2, c2);  // p_j = back term(z_j, rr) / all2.s
-    float g2 = kt * (mass * back / all2.s - (held > 0.0f ? held / rest2.s : 0.0f));
-    const float g1 = kc / all1.s;
-    if (!kTwo) g2 = g2 + g1 * back;
-    __syncthreads();  // zk and zl, whose places may be out's, have been read
-    z.template each<false>([&](uint32_t c, float(&v)[N], uint32_t cnt) {
-        Pack<Store, N> g;
-#pragma unroll
-        for (int u = 0; u < N; ++u) {
-            float x = g2 * term(v[u], rr, c2);
-            if (kTwo) x = x + g1 * term(v[u], r1, c1);
-            g.v[u] = T::from_f32(x);
-        }
-        if (cnt == N) *reinterpret_cast<Pack<Store, N> *>(out + c) = g;
-        else
-#pragma unroll
-            for (uint32_t u = 0; u < N; ++u)
-                if (u < cnt) out[c + u] = g.v[u];
-    }, next);
-    __syncthreads();
-    // columns that an entry or the label names
-    bool own_label = label != kNone;  // no entry names it
-    if (entries && label != kNone)
-        for (uint32_t j = 0; j < K; ++j) own_label = own_label && col[j] != label;
-    for (uint32_t e = t; e < K + 1; e += NT) {
-        if (e < K ? !entries || col[e] == kNone || qs[e] < 0.0f : !own_label) continue;
-        const uint32_t c = e < K ? col[e] : label;
-        const float x = e < K ? zk[e] : zl, p = term(x, r2, c2) / all2.s;
-        float g = kt * (mass * p - (e < K ? qs[e] : 0.0f)) + kc * (term(x, r1, c1) / all1.s - (c == label ? 1.0f : 0.0f));
-        if (e == K && held > 0.0f) g = g - kt * held * (term(x, rr, c2) / rest2.s);  // a label of the rest
-        out[c] = T::from_f32(g);
-    }
-    }
+    if (label != kNone) loss = loss + d.ce * (logf(all1.s) - (kTwo ? zl - r1 : (zl - r1) * d.inv_t));
+    if (t == 0) d.loss[r] = weight * loss;
 }
 
 // --------------------------------------------------------------- host side
@@ -672,30 +697,30 @@ extern "C" gc_status gc_distill_loss(const void *logits, int type, uint64_t stri
         if (dlogits == logits && dstride != stride)
             return fail(fn, GC_EINVAL, "dlogits in place of logits must have their stride");
     }
-    Distill d{logits, idx, t, labels, t_lse, weights, loss, dlogits, stride, idx_stride, t_stride, dstride, n_rows, vocab, k, idx_type, t_type,
+    Distill d{logits, idx, t, labels, t_lse, weights, loss, dlogits, stride, idx_stride, t_stride, dstride, vocab, k, idx_type, t_type,
               opt->mode == GC_DISTILL_REST, 1.0f / T, kd, opt->kd_weight * T, opt->ce_weight, opt->grad_scale};
     if (!k) d.kd = 0.0f;
     const size_t lds = 16 * ((size_t(k) + 3) & ~size_t(3)) + (d.rest ? 4 * ((size_t(vocab) + 31) / 32 + 1) : 0);
     const bool two = labels && opt->ce_weight != 0.0f && T != 1.0f;
     hipError_t e = hipSuccess;
-    auto go = [&](auto kernel, int threads, uint64_t most) {
+    auto go = [&](auto kernel, int threads) {
         if (lds > 48 * 1024)
             e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
         if (e != hipSuccess) return;
-        GC_LAUNCH("distill", stream, kernel<<<static_cast<unsigned>(umin64(n_rows, most)), threads, lds, stream>>>(d));
+        GC_LAUNCH("distill", stream, kernel<<<static_cast<unsigned>(n_rows), threads, lds, stream>>>(d));
     };
     auto with = [&](auto type_tag, auto is_two) {
         using Tp = decltype(type_tag);
         constexpr bool kTwo = decltype(is_two)::value;
         const uint64_t vecs = ceil_div(vocab, kVec<Tp>);
-        constexpr uint64_t kAll = kMaxRows;
-        if (vecs < 2) go(distill_kernel<Tp, 256, 0, kTwo>, 256, kAll);
-        else if (vecs <= 256 * 4) go(distill_kernel<Tp, 256, 4, kTwo>, 256, kAll);
-        else if (vecs <= 256 * 8) go(distill_kernel<Tp, 256, 8, kTwo>, 256, kAll);
-        else if (vecs <= 256 * 16) go(distill_kernel<Tp, 256, 16, kTwo>, 256, kAll);
-        else if (vecs <= 1024 * 8) go(distill_kernel<Tp, 1024, 8, kTwo>, 1024, 256);
-        else if (vecs <= 1024 * 16) go(distill_kernel<Tp, 1024, 16, kTwo>, 1024, 256);
-        else go(distill_kernel<Tp, 1024, 0, kTwo>, 1024, kAll);
+        // as few threads as hold the row: several rows a unit overlap better than one (us, 4096 rows of 65536 bf16:
+        // 227 with 512 threads, 352 with 1024)
+        if (vecs < 2) go(distill_kernel<Tp, 256, 0, true, kTwo>, 256);
+        else if (vecs <= 256 * 4) go(distill_kernel<Tp, 256, 4, false, kTwo>, 256);
+        else if (vecs <= 256 * 8) go(distill_kernel<Tp, 256, 8, false, kTwo>, 256);
+        else if (vecs <= 256 * 16) go(distill_kernel<Tp, 256, 16, false, kTwo>, 256);
+        else if (vecs <= 512 * 16) go(distill_kernel<Tp, 512, 16, false, kTwo>, 512);
+        else go(distill_kernel<Tp, 512, 16, true, kTwo>, 512);
     };
     auto of = [&](auto type_tag) {
         if (two) with(type_tag, std::true_type{});
