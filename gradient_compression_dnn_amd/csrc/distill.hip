@@ -1,6 +1,7 @@
 // Distillation from a teacher's top logits: the exact top k of every row
 // (gc_top_logits), and the loss of a student's rows with its gradient
 // (gc_distill_loss).  One workgroup a row.
+#include <algorithm>
 #include <string>
 #include <type_traits>
 
@@ -17,16 +18,24 @@ constexpr uint32_t kNone = 0xFFFFFFFFu;
 template <class T>
 constexpr int kVec = 16 / int(sizeof(typename T::Store));
 
-// N elements of a row from c on; those at or past `cols` are -Inf.
+// How many elements a row's first one is past 16 bytes.  Vectors are cut there, so that they are aligned wherever
+// the row starts: column v N - skew on is vector v (4096 rows of 131071 bf16, which start anywhere: 600 us for
+// the loss with its gradient by unaligned vectors, 467 for 131072).
+template <class T>
+__device__ __forceinline__ uint32_t skew_of(const typename T::Store *row) {
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) / sizeof(typename T::Store)) % kVec<T>;
+}
+
+// N elements of a row from c on; those before it, and at or past `cols`, are -Inf.
 template <class T, int N>
-__device__ __forceinline__ void load_logits(const typename T::Store *row, uint32_t c, uint32_t cols, float (&v)[N]) {
-    if (c + N <= cols) {
+__device__ __forceinline__ void load_logits(const typename T::Store *row, int64_t c, uint32_t cols, float (&v)[N]) {
+    if (c >= 0 && c + N <= cols) {
         const auto t = *reinterpret_cast<const Pack<typename T::Store, N> *>(row + c);
 #pragma unroll
         for (int u = 0; u < N; ++u) v[u] = T::to_f32(t.v[u]);
     } else {
 #pragma unroll
-        for (uint32_t u = 0; u < N; ++u) v[u] = c + u < cols ? T::to_f32(row[c + u]) : -INFINITY;
+        for (int u = 0; u < N; ++u) v[u] = c + u >= 0 && c + u < cols ? T::to_f32(row[c + u]) : -INFINITY;
     }
 }
 
@@ -165,44 +174,53 @@ __device__ __forceinline__ void select_entries(uint32_t want, Each each, uint32_
     *prefix_out = prefix;
 }
 
-// The top k of a row.  A bound under the k-th largest comes from a sample: the maxima of kSample vectors a
-// thread, spread over the row; k of those are above it.  One pass then lists what is above the bound, with the
-// sums beside it, and the list's top k are found digit by digit and ranked by counting.  A row that fills the
-// list (many ties, a sample that misses the large ones) is read again, digit by digit.  Memory bounds
-// the pass.
-constexpr uint32_t kListEntries = 4096;
-
-template <class T, int NT>
+// The top k of a row.  A bound under the k-th largest comes from a sample: the maxima of vectors spread over the
+// row; k of those are above it.  One pass then notes the vectors with an element above the bound, with the sums
+// beside it (their elements at once, with an atomic each: 350 us at 4096 x 131072, where the loss takes 213); the elements' top k are found digit by digit and ranked by counting.  A row that fills the list (many ties, a sample that
+// misses the large ones) is read again, digit by digit.  The sample is chosen so that half of the list is
+// expected to fill.  Memory bounds the pass, with several rows a unit; a few rows take 1,024 threads each.
+template <class T, int NT, uint32_t kList, uint32_t kMost>
 __global__ __launch_bounds__(NT) void top_kernel(const typename T::Store *__restrict__ logits, uint64_t stride, uint32_t vocab,
-                                                 uint32_t k, float scale, int32_t *__restrict__ idx, float *__restrict__ val,
-                                                 float *__restrict__ lse) {
-    constexpr int N = kVec<T>;
-    constexpr uint32_t kSample = 4, kAhead = 4;
-    __shared__ uint32_t hist[2048];
-    __shared__ uint64_t list[kListEntries], best[GC_MAX_TOP_LOGITS];
+                                                 uint32_t k, uint32_t groups, float scale, int32_t *__restrict__ idx,
+                                                 float *__restrict__ val, float *__restrict__ lse) {
+    constexpr int N = kVec<T>, kAhead = 4;
+    __shared__ uint32_t hist[kList > 2048 ? kList : 2048];
+    __shared__ uint64_t list[kList], best[kMost];
     __shared__ float red[NT / kWave];
     __shared__ Sum sums[NT / kWave];
-    __shared__ uint32_t listed, taken;
+    __shared__ uint32_t listed, spotted, taken;
+    float *tops = reinterpret_cast<float *>(list);  // the sample's maxima, before there is a list
+    uint32_t *spots = hist;                         // vectors with an element above the bound, while no digits are counted
     const uint64_t r = blockIdx.x;
     const typename T::Store *row = logits + r * stride;
-    const uint32_t t = threadIdx.x, vecs = static_cast<uint32_t>(ceil_div(vocab, N));
-    // The sample.
-    const uint32_t most = (vecs + NT - 1) / NT, ns = min(min(kSample, (4 * k + NT - 1) / NT), most);
-    float top[kSample], high = -INFINITY, low = INFINITY;
+    const uint32_t t = threadIdx.x, skew = skew_of<T>(row), vecs = (vocab + skew + N - 1) / N;
+    // vectors that lie inside the row, read without a check each: with one, no load went out before the last was there
+    const uint32_t first = skew ? 1 : 0, whole = (vocab + skew) / N > first ? (vocab + skew) / N - first : 0;
+    auto inside = [&](uint32_t at, float(&v)[N]) {
+        const auto x = *reinterpret_cast<const Pack<typename T::Store, N> *>(row + (at * N - skew));
 #pragma unroll
-    for (uint32_t i = 0; i < kSample; ++i) {
-        top[i] = -INFINITY;
-        const uint32_t g = i * NT + t;  // group g of ns NT, or of all vectors where those are fewer
-        if (i < ns && g < vecs) {
-            const uint32_t at = vecs <= ns * NT ? g : static_cast<uint32_t>(static_cast<uint64_t>(g) * vecs / (ns * NT));
-            float v[N];
-            load_logits<T>(row, at * N, vocab, v);
-            top[i] = largest(v);
-            high = fmaxf(high, top[i]);
-            if (top[i] > -INFINITY) low = fminf(low, top[i]);
+        for (int u = 0; u < N; ++u) v[u] = T::to_f32(x.v[u]);
+    };
+    // the sample: runs of 64 vectors, spread evenly (single vectors take as many lines of memory as the row has)
+    const uint32_t ng = groups < whole ? groups / kWave * kWave : whole;  // at most 2 kList, what tops holds
+    float high = -INFINITY, low = INFINITY;
+    for (uint32_t g0 = t; g0 < ng; g0 += NT * kAhead) {
+        float v[kAhead][N];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const uint32_t g = min(g0 + i * NT, ng - 1), run = g / kWave;
+            inside(first + (ng < whole ? static_cast<uint32_t>(static_cast<uint64_t>(run * kWave) * whole / ng) + g % kWave : g), v[i]);
         }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (g0 + i * NT < ng) {
+                const float top = largest(v[i]);
+                tops[g0 + i * NT] = top;
+                high = fmaxf(high, top);
+                if (top > -INFINITY) low = fminf(low, top);
+            }
     }
-    if (t == 0) listed = taken = 0;
+    if (t == 0) listed = spotted = taken = 0;
     for (uint32_t i = t; i < 2048; i += NT) hist[i] = 0;
     high = block_max<NT>(high, red);
     low = -block_max<NT>(-low, red);
@@ -212,61 +230,78 @@ __global__ __launch_bounds__(NT) void top_kernel(const typename T::Store *__rest
     float limit = INFINITY;  // listed is what has (high - x) per < limit
     if (usable) {
         uint32_t mine = 0;
-#pragma unroll
-        for (uint32_t i = 0; i < kSample; ++i)
-            if (top[i] > -INFINITY) {
-                atomicAdd(&hist[2047 - static_cast<uint32_t>((high - top[i]) * per)], 1u);
+        for (uint32_t g = t; g < ng; g += NT)
+            if (tops[g] > -INFINITY) {
+                atomicAdd(&hist[2047 - static_cast<uint32_t>((high - tops[g]) * per)], 1u);
                 ++mine;
             }
-        uint32_t groups;
-        (void)block_exclusive_scan<uint32_t, NT>(mine, &groups);
-        if (groups >= k) {
+        uint32_t count;
+        (void)block_exclusive_scan<uint32_t, NT>(mine, &count);
+        if (count >= k) {
             uint32_t above;
             limit = static_cast<float>(2048 - block_find_bucket<2048, NT>(k, [&](int b) { return hist[b]; }, &above));
         }
     }
     const float from = usable ? high : 0.0f, by = usable ? per : 0.0f;
-    // (x - 0) 0 is NaN for an infinite x, which has no place below the limit
+    // not below the limit: (x - 0) 0 is NaN for +Inf, which passes
+    auto passes = [&](float x) { return x > -INFINITY && !((from - x) * by >= limit); };
     __syncthreads();
     const float c2 = scale * kLog2e;
     Sum sum = kNoTerms;
-    for (uint32_t b = 0; b < vecs; b += NT * kAhead) {
+    auto look = [&](uint32_t at, const float(&v)[N]) {
+        const float m = largest(v);
+        if (passes(m)) {
+            const uint32_t p = atomicAdd(&spotted, 1u);
+            if (p < kList) spots[p] = at;
+        }
+        if (lse) add_terms(sum, c2, v, m);
+    };
+    uint32_t at = first + t;
+    for (; at + (kAhead - 1) * NT < first + whole; at += NT * kAhead) {
         float v[kAhead][N];
 #pragma unroll
-        for (uint32_t i = 0; i < kAhead; ++i) {
-            const uint32_t at = b + i * NT + t;
-            if (at < vecs) load_logits<T>(row, at * N, vocab, v[i]);
-            else
+        for (int i = 0; i < kAhead; ++i) inside(at + i * NT, v[i]);
 #pragma unroll
-                for (int u = 0; u < N; ++u) v[i][u] = -INFINITY;
-        }
-#pragma unroll
-        for (uint32_t i = 0; i < kAhead; ++i) {
-            const float m = largest(v[i]);
-            if (m > -INFINITY && !((from - m) * by >= limit)) {
-#pragma unroll
-                for (uint32_t u = 0; u < N; ++u)
-                    if (v[i][u] > -INFINITY && !((from - v[i][u]) * by >= limit)) {
-                        const uint32_t p = atomicAdd(&listed, 1u);
-                        if (p < kListEntries) list[p] = entry_of(order_key(v[i][u]), (b + i * NT + t) * N + u);
-                    }
-            }
-            if (lse) add_terms(sum, c2, v[i], m);
-        }
+        for (int i = 0; i < kAhead; ++i) look(at + i * NT, v[i]);
+    }
+    for (; at < first + whole; at += NT) {
+        float v[N];
+        inside(at, v);
+        look(at, v);
+    }
+    // the vectors that the row begins and ends in
+    if (t < 2 && (t == 0 ? first == 1 : first + whole < vecs)) {
+        float v[N];
+        at = t == 0 ? 0 : first + whole;
+        load_logits<T>(row, static_cast<int64_t>(at) * N - skew, vocab, v);
+        look(at, v);
     }
     if (lse) {
         sum = block_join<NT>(sum, c2, sums);
         if (t == 0) lse[r] = base(sum) * scale + logf(sum.s);
     }
     __syncthreads();
+    const bool all_spots = spotted <= kList;
+    if (all_spots)
+        for (uint32_t i = t; i < spotted; i += NT) {
+            float v[N];
+            load_logits<T>(row, static_cast<int64_t>(spots[i]) * N - skew, vocab, v);
+#pragma unroll
+            for (int u = 0; u < N; ++u)
+                if (passes(v[u])) {
+                    const uint32_t p = atomicAdd(&listed, 1u);
+                    if (p < kList) list[p] = entry_of(order_key(v[u]), spots[i] * N + u - skew);
+                }
+        }
+    __syncthreads();
     // a list of fewer than k holds every candidate: a bound has k above it
-    const uint32_t n = listed, want = min(k, n);
+    const uint32_t n = all_spots ? listed : spotted, want = min(k, n);
     if (want) {
         uint64_t known, prefix;
         auto take = [&](uint64_t e) {
             if ((e & known) >= prefix) best[atomicAdd(&taken, 1u)] = e;  // in any order: ranked below
         };
-        if (n <= kListEntries) {
+        if (n <= kList) {
             auto each = [&](auto f) {
                 for (uint32_t i = t; i < n; i += NT) f(list[i]);
             };
@@ -276,11 +311,11 @@ __global__ __launch_bounds__(NT) void top_kernel(const typename T::Store *__rest
             auto each = [&](auto f) {
                 for (uint32_t at = t; at < vecs; at += NT) {
                     float v[N];
-                    load_logits<T>(row, at * N, vocab, v);
+                    load_logits<T>(row, static_cast<int64_t>(at) * N - skew, vocab, v);
 #pragma unroll
-                    for (uint32_t u = 0; u < N; ++u) {
+                    for (int u = 0; u < N; ++u) {
                         const uint32_t key = order_key(v[u]);
-                        if (key) f(entry_of(key, at * N + u));
+                        if (key) f(entry_of(key, at * N + u - skew));
                     }
                 }
             };
@@ -332,13 +367,14 @@ struct Row {
     static constexpr uint32_t kStep = NT * N;
     using Store = typename T::Store;
     const Store *row;
-    uint32_t vocab;
+    uint32_t vocab, skew;
     u32x4 raw[C ? C : 1];
 
-    // The vector that ends with the row stands for the one that crosses its end, and for those past it.
-    __device__ __forceinline__ uint32_t column(int i, uint32_t t) const {
-        const uint32_t c = i * kStep + t * N;
-        return kMore ? c : min(c, vocab - N);
+    __device__ __forceinline__ int32_t own_column(int i, uint32_t t) const { return static_cast<int32_t>(i * kStep + t * N - skew); }
+    // The vector that the row begins or ends with stands for the one that crosses its start or end, and for those past it.
+    __device__ __forceinline__ int32_t column(int i, uint32_t t) const {
+        const int32_t c = own_column(i, t), in = i ? c : max(c, 0);
+        return kMore ? in : min(in, static_cast<int32_t>(vocab - N));
     }
     __device__ __forceinline__ u32x4 vector_at(uint32_t c) const {
         return __builtin_bit_cast(u32x4, *reinterpret_cast<const Pack<Store, N> *>(row + c));
@@ -362,30 +398,41 @@ struct Row {
             // not fit the registers
             uint32_t t = threadIdx.x;
             asm volatile("" : "+v"(raw[i]), "+v"(t));
-            const uint32_t c = column(i, t), own = i * kStep + t * N;
+            const int32_t c = column(i, t), own = own_column(i, t);
             values(raw[i]);
-            if (!kMore && kOnce && (i + 1) * kStep > vocab)
+            if (kOnce && (i == 0 || !kMore) && __ballot(c != own))
 #pragma unroll
-                for (uint32_t u = 0; u < N; ++u) v[u] = c + u < own ? -INFINITY : v[u];
-            if (kMore || kOnce || own < vocab) f(c, v, uint32_t(N));
+                for (int32_t u = 0; u < N; ++u) v[u] = c + u < own || c + u >= own + N ? -INFINITY : v[u];
+            if (kMore || kOnce || own < static_cast<int32_t>(vocab)) f(c, v, uint32_t(N));
             __builtin_amdgcn_sched_barrier(0);
         }
         if constexpr (kMore) {
             constexpr int kAhead = 4;
-            uint32_t c = C * kStep + threadIdx.x * N;
-            for (; c + (kAhead - 1) * kStep + N <= vocab; c += kAhead * kStep) {
-                u32x4 w[kAhead];
+            int64_t c = static_cast<int64_t>(C * kStep + threadIdx.x * N) - skew;
+            if (c >= 0)
+                for (; c + (kAhead - 1) * kStep + N <= vocab; c += kAhead * kStep) {
+                    u32x4 w[kAhead];
 #pragma unroll
-                for (int i = 0; i < kAhead; ++i) w[i] = vector_at(c + i * kStep);
+                    for (int i = 0; i < kAhead; ++i) w[i] = vector_at(c + i * kStep);
 #pragma unroll
-                for (int i = 0; i < kAhead; ++i) {
-                    values(w[i]);
-                    f(c + i * kStep, v, uint32_t(N));
+                    for (int i = 0; i < kAhead; ++i) {
+                        values(w[i]);
+                        f(c + i * kStep, v, uint32_t(N));
+                    }
                 }
-            }
             for (; c < vocab; c += kStep) {
-                load_logits<T>(row, c, vocab, v);
-                f(c, v, min(vocab - c, uint32_t(N)));
+                if (c < 0 || c + N > vocab) {  // the elements that the row has, one by one
+                    for (int u = 0; u < N; ++u) {
+                        if (c + u < 0 || c + u >= vocab) continue;
+                        v[0] = T::to_f32(row[c + u]);
+#pragma unroll
+                        for (int x = 1; x < N; ++x) v[x] = -INFINITY;
+                        f(static_cast<int32_t>(c + u), v, 1u);
+                    }
+                } else {
+                    values(vector_at(c));
+                    f(static_cast<int32_t>(c), v, uint32_t(N));
+                }
             }
         }
     }
@@ -429,7 +476,7 @@ __global__ __launch_bounds__(NT) void distill_kernel(Distill d) {
         const int64_t l = id_at(d.labels, d.id_type, r);
         if (l >= 0 && l < static_cast<int64_t>(V)) label = static_cast<uint32_t>(l);
     }
-    Row<T, NT, C, kMore> z{row, V};
+    Row<T, NT, C, kMore> z{row, V, skew_of<T>(row)};
     z.load();
     const float my_z = student(my_col), zl = student(label);
     const float weight = d.weights ? d.weights[r] : 1.0f;
@@ -596,7 +643,8 @@ __global__ __launch_bounds__(NT) void distill_kernel(Distill d) {
 
 // --------------------------------------------------------------- host side
 constexpr uint64_t kMaxRows = uint64_t(1) << 22;
-constexpr uint64_t kShortVecs = 2048;  // rows of at most so many 16-byte vectors take 256 threads
+constexpr uint64_t kFewRows = 256;  // rows that have a unit each
+constexpr uint32_t kSmallList = 1024, kBigList = 4096, kSmallK = 128;
 
 size_t type_bytes(int type) { return type == GC_F32 ? 4 : 2; }
 bool known_type(int type) { return type == GC_F32 || type == GC_BF16 || type == GC_F16; }
@@ -648,14 +696,18 @@ extern "C" gc_status gc_top_logits(const void *logits, int type, uint64_t stride
     if (misaligned(lse, 4)) return fail(fn, GC_EINVAL, "buffers must be aligned to their elements");
     auto go = [&](auto t) {
         using T = decltype(t);
-        auto with = [&](auto threads) {
-            constexpr int NT = decltype(threads)::value;
+        constexpr uint64_t N = kVec<T>;
+        auto with = [&](auto kernel, int threads, uint64_t room) {
+            // v k / (groups N) of a row are expected above the bound: half of the list
+            const uint64_t groups = ceil_div(std::max<uint64_t>(ceil_div(2 * uint64_t(vocab) * k, N * room), 2 * k), kWave) * kWave;
             GC_LAUNCH("top_logits", stream,
-                      top_kernel<T, NT><<<static_cast<unsigned>(n_rows), NT, 0, stream>>>(
-                          static_cast<const typename T::Store *>(logits), stride, vocab, k, 1.0f / temperature, idx, val, lse));
+                      kernel<<<static_cast<unsigned>(n_rows), threads, 0, stream>>>(
+                          static_cast<const typename T::Store *>(logits), stride, vocab, k, static_cast<uint32_t>(umin64(groups, 2 * room)),
+                          1.0f / temperature, idx, val, lse));
         };
-        if (ceil_div(vocab, kVec<T>) <= kShortVecs) with(std::integral_constant<int, 256>{});
-        else with(std::integral_constant<int, 1024>{});
+        const bool few = n_rows <= kFewRows, small = k <= kSmallK && uint64_t(vocab) * k <= N * kSmallList * kSmallList;
+        if (few) small ? with(top_kernel<T, 1024, kSmallList, kSmallK>, 1024, kSmallList) : with(top_kernel<T, 1024, kBigList, GC_MAX_TOP_LOGITS>, 1024, kBigList);
+        else small ? with(top_kernel<T, 256, kSmallList, kSmallK>, 256, kSmallList) : with(top_kernel<T, 256, kBigList, GC_MAX_TOP_LOGITS>, 256, kBigList);
     };
     if (type == GC_F32) go(F32{});
     else if (type == GC_BF16) go(BF16{});
@@ -712,10 +764,12 @@ extern "C" gc_status gc_distill_loss(const void *logits, int type, uint64_t stri
     auto with = [&](auto type_tag, auto is_two) {
         using Tp = decltype(type_tag);
         constexpr bool kTwo = decltype(is_two)::value;
-        const uint64_t vecs = ceil_div(vocab, kVec<Tp>);
+        // rows that start on 16 bytes, or anywhere
+        const bool even = !misaligned(logits, 16) && stride * type_bytes(type) % 16 == 0;
+        const uint64_t vecs = ceil_div(even ? vocab : vocab + kVec<Tp> - 1, kVec<Tp>);
         // as few threads as hold the row: several rows a unit overlap better than one (us, 4096 rows of 65536 bf16:
         // 227 with 512 threads, 352 with 1024)
-        if (vecs < 2) go(distill_kernel<Tp, 256, 0, true, kTwo>, 256);
+        if (vocab < uint32_t(kVec<Tp>)) go(distill_kernel<Tp, 256, 0, true, kTwo>, 256);
         else if (vecs <= 256 * 4) go(distill_kernel<Tp, 256, 4, false, kTwo>, 256);
         else if (vecs <= 256 * 8) go(distill_kernel<Tp, 256, 8, false, kTwo>, 256);
         else if (vecs <= 256 * 16) go(distill_kernel<Tp, 256, 16, false, kTwo>, 256);
