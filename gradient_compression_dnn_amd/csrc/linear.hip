@@ -81,8 +81,8 @@ struct ShapeModel {
     double stage16, stage32;  // us a stage of 128 bytes of k, with every slot busy
 };
 constexpr ShapeModel kShapes[] = {
-    {kBig, Big::kTM, Big::kTN, 256, 2.0, 8.5},
-    {kMid, Mid::kTM, Mid::kTN, 512, 1.3, 4.5},
+    {kBig, Big::kTM, Big::kTN, 256, 2.0, 0.0},  // not for fp32
+    {kMid, Mid::kTM, Mid::kTN, 512, 1.3, 1.7},
     {kThin, Thin::kTM, Thin::kTN, 1024, 1.3, 3.0},
 };
 constexpr double kTileUs = 3.0, kJoinUs = 4.0, kPartialBytesPerUs = 4e6;
@@ -105,7 +105,7 @@ Cut plan_cut(Kind kind, int type, uint32_t M, uint32_t N, uint32_t K, bool any) 
     double least = 0.0;
     const uint32_t stages = static_cast<uint32_t>(ceil_div(K, 128 / type_bytes(type)));
     for (const ShapeModel &s : kShapes) {
-        if (s.shape != kMid && any) continue;
+        if ((s.shape != kMid && any) || (s.shape == kBig && type == GC_F32)) continue;
         if (s.shape == kThin && (kind == kWeight || M > kThinTokens)) continue;
         const uint64_t tm = ceil_div(M, s.tm), tn = ceil_div(N, s.tn), tiles = tm * tn;
         for (uint32_t parts = 1; parts <= std::min(kMaxParts, std::max(stages, 1u)); ++parts) {

@@ -86,6 +86,42 @@ struct Operand {
     }
 };
 
+// A stage of an fp32 operand as three bf16 planes (32 k): x = hi + mid + lo exactly, 8 bits each (hi cut, so that
+// nothing overflows, mid rounded, so that lo has either sign; bits below 2^-133 are dropped).  Six of the nine
+// products of two such sums are formed, all but those with 2^-21 of the whole at most, of either sign, where a
+// rounding of the product would cost 2^-24.  6 bf16 matrix instructions take 96 cycles where fp32's own take 256.
+// An Inf is its hi alone, a NaN stays one.
+//   k contiguous: [row][64 bytes], 16-byte part c at c ^ ((row >> 2) & 3);  k slow: as an operand of 16 bits
+template <bool kSlow, int kTile>
+struct Planes {
+    static constexpr uint32_t kBytes = kTile * 64;  // a plane
+    using Half = Operand<BF16, true, kTile>;
+    // 4 elements: piece `piece` of line `line` (a row, or a k) of the fp32 operand
+    static __device__ __forceinline__ void put(char *to, uint32_t line, uint32_t piece, u32x4 x) {
+        const uint32_t at = kSlow ? line * (kTile * 2) + ((piece >> 2) ^ Half::spread(line)) * 32 + (piece & 3) * 8
+                                  : line * 64 + (((piece >> 1) ^ ((line >> 2) & 3)) << 4) + (piece & 1) * 8;
+        uint32_t h[4], m[4], l[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t b = x[e];
+            h[e] = b & 0xFFFF0000u;
+            const float r = dev_u2f(h[e]) == dev_u2f(b) ? 0.0f : dev_u2f(b) - dev_u2f(h[e]);  // Inf - Inf is none
+            m[e] = (dev_f2u(r) + 0x8000u) & 0xFFFF0000u;
+            l[e] = dev_f2u(r - dev_u2f(m[e]));
+        }
+        auto pair = [](uint32_t high, uint32_t low) { return __builtin_amdgcn_perm(high, low, 0x07060302u); };
+        *reinterpret_cast<uint2 *>(to + at) = make_uint2(pair(h[1], h[0]), pair(h[3], h[2]));
+        *reinterpret_cast<uint2 *>(to + kBytes + at) = make_uint2(pair(m[1], m[0]), pair(m[3], m[2]));
+        *reinterpret_cast<uint2 *>(to + 2 * kBytes + at) = make_uint2(pair(l[1], l[0]), pair(l[3], l[2]));
+    }
+    // rows row0 .. row0 + 15 of a plane, 8 k a lane
+    static __device__ __forceinline__ u32x4 read(const char *lds, uint32_t row0, int plane) {
+        if (kSlow) return Half::read(lds + plane * kBytes, row0, 0);
+        const uint32_t row = row0 + (lane_id() & 15), part = lane_id() >> 4;
+        return *reinterpret_cast<const u32x4 *>(lds + plane * kBytes + row * 64 + ((part ^ ((row >> 2) & 3)) << 4));
+    }
+};
+
 // d[i][j] += sum over 16 bytes of k of a[i] b[j]
 template <class T>
 __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 d) {
@@ -167,11 +203,14 @@ __device__ __forceinline__ void finish(const Product &p, const Beside<T, kKind, 
     }
 }
 
-template <class S>
+template <class T, class S>
 struct Shape : S {
     static constexpr int kWaves = S::kWR * S::kWC, kThreads = kWaves * int(kWave);
     static constexpr int kRA = S::kTM / S::kWR / 16, kRB = S::kTN / S::kWC / 16;  // blocks of 16 x 16 of a wave
-    static constexpr int kBytesA = S::kTM * 128, kBytes = kBytesA + S::kTN * 128;  // a stage
+    // kWide: fp32 by planes, one buffer of them; else two buffers of stages
+    static constexpr bool kWide = sizeof(typename T::Store) == 4 && std::is_same<S, Mid>::value;
+    static constexpr int kLine = kWide ? 192 : 128, kBytesA = S::kTM * kLine, kBytes = kBytesA + S::kTN * kLine;  // a stage
+    static constexpr int kLds = kWide ? kBytes : 2 * kBytes;
     static constexpr int kLoadsA = S::kTM * 8 / kThreads, kLoadsB = S::kTN * 8 / kThreads;  // 16 bytes a thread each
     static_assert(S::kTM * 8 % kThreads == 0 && S::kTN * 8 % kThreads == 0, "every thread loads alike");
 };
@@ -185,7 +224,7 @@ __device__ __forceinline__ u32x4 shift_down(u32x4 x, uint32_t bits) {
 }
 
 // One operand's way into LDS: part i * kThreads + thread of a stage.
-template <class T, Mode kMode, bool kSlow, int kTile, int kLoads, int kThreads>
+template <class T, Mode kMode, bool kWide, bool kSlow, int kTile, int kLoads, int kThreads>
 struct Feed {
     using Op = Operand<T, kSlow, kTile>;
     using Store = typename T::Store;
@@ -247,6 +286,10 @@ struct Feed {
         }
     }
     __device__ __forceinline__ void put(char *to, int i, u32x4 x) const {
+        if constexpr (kWide) {
+            Planes<kSlow, kTile>::put(to, line_of(i), piece_of(), x);
+            return;
+        }
         uint32_t line, piece;
         const uint32_t where = kRegular ? Op::place(threadIdx.x, line, piece) + i * kThreads * 16 : Op::place(i * kThreads + threadIdx.x, line, piece);
         *reinterpret_cast<u32x4 *>(to + where) = x;
@@ -311,14 +354,21 @@ struct Feed {
     }
 };
 
+// Every wave of the workgroup is here and its LDS accesses are done; loads may be on their way.
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 template <class T, Kind kKind, class S, Mode kMode>
 struct Run {
-    using C = Shape<S>;
+    using C = Shape<T, S>;
     static constexpr bool kSlowA = kKind == kWeight, kSlowB = kKind != kForward;
     using OpA = Operand<T, kSlowA, C::kTM>;
     using OpB = Operand<T, kSlowB, C::kTN>;
-    using FeedA = Feed<T, kMode, kSlowA, C::kTM, C::kLoadsA, C::kThreads>;
-    using FeedB = Feed<T, kMode, kSlowB, C::kTN, C::kLoadsB, C::kThreads>;
+    using FeedA = Feed<T, kMode, C::kWide, kSlowA, C::kTM, C::kLoadsA, C::kThreads>;
+    using FeedB = Feed<T, kMode, C::kWide, kSlowB, C::kTN, C::kLoadsB, C::kThreads>;
     using Acc = f32x4[C::kRA][C::kRB];
     using Sums = float[C::kRA];  // a lane's part of the sums of A's rows over k
 
@@ -326,8 +376,32 @@ struct Run {
     // Where registers hold the next stage meanwhile, half of this one's k at a time.
     template <bool kSums>
     static __device__ __forceinline__ void multiply(const char *__restrict__ lds, uint32_t wm, uint32_t wn, Acc &acc, Sums &sums) {
-        constexpr int kTogether = kMode == kDirect ? 2 : 1;
         const char *la = lds, *lb = lds + C::kBytesA;
+        if constexpr (C::kWide) {
+            using PlanesA = Planes<kSlowA, C::kTM>;
+            using PlanesB = Planes<kSlowB, C::kTN>;
+            constexpr int kPairs[6][2] = {{1, 1}, {2, 0}, {0, 2}, {1, 0}, {0, 1}, {0, 0}};  // planes of B and A, the small products first
+            u32x4 fb[3][C::kRB];
+#pragma unroll
+            for (int q = 0; q < 3; ++q)
+#pragma unroll
+                for (int b = 0; b < C::kRB; ++b) fb[q][b] = PlanesB::read(lb, wn + 16 * b, q);
+#pragma unroll
+            for (int a = 0; a < C::kRA; ++a) {
+                u32x4 fa[3];
+#pragma unroll
+                for (int q = 0; q < 3; ++q) fa[q] = PlanesA::read(la, wm + 16 * a, q);
+#pragma unroll
+                for (int q = 0; q < 6; ++q)
+#pragma unroll
+                    for (int b = 0; b < C::kRB; ++b) acc[a][b] = mma<BF16>(fb[kPairs[q][0]][b], fa[kPairs[q][1]], acc[a][b]);
+                if (kSums)
+#pragma unroll
+                    for (int q = 2; q >= 0; --q) sums[a] = add_all<BF16>(fa[q], sums[a]);
+            }
+            return;
+        } else {
+        constexpr int kTogether = kMode == kDirect ? 2 : 1;
 #pragma unroll
         for (int h0 = 0; h0 < 2; h0 += kTogether) {
             u32x4 fb[kTogether][C::kRB], fa[kTogether], na[kTogether];
@@ -351,6 +425,7 @@ struct Run {
                 for (int h = 0; h < kTogether; ++h) fa[h] = na[h];
                 __builtin_amdgcn_sched_barrier(0);
             }
+        }
         }
     }
 
@@ -385,6 +460,25 @@ struct Run {
             fa.stash(lds);
             fb.stash(lds + C::kBytesA);
         }
+        if constexpr (C::kWide) {
+            // one buffer: a unit's other workgroup multiplies while this one splits its next stage
+            for (uint32_t i = 0; i < n; ++i) {
+                const uint32_t s = s0 + i + 1 - ragged;
+                const bool more = i + 1 < n;
+                if (more) {
+                    fa.fetch(s);
+                    fb.fetch(s);
+                }
+                lds_barrier();
+                if (kActive) multiply<kSums>(lds, wm, wn, acc, sums);
+                lds_barrier();
+                if (more) {
+                    fa.stash(lds);
+                    fb.stash(lds + C::kBytesA);
+                }
+            }
+            return;
+        }
         for (uint32_t i = 0; i < n; ++i) {
             // this stage has landed, and every wave is done with the buffer that is filled next
             if (kMode == kDirect) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
@@ -411,8 +505,8 @@ struct Run {
 
     // The sums of kRows rows of the wave (blocks a0 on) by way of LDS, so that a lane gets 8 columns of a row and
     // the code of an epilogue stands there once.  Pieces of 4 columns are permuted against bank conflicts.
-    static constexpr int kCols = C::kRB * 16, kRows = C::kRA < 4 ? C::kRA * 16 : 64, kWaveBytes = kRows * kCols * 4;
-    static_assert(C::kWaves * kWaveBytes <= 2 * C::kBytes, "a block of results per wave");
+    static constexpr int kCols = C::kRB * 16, kRows = C::kRA < 4 ? C::kRA * 16 : C::kWide ? 32 : 64, kWaveBytes = kRows * kCols * 4;
+    static_assert(C::kWaves * kWaveBytes <= C::kLds, "a block of results per wave");
     static __device__ __forceinline__ uint32_t block_at(uint32_t row, uint32_t piece) {
         return row * (kCols * 4) + ((piece ^ (row & (kCols / 4 - 1))) << 4);
     }
@@ -487,10 +581,10 @@ __device__ __forceinline__ void tile_of(uint32_t t, uint32_t tiles_m, uint32_t t
 }
 
 template <class T, Kind kKind, class S, Mode kMode>
-__global__ __launch_bounds__(Shape<S>::kThreads, S::kWavesPerSimd) void linear_kernel(Product p, Cut c) {
+__global__ __launch_bounds__((Shape<T, S>::kThreads), S::kWavesPerSimd) void linear_kernel(Product p, Cut c) {
     using R = Run<T, kKind, S, kMode>;
-    using C = Shape<S>;
-    __shared__ __attribute__((aligned(128))) char lds[2 * C::kBytes];
+    using C = Shape<T, S>;
+    __shared__ __attribute__((aligned(128))) char lds[C::kLds];
     const uint32_t id = xcd_order(blockIdx.x, gridDim.x), tiles = c.tiles_m * c.tiles_n;
     const uint32_t part = id / tiles, tile = id - part * tiles;
     uint32_t tm, tn;
@@ -555,7 +649,7 @@ __global__ __launch_bounds__(Shape<S>::kThreads, S::kWavesPerSimd) void linear_k
 // The parts' sums added in order: a workgroup per 4 blocks of 16 x 16 of a tile.
 template <class T, Kind kKind, class S>
 __global__ __launch_bounds__(kBlock) void linear_join_kernel(Product p, Cut c) {
-    using C = Shape<S>;
+    using C = Shape<T, S>;
     constexpr uint32_t kBlocks = C::kWaves * C::kRA * C::kRB, kPer = kBlocks / kWaves;
     const uint32_t tiles = c.tiles_m * c.tiles_n, tile = blockIdx.x / kPer;
     const uint32_t block = (blockIdx.x - tile * kPer) * kWaves + __builtin_amdgcn_readfirstlane(wave_id()), lane = lane_id();
@@ -646,10 +740,11 @@ __global__ __launch_bounds__(16 * kWave) void linear_few_kernel(Product p) {
 
 template <class T, Kind kKind, class S>
 gc_status launch_shape(const char *fn, const Product &p, const Cut &c, hipStream_t stream) {
-    using C = Shape<S>;
+    using C = Shape<T, S>;
     const unsigned grid = c.tiles_m * c.tiles_n * c.parts;
     auto kernel = linear_kernel<T, kKind, S, kHeld>;
-    if (c.mode == kDirect) kernel = linear_kernel<T, kKind, S, kDirect>;
+    if constexpr (!C::kWide)
+        if (c.mode == kDirect) kernel = linear_kernel<T, kKind, S, kDirect>;
     if constexpr (std::is_same<S, Mid>::value)
         if (c.mode == kAny) kernel = linear_kernel<T, kKind, S, kAny>;
     GC_LAUNCH("linear_product", stream, kernel<<<grid, C::kThreads, 0, stream>>>(p, c));
@@ -675,7 +770,8 @@ gc_status linear_launch(const char *fn, Kind kind, const Product &p, const Cut &
         const hipError_t e = hipGetLastError();
         return e == hipSuccess ? GC_OK : hip_error(e, fn);
     }
-    if (c.shape == kBig) return of(Big{});
+    if constexpr (sizeof(typename T::Store) == 2)
+        if (c.shape == kBig) return of(Big{});
     if (c.shape == kMid || kind == kWeight) return of(Mid{});
     if (kind == kForward) return launch_shape<T, kForward, Thin>(fn, p, c, stream);
     return launch_shape<T, kInput, Thin>(fn, p, c, stream);
