@@ -96,10 +96,8 @@ template <bool kSlow, int kTile>
 struct Planes {
     static constexpr uint32_t kBytes = kTile * 64;  // a plane
     using Half = Operand<BF16, true, kTile>;
-    // 4 elements: piece `piece` of line `line` (a row, or a k) of the fp32 operand
-    static __device__ __forceinline__ void put(char *to, uint32_t line, uint32_t piece, u32x4 x) {
-        const uint32_t at = kSlow ? line * (kTile * 2) + ((piece >> 2) ^ Half::spread(line)) * 32 + (piece & 3) * 8
-                                  : line * 64 + (((piece >> 1) ^ ((line >> 2) & 3)) << 4) + (piece & 1) * 8;
+    // 4 elements' planes
+    static __device__ __forceinline__ void split(u32x4 x, uint2 (&planes)[3]) {
         uint32_t h[4], m[4], l[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -110,9 +108,16 @@ struct Planes {
             l[e] = dev_f2u(r - dev_u2f(m[e]));
         }
         auto pair = [](uint32_t high, uint32_t low) { return __builtin_amdgcn_perm(high, low, 0x07060302u); };
-        *reinterpret_cast<uint2 *>(to + at) = make_uint2(pair(h[1], h[0]), pair(h[3], h[2]));
-        *reinterpret_cast<uint2 *>(to + kBytes + at) = make_uint2(pair(m[1], m[0]), pair(m[3], m[2]));
-        *reinterpret_cast<uint2 *>(to + 2 * kBytes + at) = make_uint2(pair(l[1], l[0]), pair(l[3], l[2]));
+        planes[0] = make_uint2(pair(h[1], h[0]), pair(h[3], h[2]));
+        planes[1] = make_uint2(pair(m[1], m[0]), pair(m[3], m[2]));
+        planes[2] = make_uint2(pair(l[1], l[0]), pair(l[3], l[2]));
+    }
+    // into LDS: piece `piece` of line `line` (a row, or a k) of the fp32 operand
+    static __device__ __forceinline__ void put(char *to, uint32_t line, uint32_t piece, const uint2 (&planes)[3]) {
+        const uint32_t at = kSlow ? line * (kTile * 2) + ((piece >> 2) ^ Half::spread(line)) * 32 + (piece & 3) * 8
+                                  : line * 64 + (((piece >> 1) ^ ((line >> 2) & 3)) << 4) + (piece & 1) * 8;
+#pragma unroll
+        for (int q = 0; q < 3; ++q) *reinterpret_cast<uint2 *>(to + q * kBytes + at) = planes[q];
     }
     // rows row0 .. row0 + 15 of a plane, 8 k a lane
     static __device__ __forceinline__ u32x4 read(const char *lds, uint32_t row0, int plane) {
@@ -239,6 +244,7 @@ struct Feed {
     static constexpr int kPlaces = kSlow && kRegular ? 1 : kLoads;
     uint32_t at[kPlaces];   // from the stage's first byte
     u32x4 held[kLoads];
+    uint2 planes[kWide ? kLoads : 1][3];
 
     // the line (row, or k) and the piece of it at a thread's part, as it is read from memory
     static __device__ __forceinline__ uint32_t line_of(int i) { return (i * kThreads + threadIdx.x) / kLineParts; }
@@ -287,7 +293,9 @@ struct Feed {
     }
     __device__ __forceinline__ void put(char *to, int i, u32x4 x) const {
         if constexpr (kWide) {
-            Planes<kSlow, kTile>::put(to, line_of(i), piece_of(), x);
+            uint2 p[3];
+            Planes<kSlow, kTile>::split(x, p);
+            Planes<kSlow, kTile>::put(to, line_of(i), piece_of(), p);
             return;
         }
         uint32_t line, piece;
@@ -303,6 +311,19 @@ struct Feed {
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) put(to, i, held[i]);
         }
+    }
+    // The same in steps, for kWide: pieces into their place, part i of the registers into planes, all planes into LDS.
+    __device__ __forceinline__ void settle() {
+        if (kMode == kHeld && kSlow && row0 + kTile > rows) {
+            const uint32_t bits = over(row0, rows) * kSize * 8;
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) held[i] = shift_down(held[i], bits);
+        }
+    }
+    __device__ __forceinline__ void split(int i) { Planes<kSlow, kTile>::split(held[i], planes[i]); }
+    __device__ __forceinline__ void put_planes(char *to) const {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) Planes<kSlow, kTile>::put(to, line_of(i), piece_of(), planes[i]);
     }
     // How many elements of this thread's piece lie past the end, less than all.
     __device__ __forceinline__ uint32_t over(uint32_t start, uint32_t end) const {
@@ -374,23 +395,26 @@ struct Run {
 
     // acc += a stage's product; blocks of A one ahead, and no further: hoisted, they do not fit the registers.
     // Where registers hold the next stage meanwhile, half of this one's k at a time.
-    template <bool kSums>
-    static __device__ __forceinline__ void multiply(const char *__restrict__ lds, uint32_t wm, uint32_t wn, Acc &acc, Sums &sums) {
+    template <bool kSums, class Beneath>
+    static __device__ __forceinline__ void multiply(const char *__restrict__ lds, uint32_t wm, uint32_t wn, Acc &acc, Sums &sums, Beneath beneath) {
         const char *la = lds, *lb = lds + C::kBytesA;
         if constexpr (C::kWide) {
             using PlanesA = Planes<kSlowA, C::kTM>;
             using PlanesB = Planes<kSlowB, C::kTN>;
             constexpr int kPairs[6][2] = {{1, 1}, {2, 0}, {0, 2}, {1, 0}, {0, 1}, {0, 0}};  // planes of B and A, the small products first
-            u32x4 fb[3][C::kRB];
+            u32x4 fb[3][C::kRB], fa[3], na[3];
 #pragma unroll
-            for (int q = 0; q < 3; ++q)
+            for (int q = 0; q < 3; ++q) {
 #pragma unroll
                 for (int b = 0; b < C::kRB; ++b) fb[q][b] = PlanesB::read(lb, wn + 16 * b, q);
+                fa[q] = PlanesA::read(la, wm, q);
+            }
 #pragma unroll
             for (int a = 0; a < C::kRA; ++a) {
-                u32x4 fa[3];
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int q = 0; q < 3; ++q) fa[q] = PlanesA::read(la, wm + 16 * a, q);
+                for (int q = 0; q < 3; ++q) na[q] = a + 1 < C::kRA ? PlanesA::read(la, wm + 16 * (a + 1), q) : fa[q];
+                beneath(a);
 #pragma unroll
                 for (int q = 0; q < 6; ++q)
 #pragma unroll
@@ -398,7 +422,16 @@ struct Run {
                 if (kSums)
 #pragma unroll
                     for (int q = 2; q >= 0; --q) sums[a] = add_all<BF16>(fa[q], sums[a]);
+#pragma unroll
+                for (int q = 0; q < 3; ++q) fa[q] = na[q];
+                // a few vector instructions under each matrix instruction
+#pragma unroll
+                for (int q = 0; q < 6 * C::kRB; ++q) {
+                    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);
+                }
             }
+            __builtin_amdgcn_sched_barrier(0);
             return;
         } else {
         constexpr int kTogether = kMode == kDirect ? 2 : 1;
@@ -438,7 +471,7 @@ struct Run {
             fa.direct(s, next);
             fb.direct(s, next + C::kBytesA);
         }
-        if (kActive) multiply<kSums>(cur, wm, wn, acc, sums);
+        if (kActive) multiply<kSums>(cur, wm, wn, acc, sums, [](int) {});
     }
 
     // Stages s0 .. s1 - 1 of the tile.  kActive: the wave has rows and columns of the result.
@@ -461,20 +494,34 @@ struct Run {
             fb.stash(lds + C::kBytesA);
         }
         if constexpr (C::kWide) {
-            // one buffer: a unit's other workgroup multiplies while this one splits its next stage
+            // One buffer.  While stage i is multiplied, the next is split in registers, and the one behind it is
+            // fetched into the registers that leaves.
+            static_assert(C::kLoadsA == C::kRA && C::kLoadsB == C::kRA, "a part of each operand per row of blocks");
+            const uint32_t last = s1 > whole ? whole - 1 : s1 - 1;  // the last whole stage; fetched again where there is no next
+            auto fetch = [&](uint32_t i) {
+                const uint32_t s = min(s0 + i - ragged, last);
+                fa.fetch(s);
+                fb.fetch(s);
+            };
+            if (n > 1) fetch(1);
             for (uint32_t i = 0; i < n; ++i) {
-                const uint32_t s = s0 + i + 1 - ragged;
                 const bool more = i + 1 < n;
-                if (more) {
-                    fa.fetch(s);
-                    fb.fetch(s);
-                }
                 lds_barrier();
-                if (kActive) multiply<kSums>(lds, wm, wn, acc, sums);
+                fa.settle();
+                fb.settle();
+                auto beneath = [&](int a) {
+                    fa.split(a);
+                    fb.split(a);
+                };
+                if (kActive) multiply<kSums>(lds, wm, wn, acc, sums, beneath);
+                else
+#pragma unroll
+                    for (int a = 0; a < C::kRA; ++a) beneath(a);
+                if (more) fetch(i + 2);
                 lds_barrier();
                 if (more) {
-                    fa.stash(lds);
-                    fb.stash(lds + C::kBytesA);
+                    fa.put_planes(lds);
+                    fb.put_planes(lds + C::kBytesA);
                 }
             }
             return;
@@ -494,7 +541,7 @@ struct Run {
                     fa.fetch(s);
                     fb.fetch(s);
                 }
-                if (kActive) multiply<kSums>(lds + cur, wm, wn, acc, sums);
+                if (kActive) multiply<kSums>(lds + cur, wm, wn, acc, sums, [](int) {});
                 if (more) {
                     fa.stash(lds + next);
                     fb.stash(lds + next + C::kBytesA);
