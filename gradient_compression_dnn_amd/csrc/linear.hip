@@ -87,13 +87,14 @@ constexpr ShapeModel kShapes[] = {
 };
 constexpr double kTileUs = 3.0, kJoinUs = 4.0, kPartialBytesPerUs = 4e6;
 constexpr uint32_t kMaxParts = 32, kThinTokens = 64;
-constexpr uint64_t kFewOutputs = 1 << 16;
+constexpr uint64_t kFewRows = 1024, kFewOutputs = 1 << 16;
 
 Cut plan_cut(Kind kind, int type, uint32_t M, uint32_t N, uint32_t K, bool any) {
     Cut best{};
     // Few tokens: every 16 rows of W read all of x, so a longer batch over many rows goes by tiles (us, few and
     // tiles: 1 x 16384 rows x 4096 columns 26 and 29, 16 x 4096 x 4096 10.0 and 11.7, 16 x 16384 x 4096 35 and 29).
-    if (kind == kForward && M <= 16 && (M <= 4 || static_cast<uint64_t>(M) * N <= kFewOutputs)) {
+    // Few rows of W as well leave most of the chip idle: 15 x 81 x 5398 18 and 10.
+    if (kind == kForward && M <= 16 && (M <= 4 || (N >= kFewRows && static_cast<uint64_t>(M) * N <= kFewOutputs))) {
         const uint64_t chunks = ceil_div(static_cast<uint64_t>(K) * type_bytes(type), 256);
         best.shape = kFew;
         best.tiles_m = 1;

@@ -90,7 +90,7 @@ struct Operand {
 // nothing overflows, mid rounded, so that lo has either sign; bits below 2^-133 are dropped).  Six of the nine
 // products of two such sums are formed, all but those with 2^-21 of the whole at most, of either sign, where a
 // rounding of the product would cost 2^-24.  6 bf16 matrix instructions take 96 cycles where fp32's own take 256.
-// An Inf is its hi alone, a NaN stays one.
+// An Inf counts as a NaN.
 //   k contiguous: [row][64 bytes], 16-byte part c at c ^ ((row >> 2) & 3);  k slow: as an operand of 16 bits
 template <bool kSlow, int kTile>
 struct Planes {
@@ -103,7 +103,7 @@ struct Planes {
         for (int e = 0; e < 4; ++e) {
             const uint32_t b = x[e];
             h[e] = b & 0xFFFF0000u;
-            const float r = dev_u2f(h[e]) == dev_u2f(b) ? 0.0f : dev_u2f(b) - dev_u2f(h[e]);  // Inf - Inf is none
+            const float r = dev_u2f(b) - dev_u2f(h[e]);  // NaN for an Inf: its sums are NaN, as Inf times a plane of 0 is
             m[e] = (dev_f2u(r) + 0x8000u) & 0xFFFF0000u;
             l[e] = dev_f2u(r - dev_u2f(m[e]));
         }
@@ -739,11 +739,20 @@ __global__ __launch_bounds__(16 * kWave) void linear_few_kernel(Product p) {
     const Store *wrow = static_cast<const Store *>(p.B) + min(n0 + (lane & 15), p.N - 1) * p.ldb;
     const Store *xrow = static_cast<const Store *>(p.A) + min(lane & 15, p.M - 1) * p.lda;
     auto whole = [](const Store *q) { return __builtin_bit_cast(u32x4, *reinterpret_cast<const Pack<Store, int(kElems)> *>(q)); };
+    // the piece at k of the step with the last k: the row's last piece, moved into place
     auto part = [&](const Store *q, uint32_t k) {
-        Pack<Store, int(kElems)> t;
+        if (p.K < kElems) {
+            Pack<Store, int(kElems)> t;
 #pragma unroll
-        for (uint32_t u = 0; u < kElems; ++u) t.v[u] = k + u < p.K ? q[k + u] : Store(0);
-        return __builtin_bit_cast(u32x4, t);
+            for (uint32_t u = 0; u < kElems; ++u) t.v[u] = k + u < p.K ? q[k + u] : Store(0);
+            return __builtin_bit_cast(u32x4, t);
+        }
+        const u32x4 x = whole(q + min(k, p.K - kElems));
+        const uint32_t over = k + kElems > p.K ? k + kElems - p.K : 0;
+        u32x4 v = shift_down(x, over < kElems ? over * uint32_t(sizeof(Store)) * 8 : 0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = over < kElems ? v[e] : 0u;
+        return v;
     };
     const uint32_t chunks = p.K / kChunk;
     f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -766,8 +775,8 @@ __global__ __launch_bounds__(16 * kWave) void linear_few_kernel(Product p) {
             fx[s] = nx[s];
         }
     }
-    if (chunks % waves == w)  // the chunk with the last k, element by element
-        for (uint32_t k = chunks * kChunk; k < p.K; k += kStep) acc = mma<T>(part(wrow, k + at), part(xrow, k + at), acc);
+    for (uint32_t k = chunks * kChunk, s = chunks; k < p.K; k += kStep, ++s)  // the rest, a step a wave
+        if (s % waves == w) acc = mma<T>(part(wrow, k + at), part(xrow, k + at), acc);
     sums[w * kWave + lane] = acc;
     __syncthreads();
     // a lane's 4 sums: columns n0 + 4 (lane / 16) on of token lane % 16
