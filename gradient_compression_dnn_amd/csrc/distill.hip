@@ -328,6 +328,7 @@ __global__ __launch_bounds__(NT) void top_kernel(const typename T::Store *__rest
         if (i < want) {
             const uint64_t e = best[i];
             uint32_t rank = 0;
+#pragma unroll 8
             for (uint32_t j = 0; j < want; ++j) rank += best[j] > e;
             idx[r * k + rank] = static_cast<int32_t>((1u << kColBits) - 1 - (e & ((1u << kColBits) - 1)));
             val[r * k + rank] = key_value(static_cast<uint32_t>(e >> kColBits));
@@ -498,6 +499,12 @@ __global__ __launch_bounds__(NT) void distill_kernel(Distill d) {
         tmax = c != kNone ? fmaxf(tmax, v) : tmax;
     }
     const bool entries = __syncthreads_or(there);
+    bool own_label = label != kNone;  // no entry names it
+    if (own_label && entries) {
+        bool named_here = my_col == label;
+        for (uint32_t e = t + NT; e < K; e += NT) named_here = named_here || col[e] == label;
+        own_label = !__syncthreads_or(named_here);
+    }
     if (weight == 0.0f || !(entries || label != kNone)) {  // the row counts for nothing
         if (t == 0) d.loss[r] = 0.0f;
         if (out)
@@ -528,23 +535,27 @@ __global__ __launch_bounds__(NT) void distill_kernel(Distill d) {
         qsum = d.rest ? qsum : 1.0;
         for (uint32_t e = t; e < K; e += NT) q[e] = q[e] * inv;
         __syncthreads();
-        // a column's first entry holds the sum of all of them, the others a negative number
+        // A column's first entry holds the sum of all of them, the others a negative number.  An entry meets itself
+        // without a branch: with one, each lane of a wave took it at another time (64 entries: 5 us of a row's 16).
         for (uint32_t e = t; e < K; e += NT) {
             const uint32_t c = col[e];
-            float sum = 0.0f;
-            bool first = c != kNone;
-            if (first)
+            float sum = q[e];
+            uint32_t before = 0;  // entries of this column in front of e
+            if (c != kNone)
+#pragma unroll 4
                 for (uint32_t j = 0; j < K4; j += 4) {
                     const uint4 o = *reinterpret_cast<const uint4 *>(col + j);
-                    if (o.x == c || o.y == c || o.z == c || o.w == c)
-#pragma unroll
-                        for (uint32_t u = 0; u < 4; ++u)
-                            if ((u == 0 ? o.x : u == 1 ? o.y : u == 2 ? o.z : o.w) == c) {
-                                first = first && j + u >= e;
-                                sum = sum + q[j + u];
-                            }
+                    const uint32_t self = e - j;  // below 4 in this piece
+                    const bool x = o.x == c && self != 0, y = o.y == c && self != 1, z = o.z == c && self != 2, w = o.w == c && self != 3;
+                    if (x || y || z || w) {
+                        sum = sum + (x ? q[j] : 0.0f);
+                        sum = sum + (y ? q[j + 1] : 0.0f);
+                        sum = sum + (z ? q[j + 2] : 0.0f);
+                        sum = sum + (w ? q[j + 3] : 0.0f);
+                        before += (x && j < e) + (y && j + 1 < e) + (z && j + 2 < e) + (w && j + 3 < e);
+                    }
                 }
-            qs[e] = first ? sum : -1.0f;
+            qs[e] = c != kNone && before == 0 ? sum : -1.0f;
         }
         __syncthreads();
     }
@@ -618,12 +629,7 @@ __global__ __launch_bounds__(NT) void distill_kernel(Distill d) {
             each_own([&](uint32_t e, float x) {
                 if (col[e] != kNone && !(qs[e] < 0.0f)) set(col[e], x, qs[e], false);
             });
-        if (label != kNone && t == NT - 1) {
-            bool own = true;  // no entry names it
-            if (entries)
-                for (uint32_t j = 0; j < K; ++j) own = own && col[j] != label;
-            if (own) set(label, zl, 0.0f, true);
-        }
+        if (own_label && t == NT - 1) set(label, zl, 0.0f, true);
     }
     // the loss, while the gradient is on its way
     float loss = 0.0f;
