@@ -131,6 +131,11 @@ __device__ __forceinline__ float key_value(uint32_t key) {
     return dev_u2f(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
 
+struct Range {
+    float high, low;
+};
+__device__ __forceinline__ Range across(Range x, int d) { return Range{__shfl_xor(x.high, d, kWave), __shfl_xor(x.low, d, kWave)}; }
+
 // The order of entries as one number: the key above, and below it 2^20 - 1 - column.
 constexpr int kColBits = 20;
 static_assert(GC_MAX_VOCAB <= 1u << kColBits, "columns fit");
@@ -186,7 +191,7 @@ __global__ __launch_bounds__(NT) void top_kernel(const typename T::Store *__rest
     constexpr int N = kVec<T>, kAhead = 4;
     __shared__ uint32_t hist[kList > 2048 ? kList : 2048];
     __shared__ uint64_t list[kList], best[kMost];
-    __shared__ float red[NT / kWave];
+    __shared__ Range red[NT / kWave];
     __shared__ Sum sums[NT / kWave];
     __shared__ uint32_t listed, spotted, taken;
     float *tops = reinterpret_cast<float *>(list);  // the sample's maxima, before there is a list
@@ -202,6 +207,11 @@ __global__ __launch_bounds__(NT) void top_kernel(const typename T::Store *__rest
         for (int u = 0; u < N; ++u) v[u] = T::to_f32(x.v[u]);
     };
     // the sample: runs of 64 vectors, spread evenly (single vectors take as many lines of memory as the row has)
+    // the vectors that the row begins and ends in, a thread each
+    const uint32_t cut_at = t == 0 ? 0 : first + whole;
+    const bool cut = t < 2 && (t == 0 ? first == 1 : first + whole < vecs);
+    float cut_v[N];
+    if (cut) load_logits<T>(row, static_cast<int64_t>(cut_at) * N - skew, vocab, cut_v);
     const uint32_t ng = groups < whole ? groups / kWave * kWave : whole;  // at most 2 kList, what tops holds
     float high = -INFINITY, low = INFINITY;
     for (uint32_t g0 = t; g0 < ng; g0 += NT * kAhead) {
@@ -222,8 +232,9 @@ __global__ __launch_bounds__(NT) void top_kernel(const typename T::Store *__rest
     }
     if (t == 0) listed = spotted = taken = 0;
     for (uint32_t i = t; i < 2048; i += NT) hist[i] = 0;
-    high = block_max<NT>(high, red);
-    low = -block_max<NT>(-low, red);
+    const Range range = block_reduce<NT>(Range{high, low}, red, [](Range a, Range b) { return Range{fmaxf(a.high, b.high), fminf(a.low, b.low)}; });
+    high = range.high;
+    low = range.low;
     // bins of the distance from the largest; its order is the values' reversed
     const float per = 2047.0f / (high - low);
     const bool usable = high < INFINITY && per > 0.0f && per < INFINITY;
@@ -256,26 +267,15 @@ __global__ __launch_bounds__(NT) void top_kernel(const typename T::Store *__rest
         }
         if (lse) add_terms(sum, c2, v, m);
     };
-    uint32_t at = first + t;
-    for (; at + (kAhead - 1) * NT < first + whole; at += NT * kAhead) {
+    for (uint32_t at = first + t, end = first + whole; at < end; at += NT * kAhead) {
         float v[kAhead][N];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) inside(at + i * NT, v[i]);
+        for (int i = 0; i < kAhead; ++i) inside(min(at + i * NT, end - 1), v[i]);
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) look(at + i * NT, v[i]);
+        for (int i = 0; i < kAhead; ++i)
+            if (at + i * NT < end) look(at + i * NT, v[i]);
     }
-    for (; at < first + whole; at += NT) {
-        float v[N];
-        inside(at, v);
-        look(at, v);
-    }
-    // the vectors that the row begins and ends in
-    if (t < 2 && (t == 0 ? first == 1 : first + whole < vecs)) {
-        float v[N];
-        at = t == 0 ? 0 : first + whole;
-        load_logits<T>(row, static_cast<int64_t>(at) * N - skew, vocab, v);
-        look(at, v);
-    }
+    if (cut) look(cut_at, cut_v);
     if (lse) {
         sum = block_join<NT>(sum, c2, sums);
         if (t == 0) lse[r] = base(sum) * scale + logf(sum.s);
