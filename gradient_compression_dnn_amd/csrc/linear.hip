@@ -73,21 +73,33 @@ gc_status check_rows(const char *fn, const void *p, uint64_t stride, uint64_t n,
 }
 
 // ------------------------------------------------------------- the cut
-// A product is cut into tiles, and where they do not fill the chip, into parts
-// of the common index as well; the choice is the least of a model of the time.
+// A product is cut into tiles, and where those do not fill the chip, into parts of the common index as well; the
+// choice is the least of a model of the time.  Its costs are fitted to sweeps over shapes and parts of 26 products
+// from 1 to 8,192 tokens (bf16 with 512 x 4096 x 4096: 128 tiles in 4 parts 31 us, in 2 32, in 8 37; 2048 x 4096 x
+// 4096: 128 x 128 65 us, 256 x 256 92; 8192 x 4096 x 16384: 1,152 and 944).
 struct ShapeModel {
     TileShape shape;
     uint32_t tm, tn, slots;   // workgroups that run at once
-    double stage16, stage32;  // us a stage of 128 bytes of k, with every slot busy
+    double stage16, stage32;  // us a stage of 128 bytes of k, with every slot busy; 0: not for the type
+    uint32_t parts;           // at most
 };
 constexpr ShapeModel kShapes[] = {
-    {kBig, Big::kTM, Big::kTN, 256, 2.0, 0.0},  // not for fp32
-    {kMid, Mid::kTM, Mid::kTN, 512, 1.3, 1.7},
-    {kThin, Thin::kTM, Thin::kTN, 1024, 1.3, 3.0},
+    {kBig, Big::kTM, Big::kTN, 256, 2.0, 0.0, 1},  // in parts it was never the fastest
+    {kMid, Mid::kTM, Mid::kTN, 512, 1.3, 1.7, 32},
+    {kThin, Thin::kTM, Thin::kTN, 1024, 1.3, 3.0, 32},
 };
 constexpr double kTileUs = 3.0, kJoinUs = 4.0, kPartialBytesPerUs = 4e6;
-constexpr uint32_t kMaxParts = 32, kThinTokens = 64;
+constexpr uint32_t kThinTokens = 64;
 constexpr uint64_t kFewRows = 1024, kFewOutputs = 1 << 16;
+
+uint32_t stages_of(int type, uint32_t K) { return static_cast<uint32_t>(ceil_div(K, 128 / type_bytes(type))); }
+
+// Whether a kind of product takes a shape.
+bool takes(const ShapeModel &s, Kind kind, int type, uint32_t M, bool any) {
+    if (any) return s.shape == kMid;
+    if (s.shape == kThin) return kind != kWeight && M <= kThinTokens;
+    return s.shape == kMid || type != GC_F32;
+}
 
 Cut plan_cut(Kind kind, int type, uint32_t M, uint32_t N, uint32_t K, bool any) {
     Cut best{};
@@ -104,12 +116,11 @@ Cut plan_cut(Kind kind, int type, uint32_t M, uint32_t N, uint32_t K, bool any) 
         return best;
     }
     double least = 0.0;
-    const uint32_t stages = static_cast<uint32_t>(ceil_div(K, 128 / type_bytes(type)));
+    const uint32_t stages = stages_of(type, K);
     for (const ShapeModel &s : kShapes) {
-        if ((s.shape != kMid && any) || (s.shape == kBig && type == GC_F32)) continue;
-        if (s.shape == kThin && (kind == kWeight || M > kThinTokens)) continue;
+        if (!takes(s, kind, type, M, any)) continue;
         const uint64_t tm = ceil_div(M, s.tm), tn = ceil_div(N, s.tn), tiles = tm * tn;
-        for (uint32_t parts = 1; parts <= std::min(kMaxParts, std::max(stages, 1u)); ++parts) {
+        for (uint32_t parts = 1; parts <= std::min(s.parts, std::max(stages, 1u)); ++parts) {
             if (parts > 1 && tiles * parts > s.slots) break;
             const uint32_t per = static_cast<uint32_t>(ceil_div(stages, parts));
             if (parts > 1 && static_cast<uint64_t>(per) * (parts - 1) >= stages) continue;  // a part without stages
@@ -131,26 +142,38 @@ Cut plan_cut(Kind kind, int type, uint32_t M, uint32_t N, uint32_t K, bool any) 
 
 const ShapeModel &model_of(const Cut &c) { return kShapes[c.shape == kBig ? 0 : c.shape == kMid ? 1 : 2]; }
 
-// Lays the parts' sums out in the workspace; the bytes it needs.
-size_t cut_ws(Cut &c, void *ws) {
+// Lays the parts' sums out in the workspace.
+void cut_ws(Cut &c, void *ws) {
+    if (c.parts == 1 || c.shape == kFew) return;
     const ShapeModel &s = model_of(c);
     WsCursor at(ws);
-    if (c.parts > 1 && c.shape != kFew) {
-        c.partial = at.take<float>(static_cast<size_t>(c.tiles_m) * c.tiles_n * c.parts * s.tm * s.tn);
-        c.colsums = at.take<float>(static_cast<size_t>(c.parts) * c.tiles_m * s.tm);
-    }
-    return at.used + 256;  // room to round the base up to 256 bytes
+    c.partial = at.take<float>(static_cast<size_t>(c.tiles_m) * c.tiles_n * c.parts * s.tm * s.tn);
+    c.colsums = at.take<float>(static_cast<size_t>(c.parts) * c.tiles_m * s.tm);
 }
 
+// Bytes that hold the parts of every batch of up to n tokens (a smaller one may be cut into more).
 size_t workspace_bytes(const gc_linear *l, uint32_t cols, uint64_t n) {
+    size_t most = 0;
     const uint32_t n32 = static_cast<uint32_t>(n);
-    size_t most = 256;
-    if (!n) return most;
-    for (bool any : {false, true})
-        for (Cut c : {plan_cut(kForward, l->type, n32, l->rows, cols, any), plan_cut(kInput, l->type, n32, cols, l->rows, any),
-                      plan_cut(kWeight, l->type, l->rows, cols, n32, any)})
-            most = std::max(most, cut_ws(c, nullptr));
-    return most;
+    auto product = [&](Kind kind, uint32_t M, uint32_t N, uint32_t K) {
+        const uint32_t stages = stages_of(l->type, K);
+        for (const ShapeModel &s : kShapes) {
+            const uint32_t parts = std::min(s.parts, stages);
+            if (parts < 2 || !takes(s, kind, l->type, kind == kWeight ? M : 1, false)) continue;
+            const uint64_t tiles = ceil_div(std::min(M, s.shape == kThin ? kThinTokens : M), s.tm) * ceil_div(N, s.tn);
+            const uint64_t units = umin64(tiles * parts, s.slots);  // no more are ever cut
+            WsCursor at(nullptr);
+            (void)at.take<float>(units * s.tm * s.tn);
+            (void)at.take<float>(units * s.tm);
+            most = std::max(most, at.used);
+        }
+    };
+    if (n) {
+        product(kForward, n32, l->rows, cols);
+        product(kInput, n32, cols, l->rows);
+        product(kWeight, l->rows, cols, n32);
+    }
+    return most + 256;  // room to round the base up to 256 bytes
 }
 
 void *align256(void *p) {
@@ -172,7 +195,7 @@ gc_status launch(const char *fn, Kind kind, int type, const Product &p, void *ws
     c.mode = mode;
     const uint64_t groups = c.shape == kFew ? c.tiles_n : ceil_div(p.M, model_of(c).tm) * ceil_div(p.N, model_of(c).tn);
     if (groups > max_grid(1024)) return fail(fn, GC_ERANGE, "more workgroups than a launch has");
-    (void)cut_ws(c, align256(ws));
+    cut_ws(c, align256(ws));
     if (type == GC_F32) return linear_launch<F32>(fn, kind, p, c, stream);
     if (type == GC_BF16) return linear_launch<BF16>(fn, kind, p, c, stream);
     return linear_launch<F16>(fn, kind, p, c, stream);

@@ -804,9 +804,11 @@ gc_status launch_shape(const char *fn, const Product &p, const Cut &c, hipStream
     if constexpr (std::is_same<S, Mid>::value)
         if (c.mode == kAny) kernel = linear_kernel<T, kKind, S, kAny>;
     GC_LAUNCH("linear_product", stream, kernel<<<grid, C::kThreads, 0, stream>>>(p, c));
-    if (c.parts > 1) {
-        const unsigned joins = c.tiles_m * c.tiles_n * (C::kWaves * C::kRA * C::kRB / kWaves);
-        GC_LAUNCH("linear_join", stream, linear_join_kernel<T, kKind, S><<<joins, kBlock, 0, stream>>>(p, c));
+    if constexpr (!std::is_same<S, Big>::value) {  // whole tiles only
+        if (c.parts > 1) {
+            const unsigned joins = c.tiles_m * c.tiles_n * (C::kWaves * C::kRA * C::kRB / kWaves);
+            GC_LAUNCH("linear_join", stream, linear_join_kernel<T, kKind, S><<<joins, kBlock, 0, stream>>>(p, c));
+        }
     }
     const hipError_t e = hipGetLastError();
     return e == hipSuccess ? GC_OK : hip_error(e, fn);

@@ -795,8 +795,9 @@ typedef struct gc_linear {
     uint32_t reserved[2];   /* must be 0                                        */
 } gc_linear;
 
-/* Device workspace bytes of the three calls below for up to n_tokens rows (0
- * on an argument error).  Calls that run one after the other can share one. */
+/* Device workspace bytes of the three calls below for any batch of up to
+ * n_tokens rows (0 on an argument error): the parts of sums that are cut, at most
+ * 33 MiB.  Calls that run one after the other can share one. */
 size_t gc_linear_workspace_bytes(const gc_plan *plan, const gc_linear *layer, uint64_t n_tokens);
 
 /*

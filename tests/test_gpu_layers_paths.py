@@ -84,6 +84,28 @@ def test_the_same_bits_again_and_in_any_workspace(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,cols", [(700, 3000), (64, 20000), (5000, 300)])
+def test_a_workspace_serves_every_smaller_batch(rows, cols, dtype):
+    """Smaller batches may be cut into more parts; the bytes for the largest hold them."""
+    L = Layer(rows, cols, dtype, 0, True)
+    most = 3000
+    need = B.gc_linear_workspace_bytes(L.plan, L.layer, most)
+    guard = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    ws = guard[:need]
+    for n in (1, 5, 16, 17, 64, 65, 100, 128, 129, 300, 512, 1000, 2048, most):
+        assert B.gc_linear_workspace_bytes(L.plan, L.layer, n) <= need
+        x, dz = normal(n, cols, 1).to(DTYPES[dtype]), normal(n, rows, 2).to(DTYPES[dtype])
+        y, dx, g = torch.empty_like(dz), torch.empty_like(x), torch.zeros(L.plan.n_total, device="cuda")
+        B.gc_linear_forward(L.plan, L.layer, L.w, x, y, ws)
+        B.gc_linear_grad_input(L.plan, L.layer, L.w, dz, dx, ws)
+        B.gc_linear_grad_weight(L.plan, L.layer, dz, x, g, False, ws)
+        within(y, x.double() @ L.weights().double().T + L.bias().double(), 1.1 * sum_bound(x.double(), L.weights().double().T, cols) + 8 * U32, DTYPES[dtype], "y")
+        within(dx, dz.double() @ L.weights().double(), sum_bound(dz.double(), L.weights().double(), rows), DTYPES[dtype], "dx")
+        within(L.weights(g), dz.double().T @ x.double(), sum_bound(dz.double().T, x.double(), n), torch.float32, "g")
+    assert bool((guard[need:] == 0x5A).all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_rows_far_apart(dtype):
     """Offsets past 2^32 bytes and elements: every array's rows 2^31 + 8 elements apart."""
     D = DTYPES[dtype]
@@ -205,3 +227,11 @@ def test_outlier_columns_in_fp32():
     keep = torch.arange(rows, device="cuda") != 11
     assert bool((torch.isnan(y[3]) | (y[3] == float("inf"))).all()) and bool((torch.isnan(y[4]) | (y[4] == float("-inf"))).all())
     assert bool((y[5, keep] > 1e38).all()) and bool(torch.isfinite(y[5]).all()) and bool(torch.isfinite(y[6:]).all())
+
+
+def test_more_entries_than_columns():
+    z = torch.tensor([[1.0, 3.0, 2.0, -float("inf"), 3.0]], device="cuda")
+    idx, val = torch.empty(1, 9, dtype=torch.int32, device="cuda"), torch.empty(1, 9, device="cuda")
+    B.gc_top_logits(z, idx, val)
+    assert idx.tolist() == [[1, 4, 2, 0, -1, -1, -1, -1, -1]]
+    assert val.tolist() == [[3.0, 3.0, 2.0, 1.0] + [-float("inf")] * 5]
