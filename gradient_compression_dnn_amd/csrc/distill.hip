@@ -462,7 +462,7 @@ __global__ __launch_bounds__(NT) void distill_kernel(Distill d) {
     auto entry = [&](uint32_t e, uint32_t &c, float &v) {
         c = kNone;
         v = -INFINITY;
-        if (e >= K || d.kd == 0.0f) return;
+        if (e >= K || d.kd_slope == 0.0f) return;
         const int64_t id = id_at(d.idx, d.id_type, r * d.idx_stride + e);
         v = teacher_value(d, r * d.t_stride + e);
         if (id >= 0 && id < static_cast<int64_t>(V) && v != -INFINITY) c = static_cast<uint32_t>(id);
@@ -592,7 +592,8 @@ __global__ __launch_bounds__(NT) void distill_kernel(Distill d) {
         all2 = join(rest2, block_join<NT>(s2, c2, reds), c2);
         all1 = kTwo ? join(all1, block_join<NT>(s1, c1, reds), c1) : all2;
     }
-    const float r2 = base(all2), r1 = base(all1), rr = base(rest2);
+    // where nothing is left, as for entries that name all columns but masked ones, rr is r2 and rest2.s 0
+    const float r2 = base(all2), r1 = base(all1), rr = rest2.r == -INFINITY ? r2 : rest2.r;
     const float held = rest && rest2.s != 0.0f ? fmaxf(static_cast<float>(1.0 - qsum), 0.0f) : 0.0f;
     if (out) {
         // the gradient: kd T (mass p_j - held p_j / p_r - q_j) + ce (softmax_j - [j = label])
@@ -670,7 +671,7 @@ gc_status check_sizes(const char *fn, int type, uint64_t n, uint32_t vocab, uint
     if (vocab < 1) return fail(fn, GC_EINVAL, "vocab must be at least 1");
     if (vocab > GC_MAX_VOCAB) return fail(fn, GC_ENOTSUP, "vocab must be <= GC_MAX_VOCAB");
     if (k > GC_MAX_TOP_LOGITS) return fail(fn, GC_ENOTSUP, "k must be <= GC_MAX_TOP_LOGITS");
-    const float inverse = 1.0f / temperature;
+    const float inverse = kLog2e / temperature;  // the largest that the kernels form
     if (!(temperature > 0.0f) || !(temperature - temperature == 0.0f) || !(inverse - inverse == 0.0f))
         return fail(fn, GC_EINVAL, "temperature must be positive, and finite with its inverse");
     if (n >= kMaxRows) return fail(fn, GC_ERANGE, "n_rows must be < 2^22");
@@ -757,7 +758,7 @@ extern "C" gc_status gc_distill_loss(const void *logits, int type, uint64_t stri
     }
     Distill d{logits, idx, t, labels, t_lse, weights, loss, dlogits, stride, idx_stride, t_stride, dstride, vocab, k, idx_type, t_type,
               opt->mode == GC_DISTILL_REST, 1.0f / T, kd, opt->kd_weight * T, opt->ce_weight, opt->grad_scale};
-    if (!k) d.kd = 0.0f;
+    if (!k) d.kd = d.kd_slope = 0.0f;
     const size_t lds = 16 * ((size_t(k) + 3) & ~size_t(3)) + (d.rest ? 4 * ((size_t(vocab) + 31) / 32 + 1) : 0);
     const bool two = labels && opt->ce_weight != 0.0f && T != 1.0f;
     hipError_t e = hipSuccess;

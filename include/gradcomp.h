@@ -769,13 +769,16 @@ gc_status gc_muon_step(const gc_matrix_plan *mplan, const float *G, float *U, fl
  * row to the next (at least the row's length; the elements between are neither
  * read nor written).  w is the flat model in that type: the fp32 buffer itself,
  * or a copy of it in bf16 or fp16 with the same offsets.
- * Sums are fp32, over exact products for bf16 and fp16.  For fp32 a product is
+ * Sums are fp32, over exact products for bf16 and fp16 (in their rounding a
+ * subnormal operand counts as the smallest normal one).  For fp32 a product is
  * off by 2^-21 of itself at most, of either sign and by less than 2^-24 on
- * average (three bf16 parts an operand, six products of them; up to 64 tokens of
- * forward and grad_input go by fp32 products); each output is rounded once.  The order of a
- * sum is fixed by the sizes and alignments, so the same call gives the same bits.  NaN and Inf go where the
- * formulas take them, but for an Inf in an fp32 operand, whose sums are NaN or
- * that Inf; no row or column reaches another's results.
+ * average (three bf16 parts an operand, six products of them), and what an
+ * operand has below 2^-133 is dropped; short batches of forward and grad_input
+ * may go by fp32 products instead.  Each output is rounded once.  The order of
+ * a sum is fixed by the sizes and alignments, so the same call gives the same
+ * bits.  NaN and Inf go where the formulas take them, but for an Inf in an fp32
+ * operand, whose sums are NaN or that Inf; no row or column reaches another's
+ * results.
  *
  * Activations: act(z) is z (GC_ACT_NONE), max(z, 0) (RELU; NaN stays),
  * z Phi(z) (GELU; Phi the normal distribution), z s(2 u) with
@@ -873,10 +876,11 @@ gc_status gc_linear_grad_weight(const gc_plan *plan, const gc_linear *layer, con
  *   idx [n_rows][k] out: int32 columns; -1 behind a row's last entry.
  *   val [n_rows][k] out: the logits in fp32 (exact); -Inf there.
  *   lse [n_rows] out, or NULL: log sum_j exp(z_j / temperature) over the whole
- *     row (-Inf where every column is masked, NaN where one is NaN).
+ *     row (-Inf where every column is masked, NaN where one is NaN or +Inf).
  * n_rows == 0 enqueues nothing.
  * Errors: GC_EINVAL (null, unknown type, k = 0, stride < vocab, vocab = 0,
- *         temperature not positive and finite, misaligned buffers), GC_ENOTSUP
+ *         temperature not positive, or it or log2(e) / temperature not finite
+ *         in fp32, misaligned buffers), GC_ENOTSUP
  *         (vocab > GC_MAX_VOCAB, k > GC_MAX_TOP_LOGITS), GC_ERANGE (n_rows >=
  *         2^22, n_rows * stride > 2^48).
  */
@@ -897,11 +901,12 @@ gc_status gc_top_logits(const void *logits, int type, uint64_t stride, uint64_t 
  *   dlogits = grad_scale d loss / d z
  * An entry whose column lies outside [0, vocab), or whose t_k is -Inf, is no
  * entry; without any, or with kd_weight 0, there is no KL term.  Without a
- * label in [0, vocab), or with ce_weight 0, there is no label's term.  A row with neither, or with weight 0, has loss 0 and a
- * gradient of +0, whatever its logits are.  A column that several entries name
- * takes each of them.  A NaN or +Inf in a row that counts makes its loss and its
- * gradient NaN; a masked column's gradient is +-0 unless the teacher or the
- * label names it.
+ * label in [0, vocab), or with ce_weight 0, there is no label's term.  A row with
+ * neither, or with weight 0, has loss 0 and a gradient of +0, whatever its logits
+ * are.  A column that several entries name takes each of them.  In a row that
+ * counts, a NaN or +Inf, or every column masked, makes the loss and the gradient
+ * NaN; a masked column's gradient is +-0 unless the teacher or the label names
+ * it, and if it does the loss is +Inf.
  *   idx [n_rows][idx_stride]: k int32 or int64 (idx_type GC_TOKENS_*); t
  *   [n_rows][t_stride]: k values of t_type; t_lse [n_rows] fp32 for
  *   GC_DISTILL_REST (gc_top_logits writes it, for the same T); labels [n_rows]

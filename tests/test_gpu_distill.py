@@ -285,3 +285,72 @@ def test_no_rows_and_labels_alone():
     B.gc_distill_loss(z, idx, t, B.distill_options(2.0, 1.0, 1.0), loss, dz, labels=lab)
     want_l, want_g = reference(z.double(), idx, t.double(), 2.0, 1.0, 1.0, 1.0, False, None, lab, None)
     assert bool(((loss.double() - want_l).abs() <= 1100 * 2.0 ** -23).all()) and bool(((dz.double() - want_g).abs() <= 1100 * 2.0 ** -23 * want_g.abs() + 4 * U32).all())
+
+
+@pytest.mark.parametrize("middle", [-300.0, 300.0])
+def test_all_columns_left_are_named_far_from_0(middle):
+    """A padded vocabulary whose other columns the entries name, logits far from 0."""
+    V, k = 70, 8
+    z = torch.full((2, V), -INF, device="cuda")
+    idx = torch.tensor([[3, 60, 17, 5, 69, 0, 31, 33]], dtype=torch.int32, device="cuda").repeat(2, 1)
+    z.scatter_(1, idx.long(), middle + torch.randn(2, k, device="cuda"))
+    t = torch.randn(2, k, device="cuda")
+    tlse = torch.logsumexp(t, 1) + 0.25
+    for rest in (False, True):
+        loss, dz = torch.zeros(2, device="cuda"), torch.full_like(z, 9.0)
+        B.gc_distill_loss(z, idx, t, B.distill_options(1.0, tail=rest), loss, dz, t_lse=tlse)
+        want_l, want_g = reference(z.double(), idx, t.double(), 1.0, 1.0, 0.0, 1.0, rest, tlse, None, None)
+        assert bool(((loss.double() - want_l).abs() < 3000 * 2.0 ** -23).all()) and bool(((dz.double() - want_g).abs() < 3000 * 2.0 ** -23).all())
+
+
+def test_rows_with_nothing_to_choose_from():
+    """Every column masked in a row that counts: NaN; +Inf in a row: NaN in its sum as well."""
+    z = torch.full((3, 40), -INF, device="cuda")
+    z[1] = 0.5
+    z[2, :20] = torch.arange(20, device="cuda").float()
+    z[2, 4] = INF
+    idx, t = torch.tensor([[1], [1], [1]], dtype=torch.int32, device="cuda"), torch.zeros(3, 1, device="cuda")
+    for labels in (None, torch.tensor([3, 3, 3], dtype=torch.int32, device="cuda")):
+        loss, dz = torch.zeros(3, device="cuda"), torch.zeros_like(z)
+        B.gc_distill_loss(z, idx, t, B.distill_options(2.0, 1.0, 0.5 if labels is not None else 0.0), loss, dz, labels=labels)
+        for r in (0, 2):
+            assert bool(torch.isnan(loss[r])) and bool(torch.isnan(dz[r]).all())
+        assert bool(torch.isfinite(loss[1])) and bool(torch.isfinite(dz[1]).all())
+    top, val, lse = torch.zeros(3, 2, dtype=torch.int32, device="cuda"), torch.zeros(3, 2, device="cuda"), torch.zeros(3, device="cuda")
+    B.gc_top_logits(z, top, val, lse)
+    assert top.tolist() == [[-1, -1], [0, 1], [4, 19]] and float(lse[0]) == -INF and bool(torch.isfinite(lse[1])) and bool(torch.isnan(lse[2]))
+
+
+@pytest.mark.parametrize("T", [1e-30, 2.0 ** -60, 1e-3])
+def test_low_temperatures(T):
+    """1 / T near the largest float: the softmax is the largest column's."""
+    z = torch.tensor([[1.0, 2.0, -3.0, 2.0]], device="cuda")
+    idx, t = torch.tensor([[0, 2]], dtype=torch.int32, device="cuda"), torch.tensor([[1.0, 4.0]], device="cuda")
+    top, val, lse = torch.zeros(1, 2, dtype=torch.int32, device="cuda"), torch.zeros(1, 2, device="cuda"), torch.zeros(1, device="cuda")
+    B.gc_top_logits(z, top, val, lse, temperature=T)
+    assert top.tolist() == [[1, 3]] and abs(float(lse) * T - 2.0) < 1e-2
+    loss, dz = torch.zeros(1, device="cuda"), torch.full_like(z, 9.0)
+    B.gc_distill_loss(z, idx, t, B.distill_options(T, 1.0, 0.0, 1.0), loss, dz)
+    want = T * torch.tensor([0.0, 0.5, -1.0, 0.5], dtype=torch.float64, device="cuda")
+    assert bool(((dz.double()[0] - want).abs() <= 8 * U32 * T).all()), dz
+
+
+def test_a_captured_call_with_many_columns():
+    """More LDS than a launch has by itself, under capture."""
+    n, V, k = 2, 600001, 5
+    z = torch.randn(n, V, device="cuda")
+    idx, t = torch.randint(0, V, (n, k), device="cuda"), torch.randn(n, k, device="cuda")
+    tlse = torch.logsumexp(t, 1) + 0.5
+    opt = B.distill_options(2.0, tail=True)
+    want_l, want = torch.zeros(n, device="cuda"), torch.zeros_like(z)
+    loss, dz = torch.zeros_like(want_l), torch.zeros_like(z)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.gc_distill_loss(z, idx, t, opt, loss, dz, t_lse=tlse)
+    for i in range(3):
+        z.mul_(0.9)
+        t.add_(0.125)
+        loss.zero_(), dz.zero_()
+        graph.replay()
+        B.gc_distill_loss(z, idx, t, opt, want_l, want, t_lse=tlse)
+        assert torch.equal(loss, want_l) and torch.equal(dz, want)

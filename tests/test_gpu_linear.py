@@ -275,3 +275,27 @@ def test_residual_in_place_and_batches_of_more_dimensions():
         outs.append((dx, dzx))
     for o in outs[1:]:
         assert torch.equal(o[0], outs[0][0]) and torch.equal(o[1], outs[0][1])
+
+
+@pytest.mark.parametrize("n", [3, 40, 300])
+@pytest.mark.parametrize("dtype,scale", [("f16", 2.0 ** -20), ("bf16", 2.0 ** -128), ("f32", 2.0 ** -118), ("f32", 2.0 ** -130)])
+def test_gradients_of_subnormal_size(dtype, scale, n):
+    """The sums keep operands below the smallest normal value; an fp32 operand is held to 2^-133.  A matrix
+    instruction aligns the terms of its sum by their factors' exponents, where a subnormal factor has the smallest
+    normal one: its term is cut as one of that size (3 terms of fp16: 1 x 2^-24 times 3 stands as 2^-14 times 3, cut
+    at 2^-13 2^-24).  So sizes count factors of at least that."""
+    rows, cols = 48, 200
+    L = Layer(rows, cols, dtype, 0, True)
+    D = DTYPES[dtype]
+    dz, x = (normal(n, rows, 2).double() * scale).to(D), normal(n, cols, 3).to(D)
+    dx, g = torch.empty(n, cols, dtype=D, device="cuda:0"), torch.zeros(L.plan.n_total, device="cuda:0")
+    B.gc_linear_grad_input(L.plan, L.layer, L.w, dz, dx, L.ws(n))
+    B.gc_linear_grad_weight(L.plan, L.layer, dz, x, g, False, L.ws(n))
+    held = 2.0 ** -133 if dtype == "f32" else 0.0
+    step = 2.0 ** -150 if dtype != "f16" else 2.0 ** -25  # half the distance of subnormal results
+    one = torch.ones_like(dz.double())
+    for got, a, b, k, s in ((dx, dz.double(), L.weights().double(), rows, step if dtype != "bf16" else 2.0 ** -134),
+                            (L.weights(g), dz.double().T, x.double(), n, 2.0 ** -150), (L.bias(g)[:, None], dz.double().T, one[:, :1], n, 2.0 ** -150)):
+        want, size = a @ b, a.abs().clamp(min=torch.finfo(D).smallest_normal if dtype != "f32" else 0.0) @ b.abs()
+        room = (k + 8) * (U32 if dtype != "f32" else 2 * U32) * size + 2.0 ** -21 * (dtype == "f32") * size + held * b.abs().sum(0) + (k + 1) * 2.0 ** -149
+        assert bool(((got.double() - want).abs() <= room + half_step(got.dtype) * (want.abs() + room) + s).all()), (dtype, scale, float(((got.double() - want).abs() / room).max()))

@@ -139,7 +139,7 @@ def test_act_grad_refusals(kw, code):
     (dict(type=3), B.GC_EINVAL), (dict(k=0), B.GC_EINVAL), (dict(k=1025), B.GC_ENOTSUP), (dict(vocab=0), B.GC_EINVAL),
     (dict(vocab=(1 << 20) + 1, stride=1 << 21), B.GC_ENOTSUP), (dict(stride=99), B.GC_EINVAL), (dict(n=1 << 22), B.GC_ERANGE),
     (dict(stride=1 << 47), B.GC_ERANGE), (dict(t=0.0), B.GC_EINVAL), (dict(t=-1.0), B.GC_EINVAL), (dict(t=NAN), B.GC_EINVAL),
-    (dict(t=INF), B.GC_EINVAL), (dict(t=1e-40), B.GC_EINVAL), (dict(z=None), B.GC_EINVAL), (dict(idx=None), B.GC_EINVAL),
+    (dict(t=INF), B.GC_EINVAL), (dict(t=1e-40), B.GC_EINVAL), (dict(t=3.2e-39), B.GC_EINVAL), (dict(z=None), B.GC_EINVAL), (dict(idx=None), B.GC_EINVAL),
     (dict(val=None), B.GC_EINVAL), (dict(z=P(1)), B.GC_EINVAL), (dict(idx=P(2)), B.GC_EINVAL), (dict(val=P(2)), B.GC_EINVAL),
     (dict(lse=P(2)), B.GC_EINVAL), (dict(n=0, z=None), B.GC_OK),
 ])
