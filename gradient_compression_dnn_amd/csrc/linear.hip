@@ -12,7 +12,7 @@ namespace gc {
 
 namespace {
 
-// dz = dy act'(z): 8 elements a thread.  Memory bounds it.
+// dz = dy act'(z): 8 elements a thread.  Memory bounds it: 6 bytes an element of bf16.
 constexpr int kActCols = 8;
 template <class T>
 __global__ __launch_bounds__(kBlock) void act_grad_kernel(const void *dy, uint64_t ldy, const void *z, uint64_t ldz, int act,
@@ -74,21 +74,23 @@ gc_status check_rows(const char *fn, const void *p, uint64_t stride, uint64_t n,
 
 // ------------------------------------------------------------- the cut
 // A product is cut into tiles, and where those do not fill the chip, into parts of the common index as well; the
-// choice is the least of a model of the time.  Its costs are fitted to sweeps over shapes and parts of 26 products
-// from 1 to 8,192 tokens (bf16 with 512 x 4096 x 4096: 128 tiles in 4 parts 31 us, in 2 32, in 8 37; 2048 x 4096 x
-// 4096: 128 x 128 65 us, 256 x 256 92; 8192 x 4096 x 16384: 1,152 and 944).
+// choice is the least of a model of the time.  Its costs are fitted to sweeps over shapes and parts of 59 products
+// from 1 to 8,192 tokens, where it is within 10% of the fastest (bf16 with 512 x 4096 x 4096: 128 tiles in 4 parts 31 us, in 2 32, in 8 37; 2048 x 4096 x
+// 4096: 128 x 128 65 us, 256 x 256 92; 8192 x 4096 x 16384: 1,152 and 944; weight gradient 4100 x 4100 of 1024
+// tokens, 1,089 tiles and 289: 59 and 74).
 struct ShapeModel {
     TileShape shape;
     uint32_t tm, tn, slots;   // workgroups that run at once
     double stage16, stage32;  // us a stage of 128 bytes of k, with every slot busy; 0: not for the type
+    double half16, half32;    // what is left of that with half of the slots busy at most
     uint32_t parts;           // at most
 };
 constexpr ShapeModel kShapes[] = {
-    {kBig, Big::kTM, Big::kTN, 256, 2.0, 0.0, 1},  // in parts it was never the fastest
-    {kMid, Mid::kTM, Mid::kTN, 512, 1.3, 1.7, 32},
-    {kThin, Thin::kTM, Thin::kTN, 1024, 1.3, 3.0, 32},
+    {kBig, Big::kTM, Big::kTN, 256, 2.0, 0.0, 1.0, 1.0, 1},  // in parts it was never the fastest
+    {kMid, Mid::kTM, Mid::kTN, 512, 1.3, 1.7, 0.75, 1.0, 32},
+    {kThin, Thin::kTM, Thin::kTN, 1024, 1.3, 3.0, 0.65, 0.65, 32},
 };
-constexpr double kTileUs = 3.0, kJoinUs = 4.0, kPartialBytesPerUs = 4e6;
+constexpr double kTileUs = 3.0, kJoinUs = 2.0, kPartialBytesPerUs = 4e6;
 constexpr uint32_t kThinTokens = 64;
 constexpr uint64_t kFewRows = 1024, kFewOutputs = 1 << 16;
 
@@ -105,7 +107,7 @@ Cut plan_cut(Kind kind, int type, uint32_t M, uint32_t N, uint32_t K, bool any) 
     Cut best{};
     // Few tokens: every 16 rows of W read all of x, so a longer batch over many rows goes by tiles (us, few and
     // tiles: 1 x 16384 rows x 4096 columns 26 and 29, 16 x 4096 x 4096 10.0 and 11.7, 16 x 16384 x 4096 35 and 29).
-    // Few rows of W as well leave most of the chip idle: 15 x 81 x 5398 18 and 10.
+    // Few rows of W as well leave most of the chip idle: 15 x 81 x 5398 18 and 7.6.
     if (kind == kForward && M <= 16 && (M <= 4 || (N >= kFewRows && static_cast<uint64_t>(M) * N <= kFewOutputs))) {
         const uint64_t chunks = ceil_div(static_cast<uint64_t>(K) * type_bytes(type), 256);
         best.shape = kFew;
@@ -124,7 +126,9 @@ Cut plan_cut(Kind kind, int type, uint32_t M, uint32_t N, uint32_t K, bool any) 
             if (parts > 1 && tiles * parts > s.slots) break;
             const uint32_t per = static_cast<uint32_t>(ceil_div(stages, parts));
             if (parts > 1 && static_cast<uint64_t>(per) * (parts - 1) >= stages) continue;  // a part without stages
-            double us = static_cast<double>(ceil_div(tiles * parts, s.slots)) * (per * (type == GC_F32 ? s.stage32 : s.stage16) + kTileUs);
+            const uint64_t rounds = ceil_div(tiles * parts, s.slots), last = tiles * parts - (rounds - 1) * s.slots;
+            const double stage = type == GC_F32 ? s.stage32 : s.stage16, half = 2 * last > s.slots ? 1.0 : type == GC_F32 ? s.half32 : s.half16;
+            double us = per * stage * (static_cast<double>(rounds - 1) + half) + kTileUs * static_cast<double>(rounds);
             if (parts > 1) us += kJoinUs + 2.0 * static_cast<double>(tiles * parts) * s.tm * s.tn * 4 / kPartialBytesPerUs;
             if (best.per == 0 || us < least) {
                 least = us;
