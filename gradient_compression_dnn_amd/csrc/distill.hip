@@ -20,7 +20,7 @@ constexpr int kVec = 16 / int(sizeof(typename T::Store));
 
 // How many elements a row's first one is past 16 bytes.  Vectors are cut there, so that they are aligned wherever
 // the row starts: column v N - skew on is vector v (4096 rows of 131071 bf16, which start anywhere: 600 us for
-// the loss with its gradient by unaligned vectors, 467 for 131072).
+// the loss with its gradient by unaligned vectors, 506 by these).
 template <class T>
 __device__ __forceinline__ uint32_t skew_of(const typename T::Store *row) {
     return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) / sizeof(typename T::Store)) % kVec<T>;
@@ -181,9 +181,14 @@ __device__ __forceinline__ void select_entries(uint32_t want, Each each, uint32_
 
 // The top k of a row.  A bound under the k-th largest comes from a sample: the maxima of vectors spread over the
 // row; k of those are above it.  One pass then notes the vectors with an element above the bound, with the sums
-// beside it (their elements at once, with an atomic each: 350 us at 4096 x 131072, where the loss takes 213); the elements' top k are found digit by digit and ranked by counting.  A row that fills the list (many ties, a sample that
-// misses the large ones) is read again, digit by digit.  The sample is chosen so that half of the list is
-// expected to fill.  Memory bounds the pass, with several rows a unit; a few rows take 1,024 threads each.
+// beside it (their elements at once, with an atomic each: 350 us at 4096 x 131072 bf16, k = 64, where this takes
+// 243); the elements' top k are found digit by digit and ranked by counting.  A row that fills the list (many ties,
+// a sample that misses the large ones) is read again, digit by digit.  The sample is chosen so that half of the
+// list is expected to fill at most.
+// Memory bounds the pass, with several rows a unit: 243 us are 4.4 TB/s, where a copy reaches 5.1.  A few rows, and
+// long lists, take 1,024 threads each (4096 x 131071, k = 1024: 608 us, and 1,010 with 256 threads; one row of
+// 131071, k = 64: 22 us, the latency of its 4 rounds of loads and 5 digits).
+constexpr uint32_t kRanked = 256;
 template <class T, int NT, uint32_t kList, uint32_t kMost>
 __global__ __launch_bounds__(NT) void top_kernel(const typename T::Store *__restrict__ logits, uint64_t stride, uint32_t vocab,
                                                  uint32_t k, uint32_t groups, float scale, int32_t *__restrict__ idx,
@@ -206,12 +211,12 @@ __global__ __launch_bounds__(NT) void top_kernel(const typename T::Store *__rest
 #pragma unroll
         for (int u = 0; u < N; ++u) v[u] = T::to_f32(x.v[u]);
     };
-    // the sample: runs of 64 vectors, spread evenly (single vectors take as many lines of memory as the row has)
     // the vectors that the row begins and ends in, a thread each
     const uint32_t cut_at = t == 0 ? 0 : first + whole;
     const bool cut = t < 2 && (t == 0 ? first == 1 : first + whole < vecs);
     float cut_v[N];
     if (cut) load_logits<T>(row, static_cast<int64_t>(cut_at) * N - skew, vocab, cut_v);
+    // the sample: runs of 64 vectors, spread evenly (single vectors take as many lines of memory as the row has)
     const uint32_t ng = groups < whole ? groups / kWave * kWave : whole;  // at most 2 kList, what tops holds
     float high = -INFINITY, low = INFINITY;
     for (uint32_t g0 = t; g0 < ng; g0 += NT * kAhead) {
@@ -296,7 +301,8 @@ __global__ __launch_bounds__(NT) void top_kernel(const typename T::Store *__rest
     __syncthreads();
     // a list of fewer than k holds every candidate: a bound has k above it
     const uint32_t n = all_spots ? listed : spotted, want = min(k, n);
-    if (want) {
+    const bool ranked = n <= kRanked;  // few enough to be ranked without being selected first
+    if (!ranked) {
         uint64_t known, prefix;
         auto take = [&](uint64_t e) {
             if ((e & known) >= prefix) best[atomicAdd(&taken, 1u)] = e;  // in any order: ranked below
@@ -324,18 +330,21 @@ __global__ __launch_bounds__(NT) void top_kernel(const typename T::Store *__rest
         }
         __syncthreads();
     }
-    for (uint32_t i = t; i < k; i += NT) {
-        if (i < want) {
-            const uint64_t e = best[i];
-            uint32_t rank = 0;
+    const uint64_t *of = ranked ? list : best;
+    const uint32_t count = ranked ? n : want;
+    for (uint32_t i = t; i < count; i += NT) {
+        const uint64_t e = of[i];
+        uint32_t rank = 0;
 #pragma unroll 8
-            for (uint32_t j = 0; j < want; ++j) rank += best[j] > e;
+        for (uint32_t j = 0; j < count; ++j) rank += of[j] > e;
+        if (rank < want) {
             idx[r * k + rank] = static_cast<int32_t>((1u << kColBits) - 1 - (e & ((1u << kColBits) - 1)));
             val[r * k + rank] = key_value(static_cast<uint32_t>(e >> kColBits));
-        } else {
-            idx[r * k + i] = -1;
-            val[r * k + i] = -INFINITY;
         }
+    }
+    for (uint32_t i = want + t; i < k; i += NT) {
+        idx[r * k + i] = -1;
+        val[r * k + i] = -INFINITY;
     }
 }
 
@@ -347,7 +356,7 @@ struct Distill {
     void *dlogits;
     uint64_t stride, idx_stride, t_stride, dstride;
     uint32_t vocab, k;
-    int id_type, t_type, rest;
+    int id_type, t_type, rest, bits;
     float inv_t, kd, kd_slope, ce, grad;  // 1 / T; kd T^2 and kd T
 };
 
@@ -439,9 +448,14 @@ struct Row {
     }
 };
 
-// A workgroup a row; several rows share a unit, so that one's sums and exponentials run while
-// others are on their way.  LDS: columns, q, q summed over a column's entries, and student logits of the
-// entries, and (GC_DISTILL_REST) a bit per column that an entry names.
+// A workgroup a row; several rows share a unit, so that one's sums and exponentials run while others are on their
+// way (a loop over rows that fetches the next row meanwhile was slower).  The sums run over the row with the maximum
+// beside them, once, and the gradient is formed from the registers that hold it: memory bounds it, one read and one
+// write of the logits.  us, 4096 rows of bf16, k = 64: 131072 columns 466 (a copy's rate: 421), 131071 506 (rows
+// start anywhere), 65536 210, 32000 114; the loss alone at 131071 237 (211).  Labels at another temperature take a
+// second exponential an element: 573.  700 rows of 10000 fp32, k = 32: 22, of which a launch and a row's latency are most.
+// LDS: columns, q, q summed over a column's entries, and student logits of the entries, and (GC_DISTILL_REST, or up
+// to kBitsVocab columns) a bit per column that an entry names.
 // kTwo: the labels' softmax has another temperature than the teacher's.
 template <class T, int NT, int C, bool kMore, bool kTwo>
 __global__ __launch_bounds__(NT) void distill_kernel(Distill d) {
@@ -518,30 +532,32 @@ __global__ __launch_bounds__(NT) void distill_kernel(Distill d) {
     const bool rest = d.rest && entries;
     double qsum = 0.0;
     if (entries) {
-        if (rest)
+        if (d.bits)
             for (uint32_t i = t; i < (V + 31) / 32 + 1; i += NT) named[i] = 0;
         if (!d.rest) tmax = block_max<NT>(tmax, red);
         else __syncthreads();
         tmax = tmax == -INFINITY ? 0.0f : tmax;
         const float tlse = d.rest ? d.t_lse[r] : 0.0f;
+        bool again = !d.bits;  // a column may be named again
         for (uint32_t e = t; e < K; e += NT) {
             const uint32_t c = col[e];
             q[e] = c != kNone ? expf(d.rest ? q[e] * d.inv_t - tlse : (q[e] - tmax) * d.inv_t) : 0.0f;
             qsum += q[e];
-            if (rest && c != kNone) atomicOr(&named[c / 32], 1u << (c % 32));
+            if (d.bits && c != kNone) again = again || (atomicOr(&named[c / 32], 1u << (c % 32)) >> (c % 32) & 1);
         }
         qsum = block_sum<NT>(qsum, redd);
         const float inv = d.rest ? 1.0f : static_cast<float>(1.0 / qsum);
         qsum = d.rest ? qsum : 1.0;
         for (uint32_t e = t; e < K; e += NT) q[e] = q[e] * inv;
-        __syncthreads();
-        // A column's first entry holds the sum of all of them, the others a negative number.  An entry meets itself
-        // without a branch: with one, each lane of a wave took it at another time (64 entries: 5 us of a row's 16).
+        again = __syncthreads_or(again);
+        // A column's first entry holds the sum of all of them, the others a negative number.  Every entry against
+        // every other is left to rows that name a column again (4096 x 131071, 1,024 entries: 878 us, and 634 without).  An
+        // entry meets itself without a branch: with one, each lane of a wave took it at another time.
         for (uint32_t e = t; e < K; e += NT) {
             const uint32_t c = col[e];
             float sum = q[e];
             uint32_t before = 0;  // entries of this column in front of e
-            if (c != kNone)
+            if (c != kNone && again)
 #pragma unroll 4
                 for (uint32_t j = 0; j < K4; j += 4) {
                     const uint4 o = *reinterpret_cast<const uint4 *>(col + j);
@@ -651,6 +667,7 @@ __global__ __launch_bounds__(NT) void distill_kernel(Distill d) {
 // --------------------------------------------------------------- host side
 constexpr uint64_t kMaxRows = uint64_t(1) << 22;
 constexpr uint64_t kFewRows = 256;  // rows that have a unit each
+constexpr uint32_t kBitsVocab = 1u << 18;  // 32 KiB of bits: as many rows a unit as without
 constexpr uint32_t kSmallList = 1024, kBigList = 4096, kSmallK = 128;
 
 size_t type_bytes(int type) { return type == GC_F32 ? 4 : 2; }
@@ -704,17 +721,21 @@ extern "C" gc_status gc_top_logits(const void *logits, int type, uint64_t stride
     auto go = [&](auto t) {
         using T = decltype(t);
         constexpr uint64_t N = kVec<T>;
+        const bool few = n_rows <= kFewRows, small = k <= kSmallK && uint64_t(vocab) * k <= N * kSmallList * kSmallList;
         auto with = [&](auto kernel, int threads, uint64_t room) {
-            // v k / (groups N) of a row are expected above the bound: half of the list
-            const uint64_t groups = ceil_div(std::max<uint64_t>(ceil_div(2 * uint64_t(vocab) * k, N * room), 2 * k), kWave) * kWave;
+            // v k / (groups N) of a row are expected above the bound: half of the list, and for a small k, whose
+            // bound scatters more, k / (2 k + 16) of it (a row in 100 overflowed half of it at k = 8, which took twice
+            // the time: 4096 x 131071 bf16 444 us, and 217 like this); or fewer, as a load a thread costs no time
+            const uint64_t sample = ceil_div((2 * uint64_t(k) + 16) * vocab, N * room);
+            const uint64_t groups = ceil_div(std::max<uint64_t>({sample, 2 * uint64_t(k), few ? uint64_t(threads) : 0}), kWave) * kWave;
             GC_LAUNCH("top_logits", stream,
                       kernel<<<static_cast<unsigned>(n_rows), threads, 0, stream>>>(
                           static_cast<const typename T::Store *>(logits), stride, vocab, k, static_cast<uint32_t>(umin64(groups, 2 * room)),
                           1.0f / temperature, idx, val, lse));
         };
-        const bool few = n_rows <= kFewRows, small = k <= kSmallK && uint64_t(vocab) * k <= N * kSmallList * kSmallList;
-        if (few) small ? with(top_kernel<T, 1024, kSmallList, kSmallK>, 1024, kSmallList) : with(top_kernel<T, 1024, kBigList, GC_MAX_TOP_LOGITS>, 1024, kBigList);
-        else small ? with(top_kernel<T, 256, kSmallList, kSmallK>, 256, kSmallList) : with(top_kernel<T, 256, kBigList, GC_MAX_TOP_LOGITS>, 256, kBigList);
+        if (!small) with(top_kernel<T, 1024, kBigList, GC_MAX_TOP_LOGITS>, 1024, kBigList);
+        else if (few) with(top_kernel<T, 1024, kSmallList, kSmallK>, 1024, kSmallList);
+        else with(top_kernel<T, 256, kSmallList, kSmallK>, 256, kSmallList);
     };
     if (type == GC_F32) go(F32{});
     else if (type == GC_BF16) go(BF16{});
@@ -757,9 +778,10 @@ extern "C" gc_status gc_distill_loss(const void *logits, int type, uint64_t stri
             return fail(fn, GC_EINVAL, "dlogits in place of logits must have their stride");
     }
     Distill d{logits, idx, t, labels, t_lse, weights, loss, dlogits, stride, idx_stride, t_stride, dstride, vocab, k, idx_type, t_type,
-              opt->mode == GC_DISTILL_REST, 1.0f / T, kd, opt->kd_weight * T, opt->ce_weight, opt->grad_scale};
+              opt->mode == GC_DISTILL_REST, 0, 1.0f / T, kd, opt->kd_weight * T, opt->ce_weight, opt->grad_scale};
     if (!k) d.kd = d.kd_slope = 0.0f;
-    const size_t lds = 16 * ((size_t(k) + 3) & ~size_t(3)) + (d.rest ? 4 * ((size_t(vocab) + 31) / 32 + 1) : 0);
+    d.bits = k && (d.rest || vocab <= kBitsVocab);
+    const size_t lds = 16 * ((size_t(k) + 3) & ~size_t(3)) + (d.bits ? 4 * ((size_t(vocab) + 31) / 32 + 1) : 0);
     const bool two = labels && opt->ce_weight != 0.0f && T != 1.0f;
     hipError_t e = hipSuccess;
     auto go = [&](auto kernel, int threads) {

@@ -12,7 +12,7 @@ namespace gc {
 
 namespace {
 
-// dz = dy act'(z): 8 elements a thread.  Memory bounds it: 6 bytes an element of bf16.
+// dz = dy act'(z): 8 elements a thread.  Memory bounds it: 8192 x 16384 bf16 147 us, 5.5 TB/s.
 constexpr int kActCols = 8;
 template <class T>
 __global__ __launch_bounds__(kBlock) void act_grad_kernel(const void *dy, uint64_t ldy, const void *z, uint64_t ldz, int act,
@@ -75,9 +75,9 @@ gc_status check_rows(const char *fn, const void *p, uint64_t stride, uint64_t n,
 // ------------------------------------------------------------- the cut
 // A product is cut into tiles, and where those do not fill the chip, into parts of the common index as well; the
 // choice is the least of a model of the time.  Its costs are fitted to sweeps over shapes and parts of 59 products
-// from 1 to 8,192 tokens, where it is within 10% of the fastest (bf16 with 512 x 4096 x 4096: 128 tiles in 4 parts 31 us, in 2 32, in 8 37; 2048 x 4096 x
-// 4096: 128 x 128 65 us, 256 x 256 92; 8192 x 4096 x 16384: 1,152 and 944; weight gradient 4100 x 4100 of 1024
-// tokens, 1,089 tiles and 289: 59 and 74).
+// from 1 to 8,192 tokens, where it is within 12% of the fastest (us, bf16: 512 x 4096 x 4096, 128 tiles in 4 parts 30,
+// in 2 32, in 8 39; 2048 x 4096 x 4096, 128 x 128 64 and 256 x 256 92; 8192 x 4096 x 16384, 1,152 and 944; the weight
+// gradient of 4100 x 4100 with 1024 tokens, 1,089 tiles and 289: 59 and 74).
 struct ShapeModel {
     TileShape shape;
     uint32_t tm, tn, slots;   // workgroups that run at once
