@@ -182,15 +182,17 @@ __device__ __forceinline__ void select_entries(uint32_t want, Each each, uint32_
 // The top k of a row.  A bound under the k-th largest comes from a sample: the maxima of vectors spread over the
 // row; k of those are above it.  One pass then notes the vectors with an element above the bound, with the sums
 // beside it (their elements at once, with an atomic each: 350 us at 4096 x 131072 bf16, k = 64, where this takes
-// 243); the elements' top k are found digit by digit and ranked by counting.  A row that fills the list (many ties,
-// a sample that misses the large ones) is read again, digit by digit.  The sample is chosen so that half of the
-// list is expected to fill at most.
+// 243); the elements' top k are found digit by digit and ranked by counting.  The sample is chosen so that half of
+// the list is expected to fill at most.  Where it overflows, with large ones side by side, the vectors that were
+// noted are read again, digit by digit (the first 2000 of 131071 columns 9 larger: 221 us, and 803 by the row), and
+// where those are too many (ties, a sample that misses the large ones), the row (all equal: 7.3 ms).
 // Memory bounds the pass, with several rows a unit: 243 us are 4.4 TB/s, where a copy reaches 5.1.  A few rows, and
 // long lists, take 1,024 threads each (4096 x 131071, k = 1024: 608 us, and 1,010 with 256 threads; one row of
-// 131071, k = 64: 22 us, the latency of its 4 rounds of loads and 5 digits).
+// 131071, k = 64: 22 us, the latency of its 4 rounds of loads and 5 digits).  Two of those share a unit, for which
+// the bounds hold the scalar registers as well (without: 452 us where k = 128 takes 316).
 constexpr uint32_t kRanked = 256;
 template <class T, int NT, uint32_t kList, uint32_t kMost>
-__global__ __launch_bounds__(NT) void top_kernel(const typename T::Store *__restrict__ logits, uint64_t stride, uint32_t vocab,
+__global__ __launch_bounds__(NT, NT == 1024 ? 8 : 1) void top_kernel(const typename T::Store *__restrict__ logits, uint64_t stride, uint32_t vocab,
                                                  uint32_t k, uint32_t groups, float scale, int32_t *__restrict__ idx,
                                                  float *__restrict__ val, float *__restrict__ lse) {
     constexpr int N = kVec<T>, kAhead = 4;
@@ -314,8 +316,15 @@ __global__ __launch_bounds__(NT) void top_kernel(const typename T::Store *__rest
             select_entries<NT>(want, each, hist, &known, &prefix);
             each(take);
         } else {
+            // the vectors that were noted, if all of them were, or the row
+            uint32_t *noted = reinterpret_cast<uint32_t *>(list);
+            const uint32_t vectors = all_spots ? spotted : vecs;
+            if (all_spots)
+                for (uint32_t i = t; i < vectors; i += NT) noted[i] = spots[i];
+            __syncthreads();  // the digits are counted where the spots are
             auto each = [&](auto f) {
-                for (uint32_t at = t; at < vecs; at += NT) {
+                for (uint32_t i = t; i < vectors; i += NT) {
+                    const uint32_t at = all_spots ? noted[i] : i;
                     float v[N];
                     load_logits<T>(row, static_cast<int64_t>(at) * N - skew, vocab, v);
 #pragma unroll

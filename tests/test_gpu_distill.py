@@ -354,3 +354,22 @@ def test_a_captured_call_with_many_columns():
         graph.replay()
         B.gc_distill_loss(z, idx, t, opt, want_l, want, t_lse=tlse)
         assert torch.equal(loss, want_l) and torch.equal(dz, want)
+
+
+@pytest.mark.parametrize("n", [3, 300])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_large_logits_side_by_side(n, dtype):
+    """More of them than the sample expects: in few vectors, in too many to note, and where it does not look."""
+    V = 60001
+    g = torch.Generator(device="cuda").manual_seed(n)
+    base = torch.randn(n, V, generator=g, device="cuda")
+    for first, width in ((0, 2000), (40000, 3000), (100, 20000), (59000, 1001), (30011, 450)):
+        z = base.clone()
+        z[:, first:first + width] += 9.0
+        z = z.to(DTYPES[dtype])
+        s, j = torch.sort(z.double() + 0.0, dim=1, descending=True, stable=True)
+        for k in (1, 8, 64, 500):
+            say(f"side by side {n} {dtype} {first} {width} {k}")
+            idx, val = torch.empty(n, k, dtype=torch.int32, device="cuda"), torch.empty(n, k, device="cuda")
+            B.gc_top_logits(z, idx, val)
+            assert torch.equal(idx, j[:, :k].int()) and torch.equal(val.double(), s[:, :k])
