@@ -179,6 +179,8 @@ __device__ __forceinline__ void select_entries(uint32_t want, Each each, uint32_
     *prefix_out = prefix;
 }
 
+constexpr uint32_t kRanked = 256;  // entries that are ranked without a selection
+
 // The top k of a row.  A bound under the k-th largest comes from a sample: the maxima of vectors spread over the
 // row; k of those are above it.  One pass then notes the vectors with an element above the bound, with the sums
 // beside it (their elements at once, with an atomic each: 350 us at 4096 x 131072 bf16, k = 64, where this takes
@@ -190,11 +192,11 @@ __device__ __forceinline__ void select_entries(uint32_t want, Each each, uint32_
 // long lists, take 1,024 threads each (4096 x 131071, k = 1024: 608 us, and 1,010 with 256 threads; one row of
 // 131071, k = 64: 22 us, the latency of its 4 rounds of loads and 5 digits).  Two of those share a unit, for which
 // the bounds hold the scalar registers as well (without: 452 us where k = 128 takes 316).
-constexpr uint32_t kRanked = 256;
 template <class T, int NT, uint32_t kList, uint32_t kMost>
-__global__ __launch_bounds__(NT, NT == 1024 ? 8 : 1) void top_kernel(const typename T::Store *__restrict__ logits, uint64_t stride, uint32_t vocab,
-                                                 uint32_t k, uint32_t groups, float scale, int32_t *__restrict__ idx,
-                                                 float *__restrict__ val, float *__restrict__ lse) {
+__global__ __launch_bounds__(NT, NT == 1024 ? 8 : 1) void top_kernel(const typename T::Store *__restrict__ logits,
+                                                                     uint64_t stride, uint32_t vocab, uint32_t k, uint32_t groups,
+                                                                     float scale, int32_t *__restrict__ idx,
+                                                                     float *__restrict__ val, float *__restrict__ lse) {
     constexpr int N = kVec<T>, kAhead = 4;
     __shared__ uint32_t hist[kList > 2048 ? kList : 2048];
     __shared__ uint64_t list[kList], best[kMost];
@@ -303,7 +305,7 @@ __global__ __launch_bounds__(NT, NT == 1024 ? 8 : 1) void top_kernel(const typen
     __syncthreads();
     // a list of fewer than k holds every candidate: a bound has k above it
     const uint32_t n = all_spots ? listed : spotted, want = min(k, n);
-    const bool ranked = n <= kRanked;  // few enough to be ranked without being selected first
+    const bool ranked = n <= kRanked;
     if (!ranked) {
         uint64_t known, prefix;
         auto take = [&](uint64_t e) {
@@ -462,7 +464,7 @@ struct Row {
 // beside them, once, and the gradient is formed from the registers that hold it: memory bounds it, one read and one
 // write of the logits.  us, 4096 rows of bf16, k = 64: 131072 columns 466 (a copy's rate: 421), 131071 506 (rows
 // start anywhere), 65536 210, 32000 114; the loss alone at 131071 237 (211).  Labels at another temperature take a
-// second exponential an element: 573.  700 rows of 10000 fp32, k = 32: 22, of which a launch and a row's latency are most.
+// second exponential an element: 573.  700 rows of 10000 fp32, k = 32: 22, most of it a launch and a row's latency.
 // LDS: columns, q, q summed over a column's entries, and student logits of the entries, and (GC_DISTILL_REST, or up
 // to kBitsVocab columns) a bit per column that an entry names.
 // kTwo: the labels' softmax has another temperature than the teacher's.
@@ -560,8 +562,8 @@ __global__ __launch_bounds__(NT) void distill_kernel(Distill d) {
         for (uint32_t e = t; e < K; e += NT) q[e] = q[e] * inv;
         again = __syncthreads_or(again);
         // A column's first entry holds the sum of all of them, the others a negative number.  Every entry against
-        // every other is left to rows that name a column again (4096 x 131071, 1,024 entries: 878 us, and 634 without).  An
-        // entry meets itself without a branch: with one, each lane of a wave took it at another time.
+        // every other is left to rows that name a column again (4096 x 131071, 1,024 entries: 878 us, 634 without).
+        // An entry meets itself without a branch: with one, each lane of a wave took it at another time.
         for (uint32_t e = t; e < K; e += NT) {
             const uint32_t c = col[e];
             float sum = q[e];
