@@ -630,10 +630,12 @@ __device__ __forceinline__ void tile_of(uint32_t t, uint32_t tiles_m, uint32_t t
 // A tile a workgroup, or a part of its sum.  Both operands come through LDS in stages of 128 bytes of k, the next
 // one on its way while this one is multiplied; a wave keeps its block of the result in registers, and the epilogue
 // is applied to the fp32 sums before the one rounding.
-//   Matrix instructions bound long batches.  Rates reached, bf16, where the library's product of 8192 x 4096 x
-//   16384 runs at 1.23 PFLOP/s: 256 x 256 (8 waves, one workgroup a unit) 945 us, 1.16 PFLOP/s; 2048 x 4096 x 4096
-//   by 128 x 128 (4 waves, two a unit) 64 us, 1.07 PFLOP/s.  What an epilogue reads and writes is not hidden behind
-//   other tiles' products: GELU and z add 25 us of 945, a residual, z, dx and dzx 215.
+//   Matrix instructions bound long batches, at the clock that the card holds under them (1.8 GHz, 53% of the cycles
+//   busy, a third of the waves' time at the stages' barriers).  bf16, us: 8192 x 4096 x 16384 by 256 x 256 (8 waves,
+//   one workgroup a unit) 870 to 945, 1.16 to 1.26 PFLOP/s, where the library's product takes 711 to 905 by its
+//   operands' order; 2048 x 4096 x 4096 by 128 x 128 (4 waves, two a unit) 64, the library 58.  Four waves of 128 x
+//   128 each took 920 to 1,050, stages of 64 bytes in four buffers 910 to 990.  What an epilogue reads and writes is
+//   not hidden behind other tiles' products: GELU and z add 25, a residual, z, dx and dzx 215.
 //   Operands whose rows are not aligned to 16 bytes go through registers (us, and with aligned ones: 1023 x 4099 x
 //   1501 fp16 31 and 26, 700 x 10000 x 1500 bf16 41 and 37; two stages on their way at once made no difference).
 //   fp32 by planes: 2048 x 4096 x 4096 330 us, 208 TFLOP/s, 1.25 PFLOP/s of the bf16 products that are formed; by
