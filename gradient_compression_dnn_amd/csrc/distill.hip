@@ -6,6 +6,7 @@
 #include <type_traits>
 
 #include "gc_internal.hpp"
+#include "row_vectors.hpp"
 
 namespace gc {
 
@@ -385,24 +386,19 @@ __device__ __forceinline__ float teacher_value(const Distill &d, uint64_t at) {
 template <class T, int NT, int C, bool kMore>
 struct Row {
     static constexpr int N = kVec<T>;
-    static constexpr uint32_t kStep = NT * N;
+    using Vectors = RowVectors<N, NT, C, kMore>;
+    static constexpr uint32_t kStep = Vectors::kStep;
     using Store = typename T::Store;
     const Store *row;
     uint32_t vocab, skew;
     u32x4 raw[C ? C : 1];
 
-    __device__ __forceinline__ int32_t own_column(int i, uint32_t t) const { return static_cast<int32_t>(i * kStep + t * N - skew); }
-    // The vector that the row begins or ends with stands for the one that crosses its start or end, and for those past it.
-    __device__ __forceinline__ int32_t column(int i, uint32_t t) const {
-        const int32_t c = own_column(i, t), in = i ? c : max(c, 0);
-        return kMore ? in : min(in, static_cast<int32_t>(vocab - N));
-    }
     __device__ __forceinline__ u32x4 vector_at(uint32_t c) const {
         return __builtin_bit_cast(u32x4, *reinterpret_cast<const Pack<Store, N> *>(row + c));
     }
     __device__ __forceinline__ void load() {
 #pragma unroll
-        for (int i = 0; i < C; ++i) raw[i] = vector_at(column(i, threadIdx.x));
+        for (int i = 0; i < C; ++i) raw[i] = vector_at(Vectors::column(i, threadIdx.x, skew, vocab));
     }
     // f(column, values, count): columns that another call has already are -Inf for kOnce; count of them exist.
     template <bool kOnce, class F>
@@ -419,9 +415,9 @@ struct Row {
             // not fit the registers
             uint32_t t = threadIdx.x;
             asm volatile("" : "+v"(raw[i]), "+v"(t));
-            const int32_t c = column(i, t), own = own_column(i, t);
+            const int32_t c = Vectors::column(i, t, skew, vocab), own = Vectors::own(i, t, skew);
             values(raw[i]);
-            if (kOnce && (i == 0 || !kMore) && __ballot(c != own))
+            if (kOnce && Vectors::moves(i) && __ballot(c != own))
 #pragma unroll
                 for (int32_t u = 0; u < N; ++u) v[u] = c + u < own || c + u >= own + N ? -INFINITY : v[u];
             if (kMore || kOnce || own < static_cast<int32_t>(vocab)) f(c, v, uint32_t(N));
@@ -806,14 +802,12 @@ extern "C" gc_status gc_distill_loss(const void *logits, int type, uint64_t stri
         constexpr bool kTwo = decltype(is_two)::value;
         // rows that start on 16 bytes, or anywhere
         const bool even = !misaligned(logits, 16) && stride * type_bytes(type) % 16 == 0;
-        const uint64_t vecs = ceil_div(even ? vocab : vocab + kVec<Tp> - 1, kVec<Tp>);
-        // as few threads as hold the row: several rows a unit overlap better than one (us, 4096 rows of 65536 bf16:
-        // 227 with 512 threads, 352 with 1024)
-        if (vocab < uint32_t(kVec<Tp>)) go(distill_kernel<Tp, 256, 0, true, kTwo>, 256);
-        else if (vecs <= 256 * 4) go(distill_kernel<Tp, 256, 4, false, kTwo>, 256);
-        else if (vecs <= 256 * 8) go(distill_kernel<Tp, 256, 8, false, kTwo>, 256);
-        else if (vecs <= 256 * 16) go(distill_kernel<Tp, 256, 16, false, kTwo>, 256);
-        else if (vecs <= 512 * 16) go(distill_kernel<Tp, 512, 16, false, kTwo>, 512);
+        const LossShape s = loss_shape(vocab, kVec<Tp>, even);
+        if (s.held == 0) go(distill_kernel<Tp, 256, 0, true, kTwo>, 256);
+        else if (s.held == 4) go(distill_kernel<Tp, 256, 4, false, kTwo>, 256);
+        else if (s.held == 8) go(distill_kernel<Tp, 256, 8, false, kTwo>, 256);
+        else if (s.threads == 256) go(distill_kernel<Tp, 256, 16, false, kTwo>, 256);
+        else if (!s.more) go(distill_kernel<Tp, 512, 16, false, kTwo>, 512);
         else go(distill_kernel<Tp, 512, 16, true, kTwo>, 512);
     };
     auto of = [&](auto type_tag) {
