@@ -263,8 +263,10 @@ __global__ __launch_bounds__(NT, NT == 1024 ? 8 : 1) void top_kernel(const typen
             limit = static_cast<float>(2048 - block_find_bucket<2048, NT>(k, [&](int b) { return hist[b]; }, &above));
         }
     }
-    const float from = usable ? high : 0.0f, by = usable ? per : 0.0f;
-    // not below the limit: (x - 0) 0 is NaN for +Inf, which passes
+    // without a bound every logit passes: the distance of a very low one could overflow, and is not below an infinite limit
+    const bool bounded = limit < INFINITY;
+    const float from = bounded ? high : 0.0f, by = bounded ? per : 0.0f;
+    // not below the limit: (0 - x) 0 is NaN for +Inf, which passes
     auto passes = [&](float x) { return x > -INFINITY && !((from - x) * by >= limit); };
     __syncthreads();
     const float c2 = scale * kLog2e;
