@@ -657,8 +657,8 @@ __global__ __launch_bounds__(NT) void distill_kernel(Distill d) {
             });
         if (own_label && t == NT - 1) set(label, zl, 0.0f, true);
     }
-    // the loss, while the gradient is on its way
-    float loss = 0.0f;
+    // the loss, while the gradient is on its way; NaN for a row without a distribution, also where no entry has a term
+    float loss = all2.s > 0.0f ? 0.0f : NAN;
     const float log2s = logf(all2.s);
     if (entries) {
         double kl = 0.0;
@@ -667,7 +667,7 @@ __global__ __launch_bounds__(NT) void distill_kernel(Distill d) {
         });
         kl = block_sum<NT>(kl, redd);
         if (held > 0.0f) kl += held * (logf(held) - ((rr - r2) * d.inv_t + logf(rest2.s) - log2s));
-        loss = d.kd * static_cast<float>(kl);
+        loss = loss + d.kd * static_cast<float>(kl);
     }
     if (label != kNone) loss = loss + d.ce * (logf(all1.s) - (kTwo ? zl - r1 : (zl - r1) * d.inv_t));
     if (t == 0) d.loss[r] = weight * loss;
