@@ -21,7 +21,7 @@ constexpr int kVec = 16 / int(sizeof(typename T::Store));
 
 // How many elements a row's first one is past 16 bytes.  Vectors are cut there, so that they are aligned wherever
 // the row starts: column v N - skew on is vector v (4096 rows of 131071 bf16, which start anywhere: 600 us for
-// the loss with its gradient by unaligned vectors, 506 by these).
+// the loss with its gradient by unaligned vectors, 505 by these).
 template <class T>
 __device__ __forceinline__ uint32_t skew_of(const typename T::Store *row) {
     return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) / sizeof(typename T::Store)) % kVec<T>;
@@ -185,12 +185,15 @@ constexpr uint32_t kRanked = 256;  // entries that are ranked without a selectio
 // The top k of a row.  A bound under the k-th largest comes from a sample: the maxima of vectors spread over the
 // row; k of those are above it.  One pass then notes the vectors with an element above the bound, with the sums
 // beside it (their elements at once, with an atomic each: 350 us at 4096 x 131072 bf16, k = 64, where this takes
-// 243); the elements' top k are found digit by digit and ranked by counting.  The sample is chosen so that half of
+// 240); the elements' top k are found digit by digit and ranked by counting.  The sample is chosen so that half of
 // the list is expected to fill at most.  Where it overflows, with large ones side by side, the vectors that were
 // noted are read again, digit by digit (the first 2000 of 131071 columns 9 larger: 221 us, and 803 by the row), and
-// where those are too many (ties, a sample that misses the large ones), the row (all equal: 7.3 ms).
-// Memory bounds the pass, with several rows a unit: 243 us are 4.4 TB/s, where a copy reaches 5.1.  A few rows, and
-// long lists, take 1,024 threads each (4096 x 131071, k = 1024: 608 us, and 1,010 with 256 threads; one row of
+// where those are too many (ties, a sample that misses the large ones), the row (all equal: 7.3 ms).  The bound is
+// one of 2047 equal steps from the sample's largest to its lowest: a finite mask that fills a vector of the sample
+// leaves all other logits in the first of them, and the row is read digit by digit (the last 3% of 131071 columns
+// -1e4: 1.26 ms, the type's lowest value: 1.36, half of them 1.65; as -Inf, which the sample leaves out, 240 us).
+// Memory bounds the pass, with several rows a unit: 240 us are 4.5 TB/s, where a copy reaches 5.1.  A few rows, and
+// long lists, take 1,024 threads each (4096 x 131071, k = 1024: 586 us, and 1,010 with 256 threads; one row of
 // 131071, k = 64: 22 us, the latency of its 4 rounds of loads and 5 digits).  Two of those share a unit, for which
 // the bounds hold the scalar registers as well (without: 452 us where k = 128 takes 316).
 template <class T, int NT, uint32_t kList, uint32_t kMost>
@@ -460,9 +463,10 @@ struct Row {
 // A workgroup a row; several rows share a unit, so that one's sums and exponentials run while others are on their
 // way (a loop over rows that fetches the next row meanwhile was slower).  The sums run over the row with the maximum
 // beside them, once, and the gradient is formed from the registers that hold it: memory bounds it, one read and one
-// write of the logits.  us, 4096 rows of bf16, k = 64: 131072 columns 466 (a copy's rate: 421), 131071 506 (rows
-// start anywhere), 65536 210, 32000 114; the loss alone at 131071 237 (211).  Labels at another temperature take a
-// second exponential an element: 573.  700 rows of 10000 fp32, k = 32: 22, most of it a launch and a row's latency.
+// write of the logits.  us, 4096 rows of bf16, k = 64: 131072 columns 465 (a copy's rate: 421), 131071 505 (rows
+// start anywhere), 65536 213, 32000 118; the loss alone at 131071 235 (211).  Labels at another temperature take a
+// second exponential an element: 605.  700 rows of 10000 fp32, k = 32: 22, most of it a launch, a row's latency and
+// the sums over 16 vectors a thread, of which the row fills 10.
 // LDS: columns, q, q summed over a column's entries, and student logits of the entries, and (GC_DISTILL_REST, or up
 // to kBitsVocab columns) a bit per column that an entry names.
 // kTwo: the labels' softmax has another temperature than the teacher's.
@@ -734,7 +738,7 @@ extern "C" gc_status gc_top_logits(const void *logits, int type, uint64_t stride
         auto with = [&](auto kernel, int threads, uint64_t room) {
             // v k / (groups N) of a row are expected above the bound: half of the list, and for a small k, whose
             // bound scatters more, k / (2 k + 16) of it (a row in 100 overflowed half of it at k = 8, which took twice
-            // the time: 4096 x 131071 bf16 444 us, and 217 like this); or fewer, as a load a thread costs no time
+            // the time: 4096 x 131071 bf16 444 us, and 211 like this); or fewer, as a load a thread costs no time
             const uint64_t sample = ceil_div((2 * uint64_t(k) + 16) * vocab, N * room);
             const uint64_t groups = ceil_div(std::max<uint64_t>({sample, 2 * uint64_t(k), few ? uint64_t(threads) : 0}), kWave) * kWave;
             GC_LAUNCH("top_logits", stream,

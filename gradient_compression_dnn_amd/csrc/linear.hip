@@ -75,8 +75,8 @@ gc_status check_rows(const char *fn, const void *p, uint64_t stride, uint64_t n,
 // ------------------------------------------------------------- the cut
 // A product is cut into tiles, and where those do not fill the chip, into parts of the common index as well; the
 // choice is the least of a model of the time.  Its costs are fitted to sweeps over shapes and parts of 59 products
-// from 1 to 8,192 tokens, where it is within 12% of the fastest (us, bf16: 512 x 4096 x 4096, 128 tiles in 4 parts 30,
-// in 2 32, in 8 39; 2048 x 4096 x 4096, 128 x 128 64 and 256 x 256 92; 8192 x 4096 x 16384, 1,152 and 944; the weight
+// from 1 to 8,192 tokens, where it is within 13% of the fastest (us, bf16: 512 x 4096 x 4096, 128 tiles in 4 parts 30,
+// in 2 32, in 8 39; 2048 x 4096 x 4096, 128 x 128 63 and 256 x 256 92; 8192 x 4096 x 16384, 1,152 and 944; the weight
 // gradient of 4100 x 4100 with 1024 tokens, 1,089 tiles and 289: 59 and 74).
 struct ShapeModel {
     TileShape shape;

@@ -633,7 +633,7 @@ __device__ __forceinline__ void tile_of(uint32_t t, uint32_t tiles_m, uint32_t t
 //   Matrix instructions bound long batches, at the clock that the card holds under them (1.8 GHz, 53% of the cycles
 //   busy, a third of the waves' time at the stages' barriers).  bf16, us: 8192 x 4096 x 16384 by 256 x 256 (8 waves,
 //   one workgroup a unit) 870 to 945, 1.16 to 1.26 PFLOP/s, where the library's product takes 711 to 905 by its
-//   operands' order; 2048 x 4096 x 4096 by 128 x 128 (4 waves, two a unit) 64, the library 58.  Four waves of 128 x
+//   operands' order; 2048 x 4096 x 4096 by 128 x 128 (4 waves, two a unit) 63, the library 57.  Four waves of 128 x
 //   128 each took 920 to 1,050, stages of 64 bytes in four buffers 910 to 990.  What an epilogue reads and writes is
 //   not hidden behind other tiles' products: GELU and z add 25, a residual, z, dx and dzx 215.
 //   Operands whose rows are not aligned to 16 bytes go through registers (us, and with aligned ones: 1023 x 4099 x
@@ -742,7 +742,8 @@ __global__ __launch_bounds__(kBlock) void linear_join_kernel(Product p, Cut c) {
 
 // Up to 16 tokens: a workgroup has 16 rows of W, its waves take chunks of 256 bytes of k in turn, straight from
 // memory into matrix operands, the next chunk on its way meanwhile, and their sums are added in order.  W is
-// read once, at memory's rate (1 x 4096 x 16384 bf16 26.5 us, 5.1 TB/s), and nothing is launched behind it.
+// read once, at memory's rate (us, 1 x 4096 x 16384: bf16 26.5, 5.1 TB/s, fp32 56, 4.8 TB/s; x 4096 x 4096 bf16, 2 to
+// 16 tokens 8.6 to 11.1, where W alone takes 6.6), and nothing is launched behind it.
 template <class T>
 __global__ __launch_bounds__(16 * kWave) void linear_few_kernel(Product p) {
     using Store = typename T::Store;
