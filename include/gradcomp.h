@@ -786,8 +786,8 @@ gc_status gc_muon_step(const gc_matrix_plan *mplan, const float *G, float *U, fl
  * z s(z) (SILU).  RELU's slope at 0 is 0.  They are formed in fp32 before the
  * one rounding: for fp32 within (20 + 4 a) 2^-23 of themselves, a = z^2 / 2,
  * |2 u| or |z| the exponent they take, for bf16 and fp16 within 2^-14; a slope
- * within that part of its two terms' sizes, and 2^-18.  What lies below 2^-119
- * may come out as 0.
+ * within that part of its two terms' sizes.  What lies below 2^-119 may come out
+ * as 0.
  */
 #define GC_ACT_NONE       0
 #define GC_ACT_RELU       1

@@ -8,8 +8,7 @@ of the scaling to base 2, come out of the exponential a times as large: 4 a 2^-2
 The exponential, erfc (16 steps), the reciprocal, the sums and products add 20
 2^-23, the 16-bit types' Phi 2^-16.8.  An exponential or a quotient below 2^-126 may
 be 0, which stands beside |z| <= 90: 2^-119.  A slope is a sum of two terms and is
-off by that part of their sizes, and by z d 2^-23 for the rounding of 1 - s where
-z is positive: z d <= 32 where s is not yet 1."""
+off by that part of their sizes."""
 import math
 
 import pytest
@@ -69,9 +68,27 @@ def test_relative_to_themselves(act, dtype):
         y = torch.empty_like(z[:n])
         B.gc_linear_forward(L.plan, L.layer, L.w, z[:n], y, L.ws(n), act=ACTS[act])
         within(y, want[:n], relative(z64[:n], act, D) * want[:n].abs(), D, "act", z[:n])
-    err = relative(z64, act, D) * sizes(z64, act) + torch.where(z64 > 0, 32 * 2.0 ** -23, 0.0).double()
+    err = relative(z64, act, D) * sizes(z64, act)
     one, dz, dzx = torch.ones_like(z), torch.empty_like(z), torch.empty_like(z)
     B.gc_act_grad(one, z, ACTS[act], dz)
     within(dz, slope, err, D, "slope", z)
     B.gc_linear_grad_input(L.plan, L.layer, L.w, one, None, L.ws(z.shape[0]), act=ACTS[act], z=z, dzx=dzx)
     assert torch.equal(dz, dzx)
+
+
+@pytest.mark.parametrize("act", ["gelu_tanh", "silu"])
+def test_slopes_where_the_sigmoid_is_nearly_1(act):
+    """s + z s (1 - s) d in fp32: 1 - s keeps its relative precision, so the two terms cost 16 roundings of themselves,
+    and the exponent's error, 4 a 2^-23, what it changes: s (1 - s) (1 + |z| d)."""
+    z = torch.linspace(-20, 20, 1 << 14, dtype=torch.float64).float().cuda().view(128, 128)
+    z64 = z.double()
+    v, d = (z64, 1.0) if act == "silu" else (2 * math.sqrt(2 / math.pi) * (z64 + 0.044715 * z64 ** 3), 2 * math.sqrt(2 / math.pi) * (1 + 3 * 0.044715 * z64 * z64))
+    s, rest = torch.sigmoid(v), torch.sigmoid(-v)
+    want = s + z64 * s * rest * d
+    assert float((act64(z64, act)[1] - want).abs().max()) < 1e-12
+    room = 16 * 2.0 ** -24 * (s + z64.abs() * s * rest * d) + 4 * v.abs().clamp(max=128.0) * 2.0 ** -23 * s * rest * (1 + z64.abs() * d) + 2.0 ** -119
+    dz = torch.empty_like(z)
+    say(f"slopes {act}")
+    B.gc_act_grad(torch.ones_like(z), z, ACTS[act], dz)
+    off = (dz.double() - want).abs()
+    assert bool((off <= room).all()), float((off / room).max())
