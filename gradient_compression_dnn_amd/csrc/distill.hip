@@ -12,7 +12,8 @@ namespace gc {
 
 namespace {
 
-constexpr float kLog2e = 1.44269504088896340736f;
+constexpr double kLog2eExact = 1.44269504088896340736;
+constexpr float kLog2e = static_cast<float>(kLog2eExact);
 constexpr uint32_t kNone = 0xFFFFFFFFu;
 
 // 16 bytes of a row are one vector of it.
@@ -72,6 +73,18 @@ __device__ __forceinline__ V block_sum(V x, V *lds) {
 
 // exp2 of the hardware (within a step; results below 2^-126 are 0).
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// log x, within 2^-24: a row's scalars are logarithms of up to some 20 whose differences count, so they are combined in
+// double (in fp32 a KL near 0 was off by 1e-6 T^2).
+__device__ __forceinline__ double log_of(float x) {
+    float m = __builtin_amdgcn_frexp_mantf(x);
+    int e = __builtin_amdgcn_frexp_expf(x);
+    if (m < 0.70710678f) {
+        m = m + m;
+        --e;
+    }
+    return e * 0.693147180559945309 + logf(m);
+}
 
 // A sum of exp((x_j - r) / T), r an element near the largest: differences first, so that neither
 // a large common part of the logits nor a row of the type's lowest value costs anything.  c is
@@ -199,7 +212,7 @@ constexpr uint32_t kRanked = 256;  // entries that are ranked without a selectio
 template <class T, int NT, uint32_t kList, uint32_t kMost>
 __global__ __launch_bounds__(NT, NT == 1024 ? 8 : 1) void top_kernel(const typename T::Store *__restrict__ logits,
                                                                      uint64_t stride, uint32_t vocab, uint32_t k, uint32_t groups,
-                                                                     float scale, int32_t *__restrict__ idx,
+                                                                     double inverse, int32_t *__restrict__ idx,
                                                                      float *__restrict__ val, float *__restrict__ lse) {
     constexpr int N = kVec<T>, kAhead = 4;
     __shared__ uint32_t hist[kList > 2048 ? kList : 2048];
@@ -272,7 +285,7 @@ __global__ __launch_bounds__(NT, NT == 1024 ? 8 : 1) void top_kernel(const typen
     // not below the limit: (0 - x) 0 is NaN for +Inf, which passes
     auto passes = [&](float x) { return x > -INFINITY && !((from - x) * by >= limit); };
     __syncthreads();
-    const float c2 = scale * kLog2e;
+    const float c2 = static_cast<float>(inverse * kLog2eExact);
     Sum sum = kNoTerms;
     auto look = [&](uint32_t at, const float(&v)[N]) {
         const float m = largest(v);
@@ -293,7 +306,7 @@ __global__ __launch_bounds__(NT, NT == 1024 ? 8 : 1) void top_kernel(const typen
     if (cut) look(cut_at, cut_v);
     if (lse) {
         sum = block_join<NT>(sum, c2, sums);
-        if (t == 0) lse[r] = base(sum) * scale + logf(sum.s);
+        if (t == 0) lse[r] = static_cast<float>(base(sum) * inverse + log_of(sum.s));
     }
     __syncthreads();
     const bool all_spots = spotted <= kList;
@@ -374,7 +387,8 @@ struct Distill {
     uint64_t stride, idx_stride, t_stride, dstride;
     uint32_t vocab, k;
     int id_type, t_type, rest, bits;
-    float inv_t, kd, kd_slope, ce, grad;  // 1 / T; kd T^2 and kd T
+    double inverse;                       // 1 / T
+    float kd, kd_slope, ce, grad;         // kd T^2 and kd T
 };
 
 __device__ __forceinline__ int64_t id_at(const void *ids, int type, uint64_t at) {
@@ -554,7 +568,7 @@ __global__ __launch_bounds__(NT) void distill_kernel(Distill d) {
         bool again = !d.bits;  // a column may be named again
         for (uint32_t e = t; e < K; e += NT) {
             const uint32_t c = col[e];
-            q[e] = c != kNone ? expf(d.rest ? q[e] * d.inv_t - tlse : (q[e] - tmax) * d.inv_t) : 0.0f;
+            q[e] = c != kNone ? expf(static_cast<float>(d.rest ? q[e] * d.inverse - tlse : (static_cast<double>(q[e]) - tmax) * d.inverse)) : 0.0f;
             qsum += q[e];
             if (d.bits && c != kNone) again = again || (atomicOr(&named[c / 32], 1u << (c % 32)) >> (c % 32) & 1);
         }
@@ -593,7 +607,7 @@ __global__ __launch_bounds__(NT) void distill_kernel(Distill d) {
         for (uint32_t e = t + NT; e < K; e += NT) f(e, zk[e]);
     };
     // the row, or the rest of it: sums of exp at 1 / T and, for another softmax of the labels, at 1
-    const float c2 = d.inv_t * kLog2e, c1 = kTwo ? kLog2e : c2;
+    const float c2 = static_cast<float>(d.inverse * kLog2eExact), c1 = kTwo ? kLog2e : c2;
     Sum s2 = kNoTerms, s1 = kNoTerms;
     z.template each<true>([&](uint32_t c, float(&v)[N], uint32_t) {
         if (rest) {
@@ -623,7 +637,8 @@ __global__ __launch_bounds__(NT) void distill_kernel(Distill d) {
     }
     // where nothing is left, as for entries that name all columns but masked ones, rr is r2 and rest2.s 0
     const float r2 = base(all2), r1 = base(all1), rr = rest2.r == -INFINITY ? r2 : rest2.r;
-    const float held = rest && rest2.s != 0.0f ? fmaxf(static_cast<float>(1.0 - qsum), 0.0f) : 0.0f;
+    const double held_mass = rest && rest2.s != 0.0f ? fmax(1.0 - qsum, 0.0) : 0.0;
+    const float held = static_cast<float>(held_mass);
     if (out) {
         // the gradient: kd T (mass p_j - held p_j / p_r - q_j) + ce (softmax_j - [j = label])
         const float mass = entries ? static_cast<float>(qsum) + held : 0.0f, f = weight * d.grad;
@@ -662,19 +677,19 @@ __global__ __launch_bounds__(NT) void distill_kernel(Distill d) {
         if (own_label && t == NT - 1) set(label, zl, 0.0f, true);
     }
     // the loss, while the gradient is on its way; NaN for a row without a distribution, also where no entry has a term
-    float loss = all2.s > 0.0f ? 0.0f : NAN;
-    const float log2s = logf(all2.s);
+    double loss = all2.s > 0.0f ? 0.0 : NAN;
     if (entries) {
-        double kl = 0.0;
+        const double log2s = log_of(all2.s);
+        double kl = 0.0;  // sum of q (log q - z / T), with the row's log sum behind it
         each_own([&](uint32_t e, float x) {
-            if (q[e] != 0.0f) kl += q[e] * (logf(q[e]) - ((x - r2) * d.inv_t - log2s));
+            if (q[e] != 0.0f) kl += q[e] * (log_of(q[e]) - (static_cast<double>(x) - r2) * d.inverse);
         });
-        kl = block_sum<NT>(kl, redd);
-        if (held > 0.0f) kl += held * (logf(held) - ((rr - r2) * d.inv_t + logf(rest2.s) - log2s));
-        loss = loss + d.kd * static_cast<float>(kl);
+        kl = block_sum<NT>(kl, redd) + qsum * log2s;
+        if (held > 0.0f) kl += held_mass * (log_of(held) - ((static_cast<double>(rr) - r2) * d.inverse + log_of(rest2.s) - log2s));
+        loss = loss + d.kd * kl;
     }
-    if (label != kNone) loss = loss + d.ce * (logf(all1.s) - (kTwo ? zl - r1 : (zl - r1) * d.inv_t));
-    if (t == 0) d.loss[r] = weight * loss;
+    if (label != kNone) loss = loss + d.ce * (log_of(all1.s) - (static_cast<double>(zl) - r1));
+    if (t == 0) d.loss[r] = static_cast<float>(weight * loss);
 }
 
 // --------------------------------------------------------------- host side
@@ -701,7 +716,7 @@ gc_status check_sizes(const char *fn, int type, uint64_t n, uint32_t vocab, uint
     if (vocab < 1) return fail(fn, GC_EINVAL, "vocab must be at least 1");
     if (vocab > GC_MAX_VOCAB) return fail(fn, GC_ENOTSUP, "vocab must be <= GC_MAX_VOCAB");
     if (k > GC_MAX_TOP_LOGITS) return fail(fn, GC_ENOTSUP, "k must be <= GC_MAX_TOP_LOGITS");
-    const float inverse = kLog2e / temperature;  // the largest that the kernels form
+    const float inverse = static_cast<float>(1.0 / temperature * kLog2eExact);  // as the kernels form it
     if (!(temperature > 0.0f) || !(temperature - temperature == 0.0f) || !(inverse - inverse == 0.0f))
         return fail(fn, GC_EINVAL, "temperature must be positive, and finite with its inverse");
     if (n >= kMaxRows) return fail(fn, GC_ERANGE, "n_rows must be < 2^22");
@@ -744,7 +759,7 @@ extern "C" gc_status gc_top_logits(const void *logits, int type, uint64_t stride
             GC_LAUNCH("top_logits", stream,
                       kernel<<<static_cast<unsigned>(n_rows), threads, 0, stream>>>(
                           static_cast<const typename T::Store *>(logits), stride, vocab, k, static_cast<uint32_t>(umin64(groups, 2 * room)),
-                          1.0f / temperature, idx, val, lse));
+                          1.0 / temperature, idx, val, lse));
         };
         if (!small) with(top_kernel<T, 1024, kBigList, GC_MAX_TOP_LOGITS>, 1024, kBigList);
         else if (few) with(top_kernel<T, 1024, kSmallList, kSmallK>, 1024, kSmallList);
@@ -791,7 +806,7 @@ extern "C" gc_status gc_distill_loss(const void *logits, int type, uint64_t stri
             return fail(fn, GC_EINVAL, "dlogits in place of logits must have their stride");
     }
     Distill d{logits, idx, t, labels, t_lse, weights, loss, dlogits, stride, idx_stride, t_stride, dstride, vocab, k, idx_type, t_type,
-              opt->mode == GC_DISTILL_REST, 0, 1.0f / T, kd, opt->kd_weight * T, opt->ce_weight, opt->grad_scale};
+              opt->mode == GC_DISTILL_REST, 0, 1.0 / T, kd, opt->kd_weight * T, opt->ce_weight, opt->grad_scale};
     if (!k) d.kd = d.kd_slope = 0.0f;
     d.bits = k && (d.rest || vocab <= kBitsVocab);
     const size_t lds = 16 * ((size_t(k) + 3) & ~size_t(3)) + (d.bits ? 4 * ((size_t(vocab) + 31) / 32 + 1) : 0);

@@ -920,7 +920,7 @@ gc_status gc_top_logits(const void *logits, int type, uint64_t stride, uint64_t 
  *     may be logits (with its stride).
  * k == 0 leaves the labels' term alone.  n_rows == 0 enqueues nothing.
  * Sums are fp32 (over the teacher's entries in double) in an order that the
- * sizes fix.
+ * sizes fix; their logarithms, within 2^-24, are combined in double.
  * Errors: as gc_top_logits; GC_EINVAL also for unknown types, a mode,
  *         kd_weight, ce_weight or grad_scale not finite, t_lse missing,
  *         reserved not 0.
