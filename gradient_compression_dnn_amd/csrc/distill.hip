@@ -479,7 +479,7 @@ struct Row {
 // beside them, once, and the gradient is formed from the registers that hold it: memory bounds it, one read and one
 // write of the logits.  us, 4096 rows of bf16, k = 64: 131072 columns 465 (a copy's rate: 421), 131071 505 (rows
 // start anywhere), 65536 213, 32000 118; the loss alone at 131071 235 (211).  Labels at another temperature take a
-// second exponential an element: 605.  700 rows of 10000 fp32, k = 32: 22, most of it a launch, a row's latency and
+// second exponential an element: 610.  700 rows of 10000 fp32, k = 32: 22, most of it a launch, a row's latency and
 // the sums over 16 vectors a thread, of which the row fills 10.
 // LDS: columns, q, q summed over a column's entries, and student logits of the entries, and (GC_DISTILL_REST, or up
 // to kBitsVocab columns) a bit per column that an entry names.
